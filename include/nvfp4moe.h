@@ -459,6 +459,72 @@ nvfp4_status moe_grouped_nvfp4_ffn_static(const void *x, int64_t T, int64_t H, i
 size_t moe_grouped_nvfp4_ffn_static_max_bytes(void);
 
 /*
+ * FP8 block-scaled operators.  Mixed checkpoints keep part of their dense
+ * projections in 8-bit floating point next to NVFP4 (Eider page, "Qwen3.8
+ * 27B": FP8 attention, LM head and final MLP blocks).  An FP8 block-scaled
+ * matrix X [R, C] is
+ *   codes  uint8 [R, C]  row-major OCP E4M3 bytes (as for the block scales);
+ *   scales float [ceil(R / b), ceil(C / 128)]  row-major, one per block of
+ *          b x 128 elements, b = 128 for weights and 1 for activations
+ *          (blocks at the edges are smaller);
+ *   and X[r][c] = e4m3(code) * scale[r / b][c / 128].
+ * Codes must not be NaN (0x7F, 0xFF); scales must be finite.  C must be a
+ * multiple of 32, R is any number of rows.
+ */
+typedef struct {
+  const uint8_t *codes;    /* [rows, cols] E4M3                             */
+  const float *scales;     /* [ceil(rows / 128), ceil(cols / 128)]          */
+  int64_t rows, cols;
+} fp8_matrix;
+
+/*
+ * fp8_block_quantize: quantise x [rows, cols] (row stride ld_x elements, bf16
+ * or f32) to E4M3 codes [rows, cols] and one scale per block of block_rows x
+ * 128 (block_rows 1: activations, 128: weights).  Per block, every step an
+ * fp32 operation rounded to nearest-even:
+ *   a = amax |x|;  s = a > 0 ? max(a / 448, 2^-126) : 1;  i = 1 / s;
+ *   code = E4M3_rne_saturate(x * i).
+ * Requires cols % 32 == 0, ld_x >= cols, ld_x % 8 == 0, block_rows 1 or 128
+ * and rows * ceil(cols / 128) <= 2^27.
+ */
+nvfp4_status fp8_block_quantize(const void *x, nvfp4_dtype x_dtype, int64_t rows, int64_t cols,
+                                int64_t ld_x, int32_t block_rows, uint8_t *codes, float *scales,
+                                hipStream_t stream);
+
+/*
+ * fp8_block_linear: y [M, N] = x [M, K] . W^T for an FP8 W [N, K]:
+ *   y[m][n] = sum_b s_x[m][b] s_w[n / 128][b] sum_{k in block b} xq[m][k] wq[n][k]
+ * with exact products and fp32 sums, in an order fixed by the shapes; y is
+ * bf16 (round-to-nearest-even) or f32.  x_scales NULL: x is bf16 [M, K],
+ * contiguous, quantised online exactly as fp8_block_quantize with
+ * block_rows = 1.  x_scales set: x holds E4M3 codes [M, K] with x_scales
+ * [M, ceil(K / 128)] (quantised once for several projections).
+ * Requires K % 32 == 0, M, N <= 2^24.
+ * workspace: fp8_block_linear_workspace_size bytes (device, 16-byte
+ * aligned), scratch only; quantised: x_scales is set.
+ */
+nvfp4_status fp8_block_linear(const void *x, const float *x_scales, int64_t M,
+                              const fp8_matrix *w, void *y, nvfp4_dtype y_dtype, void *workspace,
+                              size_t workspace_bytes, hipStream_t stream);
+size_t fp8_block_linear_workspace_size(int64_t M, int64_t N, int64_t K, int quantised);
+
+/*
+ * fp8_block_mlp: the gated MLP with FP8 weights, x [T, H] bf16, w_gate and
+ * w_up [I, H], w_down [H, I]:
+ *   h_t = bf16_rne( silu(x_t Wg^T) * (x_t Wu^T) )
+ *   y_t = h_t Wd^T
+ * both products as fp8_block_linear computes them (x and h quantised online
+ * per row and 128 columns).  y [T, H] bf16 or f32.  Requires H % 32 == 0,
+ * I % 32 == 0, T, H, I <= 2^24.  workspace: fp8_block_mlp_workspace_size
+ * bytes (device, 16-byte aligned), scratch only.
+ */
+nvfp4_status fp8_block_mlp(const void *x, int64_t T, const fp8_matrix *w_gate,
+                           const fp8_matrix *w_up, const fp8_matrix *w_down, void *y,
+                           nvfp4_dtype y_dtype, void *workspace, size_t workspace_bytes,
+                           hipStream_t stream);
+size_t fp8_block_mlp_workspace_size(int64_t T, int64_t H, int64_t I);
+
+/*
  * moe_grouped_nvfp4_ffn_debug_h: a test aid (not part of the computation)
  * for checking h element by element where it decides an integer: its bf16
  * rounding and, in W4A4, its NVFP4 codes (Qwen3.8-Flash-Next-NVFP4-SSD-

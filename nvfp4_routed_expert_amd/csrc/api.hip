@@ -267,6 +267,59 @@ SharedWs carve_shared(Carver &c, int64_t T, int64_t H, int64_t I) {
   return w;
 }
 
+constexpr int64_t kFp8MaxRows = (int64_t)1 << 24;
+struct Fp8LinearWs {
+  F8Plan plan;
+  uint8_t *xq;
+  float *xs;
+  float *split;   // partial sums of a K split
+};
+// (sized for either output type: the workspace query does not take it)
+Fp8LinearWs carve_fp8_linear(Carver &c, int64_t M, int64_t N, int64_t K, bool quantised,
+                             OutType out) {
+  Fp8LinearWs w = {};
+  const bool inside = f8_gemv_supported(M);
+  const bool own = !quantised && !f8_gemv_quantises(M);   // x quantised by a launch of its own
+  w.xq = c.take<uint8_t>(own ? (size_t)(M * K) : 0);
+  w.xs = c.take<float>(own ? (size_t)(M * ((K + 127) / 128)) : 0);
+  if (!inside) {
+    w.plan = f8_gemm_plan(false, out, M, N, K);
+    const F8Plan other = f8_gemm_plan(
+        false, out == OutType::F32 ? OutType::BF16 : OutType::F32, M, N, K);
+    w.split = c.take<float>(w.plan.partial_floats > other.partial_floats ? w.plan.partial_floats
+                                                                         : other.partial_floats);
+  }
+  return w;
+}
+struct Fp8MlpWs {
+  F8Plan up_plan, down_plan;
+  uint8_t *xq, *hq;
+  uint16_t *h;    // bf16 h (few rows)
+  float *xs, *hs;
+  float *split;
+};
+Fp8MlpWs carve_fp8_mlp(Carver &c, int64_t T, int64_t H, int64_t I, OutType out) {
+  Fp8MlpWs w = {};
+  const bool few = f8_gemv_supported(T), own = !f8_gemv_quantises(T);
+  w.xq = c.take<uint8_t>(own ? (size_t)(T * H) : 0);
+  w.xs = c.take<float>(own ? (size_t)(T * ((H + 127) / 128)) : 0);
+  w.h = c.take<uint16_t>(few ? (size_t)(T * I) : 0);
+  w.hq = c.take<uint8_t>(own ? (size_t)(T * I) : 0);
+  w.hs = c.take<float>(own ? (size_t)(T * ((I + 127) / 128)) : 0);
+  if (!few) {
+    w.up_plan = f8_gemm_plan(true, OutType::BF16, T, I, H);
+    w.down_plan = f8_gemm_plan(false, out, T, H, I);
+    const F8Plan other = f8_gemm_plan(
+        false, out == OutType::F32 ? OutType::BF16 : OutType::F32, T, H, I);
+    size_t n = w.up_plan.partial_floats;
+    if (w.down_plan.partial_floats > n) n = w.down_plan.partial_floats;
+    if (other.partial_floats > n) n = other.partial_floats;
+    w.split = c.take<float>(n);
+  }
+  return w;
+}
+OutType out_type(nvfp4_dtype t) { return t == NVFP4_DT_F32 ? OutType::F32 : OutType::BF16; }
+
 }  // namespace
 
 extern "C" {
@@ -1312,6 +1365,190 @@ nvfp4_status moe_grouped_nvfp4_ffn_static(const void *x, int64_t T, int64_t H, i
   return moe_grouped_nvfp4_ffn(x, T, H, I, E, k, topk_ids, topk_weights, expert_offsets,
                                sorted_pairs, w, act, act_global_mode, act_globals, y, y_dtype,
                                ws, need > 0 ? kStaticScratchBytes : 0, stream);
+}
+
+// ---- FP8 block-scaled operators ---------------------------------------------------------
+
+static nvfp4_status check_fp8_matrix(const fp8_matrix *w, const char *name) {
+  if (!w) return fail(NVFP4_ERR_INVALID_ARGUMENT, "%s is NULL", name);
+  if (!w->codes || !w->scales)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "%s->%s is NULL", name, w->codes ? "scales" : "codes");
+  if (w->rows < 1) return fail(NVFP4_ERR_INVALID_ARGUMENT, "%s->rows < 1", name);
+  if (w->rows > kFp8MaxRows)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s->rows exceeds 2^24", name);
+  TRY(check_k(w->cols, name));
+  if (!aligned16(w->codes) || !aligned16(w->scales))
+    return fail(NVFP4_ERR_MISALIGNED, "%s->%s is not 16-byte aligned", name,
+                aligned16(w->codes) ? "scales" : "codes");
+  return NVFP4_OK;
+}
+
+nvfp4_status fp8_block_quantize(const void *x, nvfp4_dtype x_dtype, int64_t rows, int64_t cols,
+                                int64_t ld_x, int32_t block_rows, uint8_t *codes, float *scales,
+                                hipStream_t stream) {
+  g_last_error[0] = 0;
+  if (rows > 0) {   // (an empty batch may pass NULL for its empty arrays)
+    CHECK_NULL(x);
+    CHECK_NULL(codes);
+    CHECK_NULL(scales);
+  }
+  if (x_dtype != NVFP4_DT_BF16 && x_dtype != NVFP4_DT_F32)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "x_dtype %d is not BF16 or F32", (int)x_dtype);
+  if (block_rows != 1 && block_rows != 128)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "block_rows %d is not 1 or 128", (int)block_rows);
+  if (rows < 0) return fail(NVFP4_ERR_INVALID_ARGUMENT, "rows = %lld < 0", (long long)rows);
+  TRY(check_k(cols, "cols"));
+  if (ld_x < cols || ld_x % 8 != 0)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "ld_x = %lld must be >= cols and a multiple of 8",
+                (long long)ld_x);
+  if (rows > ((int64_t)1 << 27) / ((cols + 127) / 128))
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "rows * ceil(cols / 128) exceeds 2^27");
+  CHECK_ALIGN(x);
+  CHECK_ALIGN(codes);
+  CHECK_ALIGN(scales);
+  if (rows == 0) return NVFP4_OK;
+  LAUNCH(launch_f8_quantize(x, x_dtype == NVFP4_DT_BF16 ? InType::BF16 : InType::F32, rows, cols,
+                            ld_x, block_rows, codes, scales, stream),
+         "fp8 quantize");
+  return NVFP4_OK;
+}
+
+size_t fp8_block_linear_workspace_size(int64_t M, int64_t N, int64_t K, int quantised) {
+  if (M < 1 || N < 1 || K < 1) return 0;
+  Carver c(nullptr);
+  carve_fp8_linear(c, M, N, K, quantised != 0, OutType::BF16);
+  return c.used;
+}
+
+nvfp4_status fp8_block_linear(const void *x, const float *x_scales, int64_t M,
+                              const fp8_matrix *w, void *y, nvfp4_dtype y_dtype, void *workspace,
+                              size_t workspace_bytes, hipStream_t stream) {
+  g_last_error[0] = 0;
+  if (M > 0) {
+    CHECK_NULL(x);
+    CHECK_NULL(y);
+  }
+  TRY(check_fp8_matrix(w, "w"));
+  if (M < 0) return fail(NVFP4_ERR_INVALID_ARGUMENT, "M = %lld < 0", (long long)M);
+  if (M > kFp8MaxRows) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "M exceeds 2^24");
+  if (y_dtype != NVFP4_DT_BF16 && y_dtype != NVFP4_DT_F32)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "y_dtype %d is not BF16 or F32", (int)y_dtype);
+  CHECK_ALIGN(x);
+  CHECK_ALIGN(x_scales);
+  CHECK_ALIGN(y);
+  const int64_t K = w->cols, N = w->rows;
+  TRY(check_workspace(workspace, workspace_bytes,
+                      fp8_block_linear_workspace_size(M, N, K, x_scales != nullptr)));
+  if (M == 0) return NVFP4_OK;
+  Carver c(workspace);
+  const Fp8LinearWs ws =
+      carve_fp8_linear(c, M, N, K, x_scales != nullptr, out_type(y_dtype));
+  const void *xq = x;
+  const float *xs = x_scales;
+  if (!x_scales && !f8_gemv_quantises(M)) {
+    LAUNCH(launch_f8_quantize(x, InType::BF16, M, K, K, 1, ws.xq, ws.xs, stream), "fp8 quantize");
+    xq = ws.xq;
+    xs = ws.xs;
+  }
+  if (f8_gemv_supported(M)) {
+    const F8GemvArgs a = {xq, xs, (int)M, {w->codes, nullptr}, {w->scales, nullptr},
+                          (int)N, (int)K, y, out_type(y_dtype)};
+    LAUNCH(launch_f8_gemv(false, a, stream), "fp8 gemv");
+    return NVFP4_OK;
+  }
+  F8GemmArgs a = {};
+  a.x = static_cast<const uint8_t *>(xq);
+  a.xs = xs;
+  a.M = M;
+  a.w[0] = w->codes;
+  a.ws[0] = w->scales;
+  a.N = (int)N;
+  a.K = (int)K;
+  a.out = y;
+  a.out_type = out_type(y_dtype);
+  a.partial = ws.split;
+  LAUNCH(launch_f8_gemm(false, a, ws.plan, stream), "fp8 gemm");
+  return NVFP4_OK;
+}
+
+size_t fp8_block_mlp_workspace_size(int64_t T, int64_t H, int64_t I) {
+  if (T < 1 || H < 1 || I < 1) return 0;
+  Carver c(nullptr);
+  carve_fp8_mlp(c, T, H, I, OutType::BF16);
+  return c.used;
+}
+
+nvfp4_status fp8_block_mlp(const void *x, int64_t T, const fp8_matrix *w_gate,
+                           const fp8_matrix *w_up, const fp8_matrix *w_down, void *y,
+                           nvfp4_dtype y_dtype, void *workspace, size_t workspace_bytes,
+                           hipStream_t stream) {
+  g_last_error[0] = 0;
+  if (T > 0) {
+    CHECK_NULL(x);
+    CHECK_NULL(y);
+  }
+  TRY(check_fp8_matrix(w_gate, "w_gate"));
+  TRY(check_fp8_matrix(w_up, "w_up"));
+  TRY(check_fp8_matrix(w_down, "w_down"));
+  const int64_t H = w_gate->cols, I = w_gate->rows;
+  if (w_up->rows != I || w_up->cols != H || w_down->rows != H || w_down->cols != I)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT,
+                "w_up is not [%lld, %lld] or w_down not [%lld, %lld] (from w_gate)", (long long)I,
+                (long long)H, (long long)H, (long long)I);
+  if (T < 0) return fail(NVFP4_ERR_INVALID_ARGUMENT, "T = %lld < 0", (long long)T);
+  if (T > kFp8MaxRows) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "T exceeds 2^24");
+  if (y_dtype != NVFP4_DT_BF16 && y_dtype != NVFP4_DT_F32)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "y_dtype %d is not BF16 or F32", (int)y_dtype);
+  CHECK_ALIGN(x);
+  CHECK_ALIGN(y);
+  TRY(check_workspace(workspace, workspace_bytes, fp8_block_mlp_workspace_size(T, H, I)));
+  if (T == 0) return NVFP4_OK;
+  Carver c(workspace);
+  const Fp8MlpWs ws = carve_fp8_mlp(c, T, H, I, out_type(y_dtype));
+  const bool inside = f8_gemv_quantises(T);
+  if (!inside)
+    LAUNCH(launch_f8_quantize(x, InType::BF16, T, H, H, 1, ws.xq, ws.xs, stream), "fp8 quantize");
+  if (f8_gemv_supported(T)) {
+    const F8GemvArgs g = {inside ? x : ws.xq, inside ? nullptr : ws.xs, (int)T,
+                          {w_gate->codes, w_up->codes}, {w_gate->scales, w_up->scales},
+                          (int)I, (int)H, ws.h, OutType::BF16};
+    LAUNCH(launch_f8_gemv(true, g, stream), "fp8 gate/up");
+    if (!inside)
+      LAUNCH(launch_f8_quantize(ws.h, InType::BF16, T, I, I, 1, ws.hq, ws.hs, stream),
+             "fp8 quantize");
+    const F8GemvArgs d = {inside ? static_cast<const void *>(ws.h) : ws.hq,
+                          inside ? nullptr : ws.hs, (int)T, {w_down->codes, nullptr},
+                          {w_down->scales, nullptr}, (int)H, (int)I, y, out_type(y_dtype)};
+    LAUNCH(launch_f8_gemv(false, d, stream), "fp8 down");
+    return NVFP4_OK;
+  }
+  F8GemmArgs a = {};
+  a.x = ws.xq;
+  a.xs = ws.xs;
+  a.M = T;
+  a.w[0] = w_gate->codes;
+  a.ws[0] = w_gate->scales;
+  a.w[1] = w_up->codes;
+  a.ws[1] = w_up->scales;
+  a.N = (int)I;
+  a.K = (int)H;
+  a.hq = ws.hq;
+  a.hs = ws.hs;
+  a.partial = ws.split;
+  LAUNCH(launch_f8_gemm(true, a, ws.up_plan, stream), "fp8 gate/up");
+  F8GemmArgs d = {};
+  d.x = ws.hq;
+  d.xs = ws.hs;
+  d.M = T;
+  d.w[0] = w_down->codes;
+  d.ws[0] = w_down->scales;
+  d.N = (int)H;
+  d.K = (int)I;
+  d.out = y;
+  d.out_type = out_type(y_dtype);
+  d.partial = ws.split;
+  LAUNCH(launch_f8_gemm(false, d, ws.down_plan, stream), "fp8 down");
+  return NVFP4_OK;
 }
 
 }  // extern "C"

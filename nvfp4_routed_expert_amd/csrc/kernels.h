@@ -319,6 +319,55 @@ hipError_t launch_moe_plan(const int32_t *offsets, int E, int bm, int4 *mblocks,
 hipError_t launch_combine(const float *ypair, int64_t T, int64_t H, int k, const int32_t *ids,
                           int E, void *y, OutType t, hipStream_t s);
 
+// ---- FP8 block-scaled operators (fp8quant.hip, fp8gemm.hip, fp8gemv.hip) -----------------------
+
+// x [rows, cols] (row stride ld) -> E4M3 codes [rows, cols] and one scale per
+// block of block_rows (1 or 128) x 128.
+hipError_t launch_f8_quantize(const void *x, InType t, int64_t rows, int64_t cols, int64_t ld,
+                              int block_rows, uint8_t *codes, float *scales, hipStream_t s);
+
+struct F8GemmArgs {
+  const uint8_t *x;       // codes [M, K]
+  const float *xs;        // [M, ceil(K / 128)]
+  int64_t M;
+  const uint8_t *w[2];    // codes [N, K]; matrix 1 is `up` in the gate/up form
+  const float *ws[2];     // [ceil(N / 128), ceil(K / 128)]
+  int N, K;
+  void *out;              // linear: y [M, N]
+  OutType out_type;
+  uint8_t *hq;            // gate/up: h's codes [M, N] and scales [M, ceil(N / 128)]
+  float *hs;
+  int ksplit;
+  float *partial;         // [ksplit][M][N, or 2 N: gate then up sums]
+};
+// Tokens of a tile and K parts for a problem; a split needs partial_floats
+// floats of workspace.
+struct F8Plan {
+  int bm = 256;
+  bool exact = false;   // fp32 sums of exact products (fp32 outputs)
+  int ksplit = 1;
+  size_t partial_floats = 0;
+};
+F8Plan f8_gemm_plan(bool swiglu, OutType out, int64_t M, int64_t N, int64_t K);
+hipError_t launch_f8_gemm(bool swiglu, const F8GemmArgs &a, const F8Plan &pl, hipStream_t s);
+
+// The same product for M <= 64 rows (fp8gemv.hip).  xs null: x is bf16 [M, K]
+// and is quantised inside (M <= 16); otherwise x holds codes.  Gate/up form:
+// out = h, bf16 [M, N].
+struct F8GemvArgs {
+  const void *x;
+  const float *xs;
+  int M;
+  const uint8_t *w[2];
+  const float *ws[2];
+  int N, K;
+  void *out;
+  OutType out_type;
+};
+bool f8_gemv_supported(int64_t M);
+bool f8_gemv_quantises(int64_t M);
+hipError_t launch_f8_gemv(bool swiglu, const F8GemvArgs &a, hipStream_t s);
+
 // ---- measurement aid (probe.hip) ---------------------------------------------------
 
 // Streaming read of `bytes` (a multiple of 16) at buf; sink: >= 1024 words.

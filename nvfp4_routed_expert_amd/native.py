@@ -37,6 +37,10 @@ class Matrix(ctypes.Structure):
                 ("rows", _i64), ("cols", _i64)]
 
 
+class Fp8Matrix(ctypes.Structure):
+    _fields_ = [("codes", _vp), ("scales", _vp), ("rows", _i64), ("cols", _i64)]
+
+
 class ExpertWeightsC(ctypes.Structure):
     _fields_ = [("gate_codes", _vp), ("up_codes", _vp), ("down_codes", _vp),
                 ("gate_scales", _vp), ("up_scales", _vp), ("down_scales", _vp),
@@ -96,6 +100,14 @@ def lib():
             "moe_grouped_nvfp4_ffn_debug_h": (ctypes.c_int, [_i64, _i64, _i64, _i32, _i32, _i32,
                                                              _i32, ctypes.POINTER(_sz),
                                                              ctypes.POINTER(_sz)]),
+            "fp8_block_quantize": (_i32, [_vp, _i32, _i64, _i64, _i64, _i32, _vp, _vp, _vp]),
+            "fp8_block_linear": (_i32, [_vp, _vp, _i64, ctypes.POINTER(Fp8Matrix), _vp, _i32, _vp,
+                                        _sz, _vp]),
+            "fp8_block_linear_workspace_size": (_sz, [_i64, _i64, _i64, ctypes.c_int]),
+            "fp8_block_mlp": (_i32, [_vp, _i64, ctypes.POINTER(Fp8Matrix),
+                                     ctypes.POINTER(Fp8Matrix), ctypes.POINTER(Fp8Matrix), _vp,
+                                     _i32, _vp, _sz, _vp]),
+            "fp8_block_mlp_workspace_size": (_sz, [_i64, _i64, _i64]),
             "nvfp4_set_ffn_stage_events": (None, [_vp]),
             "nvfp4_set_ffn_separate_h_quant": (None, [ctypes.c_int]),
             "nvfp4_read_probe": (_i32, [_vp, _sz, _vp, _vp]),
@@ -125,6 +137,8 @@ def exported_symbols():
             "moe_grouped_nvfp4_ffn_workspace_size", "moe_grouped_nvfp4_ffn_debug_h",
             "moe_route_ffn_decode", "moe_route_ffn_decode_workspace_size",
             "moe_grouped_nvfp4_ffn_static", "moe_grouped_nvfp4_ffn_static_max_bytes",
+            "fp8_block_quantize", "fp8_block_linear", "fp8_block_linear_workspace_size",
+            "fp8_block_mlp", "fp8_block_mlp_workspace_size",
             "nvfp4_set_ffn_stage_events",
             "nvfp4_set_ffn_separate_h_quant", "nvfp4_read_probe",
             "nvfp4_status_string", "nvfp4_last_error"]
@@ -151,6 +165,10 @@ def _workspace(nbytes, device, workspace=None):
             raise ValueError(f"workspace needs {nbytes} bytes")
         return workspace
     return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+
+
+def _round_up(n, m):
+    return (n + m - 1) // m * m
 
 
 def _dt(dtype):
@@ -509,6 +527,121 @@ def moe_grouped_nvfp4_ffn_static(x, weights: ExpertWeights, topk_ids, topk_weigh
         _ptr(sorted_pairs), ctypes.byref(cw), act, mode, _ptr(ag), _ptr(y), _dt(y.dtype),
         _stream()))
     return y, ag
+
+
+# ---- FP8 block-scaled operators -----------------------------------------------
+
+
+def _device_of(x, /, **tensors):
+    """The cuda device of x; every other tensor must be contiguous on it."""
+    if not x.is_cuda:
+        raise ValueError(f"tensors must be on a cuda device, got {x.device}")
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.device != x.device:
+            raise ValueError(f"{name} is on {t.device}, x on {x.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    return x.device
+
+
+def _expect(name, t, shape, dtype):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+
+
+def _fp8_blocks(n):
+    return (n + 127) // 128
+
+
+def _fp8_matrix(name, codes, scales):
+    """The C view of E4M3 codes [N, K] and their 128 x 128 block scales."""
+    if codes.dim() != 2:
+        raise ValueError(f"{name} codes must be [rows, cols], got {tuple(codes.shape)}")
+    n, k = codes.shape
+    _expect(f"{name} codes", codes, (n, k), torch.uint8)
+    _expect(f"{name} scales", scales, (_fp8_blocks(n), _fp8_blocks(k)), torch.float32)
+    return Fp8Matrix(codes.data_ptr(), scales.data_ptr(), n, k)
+
+
+def fp8_block_quantize(x, block_rows=1, out=None):
+    """Quantise x [rows, cols] (bf16/f32, cuda, unit column stride) to E4M3
+    with one fp32 scale per block of block_rows x 128 (1: activations, 128:
+    weights).  Returns (codes uint8 [rows, cols], scales [ceil(rows /
+    block_rows), ceil(cols / 128)])."""
+    if x.dim() != 2:
+        raise ValueError(f"x must be [rows, cols], got {tuple(x.shape)}")
+    rows, cols = x.shape
+    if cols > 1 and x.stride(1) != 1:
+        raise ValueError("x must have unit column stride")
+    if block_rows not in (1, 128):
+        raise ValueError(f"block_rows must be 1 or 128, got {block_rows}")
+    shape = (rows if block_rows == 1 else _fp8_blocks(rows), _fp8_blocks(cols))
+    if out is None:
+        codes = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
+        scales = torch.empty(shape, dtype=torch.float32, device=x.device)
+    else:
+        codes, scales = out
+        _expect("codes", codes, (rows, cols), torch.uint8)
+        _expect("scales", scales, shape, torch.float32)
+    with torch.cuda.device(_device_of(x, codes=codes, scales=scales)):
+        ld = x.stride(0) if rows > 1 else _round_up(cols, 8)
+        _check(lib().fp8_block_quantize(_ptr(x), _dt(x.dtype), rows, cols, ld, block_rows,
+                                        _ptr(codes), _ptr(scales), _stream()))
+    return codes, scales
+
+
+def fp8_block_linear(x, codes, scales, x_scales=None, out_dtype=torch.bfloat16, workspace=None,
+                     out=None):
+    """y [M, N] = x [M, K] . W [N, K]^T for FP8 W (codes, scales from
+    fp8_block_quantize(w, 128)).  x: bf16, quantised online per row and 128
+    columns; or with x_scales, the codes of fp8_block_quantize(x)."""
+    if x.dim() != 2 or x.shape[1] != codes.shape[-1]:
+        raise ValueError(f"x {tuple(x.shape)} does not match W {tuple(codes.shape)}")
+    M, K = x.shape
+    m = _fp8_matrix("W", codes, scales)
+    if x_scales is None:
+        _expect("x", x, (M, K), torch.bfloat16)
+    else:
+        _expect("x", x, (M, K), torch.uint8)
+        _expect("x_scales", x_scales, (M, _fp8_blocks(K)), torch.float32)
+    dev = _device_of(x, x=x, codes=codes, scales=scales, x_scales=x_scales, out=out,
+                     workspace=workspace)
+    y = out if out is not None else torch.empty((M, m.rows), dtype=out_dtype, device=dev)
+    _expect("out", y, (M, m.rows), y.dtype)
+    L = lib()
+    with torch.cuda.device(dev):
+        ws = _workspace(L.fp8_block_linear_workspace_size(M, m.rows, K, x_scales is not None), dev,
+                        workspace)
+        _check(L.fp8_block_linear(_ptr(x), _ptr(x_scales), M, ctypes.byref(m), _ptr(y),
+                                  _dt(y.dtype), _ptr(ws), ws.numel() * ws.element_size(),
+                                  _stream()))
+    return y
+
+
+def fp8_block_mlp(x, gate, up, down, out_dtype=torch.bfloat16, workspace=None, out=None):
+    """y [T, H] = down(silu(x Wg^T) * (x Wu^T)) with FP8 weights: gate, up
+    ([I, H]) and down ([H, I]) are (codes, scales) pairs from
+    fp8_block_quantize(w, 128); x [T, H] bf16 and h are quantised online."""
+    mats = {n: _fp8_matrix(n, *p) for n, p in (("gate", gate), ("up", up), ("down", down))}
+    I, H = mats["gate"].rows, mats["gate"].cols
+    if x.dim() != 2:
+        raise ValueError(f"x must be [T, H], got {tuple(x.shape)}")
+    T = x.shape[0]
+    _expect("x", x, (T, H), torch.bfloat16)
+    dev = _device_of(x, x=x, gate=gate[0], up=up[0], down=down[0], gate_scales=gate[1],
+                     up_scales=up[1], down_scales=down[1], out=out, workspace=workspace)
+    y = out if out is not None else torch.empty((T, H), dtype=out_dtype, device=dev)
+    _expect("out", y, (T, H), y.dtype)
+    L = lib()
+    with torch.cuda.device(dev):
+        ws = _workspace(L.fp8_block_mlp_workspace_size(T, H, I), dev, workspace)
+        _check(L.fp8_block_mlp(_ptr(x), T, *(ctypes.byref(m) for m in mats.values()), _ptr(y),
+                               _dt(y.dtype), _ptr(ws), ws.numel() * ws.element_size(), _stream()))
+    return y
 
 
 def ffn_debug_h(workspace, T, H, I, E, k, act=W4A16, given=False):

@@ -1,0 +1,117 @@
+"""Refusals of the FP8 block-scaled entry points: the documented status before
+anything is enqueued (C ABI), and the binding's checks (no GPU needed)."""
+import ctypes
+import os
+
+import pytest
+import torch
+
+from nvfp4_routed_expert_amd import native
+
+pytestmark = pytest.mark.skipif(not os.path.exists(native.LIB_PATH),
+                                reason="library not built")
+
+FAKE = ctypes.c_void_p(1 << 20)          # aligned, never dereferenced
+MIS = ctypes.c_void_p((1 << 20) + 4)
+
+
+def _last():
+    return native.lib().nvfp4_last_error().decode()
+
+
+def test_quantize_validation():
+    L = native.lib()
+    q = lambda x=FAKE, dt=0, rows=4, cols=64, ld=64, br=1, codes=FAKE, sc=FAKE: \
+        L.fp8_block_quantize(x, dt, rows, cols, ld, br, codes, sc, None)
+    assert q(x=None) == 1 and "x is NULL" in _last()
+    assert q(codes=None) == 1 and q(sc=None) == 1
+    assert q(dt=2) == 1
+    assert q(br=64) == 1 and "block_rows" in _last()
+    assert q(rows=-1) == 1
+    assert q(cols=48) == 2 and "multiple of 32" in _last()
+    assert q(cols=0) == 2
+    assert q(ld=32) == 1 and q(ld=68) == 1
+    assert q(rows=1 << 28) == 2 and "2^27" in _last()
+    assert q(x=MIS) == 3 and q(codes=MIS) == 3 and q(sc=MIS) == 3
+    assert q(x=None, rows=0, codes=None, sc=None) == 0
+    assert q(x=None, rows=0, cols=48, codes=None, sc=None) == 2
+
+
+def test_linear_validation():
+    L = native.lib()
+    m = native.Fp8Matrix(FAKE.value, FAKE.value, 64, 96)
+    ws = L.fp8_block_linear_workspace_size(40, 64, 96, 0)   # (up to 16 rows need none)
+    assert ws > L.fp8_block_linear_workspace_size(40, 64, 96, 1)
+    lin = lambda x=FAKE, xs=None, M=40, w=m, y=FAKE, dt=0, wsp=FAKE, wsb=ws: L.fp8_block_linear(
+        x, xs, M, None if w is None else ctypes.byref(w), y, dt, wsp, wsb, None)
+    assert lin(x=None) == 1 and lin(y=None) == 1 and lin(w=None) == 1
+    assert lin(M=-1) == 1
+    assert lin(M=(1 << 24) + 1) == 2
+    assert lin(dt=5) == 1
+    assert lin(w=native.Fp8Matrix(None, FAKE.value, 64, 96)) == 1 and "codes" in _last()
+    assert lin(w=native.Fp8Matrix(FAKE.value, None, 64, 96)) == 1 and "scales" in _last()
+    assert lin(w=native.Fp8Matrix(FAKE.value, FAKE.value, 0, 96)) == 1
+    assert lin(w=native.Fp8Matrix(FAKE.value, FAKE.value, 64, 80)) == 2
+    assert lin(w=native.Fp8Matrix(FAKE.value, FAKE.value, (1 << 24) + 1, 96)) == 2
+    assert lin(w=native.Fp8Matrix(MIS.value, FAKE.value, 64, 96)) == 3
+    assert lin(x=MIS) == 3 and lin(xs=MIS) == 3 and lin(y=MIS) == 3
+    assert lin(wsb=ws - 256) == 4
+    assert lin(wsp=None) == 1
+    assert lin(x=None, y=None, M=0, wsp=None, wsb=0) == 0
+    assert lin(x=None, y=None, M=0, wsp=None, wsb=0,
+               w=native.Fp8Matrix(FAKE.value, FAKE.value, 64, 80)) == 2
+
+
+def test_mlp_validation():
+    L = native.lib()
+    g = native.Fp8Matrix(FAKE.value, FAKE.value, 64, 96)
+    d = native.Fp8Matrix(FAKE.value, FAKE.value, 96, 64)
+    ws = L.fp8_block_mlp_workspace_size(4, 96, 64)
+    assert ws > 0
+    mlp = lambda x=FAKE, T=4, gate=g, up=g, down=d, y=FAKE, dt=0, wsb=ws: L.fp8_block_mlp(
+        x, T, *(ctypes.byref(w) for w in (gate, up, down)), y, dt, FAKE, wsb, None)
+    assert mlp(x=None) == 1 and mlp(y=None) == 1 and mlp(T=-1) == 1 and mlp(dt=2) == 1
+    assert mlp(up=d) == 1 and "w_up" in _last()
+    assert mlp(down=g) == 1
+    assert mlp(gate=native.Fp8Matrix(FAKE.value, FAKE.value, 48, 96),
+               up=native.Fp8Matrix(FAKE.value, FAKE.value, 48, 96),
+               down=native.Fp8Matrix(FAKE.value, FAKE.value, 96, 48)) == 2   # I % 32
+    assert mlp(T=(1 << 24) + 1) == 2
+    assert mlp(x=MIS) == 3 and mlp(y=MIS) == 3
+    assert mlp(wsb=ws - 256) == 4
+    assert mlp(x=None, y=None, T=0, wsb=0) == 0
+
+
+def test_workspace_sizes_of_empty_problems():
+    L = native.lib()
+    assert L.fp8_block_linear_workspace_size(0, 64, 96, 0) == 0
+    assert L.fp8_block_mlp_workspace_size(0, 96, 64) == 0
+
+
+def test_binding_refusals():
+    """The binding's own checks, on host tensors (nothing reaches the library)."""
+    x = torch.zeros((4, 96), dtype=torch.bfloat16)
+    w, ws = torch.zeros((64, 96), dtype=torch.uint8), torch.ones((1, 1))
+    with pytest.raises(ValueError, match="cuda"):
+        native.fp8_block_quantize(x)
+    with pytest.raises(ValueError, match="block_rows"):
+        native.fp8_block_quantize(x, 64)
+    with pytest.raises(ValueError, match="unit column stride"):
+        native.fp8_block_quantize(x.t())
+    with pytest.raises(ValueError, match=r"\[rows, cols\]"):
+        native.fp8_block_quantize(x[0])
+    with pytest.raises(ValueError, match="cuda"):
+        native.fp8_block_linear(x, w, ws)
+    with pytest.raises(ValueError, match="does not match"):
+        native.fp8_block_linear(x[:, :64], w, ws)
+    with pytest.raises(ValueError, match="scales"):
+        native.fp8_block_linear(x, w, ws.repeat(2, 1))
+    with pytest.raises(TypeError, match="bfloat16"):
+        native.fp8_block_linear(x.float(), w, ws)
+    with pytest.raises(TypeError, match="uint8"):
+        native.fp8_block_linear(x, w, ws, x_scales=torch.ones((4, 1)))
+    with pytest.raises(ValueError, match="x_scales"):
+        native.fp8_block_linear(torch.zeros((4, 96), dtype=torch.uint8), w, ws,
+                                x_scales=torch.ones((4, 2)))
+    with pytest.raises(TypeError, match="uint8"):
+        native.fp8_block_mlp(x, (w.int(), ws), (w, ws), (w, ws))
