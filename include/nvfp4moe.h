@@ -430,6 +430,64 @@ size_t moe_route_ffn_decode_workspace_size(int64_t T, int64_t H, int64_t I, int3
                                            int32_t k);
 
 /*
+ * The weights of a whole MoE layer (host struct of device pointers, read
+ * during the call only).  All matrices row-major; the router and the shared
+ * expert are BF16 beside the NVFP4 routed experts (Qwen3.8-Flash-Next-NVFP4-
+ * SSD-Stream model card, "What this model is").
+ */
+typedef struct {
+  int64_t H, I;                /* hidden and routed intermediate size            */
+  int32_t E, k;                /* experts, experts per token                     */
+  const void *router;          /* [E, H] bf16                                    */
+  const float *router_bias;    /* [E] added to the logits, or NULL               */
+  nvfp4_expert_weights experts;
+  int64_t shared_I;            /* 0: no shared expert (its pointers are unused)  */
+  const void *shared_gate_proj, *shared_up_proj;   /* [shared_I, H] bf16         */
+  const void *shared_down_proj;                    /* [H, shared_I] bf16         */
+  const void *shared_gate;     /* [H] bf16, or NULL: the shared output unscaled  */
+} moe_layer;
+
+/*
+ * moe_layer_decode: a whole MoE layer for the few tokens of a decode step in
+ * two launches (the separate calls take seven or more).  For x [T, H] bf16:
+ *   l_t = x_t R^T (+ bias)                  as moe_router_topk's logits
+ *   topk_ids, topk_weights                  as moe_route_topk on l (k largest,
+ *                                           equal logits to the lower index)
+ *   h_p = bf16_rne( silu(g_gate[e] x_t D_gate[e]^T) * (g_up[e] x_t D_up[e]^T) )
+ *   y_t = sum_j topk_weights[p] * g_down[e] h_p D_down[e]^T      (j ascending)
+ *         + c_t * shared(x_t)
+ * with shared the BF16 expert of moe_shared_expert_ffn (its h rounded to
+ * bf16) and c_t = 1, or sigmoid(x_t . shared_gate).  Sums are fp32, y [T, H]
+ * is rounded once (bf16 round-to-nearest-even, or f32).  Logits are summed in
+ * this call's own order: ids equal moe_router_topk's except where two logits
+ * differ by less than the sums' rounding.  Calls are deterministic.
+ * Requires T <= 64, T * k <= 512, 1 <= k <= 32, k <= E <= 1024, and H, I,
+ * shared_I multiples of 32 (at most 2^20; H * I <= 2^32, H * shared_I <=
+ * 2^30: an expert's offsets are 32-bit).
+ * workspace (moe_layer_decode_workspace_size bytes, device, 16-byte aligned):
+ * moe_layer_workspace_init must have run on it once; every call leaves it
+ * ready for the next one on the stream.  Calls that may run at the same time
+ * need separate workspaces, as do graphs that may be replayed at the same
+ * time.  The launch waits on words it counts up itself; if they were not
+ * initialised, the waits end after some seconds and y is NaN until
+ * moe_layer_workspace_init runs again.
+ */
+nvfp4_status moe_layer_decode(const void *x, int64_t T, const moe_layer *layer, int renormalize,
+                              int32_t *topk_ids, float *topk_weights, void *y,
+                              nvfp4_dtype y_dtype, void *workspace, size_t workspace_bytes,
+                              hipStream_t stream);
+size_t moe_layer_decode_workspace_size(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k,
+                                       int64_t shared_I);
+
+/*
+ * moe_layer_workspace_init: makes a workspace ready for moe_layer_decode (a
+ * small kernel on `stream`, no memset, so it may be captured into a graph).
+ * Errors: NULL or misaligned workspace, workspace_bytes below 4 KiB.
+ */
+nvfp4_status moe_layer_workspace_init(void *workspace, size_t workspace_bytes,
+                                      hipStream_t stream);
+
+/*
  * moe_grouped_nvfp4_ffn_static: moe_grouped_nvfp4_ffn without a workspace
  * argument, for callers that cannot allocate device memory: code under HIP
  * graph capture, tight serving loops and harnesses that forbid hipMalloc.

@@ -320,6 +320,32 @@ Fp8MlpWs carve_fp8_mlp(Carver &c, int64_t T, int64_t H, int64_t I, OutType out) 
 }
 OutType out_type(nvfp4_dtype t) { return t == NVFP4_DT_F32 ? OutType::F32 : OutType::BF16; }
 
+struct LayerWs {
+  uint32_t *ctl;   // first: what moe_layer_workspace_init zeroes
+  float *logits;
+  int32_t *seg_pairs;
+  uint16_t *h, *sh;
+  int64_t h_ld, sh_ld;
+  float *part, *spart;
+};
+LayerWs carve_layer(Carver &c, int64_t T, int64_t H, int64_t I, int64_t E, int64_t k,
+                    int64_t Is) {
+  LayerWs w;
+  const int64_t P = T * k;
+  w.ctl = c.take<uint32_t>(layer_ctl_bytes() / sizeof(uint32_t));
+  w.logits = c.take<float>((size_t)(T * (E + 1)));
+  w.seg_pairs = c.take<int32_t>((size_t)(4 * P));
+  w.h_ld = (I + 63) / 64 * 64;
+  w.sh_ld = (Is + 63) / 64 * 64;
+  w.h = c.take<uint16_t>((size_t)(P * w.h_ld));
+  w.sh = c.take<uint16_t>((size_t)(T * w.sh_ld));
+  w.part = c.take<float>((size_t)(P * H));
+  w.spart = c.take<float>(Is ? (size_t)(T * H) : 0);
+  return w;
+}
+constexpr size_t kLayerCtlMin = 4096;
+constexpr int64_t kLayerMaxDim = (int64_t)1 << 20;
+
 }  // namespace
 
 extern "C" {
@@ -1548,6 +1574,132 @@ nvfp4_status fp8_block_mlp(const void *x, int64_t T, const fp8_matrix *w_gate,
   d.out_type = out_type(y_dtype);
   d.partial = ws.split;
   LAUNCH(launch_f8_gemm(false, d, ws.down_plan, stream), "fp8 down");
+  return NVFP4_OK;
+}
+
+// ---- moe_layer_decode --------------------------------------------------------------------
+
+size_t moe_layer_decode_workspace_size(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k,
+                                       int64_t shared_I) {
+  if (T < 1 || H < 1 || I < 1 || E < 1 || k < 1 || shared_I < 0) return 0;
+  Carver c(nullptr);
+  carve_layer(c, T, H, I, E, k, shared_I);
+  return c.used > kLayerCtlMin ? c.used : kLayerCtlMin;
+}
+
+nvfp4_status moe_layer_workspace_init(void *workspace, size_t workspace_bytes,
+                                      hipStream_t stream) {
+  g_last_error[0] = 0;
+  CHECK_NULL(workspace);
+  CHECK_ALIGN(workspace);
+  if (workspace_bytes < kLayerCtlMin || workspace_bytes < layer_ctl_bytes())
+    return fail(NVFP4_ERR_WORKSPACE_TOO_SMALL, "workspace has %zu bytes, needs at least %zu",
+                workspace_bytes, kLayerCtlMin);
+  LAUNCH(launch_layer_init(static_cast<uint32_t *>(workspace), stream), "layer workspace init");
+  return NVFP4_OK;
+}
+
+nvfp4_status moe_layer_decode(const void *x, int64_t T, const moe_layer *layer, int renormalize,
+                              int32_t *topk_ids, float *topk_weights, void *y,
+                              nvfp4_dtype y_dtype, void *workspace, size_t workspace_bytes,
+                              hipStream_t stream) {
+  g_last_error[0] = 0;
+  if (T > 0) {
+    CHECK_NULL(x);
+    CHECK_NULL(topk_ids);
+    CHECK_NULL(topk_weights);
+    CHECK_NULL(y);
+  }
+  CHECK_NULL(layer);
+  const moe_layer &l = *layer;
+  if (T < 0) return fail(NVFP4_ERR_INVALID_ARGUMENT, "T = %lld < 0", (long long)T);
+  if (l.E < 1 || l.E > 1024)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "E = %d outside 1..1024", (int)l.E);
+  if (l.k < 1 || l.k > l.E || l.k > 32)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "k = %d outside 1..min(E, 32)", (int)l.k);
+  if (!layer_supported(T, l.E, l.k))
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE,
+                "T = %lld, k = %d: at most 64 tokens and T * k <= 512 (larger batches: "
+                "moe_router_topk and moe_grouped_nvfp4_ffn)",
+                (long long)T, (int)l.k);
+  TRY(check_k(l.H, "H"));
+  TRY(check_k(l.I, "I"));
+  if (l.shared_I < 0)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "shared_I = %lld < 0", (long long)l.shared_I);
+  if (l.shared_I > 0) TRY(check_k(l.shared_I, "shared_I"));
+  if (l.H > kLayerMaxDim || l.I > kLayerMaxDim || l.shared_I > kLayerMaxDim)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "H, I or shared_I exceeds 2^20");
+  if (l.H * l.I > (int64_t)1 << 32 || l.H * l.shared_I > (int64_t)1 << 30)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "H * I exceeds 2^32 or H * shared_I 2^30");
+  if (y_dtype != NVFP4_DT_BF16 && y_dtype != NVFP4_DT_F32)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "y_dtype %d is not BF16 or F32", (int)y_dtype);
+  CHECK_NULL(l.router);
+  const nvfp4_expert_weights &w = l.experts;
+  const void *need[] = {w.gate_codes,  w.up_codes,    w.down_codes,  w.gate_scales, w.up_scales,
+                        w.down_scales, w.gate_global, w.up_global,   w.down_global};
+  for (const void *q : need)
+    if (!q) return fail(NVFP4_ERR_INVALID_ARGUMENT, "an expert weight pointer is NULL");
+  const void *shared[] = {l.shared_gate_proj, l.shared_up_proj, l.shared_down_proj};
+  for (const void *q : shared) {
+    if (l.shared_I > 0 && !q)
+      return fail(NVFP4_ERR_INVALID_ARGUMENT, "a shared expert weight pointer is NULL");
+    if (l.shared_I > 0 && !aligned16(q))
+      return fail(NVFP4_ERR_MISALIGNED, "a shared expert weight is not 16-byte aligned");
+  }
+  if (l.shared_I == 0 && l.shared_gate)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "shared_gate without a shared expert");
+  for (int i = 0; i < 6; ++i)
+    if (!aligned16(need[i]))
+      return fail(NVFP4_ERR_MISALIGNED, "an expert weight pointer is not 16-byte aligned");
+  for (int i = 6; i < 9; ++i)
+    if (reinterpret_cast<uintptr_t>(need[i]) & 3u)
+      return fail(NVFP4_ERR_MISALIGNED, "an expert global scale is not 4-byte aligned");
+  CHECK_ALIGN(x);
+  CHECK_ALIGN(l.router);
+  CHECK_ALIGN(l.router_bias);
+  CHECK_ALIGN(l.shared_gate);
+  CHECK_ALIGN(topk_ids);
+  CHECK_ALIGN(topk_weights);
+  CHECK_ALIGN(y);
+  TRY(check_workspace(workspace, workspace_bytes,
+                      moe_layer_decode_workspace_size(T, l.H, l.I, l.E, l.k, l.shared_I)));
+  if (T == 0) return NVFP4_OK;
+  Carver c(workspace);
+  const LayerWs ws = carve_layer(c, T, l.H, l.I, l.E, l.k, l.shared_I);
+  LayerArgs a = {};
+  a.x = static_cast<const uint16_t *>(x);
+  a.T = (int)T;
+  a.H = (int)l.H;
+  a.I = (int)l.I;
+  a.E = l.E;
+  a.k = l.k;
+  a.renormalize = renormalize != 0;
+  a.router = static_cast<const uint16_t *>(l.router);
+  a.rbias = l.router_bias;
+  a.codes[0] = w.gate_codes;
+  a.codes[1] = w.up_codes;
+  a.codes[2] = w.down_codes;
+  a.scales[0] = w.gate_scales;
+  a.scales[1] = w.up_scales;
+  a.scales[2] = w.down_scales;
+  a.glob[0] = w.gate_global;
+  a.glob[1] = w.up_global;
+  a.glob[2] = w.down_global;
+  a.Is = (int)l.shared_I;
+  for (int i = 0; i < 3; ++i) a.sw[i] = static_cast<const uint16_t *>(shared[i]);
+  a.sgate = static_cast<const uint16_t *>(l.shared_gate);
+  a.ids = topk_ids;
+  a.weights = topk_weights;
+  a.ctl = ws.ctl;
+  a.logits = ws.logits;
+  a.seg_pairs = ws.seg_pairs;
+  a.h = ws.h;
+  a.sh = ws.sh;
+  a.h_ld = (int)ws.h_ld;
+  a.sh_ld = (int)ws.sh_ld;
+  a.part = ws.part;
+  a.spart = ws.spart;
+  LAUNCH(launch_layer(a, y, out_type(y_dtype), stream), "moe layer");
   return NVFP4_OK;
 }
 

@@ -368,6 +368,36 @@ bool f8_gemv_supported(int64_t M);
 bool f8_gemv_quantises(int64_t M);
 hipError_t launch_f8_gemv(bool swiglu, const F8GemvArgs &a, hipStream_t s);
 
+// ---- a whole MoE layer for a few tokens (layer.hip) --------------------------------
+
+struct LayerArgs {
+  const uint16_t *x;            // [T, H] bf16
+  int T, H, I, E, k, renormalize;
+  const uint16_t *router;       // [E, H] bf16
+  const float *rbias;           // [E] or null
+  const uint8_t *codes[3], *scales[3];   // gate, up, down experts
+  const float *glob[3];
+  int Is;                       // shared intermediate size, 0: no shared expert
+  const uint16_t *sw[3];        // shared gate, up [Is, H], down [H, Is]
+  const uint16_t *sgate;        // [H] or null: shared output times sigmoid(x . sgate)
+  int32_t *ids;                 // outputs [T, k]
+  float *weights;
+  // workspace
+  uint32_t *ctl;                // control words, zero before the call
+  float *logits;                // [T, E (+ 1)]
+  int32_t *seg_pairs;           // [T k][4]
+  uint16_t *h, *sh;             // [T k][h_ld], [T][sh_ld]: rows of whole 128-byte lines
+  int h_ld, sh_ld;
+  float *part, *spart;          // [T k][H], [T][H]
+  // set by launch_layer: items per class and batches of rows per item
+  int n_router, n_su, n_sd, n_gu, n_dn;
+  int it_gu, it_dn, it_su, it_sd;
+};
+bool layer_supported(int64_t T, int E, int k);
+size_t layer_ctl_bytes();
+hipError_t launch_layer_init(uint32_t *ctl, hipStream_t s);
+hipError_t launch_layer(const LayerArgs &a, void *y, OutType yt, hipStream_t s);
+
 // ---- measurement aid (probe.hip) ---------------------------------------------------
 
 // Streaming read of `bytes` (a multiple of 16) at buf; sink: >= 1024 words.

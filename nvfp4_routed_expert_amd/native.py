@@ -47,6 +47,13 @@ class ExpertWeightsC(ctypes.Structure):
                 ("gate_global", _vp), ("up_global", _vp), ("down_global", _vp)]
 
 
+class MoeLayerC(ctypes.Structure):
+    _fields_ = [("H", _i64), ("I", _i64), ("E", _i32), ("k", _i32), ("router", _vp),
+                ("router_bias", _vp), ("experts", ExpertWeightsC), ("shared_I", _i64),
+                ("shared_gate_proj", _vp), ("shared_up_proj", _vp), ("shared_down_proj", _vp),
+                ("shared_gate", _vp)]
+
+
 _LIB = None
 
 
@@ -108,6 +115,10 @@ def lib():
                                      ctypes.POINTER(Fp8Matrix), ctypes.POINTER(Fp8Matrix), _vp,
                                      _i32, _vp, _sz, _vp]),
             "fp8_block_mlp_workspace_size": (_sz, [_i64, _i64, _i64]),
+            "moe_layer_decode": (_i32, [_vp, _i64, ctypes.POINTER(MoeLayerC), ctypes.c_int, _vp,
+                                        _vp, _vp, _i32, _vp, _sz, _vp]),
+            "moe_layer_decode_workspace_size": (_sz, [_i64, _i64, _i64, _i32, _i32, _i64]),
+            "moe_layer_workspace_init": (_i32, [_vp, _sz, _vp]),
             "nvfp4_set_ffn_stage_events": (None, [_vp]),
             "nvfp4_set_ffn_separate_h_quant": (None, [ctypes.c_int]),
             "nvfp4_read_probe": (_i32, [_vp, _sz, _vp, _vp]),
@@ -139,6 +150,7 @@ def exported_symbols():
             "moe_grouped_nvfp4_ffn_static", "moe_grouped_nvfp4_ffn_static_max_bytes",
             "fp8_block_quantize", "fp8_block_linear", "fp8_block_linear_workspace_size",
             "fp8_block_mlp", "fp8_block_mlp_workspace_size",
+            "moe_layer_decode", "moe_layer_decode_workspace_size", "moe_layer_workspace_init",
             "nvfp4_set_ffn_stage_events",
             "nvfp4_set_ffn_separate_h_quant", "nvfp4_read_probe",
             "nvfp4_status_string", "nvfp4_last_error"]
@@ -532,8 +544,8 @@ def moe_grouped_nvfp4_ffn_static(x, weights: ExpertWeights, topk_ids, topk_weigh
 # ---- FP8 block-scaled operators -----------------------------------------------
 
 
-def _device_of(x, /, **tensors):
-    """The cuda device of x; every other tensor must be contiguous on it."""
+def _device_of(x, **tensors):
+    """The cuda device of x; every tensor named must be contiguous on it."""
     if not x.is_cuda:
         raise ValueError(f"tensors must be on a cuda device, got {x.device}")
     for name, t in tensors.items():
@@ -608,7 +620,7 @@ def fp8_block_linear(x, codes, scales, x_scales=None, out_dtype=torch.bfloat16, 
     else:
         _expect("x", x, (M, K), torch.uint8)
         _expect("x_scales", x_scales, (M, _fp8_blocks(K)), torch.float32)
-    dev = _device_of(x, x=x, codes=codes, scales=scales, x_scales=x_scales, out=out,
+    dev = _device_of(x, rows=x, codes=codes, scales=scales, x_scales=x_scales, out=out,
                      workspace=workspace)
     y = out if out is not None else torch.empty((M, m.rows), dtype=out_dtype, device=dev)
     _expect("out", y, (M, m.rows), y.dtype)
@@ -632,7 +644,7 @@ def fp8_block_mlp(x, gate, up, down, out_dtype=torch.bfloat16, workspace=None, o
         raise ValueError(f"x must be [T, H], got {tuple(x.shape)}")
     T = x.shape[0]
     _expect("x", x, (T, H), torch.bfloat16)
-    dev = _device_of(x, x=x, gate=gate[0], up=up[0], down=down[0], gate_scales=gate[1],
+    dev = _device_of(x, rows=x, gate=gate[0], up=up[0], down=down[0], gate_scales=gate[1],
                      up_scales=up[1], down_scales=down[1], out=out, workspace=workspace)
     y = out if out is not None else torch.empty((T, H), dtype=out_dtype, device=dev)
     _expect("out", y, (T, H), y.dtype)
@@ -642,6 +654,84 @@ def fp8_block_mlp(x, gate, up, down, out_dtype=torch.bfloat16, workspace=None, o
         _check(L.fp8_block_mlp(_ptr(x), T, *(ctypes.byref(m) for m in mats.values()), _ptr(y),
                                _dt(y.dtype), _ptr(ws), ws.numel() * ws.element_size(), _stream()))
     return y
+
+
+# ---- a whole MoE layer for a few tokens ------------------------------------------
+
+
+def layer_workspace(T, H, I, E, k, shared_I, device):
+    """A workspace for moe_layer_decode made ready by moe_layer_workspace_init
+    (on the device's current stream); every call leaves it ready again, so one
+    serves successive (not overlapping) calls of at most this size."""
+    L = lib()
+    with torch.cuda.device(device):
+        ws = torch.empty(max(L.moe_layer_decode_workspace_size(T, H, I, E, k, shared_I), 4096),
+                         dtype=torch.uint8, device=device)
+        _check(L.moe_layer_workspace_init(_ptr(ws), ws.numel(), _stream()))
+    return ws
+
+
+def moe_layer_decode(x, router_w, weights: ExpertWeights, k, renormalize=True, bias=None,
+                     shared=None, shared_gate=None, out_dtype=torch.bfloat16, route_out=None,
+                     out=None, workspace=None):
+    """A whole MoE layer for a decode step (T <= 64, T * k <= 512) in two
+    launches: router x . router_w^T (+ bias), top-k, NVFP4 routed experts and,
+    with shared = (w_gate [Is, H], w_up [Is, H], w_down [H, Is]) bf16, the
+    shared expert (times sigmoid(x . shared_gate), bf16 [H], when given).
+    workspace: from layer_workspace (a fresh one is made when omitted).
+    Returns (y [T, H], (topk_ids [T, k], topk_weights [T, k]))."""
+    T, H = x.shape
+    E, I = weights.num_experts, weights.intermediate
+    bf = torch.bfloat16
+    _expect("x", x, (T, H), bf)
+    _expect("router_w", router_w, (E, H), bf)
+    if weights.hidden != H:
+        raise ValueError(f"weights have hidden size {weights.hidden}, x {H}")
+    tensors = dict(rows=x, router_w=router_w, bias=bias, shared_gate=shared_gate, out=out,
+                   workspace=workspace)
+    for m, rows, cols in (("gate", I, H), ("up", I, H), ("down", H, I)):
+        codes, scales = getattr(weights, m + "_codes"), getattr(weights, m + "_scales")
+        _expect(m + "_codes", codes, (E, rows, cols // 2), torch.uint8)
+        _expect(m + "_scales", scales, (E, rows, cols // 16), torch.uint8)
+        _expect(m + "_global", getattr(weights, m + "_global"), (E,), torch.float32)
+        tensors.update({m + "_codes": codes, m + "_scales": scales,
+                        m + "_global": getattr(weights, m + "_global")})
+    if bias is not None:
+        _expect("bias", bias, (E,), torch.float32)
+    Is = 0
+    if shared is not None:
+        Is = shared[0].shape[0]
+        for n, t, s in zip(("shared gate", "shared up", "shared down"), shared,
+                           ((Is, H), (Is, H), (H, Is))):
+            _expect(n, t, s, bf)
+            tensors[n] = t
+    if shared_gate is not None:
+        if shared is None:
+            raise ValueError("shared_gate needs a shared expert")
+        _expect("shared_gate", shared_gate, (H,), bf)
+    if route_out is not None:
+        _expect("topk_ids", route_out[0], (T, k), torch.int32)
+        _expect("topk_weights", route_out[1], (T, k), torch.float32)
+        tensors.update(topk_ids=route_out[0], topk_weights=route_out[1])
+    dev = _device_of(x, **tensors)
+    if route_out is None:
+        route_out = (torch.empty((T, k), dtype=torch.int32, device=dev),
+                     torch.empty((T, k), dtype=torch.float32, device=dev))
+    y = out if out is not None else torch.empty((T, H), dtype=out_dtype, device=dev)
+    _expect("out", y, (T, H), y.dtype)
+    L = lib()
+    nbytes = L.moe_layer_decode_workspace_size(T, H, I, E, k, Is)
+    ws = _workspace(nbytes, dev, workspace) if workspace is not None else \
+        layer_workspace(T, H, I, E, k, Is, dev)
+    sp = [t.data_ptr() for t in shared] if shared is not None else [None] * 3
+    layer = MoeLayerC(H, I, E, k, router_w.data_ptr(), None if bias is None else bias.data_ptr(),
+                      weights.c_struct(), Is, *sp,
+                      None if shared_gate is None else shared_gate.data_ptr())
+    with torch.cuda.device(dev):
+        _check(L.moe_layer_decode(_ptr(x), T, ctypes.byref(layer), int(bool(renormalize)),
+                                  _ptr(route_out[0]), _ptr(route_out[1]), _ptr(y), _dt(y.dtype),
+                                  _ptr(ws), ws.numel() * ws.element_size(), _stream()))
+    return y, route_out
 
 
 def ffn_debug_h(workspace, T, H, I, E, k, act=W4A16, given=False):

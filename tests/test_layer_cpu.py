@@ -1,0 +1,101 @@
+"""Refusals of moe_layer_decode: the documented status before anything is
+enqueued (C ABI), and the binding's checks (no GPU needed)."""
+import ctypes
+import os
+
+import pytest
+import torch
+
+from nvfp4_routed_expert_amd import native, weights
+
+pytestmark = pytest.mark.skipif(not os.path.exists(native.LIB_PATH),
+                                reason="library not built")
+
+FAKE, MIS = 1 << 20, (1 << 20) + 4          # never dereferenced
+
+
+def _last():
+    return native.lib().nvfp4_last_error().decode()
+
+
+def make(H=256, I=64, E=8, k=2, router=FAKE, bias=None, experts=None, Is=32, sg=FAKE, su=FAKE,
+         sd=FAKE, gate=None):
+    w = native.ExpertWeightsC(*(experts or [FAKE] * 9))
+    return native.MoeLayerC(H, I, E, k, router, bias, w, Is, sg, su, sd, gate)
+
+
+def call(layer, T=4, x=FAKE, ids=FAKE, wts=FAKE, y=FAKE, dt=0, ws=FAKE, nbytes=1 << 26):
+    v = lambda p: None if p is None else ctypes.c_void_p(p)
+    return native.lib().moe_layer_decode(v(x), T, None if layer is None else ctypes.byref(layer), 1,
+                                         v(ids), v(wts), v(y), dt, v(ws), nbytes, None)
+
+
+def test_null_and_misaligned_pointers():
+    for kw in ("x", "ids", "wts", "y"):
+        assert call(make(), **{kw: None}) == 1, kw
+        assert call(make(), **{kw: MIS}) == 3, kw
+    assert call(None) == 1
+    assert call(make(router=None)) == 1 and call(make(router=MIS)) == 3
+    assert call(make(bias=MIS)) == 3 and call(make(gate=MIS)) == 3
+    for i in range(9):
+        bad = [FAKE] * 9
+        bad[i] = None
+        assert call(make(experts=bad)) == 1
+        bad[i] = MIS if i < 6 else FAKE + 2
+        assert call(make(experts=bad)) == 3
+    for kw in ("sg", "su", "sd"):
+        assert call(make(**{kw: None})) == 1 and "shared" in _last()
+        assert call(make(**{kw: MIS})) == 3
+
+
+def test_sizes():
+    assert call(make(), T=-1) == 1
+    assert call(make(), T=65) == 2 and "64 tokens" in _last()
+    assert call(make(E=32, k=16), T=33) == 2          # T * k > 512
+    assert call(make(k=0)) == 2 and call(make(k=9)) == 2 and call(make(E=64, k=33)) == 2
+    assert call(make(E=0)) == 2 and call(make(E=1025)) == 2
+    assert call(make(H=48)) == 2 and call(make(I=80)) == 2 and call(make(Is=40)) == 2
+    assert call(make(H=0)) == 2 and call(make(Is=-32)) == 1
+    assert call(make(H=(1 << 20) + 32)) == 2
+    assert call(make(H=1 << 20, I=1 << 13)) == 2 and "2^32" in _last()
+    assert call(make(), dt=3) == 1
+    assert call(make(Is=0, sg=None, su=None, sd=None, gate=FAKE)) == 1
+
+
+def test_workspace():
+    L = native.lib()
+    n = L.moe_layer_decode_workspace_size(4, 256, 64, 8, 2, 32)
+    assert n >= 4 * 2 * 256 * 4 and n >= 4096
+    assert call(make(), nbytes=n - 1) == 4 and "workspace" in _last()
+    assert call(make(), ws=None, nbytes=n) == 1
+    assert call(make(), ws=MIS, nbytes=n) == 3
+    assert L.moe_layer_workspace_init(None, 4096, None) == 1
+    assert L.moe_layer_workspace_init(ctypes.c_void_p(MIS), 4096, None) == 3
+    assert L.moe_layer_workspace_init(ctypes.c_void_p(FAKE), 4095, None) == 4
+    assert L.moe_layer_decode_workspace_size(0, 256, 64, 8, 2, 32) == 0
+
+
+def test_empty_batch_checks_the_layer():
+    assert call(make(), T=0, x=None, ids=None, wts=None, y=None, ws=None, nbytes=0) == 0
+    assert call(make(H=48), T=0, x=None, ids=None, wts=None, y=None, ws=None, nbytes=0) == 2
+
+
+def test_binding_refusals():
+    w = weights.empty_experts(4, 64, 32, "cpu")
+    x = torch.zeros((2, 64), dtype=torch.bfloat16)
+    r = torch.zeros((4, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="cuda"):
+        native.moe_layer_decode(x, r, w, 2)
+    with pytest.raises(TypeError, match="bfloat16"):
+        native.moe_layer_decode(x.float(), r, w, 2)
+    with pytest.raises(ValueError, match="router_w"):
+        native.moe_layer_decode(x, r[:3], w, 2)
+    with pytest.raises(ValueError, match="hidden"):
+        native.moe_layer_decode(x[:, :32], r[:, :32], w, 2)
+    with pytest.raises(ValueError, match="bias"):
+        native.moe_layer_decode(x, r, w, 2, bias=torch.zeros(3))
+    with pytest.raises(ValueError, match="shared_gate"):
+        native.moe_layer_decode(x, r, w, 2, shared_gate=x[0])
+    s = torch.zeros((32, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="shared down"):
+        native.moe_layer_decode(x, r, w, 2, shared=(s, s, s))
