@@ -464,13 +464,9 @@ typedef struct {
  * Requires T <= 64, T * k <= 512, 1 <= k <= 32, k <= E <= 1024, and H, I,
  * shared_I multiples of 32 (at most 2^20; H * I <= 2^32, H * shared_I <=
  * 2^30: an expert's offsets are 32-bit).
- * workspace (moe_layer_decode_workspace_size bytes, device, 16-byte aligned):
- * moe_layer_workspace_init must have run on it once; every call leaves it
- * ready for the next one on the stream.  Calls that may run at the same time
- * need separate workspaces, as do graphs that may be replayed at the same
- * time.  The launch waits on words it counts up itself; if they were not
- * initialised, the waits end after some seconds and y is NaN until
- * moe_layer_workspace_init runs again.
+ * workspace: moe_layer_decode_workspace_size bytes (device, 16-byte
+ * aligned), scratch only (no state between calls); calls or graph replays
+ * that may run at the same time need separate ones.
  */
 nvfp4_status moe_layer_decode(const void *x, int64_t T, const moe_layer *layer, int renormalize,
                               int32_t *topk_ids, float *topk_weights, void *y,
@@ -478,14 +474,6 @@ nvfp4_status moe_layer_decode(const void *x, int64_t T, const moe_layer *layer, 
                               hipStream_t stream);
 size_t moe_layer_decode_workspace_size(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k,
                                        int64_t shared_I);
-
-/*
- * moe_layer_workspace_init: makes a workspace ready for moe_layer_decode (a
- * small kernel on `stream`, no memset, so it may be captured into a graph).
- * Errors: NULL or misaligned workspace, workspace_bytes below 4 KiB.
- */
-nvfp4_status moe_layer_workspace_init(void *workspace, size_t workspace_bytes,
-                                      hipStream_t stream);
 
 /*
  * moe_grouped_nvfp4_ffn_static: moe_grouped_nvfp4_ffn without a workspace

@@ -321,29 +321,24 @@ Fp8MlpWs carve_fp8_mlp(Carver &c, int64_t T, int64_t H, int64_t I, OutType out) 
 OutType out_type(nvfp4_dtype t) { return t == NVFP4_DT_F32 ? OutType::F32 : OutType::BF16; }
 
 struct LayerWs {
-  uint32_t *ctl;   // first: what moe_layer_workspace_init zeroes
+  uint32_t *done;
   float *logits;
-  int32_t *seg_pairs;
-  uint16_t *h, *sh;
-  int64_t h_ld, sh_ld;
+  uint16_t *sh;
+  int64_t sh_ld;
   float *part, *spart;
 };
 LayerWs carve_layer(Carver &c, int64_t T, int64_t H, int64_t I, int64_t E, int64_t k,
                     int64_t Is) {
   LayerWs w;
-  const int64_t P = T * k;
-  w.ctl = c.take<uint32_t>(layer_ctl_bytes() / sizeof(uint32_t));
+  const int64_t sw = layer_slice(T, I, k);
+  w.done = c.take<uint32_t>(64);
   w.logits = c.take<float>((size_t)(T * (E + 1)));
-  w.seg_pairs = c.take<int32_t>((size_t)(4 * P));
-  w.h_ld = (I + 63) / 64 * 64;
   w.sh_ld = (Is + 63) / 64 * 64;
-  w.h = c.take<uint16_t>((size_t)(P * w.h_ld));
   w.sh = c.take<uint16_t>((size_t)(T * w.sh_ld));
-  w.part = c.take<float>((size_t)(P * H));
+  w.part = c.take<float>((size_t)(T * k * ((I + sw - 1) / sw) * H));
   w.spart = c.take<float>(Is ? (size_t)(T * H) : 0);
   return w;
 }
-constexpr size_t kLayerCtlMin = 4096;
 constexpr int64_t kLayerMaxDim = (int64_t)1 << 20;
 
 }  // namespace
@@ -1584,19 +1579,7 @@ size_t moe_layer_decode_workspace_size(int64_t T, int64_t H, int64_t I, int32_t 
   if (T < 1 || H < 1 || I < 1 || E < 1 || k < 1 || shared_I < 0) return 0;
   Carver c(nullptr);
   carve_layer(c, T, H, I, E, k, shared_I);
-  return c.used > kLayerCtlMin ? c.used : kLayerCtlMin;
-}
-
-nvfp4_status moe_layer_workspace_init(void *workspace, size_t workspace_bytes,
-                                      hipStream_t stream) {
-  g_last_error[0] = 0;
-  CHECK_NULL(workspace);
-  CHECK_ALIGN(workspace);
-  if (workspace_bytes < kLayerCtlMin || workspace_bytes < layer_ctl_bytes())
-    return fail(NVFP4_ERR_WORKSPACE_TOO_SMALL, "workspace has %zu bytes, needs at least %zu",
-                workspace_bytes, kLayerCtlMin);
-  LAUNCH(launch_layer_init(static_cast<uint32_t *>(workspace), stream), "layer workspace init");
-  return NVFP4_OK;
+  return c.used;
 }
 
 nvfp4_status moe_layer_decode(const void *x, int64_t T, const moe_layer *layer, int renormalize,
@@ -1690,16 +1673,15 @@ nvfp4_status moe_layer_decode(const void *x, int64_t T, const moe_layer *layer, 
   a.sgate = static_cast<const uint16_t *>(l.shared_gate);
   a.ids = topk_ids;
   a.weights = topk_weights;
-  a.ctl = ws.ctl;
+  a.done = ws.done;
   a.logits = ws.logits;
-  a.seg_pairs = ws.seg_pairs;
-  a.h = ws.h;
   a.sh = ws.sh;
-  a.h_ld = (int)ws.h_ld;
   a.sh_ld = (int)ws.sh_ld;
   a.part = ws.part;
   a.spart = ws.spart;
-  LAUNCH(launch_layer(a, y, out_type(y_dtype), stream), "moe layer");
+  a.y = y;
+  a.y_type = out_type(y_dtype);
+  LAUNCH(launch_layer(a, stream), "moe layer");
   return NVFP4_OK;
 }
 

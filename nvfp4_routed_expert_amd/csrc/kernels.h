@@ -382,21 +382,20 @@ struct LayerArgs {
   const uint16_t *sgate;        // [H] or null: shared output times sigmoid(x . sgate)
   int32_t *ids;                 // outputs [T, k]
   float *weights;
+  void *y;                      // [T, H]
+  OutType y_type;
   // workspace
-  uint32_t *ctl;                // control words, zero before the call
+  uint32_t *done;               // [64] workgroups that have added to a token
   float *logits;                // [T, E (+ 1)]
-  int32_t *seg_pairs;           // [T k][4]
-  uint16_t *h, *sh;             // [T k][h_ld], [T][sh_ld]: rows of whole 128-byte lines
-  int h_ld, sh_ld;
-  float *part, *spart;          // [T k][H], [T][H]
-  // set by launch_layer: items per class and batches of rows per item
-  int n_router, n_su, n_sd, n_gu, n_dn;
-  int it_gu, it_dn, it_su, it_sd;
+  uint16_t *sh;                 // [T][sh_ld] the shared expert's h
+  int sh_ld;
+  float *part, *spart;          // [T k][slices][H], [T][H]
+  // set by launch_layer: tiles, slices of I and shared-down workgroups
+  int n_router, n_c, n_sd;
 };
 bool layer_supported(int64_t T, int E, int k);
-size_t layer_ctl_bytes();
-hipError_t launch_layer_init(uint32_t *ctl, hipStream_t s);
-hipError_t launch_layer(const LayerArgs &a, void *y, OutType yt, hipStream_t s);
+int layer_slice(int64_t T, int64_t I, int64_t k);   // columns of I per slice
+hipError_t launch_layer(const LayerArgs &a, hipStream_t s);
 
 // ---- measurement aid (probe.hip) ---------------------------------------------------
 

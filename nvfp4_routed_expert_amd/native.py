@@ -118,7 +118,6 @@ def lib():
             "moe_layer_decode": (_i32, [_vp, _i64, ctypes.POINTER(MoeLayerC), ctypes.c_int, _vp,
                                         _vp, _vp, _i32, _vp, _sz, _vp]),
             "moe_layer_decode_workspace_size": (_sz, [_i64, _i64, _i64, _i32, _i32, _i64]),
-            "moe_layer_workspace_init": (_i32, [_vp, _sz, _vp]),
             "nvfp4_set_ffn_stage_events": (None, [_vp]),
             "nvfp4_set_ffn_separate_h_quant": (None, [ctypes.c_int]),
             "nvfp4_read_probe": (_i32, [_vp, _sz, _vp, _vp]),
@@ -150,7 +149,7 @@ def exported_symbols():
             "moe_grouped_nvfp4_ffn_static", "moe_grouped_nvfp4_ffn_static_max_bytes",
             "fp8_block_quantize", "fp8_block_linear", "fp8_block_linear_workspace_size",
             "fp8_block_mlp", "fp8_block_mlp_workspace_size",
-            "moe_layer_decode", "moe_layer_decode_workspace_size", "moe_layer_workspace_init",
+            "moe_layer_decode", "moe_layer_decode_workspace_size",
             "nvfp4_set_ffn_stage_events",
             "nvfp4_set_ffn_separate_h_quant", "nvfp4_read_probe",
             "nvfp4_status_string", "nvfp4_last_error"]
@@ -659,18 +658,6 @@ def fp8_block_mlp(x, gate, up, down, out_dtype=torch.bfloat16, workspace=None, o
 # ---- a whole MoE layer for a few tokens ------------------------------------------
 
 
-def layer_workspace(T, H, I, E, k, shared_I, device):
-    """A workspace for moe_layer_decode made ready by moe_layer_workspace_init
-    (on the device's current stream); every call leaves it ready again, so one
-    serves successive (not overlapping) calls of at most this size."""
-    L = lib()
-    with torch.cuda.device(device):
-        ws = torch.empty(max(L.moe_layer_decode_workspace_size(T, H, I, E, k, shared_I), 4096),
-                         dtype=torch.uint8, device=device)
-        _check(L.moe_layer_workspace_init(_ptr(ws), ws.numel(), _stream()))
-    return ws
-
-
 def moe_layer_decode(x, router_w, weights: ExpertWeights, k, renormalize=True, bias=None,
                      shared=None, shared_gate=None, out_dtype=torch.bfloat16, route_out=None,
                      out=None, workspace=None):
@@ -678,7 +665,6 @@ def moe_layer_decode(x, router_w, weights: ExpertWeights, k, renormalize=True, b
     launches: router x . router_w^T (+ bias), top-k, NVFP4 routed experts and,
     with shared = (w_gate [Is, H], w_up [Is, H], w_down [H, Is]) bf16, the
     shared expert (times sigmoid(x . shared_gate), bf16 [H], when given).
-    workspace: from layer_workspace (a fresh one is made when omitted).
     Returns (y [T, H], (topk_ids [T, k], topk_weights [T, k]))."""
     T, H = x.shape
     E, I = weights.num_experts, weights.intermediate
@@ -720,9 +706,7 @@ def moe_layer_decode(x, router_w, weights: ExpertWeights, k, renormalize=True, b
     y = out if out is not None else torch.empty((T, H), dtype=out_dtype, device=dev)
     _expect("out", y, (T, H), y.dtype)
     L = lib()
-    nbytes = L.moe_layer_decode_workspace_size(T, H, I, E, k, Is)
-    ws = _workspace(nbytes, dev, workspace) if workspace is not None else \
-        layer_workspace(T, H, I, E, k, Is, dev)
+    ws = _workspace(L.moe_layer_decode_workspace_size(T, H, I, E, k, Is), dev, workspace)
     sp = [t.data_ptr() for t in shared] if shared is not None else [None] * 3
     layer = MoeLayerC(H, I, E, k, router_w.data_ptr(), None if bias is None else bias.data_ptr(),
                       weights.c_struct(), Is, *sp,

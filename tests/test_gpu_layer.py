@@ -63,6 +63,11 @@ class Layer:
         self.sgate = (rn(H) * H ** -0.5).to(torch.bfloat16).to(DEV) if gate else None
         self.Is = Is
 
+    def workspace(self, T=None):
+        n = native.lib().moe_layer_decode_workspace_size(T or self.T, self.H, self.I, self.E,
+                                                         self.k, self.Is)
+        return torch.empty(n, dtype=torch.uint8, device=DEV).fill_(0xA5)   # any contents will do
+
     def run(self, **kw):
         kw.setdefault("x", self.x)
         x = kw.pop("x")
@@ -169,7 +174,7 @@ def test_repeated_calls_on_one_workspace():
     a call on a fresh workspace; outputs behind the batch are left alone."""
     say("workspace reuse")
     L = Layer(16, 512, 256, 24, 4, 128, gate=True, seed=3)
-    ws = native.layer_workspace(16, 512, 256, 24, 4, 128, DEV)
+    ws = L.workspace()
     for T in (16, 1, 5, 16, 2, 2, 9):
         x = L.x[:T].contiguous()
         out = torch.full((18, 512), 3.0, dtype=torch.float32, device=DEV)
@@ -177,7 +182,6 @@ def test_repeated_calls_on_one_workspace():
         y2, (i2, w2) = L.run(x=x, out_dtype=torch.float32)
         assert torch.equal(y, y2) and torch.equal(i, i2) and torch.equal(w, w2)
         assert torch.all(out[0] == 3.0) and torch.all(out[1 + T:] == 3.0)
-    assert int(ws[:2816].sum()) == 0          # the control words, ready for the next call
 
 
 def test_empty_batch():
@@ -195,7 +199,7 @@ def test_graph_replays():
     graphs = []
     for T in (8, 3):
         x = L.x[:T].contiguous()
-        ws = native.layer_workspace(T, 512, 256, 32, 4, 128, DEV)
+        ws = L.workspace(T)
         y = torch.empty((T, 512), dtype=torch.float32, device=DEV)
         route = (torch.empty((T, 4), dtype=torch.int32, device=DEV),
                  torch.empty((T, 4), dtype=torch.float32, device=DEV))
@@ -227,7 +231,7 @@ def test_two_streams_at_once():
     M = Layer(4, 1024, 512, 64, 8, 256, seed=9)
     want = [a.run(out_dtype=torch.float32)[0] for a in (L, M)]
     streams = [torch.cuda.Stream() for _ in range(2)]
-    spaces = [native.layer_workspace(a.T, 1024, 512, 64, 8, 256, DEV) for a in (L, M)]
+    spaces = [a.workspace() for a in (L, M)]
     torch.cuda.synchronize()
     outs = [[], []]
     for _ in range(6):

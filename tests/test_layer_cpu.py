@@ -65,13 +65,10 @@ def test_sizes():
 def test_workspace():
     L = native.lib()
     n = L.moe_layer_decode_workspace_size(4, 256, 64, 8, 2, 32)
-    assert n >= 4 * 2 * 256 * 4 and n >= 4096
+    assert n >= 4 * 2 * 256 * 4
     assert call(make(), nbytes=n - 1) == 4 and "workspace" in _last()
     assert call(make(), ws=None, nbytes=n) == 1
     assert call(make(), ws=MIS, nbytes=n) == 3
-    assert L.moe_layer_workspace_init(None, 4096, None) == 1
-    assert L.moe_layer_workspace_init(ctypes.c_void_p(MIS), 4096, None) == 3
-    assert L.moe_layer_workspace_init(ctypes.c_void_p(FAKE), 4095, None) == 4
     assert L.moe_layer_decode_workspace_size(0, 256, 64, 8, 2, 32) == 0
 
 
