@@ -321,8 +321,10 @@ Fp8MlpWs carve_fp8_mlp(Carver &c, int64_t T, int64_t H, int64_t I, OutType out) 
 OutType out_type(nvfp4_dtype t) { return t == NVFP4_DT_F32 ? OutType::F32 : OutType::BF16; }
 
 struct LayerWs {
-  uint32_t *done;
+  uint32_t *ctl;
   float *logits;
+  uint8_t *x_pieces;
+  int32_t *x_shift;
   uint16_t *sh;
   int64_t sh_ld;
   float *part, *spart;
@@ -331,15 +333,18 @@ LayerWs carve_layer(Carver &c, int64_t T, int64_t H, int64_t I, int64_t E, int64
                     int64_t Is) {
   LayerWs w;
   const int64_t sw = layer_slice(T, I, k);
-  w.done = c.take<uint32_t>(64);
+  w.ctl = c.take<uint32_t>(layer_ctl_bytes() / sizeof(uint32_t));
   w.logits = c.take<float>((size_t)(T * (E + 1)));
+  w.x_pieces = c.take<uint8_t>(layer_x_bytes(T, H));
+  w.x_shift = c.take<int32_t>((size_t)T);
   w.sh_ld = (Is + 63) / 64 * 64;
   w.sh = c.take<uint16_t>((size_t)(T * w.sh_ld));
   w.part = c.take<float>((size_t)(T * k * ((I + sw - 1) / sw) * H));
   w.spart = c.take<float>(Is ? (size_t)(T * H) : 0);
   return w;
 }
-constexpr int64_t kLayerMaxDim = (int64_t)1 << 20;
+// (a segment's x is held in LDS, an expert's offsets are 32-bit)
+constexpr int64_t kLayerMaxH = (int64_t)1 << 13, kLayerMaxDim = (int64_t)1 << 20;
 
 }  // namespace
 
@@ -1610,10 +1615,10 @@ nvfp4_status moe_layer_decode(const void *x, int64_t T, const moe_layer *layer, 
   if (l.shared_I < 0)
     return fail(NVFP4_ERR_INVALID_ARGUMENT, "shared_I = %lld < 0", (long long)l.shared_I);
   if (l.shared_I > 0) TRY(check_k(l.shared_I, "shared_I"));
-  if (l.H > kLayerMaxDim || l.I > kLayerMaxDim || l.shared_I > kLayerMaxDim)
-    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "H, I or shared_I exceeds 2^20");
-  if (l.H * l.I > (int64_t)1 << 32 || l.H * l.shared_I > (int64_t)1 << 30)
-    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "H * I exceeds 2^32 or H * shared_I 2^30");
+  if (l.H > kLayerMaxH || l.I > kLayerMaxDim || l.shared_I > kLayerMaxDim)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "H exceeds 2^13, or I or shared_I 2^20");
+  if (l.H * l.I > (int64_t)1 << 32)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "H * I exceeds 2^32");
   if (y_dtype != NVFP4_DT_BF16 && y_dtype != NVFP4_DT_F32)
     return fail(NVFP4_ERR_INVALID_ARGUMENT, "y_dtype %d is not BF16 or F32", (int)y_dtype);
   CHECK_NULL(l.router);
@@ -1673,8 +1678,10 @@ nvfp4_status moe_layer_decode(const void *x, int64_t T, const moe_layer *layer, 
   a.sgate = static_cast<const uint16_t *>(l.shared_gate);
   a.ids = topk_ids;
   a.weights = topk_weights;
-  a.done = ws.done;
+  a.ctl = ws.ctl;
   a.logits = ws.logits;
+  a.x_pieces = ws.x_pieces;
+  a.x_shift = ws.x_shift;
   a.sh = ws.sh;
   a.sh_ld = (int)ws.sh_ld;
   a.part = ws.part;

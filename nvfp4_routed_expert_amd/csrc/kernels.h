@@ -385,16 +385,21 @@ struct LayerArgs {
   void *y;                      // [T, H]
   OutType y_type;
   // workspace
-  uint32_t *done;               // [64] workgroups that have added to a token
+  uint32_t *ctl;                // control words
   float *logits;                // [T, E (+ 1)]
+  uint8_t *x_pieces;            // [T][2][H padded to 1024] E4M3 pieces of x
+  int32_t *x_shift;             // [T]
   uint16_t *sh;                 // [T][sh_ld] the shared expert's h
   int sh_ld;
   float *part, *spart;          // [T k][slices][H], [T][H]
-  // set by launch_layer: tiles, slices of I and shared-down workgroups
-  int n_router, n_c, n_sd;
+  // set by launch_layer: router and shared gate/up tiles, slices of I, shared-
+  // down items
+  int n_router, n_su, n_c, n_sd;
 };
 bool layer_supported(int64_t T, int E, int k);
+size_t layer_ctl_bytes();
 int layer_slice(int64_t T, int64_t I, int64_t k);   // columns of I per slice
+size_t layer_x_bytes(int64_t T, int64_t H);          // x_pieces
 hipError_t launch_layer(const LayerArgs &a, hipStream_t s);
 
 // ---- measurement aid (probe.hip) ---------------------------------------------------

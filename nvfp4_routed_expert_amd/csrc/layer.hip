@@ -7,30 +7,52 @@
 //
 //   front  what depends on x alone: the logits (tiles of 16 router rows) and
 //          the shared expert's h (tiles of 16 gate and up rows), by MFMA.
-//   ffn    a workgroup per (segment, slice of SW columns of I), and some for
-//          the shared down rows.  Each workgroup routes the whole batch
-//          itself (a wave per token, no traffic but the logits), so no
-//          routing launch stands between the logits and the weight stream.  A segment is
-//          up to two tokens of one expert: their weight rows are read and
-//          decoded once.  The slice of h stays in LDS and its product with
-//          the slice's columns of the down rows is a partial row of y per
-//          token; the last workgroup to finish a token adds the token's rows
-//          in a fixed order and writes y.
+//   ffn    persistent workgroups.  Each routes the whole batch itself (a wave
+//          per token, no traffic but the logits), so no routing launch stands
+//          between the logits and the weight stream, and then claims items:
+//            FF  a segment's slice of SW columns of I.  A segment is up to
+//                four tokens of one expert: their weight rows are read once.
+//                The slice of h stays in LDS, and its product with the
+//                slice's columns of the down rows is a partial row of y per
+//                token;
+//            SD  shared down: 128 rows of y for every token;
+//            C   512 columns of one token's y: its partial rows added in a
+//                fixed order, once every SD and FF item of the token is done.
 //
-// No workgroup ever waits for another one.  Partial rows cross workgroups
-// through device-scope stores and loads (past the XCDs' L2s), each wave's
-// stores complete before its workgroup counts itself done for the token:
-// agent-scope fences would write back whole L2s.
-#include "common.h"
+// Items are numbered in this order and claimed from one counter, so an item
+// only ever waits for items claimed before it, which are done or held by
+// resident workgroups that wait for nothing later: every wait ends whatever
+// part of the grid is resident, also beside other kernels.  Waits are bounded
+// all the same (two calls at once on one workspace, which the interface
+// forbids): past the bound y is NaN.  Partial rows cross workgroups through
+// device-scope stores and loads (past the XCDs' L2s), each wave's stores
+// complete before its item is counted done: agent-scope fences would write
+// back whole L2s.
+//
+// The products run on the matrix unit without unpacking a code.
+// v_mfma_f32_16x16x128_f8f6f4 takes the E2M1 codes as they lie in memory (16
+// rows of 128 elements, one KiB), but its block scales are powers of two per
+// 32 elements, NVFP4's are E4M3 per 16.  So the activation operand separates
+// the eight 16-element blocks: its row b is zero outside block b, and the
+// result is a row's eight block sums, one lane each four, which meet the
+// row's four E4M3 scales (one 32-bit load) in four FMAs.  The operand's other
+// eight rows carry a second piece of the activations: with a power-of-two
+// scale per token, x = hi + lo / 16 with hi and lo E4M3 represents a bf16 x
+// to 2^-22 of the token's largest |x|.  Per KiB of codes that is one MFMA and
+// a dozen VALU instructions for each token (unpacking to bf16 pairs and
+// v_dot2 takes 45, which bound the kernel), so a batch's tokens cost little
+// beside the stream.  The unit's sums of 16 products keep about 17 bits
+// (4e-6 of the result in the Frobenius norm, measured on Gaussian data);
+// block sums, scales and K add up in fp32.
+#include "fp8.h"
 #include "kernels.h"
 #include "rowdot.h"
 
 namespace nvfp4 {
 namespace {
 
-constexpr int kXcds = 8;                   // consecutive workgroups land on different XCDs
-constexpr int kSegTokens = 2;              // most tokens of one segment
-constexpr int kNvSlice = 2048;             // elements of a row a wave covers per load
+constexpr int kSegTokens = 4;              // most tokens of one segment
+constexpr int kChunk = 128;                // K of one matrix instruction
 constexpr int kLMaxT = 64, kLMaxP = 512, kLMaxE = 1024, kLMaxK = 32;
 
 template <typename T>
@@ -44,6 +66,31 @@ __device__ __forceinline__ void dev_store(T *p, T v) {
 __device__ __forceinline__ uint32_t dev_add(uint32_t *p, uint32_t v) {
   return __hip_atomic_fetch_add(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
+// Control words, zeroed by the front launch: items done per token, the claim
+// counter and the error flag (lines of their own).
+constexpr int kCtlDone = 0, kCtlClaim = 96, kCtlError = 128, kCtlWords = 160;
+constexpr uint64_t kWaitTicks = 300000000ull;   // 100 MHz: far above any wait of a correct call
+
+// Waits until *p >= want (uniform).  False: the bound was met, here or in
+// another workgroup.
+__device__ __forceinline__ bool wait_for(uint32_t *ctl, const uint32_t *p, uint32_t want) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 0;; ++n) {
+    if (dev_load(p) >= want) break;
+    if ((n & 255u) == 255u) {
+      if (dev_load(ctl + kCtlError)) return false;
+      const uint64_t now = __builtin_amdgcn_s_memrealtime();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitTicks) {
+        dev_store(ctl + kCtlError, 1u);
+        return false;
+      }
+    }
+    __builtin_amdgcn_s_sleep(4);
+  }
+  asm volatile("" ::: "memory");
+  return true;
+}
 // this wave's stores have reached the coherence point
 __device__ __forceinline__ void stores_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
@@ -51,148 +98,37 @@ __device__ __forceinline__ int wave_index() {   // in a scalar register
   return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
 }
 
-// v[0..7]: per-lane partial sums of 8 values.  Every lane gets the total of
-// value lane & 7 over its aligned group of g lanes (8, 16, 32 or 64, uniform):
-// a butterfly within eight lanes, then the groups' halves joined.
-__device__ __forceinline__ float reduce8_g(float (&v)[8], int g, int lane) {
-  float r = reduce8<8>(v, lane);
-  if (g > 8) r += dpp_f32<0x128>(r);    // row_ror:8
-  if (g > 16) {
-    float o = r;
-    swap16(r, o);
-    r += o;
-  }
-  if (g > 32) {
-    float o = r;
-    swap32(r, o);
-    r += o;
-  }
-  return r;
-}
-
-// The same within groups of 4 lanes: every lane gets two totals, of values
-// reduce4_idx(lane) and the next one.
-__device__ __forceinline__ void reduce8_4(float (&v)[8], int lane, float (&r)[2]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) v[j] = pair_level<0x4E, 1>(v[j], v[j + 4], lane);   // lane ^ 2
-#pragma unroll
-  for (int j = 0; j < 2; ++j) r[j] = pair_level<0xB1, 0>(v[j], v[j + 2], lane);   // lane ^ 1
-}
-__device__ __forceinline__ int reduce4_idx(int lane) { return (lane & 2) * 2 + (lane & 1) * 2; }
-
-// Lanes that share a row of K elements, 32 each per load.
-__host__ __device__ inline int nv_lanes(int K) { return K <= 256 ? 8 : K <= 512 ? 16 : K <= 1024 ? 32 : 64; }
-
-// ---------------------------------------------------------------------------
-// row streams: dot products of weight rows with NT activation rows
-// ---------------------------------------------------------------------------
-//
-// A batch is eight load steps; step st of a lane reads one row (its sub-row
-// of the step), and a row longer than a wave's reach is taken in slices,
-// accumulated per lane.  The next slice's (or batch's) step is loaded right
-// after the current one is used, so eight loads stay in flight.  Addresses are
-// a uniform base and a 32-bit lane offset, clamped to the last row.
-
-template <int NT>
-struct Sums {
-  float v[NT][8];
-};
-
-// 32 codes against NT activation rows, one 16-element block at a time
-template <int NT>
-__device__ __forceinline__ void dot_step(const u32x4 codes, uint32_t scale, const uint32_t (&a)[NT][16],
-                                         int st, Sums<NT> &sums) {
-  const f32x2_t sc = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(scale, 1.0f, false);
-#pragma unroll
-  for (int b = 0; b < 2; ++b) {
-    uint32_t w[8];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const uint32_t c = codes[2 * b + q];
-      w[4 * q + 0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, 1.0f, 0));
-      w[4 * q + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, 1.0f, 1));
-      w[4 * q + 2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, 1.0f, 2));
-      w[4 * q + 3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, 1.0f, 3));
-    }
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      float d = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        d = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, w[i]),
-                                            __builtin_bit_cast(bf16x2_t, a[t][8 * b + i]), d, false);
-      sums.v[t][st] = __builtin_fmaf(d, sc[b], sums.v[t][st]);
-    }
-    __builtin_amdgcn_sched_barrier(0);   // (one block's codes decoded at a time)
-  }
-}
-
-// Rows of K elements: step st of batch it reads row0 + it * span + (st & (SM -
-// 1)) * rpl of matrix st / SM (row0: this lane's first row), at most last_row.
-// load_a(k, ok, a): the activation rows at k; done(it, sums): the batch's
-// per-lane sums.
-template <int NT, int SM, class LoadA, class Done>
-__device__ __forceinline__ void nv_stream(int K, int lpr, int its, int lane,
-                                          const uint8_t *const (&codes)[8 / SM],
-                                          const uint8_t *const (&scales)[8 / SM], int row0, int span,
-                                          int rpl, int last_row, LoadA load_a, Done done) {
-  const int seg = lane & (lpr - 1);
-  const int nsl = lpr < 64 ? 1 : (K + kNvSlice - 1) / kNvSlice;
-  const uint32_t crow = (uint32_t)K / 2, srow = (uint32_t)K / 16;
-  u32x4 bq[8];
-  uint32_t sq[8];
-  // this lane's byte offsets in slice s (masked lanes read valid bytes)
-  uint32_t c_off, c_last, s_off, s_last;
-  auto slice = [&](int s) {
-    const uint32_t k = (uint32_t)min(s * kNvSlice + 32 * seg, K - 32);
-    c_off = __umul24((uint32_t)row0, crow) + k / 2;
-    s_off = __umul24((uint32_t)row0, srow) + k / 16;
-    c_last = __umul24((uint32_t)last_row, crow) + k / 2;
-    s_last = __umul24((uint32_t)last_row, srow) + k / 16;
-  };
-  auto load = [&](int st, int it) {
-    const uint32_t r = (uint32_t)(it * span + (st & (SM - 1)) * rpl);   // uniform
-    bq[st] = __builtin_nontemporal_load(
-        reinterpret_cast<const u32x4 *>(codes[st / SM] + min(c_off + r * crow, c_last)));
-    sq[st] = *reinterpret_cast<const uint16_t *>(scales[st / SM] + min(s_off + r * srow, s_last));
-  };
-  slice(0);
-#pragma unroll
-  for (int st = 0; st < 8; ++st) load(st, 0);
-  uint32_t a[NT][16];
-  Sums<NT> sums;
-#pragma unroll 1
-  for (int it = 0; it < its; ++it) {
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int st = 0; st < 8; ++st) sums.v[t][st] = 0.0f;
-#pragma unroll 1
-    for (int s = 0; s < nsl; ++s) {
-      if (nsl > 1 || it == 0) {
-        const int k = s * kNvSlice + 32 * seg;
-        load_a(min(k, K - 32), k < K, a);
-      }
-      const bool wrap = s + 1 == nsl;
-      const int it1 = wrap ? it + 1 : it;
-      if (nsl > 1) slice(wrap ? 0 : s + 1);
-      // past the end every lane reads the matrix's first bytes (one line, no
-      // branch around each load)
-      if (it1 == its) c_last = s_last = 0;
-#pragma unroll
-      for (int st = 0; st < 8; ++st) {
-        const u32x4 c = bq[st];
-        const uint32_t sc = sq[st];
-        load(st, it1);
-        dot_step<NT>(c, sc, a, st, sums);
-      }
-    }
-    done(it, sums);
-  }
-}
-
 __device__ __forceinline__ uint16_t swiglu_bf16(float g, float u) {
   return (uint16_t)f32_to_bf16_bits(g / (1.0f + expf(-g)) * u);
+}
+
+// ---------------------------------------------------------------------------
+// activation pieces
+// ---------------------------------------------------------------------------
+
+// Chunks of weights in flight per wave (a body): a segment of one token has
+// the registers for twice as many.
+constexpr int kMaxDepth = 8;
+__host__ __device__ constexpr int ffn_depth(int nt) { return nt == 1 ? kMaxDepth : 4; }
+constexpr int kFfnWaves = 8, kFfnThreads = 64 * kFfnWaves;
+// chunks of a row of H, padded to whole bodies (x is zero there)
+__host__ __device__ inline int layer_chunks(int H) {
+  return (H + kMaxDepth * kChunk - 1) / (kMaxDepth * kChunk) * kMaxDepth;
+}
+
+// Power of two that brings a row's largest magnitude into [128, 256), and the
+// two E4M3 pieces of a scaled value: hi to nearest (4 significant bits, so
+// |v - hi| <= 8), lo the remainder times 16.
+__device__ __forceinline__ int piece_shift(uint32_t max_bits) {
+  return max_bits ? 7 - exponent_of(__uint_as_float(max_bits)) : 0;
+}
+__device__ __forceinline__ uint32_t piece_hi2(float a, float b) {
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false) & 0xFFFFu;
+}
+__device__ __forceinline__ uint32_t piece_lo2(float a, float b, uint32_t hi) {
+  const f32x2_t h = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi, 1.0f, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32((a - h[0]) * 16.0f, (b - h[1]) * 16.0f, 0,
+                                                   false) & 0xFFFFu;
 }
 
 // ---------------------------------------------------------------------------
@@ -218,32 +154,34 @@ __device__ __forceinline__ void tile_dot(const uint16_t *const (&w)[NM], const u
 #pragma unroll
     for (int j = 0; j < kTT; ++j) acc[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int steps = K / 32;
+  const uint16_t *xr[kTT];
+#pragma unroll
+  for (int j = 0; j < kTT; ++j) xr[j] = x + (int64_t)min(j * 16 + lr, T - 1) * x_ld + 8 * lg;
   for (int s0 = wave; s0 < steps; s0 += waves * kTileBatch) {
     u32x4 wv[NM][kTileBatch];
 #pragma unroll
     for (int b = 0; b < kTileBatch; ++b) {
       const int s = s0 + b * waves;
 #pragma unroll
-      for (int m = 0; m < NM; ++m) {
+      for (int m = 0; m < NM; ++m)
         wv[m][b] = *reinterpret_cast<const u32x4 *>(w[m] + 32 * min(s, steps - 1) + 8 * lg);
-        if (s >= steps) wv[m][b] = u32x4{0u, 0u, 0u, 0u};
-      }
     }
 #pragma unroll
     for (int j = 0; j < kTT; ++j) {
       if (j >= tt) break;   // uniform
-      const uint16_t *xr = x + (int64_t)min(j * 16 + lr, T - 1) * x_ld + 8 * lg;
       u32x4 xv[kTileBatch];
 #pragma unroll
       for (int b = 0; b < kTileBatch; ++b)
-        xv[b] = *reinterpret_cast<const u32x4 *>(xr + 32 * min(s0 + b * waves, steps - 1));
+        xv[b] = *reinterpret_cast<const u32x4 *>(xr[j] + 32 * min(s0 + b * waves, steps - 1));
 #pragma unroll
-      for (int b = 0; b < kTileBatch; ++b)
+      for (int b = 0; b < kTileBatch; ++b) {
+        if (s0 + b * waves >= steps) break;   // uniform
 #pragma unroll
         for (int m = 0; m < NM; ++m)
           acc[m][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
               __builtin_bit_cast(bf16x8_t, wv[m][b]), __builtin_bit_cast(bf16x8_t, xv[b]),
               acc[m][j], 0, 0, 0);
+      }
     }
   }
 }
@@ -251,15 +189,47 @@ __device__ __forceinline__ void tile_dot(const uint16_t *const (&w)[NM], const u
 // The first launch: workgroups of 16 waves, each a tile of 16 rows (K split
 // over the waves, their sums added in wave order in LDS), so all of a tile's
 // loads are in flight at once.  Tiles: the router rows (experts, then the
-// shared gate's row) and the shared expert's gate/up rows.
+// shared gate's row) and the shared expert's gate/up rows; then a workgroup
+// per token for its x pieces.
 constexpr int kFrontWaves = 16;
 constexpr int kFrontThreads = 64 * kFrontWaves;
 
 __global__ __launch_bounds__(kFrontThreads) void layer_front_kernel(const LayerArgs p) {
   __shared__ float red[kFrontWaves / 2][2][16][kLMaxT];
   if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < kLMaxT; i += kFrontThreads) p.done[i] = 0u;
+    for (int i = threadIdx.x; i < kCtlWords; i += kFrontThreads) p.ctl[i] = 0u;
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
+  if ((int)blockIdx.x >= p.n_router + p.n_su) {   // x pieces of one token
+    uint32_t *wmax = reinterpret_cast<uint32_t *>(red);
+    const int t = (int)blockIdx.x - p.n_router - p.n_su, HP = layer_chunks(p.H) * kChunk;
+    const int k = 8 * tid;   // (H <= 8192: one piece of eight per thread)
+    u32x4 v = u32x4{0u, 0u, 0u, 0u};
+    if (k < p.H) v = *reinterpret_cast<const u32x4 *>(p.x + (int64_t)t * p.H + k);
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      m = fmaxf(m, fmaxf(__builtin_fabsf(__uint_as_float(v[i] << 16)),
+                         __builtin_fabsf(__uint_as_float(v[i] & 0xFFFF0000u))));
+    m = wave_max(m);
+    if (lane == 0) wmax[wave] = __float_as_uint(m);
+    __syncthreads();
+    for (int w = 0; w < kFrontWaves; ++w) m = fmaxf(m, __uint_as_float(wmax[w]));
+    const int sh = piece_shift(__float_as_uint(m));
+    if (tid == 0) p.x_shift[t] = sh;
+    if (k >= HP) return;
+    uint32_t h[4], o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a = __builtin_ldexpf(__uint_as_float(v[i] << 16), sh);
+      const float b = __builtin_ldexpf(__uint_as_float(v[i] & 0xFFFF0000u), sh);
+      h[i] = piece_hi2(a, b);
+      o[i] = piece_lo2(a, b, h[i]);
+    }
+    uint8_t *hi = p.x_pieces + (int64_t)t * 2 * HP + k;
+    *reinterpret_cast<u32x2 *>(hi) = u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+    *reinterpret_cast<u32x2 *>(hi + HP) = u32x2{o[0] | (o[1] << 16), o[2] | (o[3] << 16)};
+    return;
+  }
   const int lr = lane & 15, lg = lane >> 4;
   const int tt = (p.T + 15) / 16;
   const bool router = (int)blockIdx.x < p.n_router;   // uniform
@@ -346,13 +316,23 @@ __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {   // every lane
   return max((uint32_t)b[0], (uint32_t)b[1]);
 }
 
-// The top-k of one token by one wave: k rounds of "largest logit, lowest
-// index" over order-preserving integer keys (element i of a lane is expert
-// lane + 64 i).  The maximum is six cross-lane steps; the lane that holds it
-// is found by a ballot, and only among equal keys by index.
+// The top-k of one token by one wave (element i of a lane is expert lane +
+// 64 i), by order-preserving integer keys, equal logits to the lower index.
+// At least k elements are >= the k-th largest of the 64 lanes' maxima, and
+// usually few more: those candidates are listed, and each lane ranks one of
+// them against all (64 independent compares instead of k dependent rounds of
+// reductions).  More than 64 candidates (many equal logits) take the rounds.
+struct TopkLds {
+  uint32_t max[64];
+  uint64_t cand[64];
+};
+__device__ __forceinline__ uint64_t topk_key(uint32_t key, int e) {
+  return ((uint64_t)key << 32) | (uint32_t)~(uint32_t)e;
+}
 template <int N>
-__device__ __forceinline__ void topk_token(const LayerArgs &p, int t, int32_t *ids, float *wts) {
-  const int lane = threadIdx.x & 63;
+__device__ __forceinline__ void topk_token(const LayerArgs &p, int t, TopkLds &l, int32_t *ids,
+                                           float *wts) {
+  const int lane = threadIdx.x & 63, k = p.k;
   const int ER = p.E + (p.sgate ? 1 : 0);
   const float *row = p.logits + (int64_t)t * ER;
   float v[N];
@@ -361,38 +341,62 @@ __device__ __forceinline__ void topk_token(const LayerArgs &p, int t, int32_t *i
   for (int i = 0; i < N; ++i) v[i] = lane + 64 * i < p.E ? row[lane + 64 * i] : 0.0f;
 #pragma unroll
   for (int i = 0; i < N; ++i) key[i] = lane + 64 * i < p.E ? order_key(v[i]) : 0u;
-  uint32_t mine_key = 0u;
-  int mine_id = 0;
-  for (int j = 0; j < p.k; ++j) {
-    uint32_t lm = key[0];
-    int li = 0;
+  uint32_t lm = key[0];
 #pragma unroll
-    for (int i = 1; i < N; ++i) {
-      const bool gt = key[i] > lm;
-      lm = gt ? key[i] : lm;
-      li = gt ? i : li;
-    }
-    const uint32_t best = wave_umax(lm);
-    const uint64_t at = __builtin_amdgcn_ballot_w64(lm == best);
-    const int cand = lane + 64 * li;
-    int id;
-    if ((at & (at - 1)) == 0) {   // one lane (uniform)
-      id = __builtin_amdgcn_readlane(cand, (int)__builtin_ctzll(at));
-    } else {                      // equal logits: the lowest index
-      id = (int)~wave_umax(lm == best ? ~(uint32_t)cand : 0u);
-      id = __builtin_amdgcn_readfirstlane(id);
-    }
+  for (int i = 1; i < N; ++i) lm = max(lm, key[i]);
+  // the k-th largest lane maximum (0 with fewer than k lanes in use)
+  l.max[lane] = lm;
+  int above = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (cand == id && li == i) key[i] = 0u;
-    if (lane == j) {
-      mine_key = best;
-      mine_id = id;
+  for (int j = 0; j < 64; j += 4) {   // (the same address in every lane: a broadcast)
+    const u32x4 o = *reinterpret_cast<const u32x4 *>(&l.max[j]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) above += o[q] > lm;
+  }
+  const uint32_t floor_key = ~wave_umax(above < k ? ~lm : 0u);   // smallest maximum of rank < k
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const bool in = key[i] >= floor_key && key[i] != 0u;
+    const uint64_t at = __builtin_amdgcn_ballot_w64(in);
+    const int pos = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(at >> 32),
+                                                  __builtin_amdgcn_mbcnt_lo((uint32_t)at, 0u));
+    if (in && pos < 64) l.cand[pos] = topk_key(key[i], lane + 64 * i);
+    n += __builtin_popcountll(at);
+  }
+  uint64_t mine = 0ull;
+  int rank = 64;
+  if (n <= 64) {   // (n >= k)
+    mine = lane < n ? l.cand[lane] : 0ull;
+    int r = 0;
+    for (int j = 0; j < n; ++j) r += l.cand[j] > mine;
+    if (lane < n) rank = r;
+  } else {
+    for (int j = 0; j < k; ++j) {
+      uint64_t best = 0ull;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const uint64_t c = key[i] ? topk_key(key[i], lane + 64 * i) : 0ull;
+        best = c > best ? c : best;
+      }
+      const uint32_t hi = wave_umax((uint32_t)(best >> 32));
+      const uint32_t lo = wave_umax((uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
+      const int id = (int)~lo;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (lane + 64 * i == id) key[i] = 0u;
+      if (lane == j) {
+        mine = ((uint64_t)hi << 32) | lo;
+        rank = j;
+      }
     }
   }
-  const float val = __uint_as_float((mine_key & 0x80000000u) ? (mine_key & 0x7FFFFFFFu) : ~mine_key);
-  const float top = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, val), 0));
-  const float ex = lane < p.k ? expf(val - top) : 0.0f;
+  const uint32_t mk = (uint32_t)(mine >> 32);
+  const float val = __uint_as_float((mk & 0x80000000u) ? (mk & 0x7FFFFFFFu) : ~mk);
+  const uint32_t tk = wave_umax(lm);   // (the largest logit; lm predates any removal)
+  const float top = __uint_as_float((tk & 0x80000000u) ? (tk & 0x7FFFFFFFu) : ~tk);
+  const bool chosen = rank < k;
+  const float ex = chosen ? expf(val - top) : 0.0f;
   float den;
   if (p.renormalize) {
     den = wave_sum(ex);
@@ -403,35 +407,38 @@ __device__ __forceinline__ void topk_token(const LayerArgs &p, int t, int32_t *i
       if (lane + 64 * i < p.E) s += expf(v[i] - top);
     den = wave_sum(s);
   }
-  if (lane < p.k) {
-    ids[t * p.k + lane] = mine_id;
-    wts[t * p.k + lane] = ex / den;
+  if (chosen) {
+    ids[t * k + rank] = (int)~(uint32_t)mine;
+    wts[t * k + rank] = ex / den;
   }
 }
 
 // The batch's routing in LDS and the segments: experts in ascending order, an
-// expert's tokens in ascending order, two to a segment.  A token chooses an
+// expert's tokens in ascending order, NTMAX to a segment.  A token chooses an
 // expert at most once, so an expert's tokens are a 64-bit mask, and the
 // experts' first segments are a prefix sum of population counts.
 struct RouteLds {
   int32_t ids[kLMaxP];
   float wts[kLMaxP];
   uint64_t mask[kLMaxE];
-  int32_t wave_sum[16];
+  TopkLds topk[kFfnWaves];
+  int32_t wave_sum[kFfnWaves];
   int32_t expert, pair[kSegTokens];   // this workgroup's segment (pair -1: none)
-  uint32_t last;                      // bit u: it finishes token u of its segment
+  uint64_t tokens;                    // its tokens and the expert's later ones
+  uint32_t hmax[kSegTokens];          // largest |h| of its tokens (float bits)
 };
 
 // Routes the batch; returns the number of segments.  first: the index of the
 // first segment of the experts this thread owns (PER consecutive ones).
 constexpr int kExpertsPer = 2;   // experts per thread (512 threads or more)
+template <int NTMAX>
 __device__ __forceinline__ int route_batch(const LayerArgs &p, RouteLds &l, int &first) {
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
   const int nw = (int)(blockDim.x >> 6), P = p.T * p.k;
   for (int t = wave; t < p.T; t += nw) {
-    if (p.E <= 128) topk_token<2>(p, t, l.ids, l.wts);
-    else if (p.E <= 512) topk_token<8>(p, t, l.ids, l.wts);
-    else topk_token<16>(p, t, l.ids, l.wts);
+    if (p.E <= 128) topk_token<2>(p, t, l.topk[wave], l.ids, l.wts);
+    else if (p.E <= 512) topk_token<8>(p, t, l.topk[wave], l.ids, l.wts);
+    else topk_token<16>(p, t, l.topk[wave], l.ids, l.wts);
   }
   for (int i = tid; i < kLMaxE; i += (int)blockDim.x) l.mask[i] = 0ull;
   __syncthreads();
@@ -442,7 +449,7 @@ __device__ __forceinline__ int route_batch(const LayerArgs &p, RouteLds &l, int 
 #pragma unroll
   for (int u = 0; u < kExpertsPer; ++u) {
     const int e = tid * kExpertsPer + u;
-    if (e < kLMaxE) sum += (__builtin_popcountll(l.mask[e]) + kSegTokens - 1) / kSegTokens;
+    if (e < kLMaxE) sum += (__builtin_popcountll(l.mask[e]) + NTMAX - 1) / NTMAX;
   }
   int incl = sum;
 #pragma unroll
@@ -461,7 +468,10 @@ __device__ __forceinline__ int route_batch(const LayerArgs &p, RouteLds &l, int 
   return total;
 }
 
-// Writes segment seg (this workgroup's) into l.
+// Writes segment seg (this workgroup's) into l: the thread that owns its
+// expert the tokens, then a thread per pair its place.  Holds one barrier; the
+// caller's next one publishes the pairs.
+template <int NTMAX>
 __device__ __forceinline__ void find_segment(const LayerArgs &p, RouteLds &l, int first, int seg) {
   const int tid = threadIdx.x;
   int at = first;
@@ -470,23 +480,23 @@ __device__ __forceinline__ void find_segment(const LayerArgs &p, RouteLds &l, in
     const int e = tid * kExpertsPer + u;
     if (e >= kLMaxE) break;
     uint64_t m = l.mask[e];
-    const int n = (__builtin_popcountll(m) + kSegTokens - 1) / kSegTokens;
+    const int n = (__builtin_popcountll(m) + NTMAX - 1) / NTMAX;
     if (seg >= at && seg < at + n) {
-      for (int q = at; q < seg; ++q) {   // drop the earlier segments' tokens
-        m &= m - 1;
-        m &= m - 1;
-      }
+      for (int q = at; q < seg; ++q)   // drop the earlier segments' tokens
+#pragma unroll
+        for (int w = 0; w < NTMAX; ++w) m &= m - 1;
       l.expert = e;
-      const int t0 = __builtin_ctzll(m);
-      m &= m - 1;
-      const int t1 = m ? __builtin_ctzll(m) : -1;
-      for (int j = 0; j < p.k; ++j) {
-        if (l.ids[t0 * p.k + j] == e) l.pair[0] = t0 * p.k + j;
-        if (t1 >= 0 && l.ids[t1 * p.k + j] == e) l.pair[1] = t1 * p.k + j;
-      }
-      if (t1 < 0) l.pair[1] = -1;
+      l.tokens = m;
     }
     at += n;
+  }
+  if (tid < kSegTokens) l.pair[tid] = -1;
+  __syncthreads();
+  const uint64_t m = l.tokens;
+  const int e = l.expert;
+  for (int i = tid; i < p.T * p.k; i += kFfnThreads) {
+    const int t = i / p.k, r = __builtin_popcountll(m & ((1ull << t) - 1ull));
+    if (((m >> t) & 1ull) && r < NTMAX && l.ids[i] == e) l.pair[r] = i;
   }
 }
 
@@ -494,40 +504,58 @@ __device__ __forceinline__ void find_segment(const LayerArgs &p, RouteLds &l, in
 // combine
 // ---------------------------------------------------------------------------
 
-// y[t] = sum_j sum_c part[t k + j][c] (slot, then slice order) + g spart[t],
-// rounded once; g is 1 or the sigmoid of the shared gate's logit.
-__device__ void combine_token(const LayerArgs &p, int t) {
+__device__ __forceinline__ f32x4 dev_load4(const float *p) {
+  const uint64_t lo = dev_load(reinterpret_cast<const uint64_t *>(p));
+  const uint64_t hi = dev_load(reinterpret_cast<const uint64_t *>(p) + 1);
+  return f32x4{__uint_as_float((uint32_t)lo), __uint_as_float((uint32_t)(lo >> 32)),
+               __uint_as_float((uint32_t)hi), __uint_as_float((uint32_t)(hi >> 32))};
+}
+// C: kCombine columns of y[t] = sum_q part[t][q] + g spart[t], q the token's k
+// n_c partial rows (slot, then slice); g is 1 or the sigmoid of the shared
+// gate's logit.  A quarter of the workgroup adds every fourth row, and the
+// four sums are added in order.  failed: NaN.
+constexpr int kCombine = 512;
+__device__ void combine_item(const LayerArgs &p, int item, bool failed, f32x4 (*sums)[kCombine / 4]) {
+  const int per = (p.H + kCombine - 1) / kCombine;
+  const int t = item / per, q0 = (int)threadIdx.x / (kCombine / 4), i = threadIdx.x % (kCombine / 4);
+  const int col = (item - t * per) * kCombine + 4 * i;
   const int n = p.k * p.n_c;
-  float g = 1.0f;
-  if (p.sgate) g = 1.0f / (1.0f + expf(-p.logits[(int64_t)t * (p.E + 1) + p.E]));
-  for (int col = 2 * (int)threadIdx.x; col < p.H; col += 2 * (int)blockDim.x) {
+  const bool in = col < p.H;   // (H is a multiple of 32)
+  f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f}, sh = acc;
+  if (in) {
     const float *base = p.part + (int64_t)t * n * p.H + col;
-    uint64_t sh = 0;
-    if (p.Is) sh = dev_load(reinterpret_cast<const uint64_t *>(p.spart + (int64_t)t * p.H + col));
-    float a0 = 0.0f, a1 = 0.0f;
-    constexpr int B = 16;   // rows in flight
-    for (int q0 = 0; q0 < n; q0 += B) {
-      uint64_t v[B];
+    if (p.Is && q0 == 0) sh = dev_load4(p.spart + (int64_t)t * p.H + col);
+    constexpr int B = 8;   // rows in flight
+    for (int q = q0; q < n; q += 4 * B) {
+      f32x4 v[B];
 #pragma unroll
       for (int u = 0; u < B; ++u)   // (past the end: a valid row, not added)
-        v[u] = dev_load(reinterpret_cast<const uint64_t *>(base + (int64_t)min(q0 + u, n - 1) * p.H));
+        v[u] = dev_load4(base + (int64_t)min(q + 4 * u, n - 1) * p.H);
 #pragma unroll
-      for (int u = 0; u < B; ++u) {
-        if (q0 + u >= n) break;   // uniform
-        a0 += __uint_as_float((uint32_t)v[u]);
-        a1 += __uint_as_float((uint32_t)(v[u] >> 32));
-      }
+      for (int u = 0; u < B; ++u)
+        if (q + 4 * u < n) acc += v[u];
     }
-    if (p.Is) {
-      a0 += g * __uint_as_float((uint32_t)sh);
-      a1 += g * __uint_as_float((uint32_t)(sh >> 32));
-    }
-    const int64_t o = (int64_t)t * p.H + col;
-    if (p.y_type == OutType::F32)
-      *reinterpret_cast<float2 *>(static_cast<float *>(p.y) + o) = make_float2(a0, a1);
-    else
-      *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.y) + o) =
-          f32_to_bf16_bits(a0) | (f32_to_bf16_bits(a1) << 16);
+  }
+  sums[q0][i] = acc;
+  __syncthreads();
+  if (q0 != 0 || !in) return;
+#pragma unroll
+  for (int w = 1; w < 4; ++w) acc += sums[w][i];
+  if (p.Is) {
+    float g = 1.0f;
+    if (p.sgate) g = 1.0f / (1.0f + expf(-p.logits[(int64_t)t * (p.E + 1) + p.E]));
+    acc += sh * g;
+  }
+  if (failed) acc = f32x4{1.f, 1.f, 1.f, 1.f} * __builtin_nanf("");
+  const int64_t o = (int64_t)t * p.H + col;
+  if (p.y_type == OutType::F32) {
+    *reinterpret_cast<f32x4 *>(static_cast<float *>(p.y) + o) = acc;
+  } else {
+    uint32_t h[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) h[q] = failed ? 0x7FC0u : f32_to_bf16_bits(acc[q]);
+    *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(p.y) + o) =
+        u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
   }
 }
 
@@ -535,203 +563,395 @@ __device__ void combine_token(const LayerArgs &p, int t) {
 // ffn
 // ---------------------------------------------------------------------------
 
-// 32 activations of one row (16-byte aligned) as 16 words; a lane past K gets
-// zeros (by a mask: no branch per word)
-__device__ __forceinline__ void load_act32(const uint16_t *p, bool ok, uint32_t (&a)[16]) {
-  const uint32_t mask = ok ? ~0u : 0u;
+// The activation operand of a chunk from a token's pieces (rows of kp bytes:
+// hi, then lo).  Operand row r: piece r / 8, block r % 8; a lane of group g
+// holds block g in words 0..3 and block 4 + g in words 4..7.
+struct PieceLane {
+  int off;            // piece and block
+  uint32_t m0, m1;    // which half this lane's block is in, if it holds it
+};
+__device__ __forceinline__ PieceLane piece_lane(int lane, int kp) {
+  const int r = lane & 15, g = lane >> 4, blk = r & 7;
+  return PieceLane{(r >> 3) * kp + blk * 16, blk == g ? ~0u : 0u, blk == 4 + g ? ~0u : 0u};
+}
+__device__ __forceinline__ i32x8 piece_operand(const uint8_t *pieces, const PieceLane &l, int chunk) {
+  const u32x4 v = *reinterpret_cast<const u32x4 *>(pieces + l.off + chunk * kChunk);
+  i32x8 a;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const u32x4 v = *reinterpret_cast<const u32x4 *>(p + 8 * q);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) a[4 * q + i] = v[i] & mask;
+  for (int i = 0; i < 4; ++i) {
+    a[i] = (int)(v[i] & l.m0);
+    a[4 + i] = (int)(v[i] & l.m1);
   }
+  return a;
 }
 
-// One slice of one segment by a workgroup of nw waves.
-template <int NT, int SW>
-__device__ __forceinline__ void segment_slice(const LayerArgs &p, const RouteLds &l, int c,
-                                              uint16_t (*h)[SW]) {
-  const int lane = threadIdx.x & 63, wave = wave_index(), nw = (int)(blockDim.x >> 6);
-  const int e = __builtin_amdgcn_readfirstlane(l.expert);
-  int pr[NT];
+// One KiB of codes (lane: row lane & 15, elements 32 g ..) and this lane's
+// four block scales against one token's operand.
+__device__ __forceinline__ float chunk_dot(const i32x8 &a, const u32x4 codes, const f32x4 sc, float c) {
+  const i32x8 b = {(int)codes[0], (int)codes[1], (int)codes[2], (int)codes[3], 0, 0, 0, 0};
+  const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+      a, b, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 4, 0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
 #pragma unroll
-  for (int t = 0; t < NT; ++t) pr[t] = __builtin_amdgcn_readfirstlane(l.pair[t]);
-  const int c0 = c * SW, cols = min(SW, p.I - c0);   // this slice's columns of I
+  for (int i = 0; i < 4; ++i) c = __builtin_fmaf(d[i], sc[i], c);
+  return c;
+}
+__device__ __forceinline__ f32x4 scales4(uint32_t s) {
+  const f32x2_t lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(s, 1.0f, false);
+  const f32x2_t hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(s, 1.0f, true);
+  return f32x4{lo[0], lo[1], hi[0], hi[1]};
+}
+// A lane's codes of chunk c of a row of K elements, and the eight block scales
+// of a chunk.  AL: K is a multiple of 128; otherwise the last chunk's missing
+// elements read valid bytes (the operand is zero there) and scales go two
+// bytes at a time.
+template <bool AL>
+__device__ __forceinline__ u32x4 load_codes(const uint8_t *m, uint32_t row_off, int K, int c, int g) {
+  const uint32_t k = AL ? (uint32_t)(c * 64 + g * 16) : (uint32_t)min(c * 64 + g * 16, K / 2 - 16);
+  return __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(m + (row_off + k)));
+}
+template <bool AL>
+__device__ __forceinline__ u32x2 load_scales(const uint8_t *m, uint32_t row_off, int K, int c) {
+  if constexpr (AL) {
+    return *reinterpret_cast<const u32x2 *>(m + (row_off + (uint32_t)c * 8));
+  } else {
+    uint32_t s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      s[i] = *reinterpret_cast<const uint16_t *>(m + (row_off + (uint32_t)min(c * 8 + 2 * i, K / 16 - 2)));
+    return u32x2{s[0] | (s[1] << 16), s[2] | (s[3] << 16)};
+  }
+}
+// Sum over the four lane groups (a row's eight blocks and two pieces).
+__device__ __forceinline__ float group_sum(float v) {
+  float o = v;
+  swap16(v, o);
+  v += o;
+  o = v;
+  swap32(v, o);
+  return v + o;
+}
 
-  // ---- gate and up rows c0 .. c0 + cols - 1.  Step st of a batch: st < 4 the
-  // gate, else the up row base + it per + (st & 3) rpl + sub; after the
-  // reduction the lane with a row's gate sum meets the up sum at lane ^ 4.
-  {
-    const int lpr = nv_lanes(p.H), rpl = 64 / lpr, sub = lane / lpr;
-    const int per = 4 * rpl, span = per * nw;   // rows of a wave's, of all waves' batch
-    const int first = per * wave;
-    if (first < cols) {
-      const int its = (cols - first + span - 1) / span;
-      const int64_t code_e = (int64_t)p.I * (p.H / 2), scale_e = (int64_t)p.I * (p.H / 16);
-      const uint8_t *const codes[2] = {p.codes[0] + e * code_e, p.codes[1] + e * code_e};
-      const uint8_t *const scales[2] = {p.scales[0] + e * scale_e, p.scales[1] + e * scale_e};
-      const float gg = p.glob[0][e], gu = p.glob[1][e];
-      nv_stream<NT, 4>(
-          p.H, lpr, its, lane, codes, scales, c0 + first + sub, span, rpl, c0 + cols - 1,
-          [&](int k, bool ok, uint32_t (&a)[NT][16]) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-              load_act32(p.x + (int64_t)(pr[t] / p.k) * p.H + k, ok, a[t]);
-          },
-          [&](int it, const Sums<NT> &s) {
-            const int row = first + it * span + (lane & 3) * rpl + lane / lpr;
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              float v[8];
-#pragma unroll
-              for (int st = 0; st < 8; ++st) v[st] = s.v[t][st];
-              const float r = reduce8_g(v, lpr, lane);
-              const float up = __shfl_xor(r, 4, kWave);
-              if ((lane & 4) == 0 && (lane & (lpr - 1)) < 8 && row < cols)
-                h[t][row] = swiglu_bf16(r * gg, up * gu);
-            }
-          });
-    }
-  }
-  // ---- down: every row's SW columns, LPR lanes per row
-  constexpr int LPR = SW / 32, RPL = 64 / LPR;
-  const int seg = lane & (LPR - 1), sub = lane / LPR;
-  const int per = 8 * RPL, span = per * nw, first = per * wave;
-  const bool ok = 32 * seg < cols;
-  const uint32_t kc = (uint32_t)(c0 + min(32 * seg, cols - 32));
-  const uint8_t *codes = p.codes[2] + (int64_t)e * p.H * (p.I / 2);
-  const uint8_t *scales = p.scales[2] + (int64_t)e * p.H * (p.I / 16);
-  const uint32_t crow = (uint32_t)p.I / 2, srow = (uint32_t)p.I / 16;
-  const uint32_t c_off = __umul24((uint32_t)sub, crow) + kc / 2;
-  const uint32_t s_off = __umul24((uint32_t)sub, srow) + kc / 16;
-  uint32_t c_last = __umul24((uint32_t)(p.H - 1), crow) + kc / 2;
-  uint32_t s_last = __umul24((uint32_t)(p.H - 1), srow) + kc / 16;
-  u32x4 bq[8];
-  uint32_t sq[8];
-  auto load = [&](int st, int base) {
-    const uint32_t r = (uint32_t)(base + st * RPL);   // uniform
-    bq[st] = __builtin_nontemporal_load(
-        reinterpret_cast<const u32x4 *>(codes + min(c_off + r * crow, c_last)));
-    sq[st] = *reinterpret_cast<const uint16_t *>(scales + min(s_off + r * srow, s_last));
+constexpr int kScaleRow = 8 * kMaxDepth + 8;   // LDS bytes of a row's scales of a body, padded
+struct FfnLds {
+  RouteLds route;
+  union {
+    __attribute__((aligned(16))) uint8_t scales[kFfnWaves][2][16 * kScaleRow];
+    f32x4 sums[4][kCombine / 4];
   };
-  if (first < p.H) {   // independent of h: in flight across the barrier
-#pragma unroll
-    for (int st = 0; st < 8; ++st) load(st, first);
-  }
-  __syncthreads();
-  if (first >= p.H) return;   // (the caller's barriers are outside)
-  uint32_t a[NT][16];
-  float wt[NT];
-  const float gd = p.glob[2][e];
+  uint32_t item;
+};
+
+// One slice of one segment.  Wave w takes the gate and up rows of the slice's
+// 16-column blocks w, w + 8, .., then every eighth batch of down rows.
+// xp: the tokens' x pieces, [NT][2][HP]; hp: [NT][2][SW].
+//
+// A body is kDepth chunks of a gate and an up block: their codes are loaded
+// two chunks at a time (the two halves of each row's 128-byte lines together)
+// as the previous body's registers fall free; the body's scales come in one
+// or two 8-byte loads per lane (each a chunk's) and go through the wave's own
+// LDS, where a lane finds its four for each chunk.  (One 4-byte load per lane
+// and chunk fetched the scales' lines again and again: 16 rows a load, far
+// more lines in use than the L1 holds.)
+template <int NT, int SW, bool AL>
+__device__ __forceinline__ void segment_slice(const LayerArgs &p, FfnLds &lds, int c, uint8_t *xp,
+                                              uint8_t *hp) {
+  constexpr int NW = kFfnWaves, TW = SW / 16 / NW;   // blocks per wave
+  constexpr int kDepth = ffn_depth(NT), SH = kDepth / 4;   // (SH: chunks' scales a lane loads)
+  RouteLds &l = lds.route;
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
+  const int lr = lane & 15, g = lane >> 4;
+  const int e = __builtin_amdgcn_readfirstlane(l.expert);
+  int pr[NT];   // (a free slot repeats the first pair; nothing of it is stored)
+  const int p0 = __builtin_amdgcn_readfirstlane(l.pair[0]);
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    load_act32(&h[t][32 * seg], ok, a[t]);
-    wt[t] = l.wts[pr[t]] * gd;
+    const int q = __builtin_amdgcn_readfirstlane(l.pair[t]);
+    pr[t] = q >= 0 ? q : p0;
   }
+  const int c0 = c * SW, cols = min(SW, p.I - c0);   // this slice's columns of I
+  const int H = p.H, nch = layer_chunks(H), HP = nch * kChunk;
+  const int last_ch = (H - 1) / kChunk;
+
+  // ---- x pieces to LDS, and the first weight loads behind them
+  u32x4 xv[NT];
+  const int xpos = 16 * tid;   // (2 HP bytes per token: one 16-byte piece per thread and pass)
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+    if (xpos < 2 * HP)
+      xv[t] = *reinterpret_cast<const u32x4 *>(p.x_pieces + (int64_t)(pr[t] / p.k) * 2 * HP + xpos);
+  int xs[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) xs[t] = p.x_shift[pr[t] / p.k];
+
+  const int64_t code_e = (int64_t)p.I * (H / 2), scale_e = (int64_t)p.I * (H / 16);
+  const uint8_t *const gc[2] = {p.codes[0] + e * code_e, p.codes[1] + e * code_e};
+  const uint8_t *const gs[2] = {p.scales[0] + e * scale_e, p.scales[1] + e * scale_e};
+  uint32_t crow, srow;
+  auto set_row = [&](int i) {   // block i of this wave
+    const uint32_t row = (uint32_t)(c0 + min(16 * (wave + NW * i) + lr, cols - 1));
+    crow = row * ((uint32_t)H / 2);
+    srow = row * ((uint32_t)H / 16);
+  };
+  u32x4 cq[kDepth][2];
+  u32x2 sq[2][SH];
+  auto load = [&](int d, int ch) {   // (chunks past H: the last one again, x is zero)
+#pragma unroll
+    for (int m = 0; m < 2; ++m) cq[d][m] = load_codes<AL>(gc[m], crow, H, min(ch, last_ch), g);
+  };
+  auto load_s = [&](int ch) {
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int q = 0; q < SH; ++q)
+        sq[m][q] = load_scales<AL>(gs[m], srow, H, min(ch + SH * g + q, last_ch));
+  };
+  set_row(0);
+  load_s(0);
+#pragma unroll
+  for (int d = 0; d < kDepth; ++d) load(d, d);
+  const float gg = p.glob[0][e], gu = p.glob[1][e], gd = p.glob[2][e];
+
+  if (tid < kSegTokens) l.hmax[tid] = 0u;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    if (xpos < 2 * HP) *reinterpret_cast<u32x4 *>(xp + 2 * t * HP + xpos) = xv[t];
+    for (int k = xpos + 16 * kFfnThreads; k < 2 * HP; k += 16 * kFfnThreads)
+      *reinterpret_cast<u32x4 *>(xp + 2 * t * HP + k) = *reinterpret_cast<const u32x4 *>(
+          p.x_pieces + (int64_t)(pr[t] / p.k) * 2 * HP + k);
+  }
+  __syncthreads();
+
+  // ---- gate and up: h = bf16(silu(gate) up).  After the group sums every
+  // lane group has the totals of row lr; group g keeps token g.
+  const PieceLane xl = piece_lane(lane, HP);
+  const float lane_f = g >= 2 ? 0.0625f : 1.0f;   // the second pieces are 16 times too large
+  uint8_t *const sw = lds.scales[wave][0] + lr * kScaleRow;   // this lane's row (gate; up behind)
+  constexpr int kUp = 16 * kScaleRow;
+  float acc[2][NT], hv[TW];
+  int i = 0, ch0 = 0;
 #pragma unroll 1
-  for (int base = first; base < p.H; base += span) {
-    Sums<NT> s;
+  while (i < TW) {
+    if (ch0 == 0)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) acc[0][t] = acc[1][t] = 0.0f;
+    const bool end = ch0 + kDepth >= nch;   // uniform: the block's last body
+    const int next = end ? 0 : ch0 + kDepth;
+    // (the wave's own LDS: its reads of the last body are done, in order)
+#pragma unroll
+    for (int q = 0; q < SH; ++q) {
+      *reinterpret_cast<u32x2 *>(sw + 8 * (SH * g + q)) = sq[0][q];
+      *reinterpret_cast<u32x2 *>(sw + kUp + 8 * (SH * g + q)) = sq[1][q];
+    }
+    if (end) {
+      set_row(min(i + 1, TW - 1));
+      if (i + 1 == TW) crow = srow = 0u;    // nothing follows: one line, not used
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    load_s(next);
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+      const f32x4 s0 = scales4(*reinterpret_cast<const uint32_t *>(sw + 8 * d + 4 * (g & 1)));
+      const f32x4 s1 = scales4(*reinterpret_cast<const uint32_t *>(sw + kUp + 8 * d + 4 * (g & 1)));
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const i32x8 a = piece_operand(xp + 2 * t * HP, xl, ch0 + d);
+        acc[0][t] = chunk_dot(a, cq[d][0], s0, acc[0][t]);
+        acc[1][t] = chunk_dot(a, cq[d][1], s1, acc[1][t]);
+      }
+      // (loaded only once the registers are free: a load issued earlier would
+      // go to others, and the copies back at the loop's end wait for it)
+      __builtin_amdgcn_sched_barrier(0);
+      if (d & 1) {
+        load(d - 1, next + d - 1);
+        load(d, next + d);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    if (end) {
+      float v = 0.0f;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const float G = __builtin_ldexpf(group_sum(acc[0][t] * lane_f), -xs[t]) * gg;
+        const float U = __builtin_ldexpf(group_sum(acc[1][t] * lane_f), -xs[t]) * gu;
+        const float w = bf16_bits_to_f32(swiglu_bf16(G, U));
+        v = g == t ? w : v;
+      }
+      if (16 * (wave + NW * i) + lr >= cols) v = 0.0f;
+#pragma unroll
+      for (int q = 0; q < TW; ++q) hv[q] = q == i ? v : hv[q];
+      ++i;
+    }
+    ch0 = next;
+  }
+
+  // ---- the first down loads, independent of h
+  constexpr int NC = SW / kChunk;           // chunks of a down row's slice
+  constexpr int TILES = 8 / NC;             // 16-row tiles of a batch (8 code loads)
+  constexpr int BROWS = 16 * TILES;
+  const uint8_t *const dc = p.codes[2] + (int64_t)e * H * (p.I / 2);
+  const uint8_t *const ds = p.scales[2] + (int64_t)e * H * (p.I / 16);
+  const int nb = (H + BROWS - 1) / BROWS;
+  const int ic = c0 / kChunk, last_ic = (p.I - 1) / kChunk;   // first chunk of the slice, last of a row
+  u32x4 dq[8];
+  u32x2 dsq[8];
+  auto load_d = [&](int u, int b) {         // load u of batch b: tile u / NC, chunk u % NC
+    // (b < 0: nothing follows; every lane reads the first row, not used)
+    const uint32_t r = b < 0 ? 0u : (uint32_t)min(b * BROWS + (u / NC) * 16 + lr, H - 1);
+    const int ch = min(ic + u % NC, last_ic);
+    dq[u] = load_codes<AL>(dc, __umul24(r, (uint32_t)p.I / 2), p.I, ch, g);
+    dsq[u] = load_scales<AL>(ds, __umul24(r, (uint32_t)p.I / 16), p.I, ch);
+  };
+#pragma unroll
+  for (int u = 0; u < 8; ++u) load_d(u, min(wave, nb - 1));
+
+  // ---- h pieces
+  if (g < NT) {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int q = 0; q < TW; ++q) m = max(m, __float_as_uint(hv[q]) & 0x7FFFFFFFu);
+    atomicMax(&l.hmax[g], m);
+  }
+  __syncthreads();
+  int hs[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) hs[t] = piece_shift(l.hmax[t]);
+  if (g < NT) {
+    const int sh = piece_shift(l.hmax[g]);
+#pragma unroll
+    for (int q = 0; q < TW; ++q) {
+      const float a = __builtin_ldexpf(hv[q], sh);
+      const uint32_t h = piece_hi2(a, 0.0f);
+      uint8_t *at = hp + 2 * g * SW + 16 * (wave + NW * q) + lr;
+      at[0] = (uint8_t)h;
+      at[SW] = (uint8_t)piece_lo2(a, 0.0f, h);
+    }
+  }
+  __syncthreads();
+
+  // ---- down
+  PieceLane hl = piece_lane(lane, SW);
+  float wt[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) wt[t] = __builtin_ldexpf(l.wts[pr[t]] * gd * lane_f, -hs[t]);
+#pragma unroll 1
+  for (int b = wave; b < nb; b += NW) {
+    float s[NT][TILES];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int st = 0; st < 8; ++st) s.v[t][st] = 0.0f;
-    if (base + span >= p.H) c_last = s_last = 0;   // past the end: one line
+      for (int q = 0; q < TILES; ++q) s[t][q] = 0.0f;
+    const int next = b + NW < nb ? b + NW : -1;
 #pragma unroll
-    for (int st = 0; st < 8; ++st) {
-      const u32x4 cq = bq[st];
-      const uint32_t sc = sq[st];
-      load(st, base + span);
-      dot_step<NT>(cq, sc, a, st, s);
-      // (the sums are formed here: the compiler otherwise sinks the second
-      // token's products behind the first one's stores and spills the codes)
+    for (int u = 0; u < 8; ++u) {
+      // (several tokens' operands are read again for every load: kept, they
+      // would spill)
+      if (NT > 1) asm volatile("" : "+v"(hl.off));
+      const f32x4 sc = scales4((g & 1) ? dsq[u][1] : dsq[u][0]);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) asm volatile("" : "+v"(s.v[t][st]));
-    }
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      float *row = p.part + ((int64_t)pr[t] * p.n_c + c) * p.H + base + sub;
-      if constexpr (LPR == 8) {
-        const int i = (lane & 7) * RPL;
-        const float r = reduce8<8>(s.v[t], lane);
-        if (base + sub + i < p.H) dev_store(row + i, r * wt[t]);
-      } else {
-        static_assert(LPR == 4 || LPR == 8, "slice widths");
-        float r[2];
-        reduce8_4(s.v[t], lane, r);
-        const int i = reduce4_idx(lane) * RPL;
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          if (base + sub + i + q * RPL < p.H) dev_store(row + i + q * RPL, r[q] * wt[t]);
+      for (int t = 0; t < NT; ++t)
+        s[t][u / NC] = chunk_dot(piece_operand(hp + 2 * t * SW, hl, u % NC), dq[u], sc,
+                                 s[t][u / NC]);
+      __builtin_amdgcn_sched_barrier(0);
+      if (u & 1) {
+        load_d(u - 1, next);
+        load_d(u, next);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
+    // four tiles' totals at a time: lane group g ends with tile g
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int q = 0; q < TILES; q += 4) {
+        float v0 = s[t][q] * wt[t], v1 = s[t][q + 1] * wt[t];
+        float v2 = s[t][q + 2] * wt[t], v3 = s[t][q + 3] * wt[t];
+        swap32(v0, v2);
+        v0 += v2;          // groups 0, 1: tile 0, groups 2, 3: tile 2
+        swap32(v1, v3);
+        v1 += v3;
+        swap16(v0, v1);
+        v0 += v1;          // group g: tile g
+        const int r = b * BROWS + 16 * (q + g) + lr;
+        if (r < H && (t == 0 || l.pair[t] >= 0))
+          dev_store(p.part + ((int64_t)pr[t] * p.n_c + c) * H + r, v0);
+      }
   }
 }
 
-// (1024 threads: at most 128 VGPRs, so sixteen waves share a CU whatever the
-// workgroup size)
-template <int SW>
-__global__ __launch_bounds__(1024) void layer_ffn_kernel(const LayerArgs p) {
-  __shared__ RouteLds l;
-  __shared__ __attribute__((aligned(16))) uint16_t h[kSegTokens][SW];
-  __shared__ uint32_t finish[kLMaxT];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int nw = (int)(blockDim.x >> 6);
-  const uint32_t all = (uint32_t)(p.k * p.n_c + p.n_sd);   // workgroups that add to a token
-  if ((int)blockIdx.x < p.n_sd) {
-    // shared down: 16 rows per wave against every token
-    const int lr = lane & 15, lg = lane >> 4;
-    const int r0 = ((int)blockIdx.x * nw + wave_index()) * 16;
-    if (r0 < p.H) {   // (H is a multiple of 32: whole tiles)
-      f32x4 acc[1][kTT];
-      tile_dot<1>({p.sw[2] + (int64_t)(r0 + lr) * p.Is}, p.sh, p.sh_ld, p.T, p.Is, 0, 1, acc);
-#pragma unroll
-      for (int j = 0; j < kTT; ++j) {
-        const int t = 16 * j + lr;
-        if (t >= p.T) continue;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          dev_store(p.spart + (int64_t)t * p.H + r0 + 4 * lg + i, acc[0][j][i]);
-      }
-    }
-    stores_done();
-    __syncthreads();
-    if (tid < p.T) finish[tid] = dev_add(p.done + tid, 1u) == all - 1u;
-    __syncthreads();
-    for (int t = 0; t < p.T; ++t)
-      if (finish[t]) combine_token(p, t);
-    return;
-  }
+template <int SW, bool AL, int NTMAX>
+__global__ __launch_bounds__(kFfnThreads, 2) void layer_ffn_kernel(const LayerArgs p) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t pieces[];   // x pieces of a segment
+  __shared__ FfnLds lds;
+  __shared__ __attribute__((aligned(16))) uint8_t h_pieces[NTMAX * 2 * SW];
+  RouteLds &l = lds.route;
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
+  uint32_t claimed = 0;
+  if (tid == 0) claimed = dev_add(p.ctl + kCtlClaim, 1u);   // (returns while the batch is routed)
   int first;
-  const int nseg = route_batch(p, l, first);
-  if ((int)blockIdx.x == p.n_sd)   // one workgroup writes the routing out
-    for (int i = tid; i < p.T * p.k; i += (int)blockDim.x) {
+  const int nseg = route_batch<NTMAX>(p, l, first);
+  if (blockIdx.x == 0)   // one workgroup writes the routing out
+    for (int i = tid; i < p.T * p.k; i += kFfnThreads) {
       p.ids[i] = l.ids[i];
       p.weights[i] = l.wts[i];
     }
-  // contiguous ranges of items per XCD: an expert's segments share its L2
-  const int b = (int)blockIdx.x - p.n_sd;
-  const int n_items = nseg * p.n_c, per = (n_items + kXcds - 1) / kXcds;
-  const int item = b % kXcds * per + b / kXcds;
-  if (b / kXcds >= per || item >= n_items) return;   // (uniform)
-  const int seg = item / p.n_c, c = item - seg * p.n_c;
-  find_segment(p, l, first, seg);
+  const uint32_t iSD = (uint32_t)(nseg * p.n_c), iC = iSD + (uint32_t)p.n_sd;
+  const uint32_t end = iC + (uint32_t)(p.T * ((p.H + kCombine - 1) / kCombine));
+  const uint32_t all = (uint32_t)(p.k * p.n_c + p.n_sd);   // items that add to a token
+  if (tid == 0) lds.item = claimed;
   __syncthreads();
-  const int second = __builtin_amdgcn_readfirstlane(l.pair[1]);
-  if (second < 0) segment_slice<1, SW>(p, l, c, h);
-  else segment_slice<2, SW>(p, l, c, h);
-  stores_done();
-  __syncthreads();
-  if (tid < kSegTokens) {
-    const int pair = l.pair[tid];
-    finish[tid] = pair >= 0 && dev_add(p.done + pair / p.k, 1u) == all - 1u;
+  uint32_t item = lds.item;
+  while (item < end) {
+    if (item < iSD) {
+      const int seg = (int)item / p.n_c, c = (int)item - seg * p.n_c;
+      find_segment<NTMAX>(p, l, first, seg);
+      if (tid == 0) claimed = dev_add(p.ctl + kCtlClaim, 1u);
+      __syncthreads();
+      if (NTMAX == 1 || __builtin_amdgcn_readfirstlane(l.pair[1]) < 0)
+        segment_slice<1, SW, AL>(p, lds, c, pieces, h_pieces);
+      else if (NTMAX == 2 || __builtin_amdgcn_readfirstlane(l.pair[2]) < 0)
+        segment_slice<NTMAX == 1 ? 1 : 2, SW, AL>(p, lds, c, pieces, h_pieces);
+      else
+        segment_slice<NTMAX, SW, AL>(p, lds, c, pieces, h_pieces);
+      stores_done();
+      __syncthreads();
+      if (tid < NTMAX && l.pair[tid] >= 0) dev_add(p.ctl + kCtlDone + l.pair[tid] / p.k, 1u);
+    } else if (item < iC) {
+      if (tid == 0) claimed = dev_add(p.ctl + kCtlClaim, 1u);
+      // shared down: 16 rows per wave against every token
+      const int lr = lane & 15, lg = lane >> 4;
+      const int r0 = ((int)(item - iSD) * kFfnWaves + wave) * 16;
+      if (r0 < p.H) {   // (H is a multiple of 32: whole tiles)
+        f32x4 acc[1][kTT];
+        tile_dot<1>({p.sw[2] + (int64_t)(r0 + lr) * p.Is}, p.sh, p.sh_ld, p.T, p.Is, 0, 1, acc);
+#pragma unroll
+        for (int j = 0; j < kTT; ++j) {
+          const int t = 16 * j + lr;
+          if (t >= p.T) continue;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            dev_store(p.spart + (int64_t)t * p.H + r0 + 4 * lg + i, acc[0][j][i]);
+        }
+      }
+      stores_done();
+      __syncthreads();
+      if (tid < p.T) dev_add(p.ctl + kCtlDone + tid, 1u);
+    } else {
+      if (tid == 0) claimed = dev_add(p.ctl + kCtlClaim, 1u);
+      const int i = (int)(item - iC), t = i / ((p.H + kCombine - 1) / kCombine);
+      const bool ok = wait_for(p.ctl, p.ctl + kCtlDone + t, all);
+      combine_item(p, i, !ok || dev_load(p.ctl + kCtlError) != 0u, lds.sums);
+    }
+    __syncthreads();
+    if (tid == 0) lds.item = claimed;
+    __syncthreads();
+    item = lds.item;
   }
-  __syncthreads();
-  for (int u = 0; u < kSegTokens; ++u)
-    if (finish[u]) combine_token(p, l.pair[u] / p.k);
 }
 
 }  // namespace
 
+size_t layer_x_bytes(int64_t T, int64_t H) { return (size_t)T * 2 * layer_chunks((int)H) * kChunk; }
+size_t layer_ctl_bytes() { return kCtlWords * sizeof(uint32_t); }
 bool layer_supported(int64_t T, int E, int k) {
   return T >= 0 && T <= kLMaxT && E >= 1 && E <= kLMaxE && k >= 1 && k <= kLMaxK && k <= E &&
          T * k <= kLMaxP;
@@ -747,19 +967,40 @@ hipError_t launch_layer(const LayerArgs &args, hipStream_t s) {
   const int64_t P = (int64_t)a.T * a.k;
   auto groups = [](int rows, int per) { return (rows + per - 1) / per; };
   const int sw = layer_slice(a.T, a.I, a.k);
-  const int waves = 16;
   a.n_c = groups(a.I, sw);
   a.n_router = groups(a.E + (a.sgate ? 1 : 0), 16);
-  a.n_sd = a.Is ? groups(a.H, waves * 16) : 0;
-  const int n_su = a.Is ? groups(a.Is, 16) : 0;
-  launch_kernel(layer_front_kernel, dim3((unsigned)(a.n_router + n_su)), dim3(kFrontThreads), 0, s,
-                a);
+  a.n_sd = a.Is ? groups(a.H, 16 * kFfnWaves) : 0;
+  a.n_su = a.Is ? groups(a.Is, 16) : 0;
+  launch_kernel(layer_front_kernel, dim3((unsigned)(a.n_router + a.n_su + a.T)),
+                dim3(kFrontThreads), 0, s, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t items = (P * a.n_c + kXcds - 1) / kXcds * kXcds;
-  const dim3 grid((unsigned)(a.n_sd + items)), block(64 * waves);
-  if (sw == 256) launch_kernel(layer_ffn_kernel<256>, grid, block, 0, s, a);
-  else launch_kernel(layer_ffn_kernel<128>, grid, block, 0, s, a);
+  // one workgroup per CU (256 VGPRs per wave)
+  const int64_t items = a.n_sd + P * a.n_c + (int64_t)a.T * groups(a.H, kCombine);
+  const dim3 grid((unsigned)(items < 256 ? items : 256)), block(kFfnThreads);
+  // Most tokens of a segment: few experts have more than two where the batch
+  // has under one pair per two experts, and the kernel for two keeps more
+  // registers free.
+  const int nt = a.T == 1 ? 1 : 2 * P <= a.E || a.T == 2 ? 2 : 4;
+  const uint32_t lds = (uint32_t)(nt * 2 * layer_chunks(a.H) * kChunk);
+  const bool al = a.H % kChunk == 0 && a.I % kChunk == 0;
+#define NVFP4_LAYER(SW, AL, NT) \
+  launch_kernel((layer_ffn_kernel<SW, AL, NT>), grid, block, lds, s, a)
+#define NVFP4_LAYER_NT(SW, AL)                \
+  do {                                        \
+    if (nt == 1) NVFP4_LAYER(SW, AL, 1);      \
+    else if (nt == 2) NVFP4_LAYER(SW, AL, 2); \
+    else NVFP4_LAYER(SW, AL, 4);              \
+  } while (0)
+  if (sw == 256) {
+    if (al) NVFP4_LAYER_NT(256, true);
+    else NVFP4_LAYER_NT(256, false);
+  } else {
+    if (al) NVFP4_LAYER_NT(128, true);
+    else NVFP4_LAYER_NT(128, false);
+  }
+#undef NVFP4_LAYER_NT
+#undef NVFP4_LAYER
   return hipGetLastError();
 }
 

@@ -56,8 +56,8 @@ def test_sizes():
     assert call(make(E=0)) == 2 and call(make(E=1025)) == 2
     assert call(make(H=48)) == 2 and call(make(I=80)) == 2 and call(make(Is=40)) == 2
     assert call(make(H=0)) == 2 and call(make(Is=-32)) == 1
-    assert call(make(H=(1 << 20) + 32)) == 2
-    assert call(make(H=1 << 20, I=1 << 13)) == 2 and "2^32" in _last()
+    assert call(make(H=(1 << 13) + 32)) == 2 and call(make(I=(1 << 20) + 32)) == 2
+    assert call(make(H=1 << 13, I=(1 << 19) + 32)) == 2 and "2^32" in _last()
     assert call(make(), dt=3) == 1
     assert call(make(Is=0, sg=None, su=None, sd=None, gate=FAKE)) == 1
 
