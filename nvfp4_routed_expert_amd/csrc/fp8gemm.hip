@@ -4,54 +4,63 @@
 //
 // A scale block is 128 columns, which is exactly the K of one
 // v_mfma_f32_16x16x128_f8f6f4: each 16 x 16 tile of a block is one MFMA from
-// a zero accumulator (exact products, fp32 sums), and its four results per
-// lane join the fp32 totals by one FMA each with s_x s_w.  Weights are the
-// A operand, so a lane's results are four consecutive n of one token: s_x is
-// one value per lane and token tile, s_w is uniform over a wave's rows (a
-// wave's rows never cross a 128-row scale block).
+// a zero accumulator, and its four results per lane join the fp32 totals by
+// one FMA each with s_x s_w.  Weights are the A operand, so a lane's results
+// are four consecutive n of one token: s_x is one value per lane and token
+// tile, s_w is uniform over a wave's rows (a wave's rows never cross a 128-row
+// scale block).
 //
-// Both operands of a block come through an LDS ring by direct global-to-LDS
-// loads, 128-byte rows (one scale block) with their 16-byte granules
-// XOR-swizzled by the row, so a fragment's 16 rows spread over the banks.
-// The order of k inside a block is free as long as both operands agree: lane
-// group g takes granules 2 g and 2 g + 1.  A partial last block (K % 128) is
-// padded with zero codes, fetched from a 16-byte zero constant.
+// Eight waves, two per SIMD: one's FMAs issue while the other's MFMAs run.
+// Both operands of a block come through LDS by direct loads, one and a half or
+// two blocks ahead.  One barrier a block, before its last token tile: by then a
+// wave holds that tile's operands in registers, so the block's part of the ring
+// is free for later blocks and the next block's first operands can be read.
+//
+// Rows lie in LDS with their 16-byte granules XOR-swizzled by the row.  The
+// order of k inside a block is free as long as both operands agree: lane group
+// g takes granules g and g + 4.  Rows past a matrix, granules past K and blocks
+// past a part's end lie behind a buffer's bound, where loads return zeros.
 #include "fp8.h"
 #include "kernels.h"
+
+#include <type_traits>
 
 namespace nvfp4 {
 namespace {
 
 constexpr int kXcds = 8;
 constexpr int kF8CUs = 256;
+constexpr int kF8Waves = 8;            // kF8WN by 2
+constexpr int kF8WN = 4;
+constexpr int kF8FN = 4;               // 16-row weight tiles of a wave
+constexpr int kF8Group = 4;            // blocks whose scales are loaded together
+constexpr int kOutside = INT32_MIN;   // a byte offset past any buffer bound
 typedef __attribute__((address_space(3))) void *lds_ptr_t;
-
-__device__ __attribute__((aligned(16))) const uint32_t kZero16[4] = {0u, 0u, 0u, 0u};
-
-template <int WN_, int WM_, int FN_, int FM_, int STAGES_>
-struct F8Cfg {
-  static constexpr int WN = WN_, WM = WM_, FN = FN_, FM = FM_, STAGES = STAGES_;
-  static constexpr int NW = WN * WM;                 // waves
-  static constexpr int BN = WN * FN * 16;            // weight rows of a tile
-  static constexpr int BM = WM * FM * 16;            // tokens of a tile
-  static constexpr int W_BYTES = BN * kF8Block, X_BYTES = BM * kF8Block;
-  static constexpr int STAGE = W_BYTES + X_BYTES + BM * 4;   // + s_x of the block
-  static constexpr int W_LOADS = W_BYTES / 1024 / NW, X_LOADS = X_BYTES / 1024 / NW;
-  static constexpr int S_WAVES = BM / 64;            // waves that load 64 scales each
-  static_assert(W_BYTES % (1024 * NW) == 0 && X_BYTES % (1024 * NW) == 0, "even loads");
-  static_assert(BM % 64 == 0 && S_WAVES <= NW, "scale loads");
-  static_assert(STAGES * STAGE <= 160 * 1024, "LDS");
-};
-
-// At most N of this wave's global loads still in flight and its LDS reads
-// done, then the workgroup barrier.
-template <int N>
-__device__ __forceinline__ void wait_then_barrier() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
-}
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
+// Where granule 0 of 64-byte rows 4 i .. 4 i + 3 lies: the 16 lanes that an LDS
+// read serves together (rows 0-3 and 12-15 of one granule with rows 4-11 of the
+// next, or the reverse) then touch all banks once.
+__device__ __forceinline__ int f8_swizzle(int i) { return (0x1320 >> (4 * i)) & 3; }
+
+// The matrix of `rows` rows of `pitch` bytes from row `row` on; an offset at
+// or past its end (or kOutside) reads zero.  A tile spans less than 2^31 bytes.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t f8_buffer(const void *base, int64_t row,
+                                                            int64_t rows, int64_t pitch) {
+  const int64_t left = row < rows ? (rows - row) * pitch : 0;
+  const uint64_t at = (uint64_t)base + (left > 0 ? row * pitch : 0);
+  // (the 64-bit arithmetic may go through vector registers: back to scalars)
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)at);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
+  const int n = __builtin_amdgcn_readfirstlane((int)(left < 0x7FFFFFFF ? left : 0x7FFFFFFF));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>((uint64_t)hi << 32 | lo), 0, n,
+                                           0x00027000);
+}
+
+// 4 x FM tiles of 16 x 16 per wave: 256 weight rows (SWIGLU: 128 of either
+// matrix) and FM x 32 tokens per workgroup.
+//
 // EXACT (fp32 outputs): the fp8 matrix instruction aligns the products of a
 // sum to the largest with about 12 bits (measured: errors up to 2^-10.9 of the
 // largest product, 1.5e-5 of the result in the Frobenius norm on Gaussian
@@ -59,265 +68,359 @@ __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f +
 // output's rounding (2^-9) but not below an fp32 one's.  The exact form turns
 // the codes into fp16 (exactly) and multiplies them on the fp16 unit, with
 // exact products and fp32 sums, at half the rate.
-template <class C, bool SWIGLU, bool EXACT>
-__global__ __launch_bounds__(64 * C::NW) void f8_gemm_kernel(const F8GemmArgs p) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[C::STAGES * C::STAGE];
+template <int FM, bool SWIGLU, bool EXACT>
+__global__ __launch_bounds__(64 * kF8Waves, 2) void f8_gemm_kernel(const F8GemmArgs p) {
+  static_assert(FM % 2 == 0 && FM <= 8, "tile");
+  constexpr int FN = kF8FN, BM = 32 * FM, BN = kF8WN * FN * 16;
+  constexpr int TN = SWIGLU ? BN / 2 : BN;       // output columns of a tile
+  // A slot of the ring holds a block (128-byte rows, three slots) or, where
+  // two blocks do not fit beside the one in use, half a block (64-byte rows,
+  // five slots).  M = 2048, N = 17408, K = 5120, 192 tokens: 390 us with a ring
+  // of two blocks, 238 with five halves; 128 tokens: 279 with six halves (a
+  // 64-byte read is half a cache line), 249 with three blocks.
+  constexpr bool HALVES = FM > 4;
+  constexpr int ROW = HALVES ? 64 : 128, R = HALVES ? 5 : 3;
+  constexpr int W_BYTES = BN * ROW, SLOT = W_BYTES + BM * ROW;
+  constexpr int WL = BN * ROW / 1024 / kF8Waves, XL = BM * ROW / 1024 / kF8Waves;   // whole loads of a wave
+  constexpr int SL = (BM / 16 + kF8Waves - 1) / kF8Waves;   // and of scales, per four blocks
+  constexpr int G_STAGE = (SWIGLU ? 2 : 1) * 256;   // s_w of a wave
+  constexpr int SX_BYTES = SL * kF8Waves * 256, S_STAGE = SX_BYTES + kF8Waves * G_STAGE;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[R * SLOT + 2 * S_STAGE];
+  uint8_t *const scales = lds + R * SLOT;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, lg = lane >> 4;
-  const int wn = wave % C::WN, wm = wave / C::WN;
+  const int wn = wave % kF8WN, wm = wave / kF8WN;
   const int K = p.K, N = p.N;
   const int64_t M = p.M;
   const int KB = (K + kF8Block - 1) / kF8Block;
-  constexpr int TN = SWIGLU ? C::BN / 2 : C::BN;      // output columns of a tile
   const int n_tiles = (N + TN - 1) / TN;
-  const int m_tiles = (int)((M + C::BM - 1) / C::BM);
+  const int m_tiles = (int)((M + BM - 1) / BM);
   const int ks = p.ksplit;
   const int n_items = n_tiles * m_tiles * ks;
   const int per = (n_items + kXcds - 1) / kXcds;
   const int slot = blockIdx.x / kXcds;
   const int item = (blockIdx.x % kXcds) * per + slot;
   if (slot >= per || item >= n_items) return;
-  // token tiles fastest: the tiles that share weights run side by side on one XCD
-  const int mt = item % m_tiles;
-  const int rest = item / m_tiles;
-  const int nt = rest % n_tiles, kz = rest / n_tiles;
-  const int64_t m0 = (int64_t)mt * C::BM;
-  const int b_begin = (int)((int64_t)KB * kz / ks), b_end = (int)((int64_t)KB * (kz + 1) / ks);
+  // up to eight token tiles side by side, then the next weight rows: the tiles
+  // that run together on an XCD share both operands in its L2
+  const int kz = item / (n_tiles * m_tiles), tile = item - kz * (n_tiles * m_tiles);
+  const int gi = tile / (8 * n_tiles), gr = tile - gi * 8 * n_tiles;
+  const int gm = m_tiles - gi * 8 < 8 ? m_tiles - gi * 8 : 8;
+  const int nt = gr / gm;
+  const int64_t m0 = (int64_t)(gi * 8 + gr - nt * gm) * BM;
+  // (64-bit divisions run on the vector unit: back to scalars)
+  const int b_begin = __builtin_amdgcn_readfirstlane((int)((int64_t)KB * kz / ks));
+  const int nb = __builtin_amdgcn_readfirstlane((int)((int64_t)KB * (kz + 1) / ks)) - b_begin;
+  const int n0 = nt * TN + wn * (TN / kF8WN);   // first output column of this wave
 
-  // ---- loader: instruction q fills LDS rows 8 q .. 8 q + 7, lane l position
-  // l % 8 of row 8 q + l / 8, which holds granule (l % 8) ^ (row & 7)
-  const int gran = (lane & 7) ^ (lane >> 3);
-  // (fixed-size arrays: with sizes that depend on the template arguments the
-  // host pass of this compiler drops the kernel's launch stub)
-  static_assert(C::W_LOADS <= 16 && C::X_LOADS <= 16, "loads per wave");
-  const uint8_t *wsrc[16], *xsrc[16];
+  // ---- loader: a load fills 1 KB, 8 (16) rows of a slot.  Granule g of row r
+  // lies at position g ^ (r % 8), or g ^ f8_swizzle(r / 4) in 64-byte rows.  Per
+  // slot, a wave has WL loads of weights and XL of tokens.  Halves come in
+  // pairs, and the four token tiles left are loaded by waves 4 .. 7 for the
+  // first half of a pair and by waves 0 .. 3 for the second.
+  const int k0 = b_begin * kF8Block;
+  const int k_end = (b_begin + nb) * kF8Block < K ? (b_begin + nb) * kF8Block : K;
+  constexpr int LR = 1024 / ROW;                  // rows of a load
+  __amdgpu_buffer_rsrc_t wbuf[4], xbuf[2], ebuf;
 #pragma unroll
-  for (int j = 0; j < C::W_LOADS; ++j) {
-    const int R = 8 * (wave * C::W_LOADS + j) + (lane >> 3);
-    int mat = 0, row;
-    if constexpr (SWIGLU) {
-      const int f = (R >> 4) % C::FN;
-      mat = f >= C::FN / 2;
-      row = nt * TN + R / (C::FN * 16) * (C::FN * 8) + (f % (C::FN / 2)) * 16 + (R & 15);
-    } else {
-      row = nt * TN + R;
+  for (int j = 0; j < WL; ++j) {
+    const int r = (wave * WL + j) * LR, f = r / 16 % FN;   // a row of weight tile f
+    if constexpr (SWIGLU)
+      wbuf[j] = f8_buffer(p.w[f / 2], nt * TN + r / 64 * 32 + f % 2 * 16 + r % 16, N, K);
+    else wbuf[j] = f8_buffer(p.w[0], nt * TN + r, N, K);
+  }
+#pragma unroll
+  for (int j = 0; j < XL; ++j) xbuf[j] = f8_buffer(p.x, m0 + (wave * XL + j) * LR, M, K);
+  const int e_tile = kF8Waves + wave % 4;
+  ebuf = f8_buffer(p.x, m0 + e_tile * 16, M, K);
+  const int gran = HALVES ? (lane & 3) ^ f8_swizzle(lane >> 4) : (lane & 7) ^ (lane >> 3);
+  const int off_ = lane / (ROW / 16) * K + gran * 16, last = k_end - gran * 16;
+  auto load1k = [&](__amdgpu_buffer_rsrc_t buf, int to, int at) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_ptr_t)(lds + to), 16,
+                                             off_ | (at < last ? 0 : kOutside), at, 0, 0);
+  };
+  // block or half u of the part, into slot s
+  auto load = [&](int u, int s) {
+    const int at = __builtin_amdgcn_readfirstlane(k0 + u * ROW), to = s * SLOT;
+#pragma unroll
+    for (int j = 0; j < WL; ++j) load1k(wbuf[j], to + (wave * WL + j) * 1024, at);
+#pragma unroll
+    for (int j = 0; j < XL; ++j) load1k(xbuf[j], to + W_BYTES + (wave * XL + j) * 1024, at);
+  };
+  auto load_left = [&](int u, int s) {
+    load1k(ebuf, s * SLOT + W_BYTES + e_tile * 1024, __builtin_amdgcn_readfirstlane(k0 + u * ROW));
+  };
+  auto load_pair = [&](int u, int s, int s2) {
+    load(u, s);
+    load_left(wave >= 4 ? u : u + 1, wave >= 4 ? s : s2);
+    load(u + 1, s2);
+  };
+  // Scales of the four blocks from i on: s_x as [row][block]; then, per wave, its rows' s_w (64 values a matrix: the four, repeated).
+  const int g_row = n0 / kF8Block, g_rows = (N + kF8Block - 1) / kF8Block;
+  const __amdgpu_buffer_rsrc_t gb0 = f8_buffer(p.ws[0], g_row, g_rows, KB * 4);
+  const __amdgpu_buffer_rsrc_t gb1 = f8_buffer(p.ws[SWIGLU ? 1 : 0], g_row, g_rows, KB * 4);
+  const __amdgpu_buffer_rsrc_t sbuf = f8_buffer(p.xs, m0, M, KB * 4);
+  auto load_scales = [&](int i, uint8_t *st) {
+    const int at = __builtin_amdgcn_readfirstlane((b_begin + i) * 4);
+    const int out = i + (lane & 3) < nb ? 0 : kOutside;
+#pragma unroll
+    for (int j = 0; j < SL; ++j) {
+      const int q = wave + kF8Waves * j;
+      const int off = (((q * 16 + (lane >> 2)) * KB + (lane & 3)) * 4) | out;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(sbuf, (lds_ptr_t)(st + q * 256), 4, off, at, 0, 0);
     }
-    row = row < N ? row : N - 1;
-    wsrc[j] = p.w[mat] + (int64_t)row * K + gran * 16;
-  }
-#pragma unroll
-  for (int j = 0; j < C::X_LOADS; ++j) {
-    const int64_t m = m0 + 8 * (wave * C::X_LOADS + j) + (lane >> 3);
-    xsrc[j] = p.x + (m < M ? m : M - 1) * K + gran * 16;
-  }
-  const int64_t ms = m0 + wave * 64 + lane;
-  const float *ssrc = p.xs + (ms < M ? ms : M - 1) * KB;
-  const int k_lane = gran * 16;
-  auto load = [&](int b, int slot_) {
-    uint8_t *st = lds + slot_ * C::STAGE;
-    const bool zero = b * kF8Block + k_lane >= K;   // granules past K: zero codes
-    const uint8_t *z = reinterpret_cast<const uint8_t *>(kZero16);
-#pragma unroll
-    for (int j = 0; j < C::W_LOADS; ++j)
-      __builtin_amdgcn_global_load_lds(zero ? z : wsrc[j] + (int64_t)b * kF8Block,
-                                       (lds_ptr_t)(st + (wave * C::W_LOADS + j) * 1024), 16, 0, 0);
-#pragma unroll
-    for (int j = 0; j < C::X_LOADS; ++j)
-      __builtin_amdgcn_global_load_lds(zero ? z : xsrc[j] + (int64_t)b * kF8Block,
-                                       (lds_ptr_t)(st + C::W_BYTES + (wave * C::X_LOADS + j) * 1024),
-                                       16, 0, 0);
-    if (wave < C::S_WAVES)
-      __builtin_amdgcn_global_load_lds(ssrc + b,
-                                       (lds_ptr_t)(st + C::W_BYTES + C::X_BYTES + wave * 256), 4,
-                                       0, 0);
+    const int goff = ((lane & 3) * 4) | out;
+    uint8_t *g = st + SX_BYTES + wave * G_STAGE;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(gb0, (lds_ptr_t)g, 4, goff, at, 0, 0);
+    if constexpr (SWIGLU)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(gb1, (lds_ptr_t)(g + 256), 4,
+                                               goff, at, 0, 0);
   };
 
-  f32x4 acc[C::FN][C::FM];
+  f32x4 acc[4][8], t[2][4];
 #pragma unroll
-  for (int f = 0; f < C::FN; ++f)
+  for (int f = 0; f < FN; ++f) {
+    t[1][f] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < C::FM; ++j) acc[f][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  // first output column of this wave, and its weight scale row(s)
-  const int n0 = nt * TN + wn * (TN / C::WN);
-  const int nb = (n0 < N ? n0 : N - 1) / kF8Block;
-  const float *sw0 = p.ws[0] + (int64_t)nb * KB;
-  const float *sw1 = SWIGLU ? p.ws[1] + (int64_t)nb * KB : nullptr;
-
-  const int p0 = ((2 * lg) ^ (lr & 7)) * 16, p1 = ((2 * lg + 1) ^ (lr & 7)) * 16;
-  auto frag = [&](const uint8_t *rows, int row) {
-    const u32x4 lo = *reinterpret_cast<const u32x4 *>(rows + row * kF8Block + p0);
-    const u32x4 hi = *reinterpret_cast<const u32x4 *>(rows + row * kF8Block + p1);
+    for (int j = 0; j < FM; ++j) acc[f][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  i32x8 a[2][4], xb[2];
+  float sx[2], sg0 = 0.0f, sg1 = 0.0f;   // s_x of the tiles in xb; s_x s_w of the last tile
+  float g0, g1 = 0.0f, h0 = 0.0f, h1 = 0.0f;
+  const int p0 = HALVES ? lr * 64 + (lg ^ f8_swizzle(lr >> 2)) * 16 : lr * 128 + (lg ^ (lr & 7)) * 16;
+  const int p1 = HALVES ? p0 : lr * 128 + ((lg + 4) ^ (lr & 7)) * 16;
+  // 16 rows of a block, which is in h0 (halves: K 0 .. 63) and h1 (64 .. 127)
+  auto frag = [&](const uint8_t *h0, const uint8_t *h1, int tile) {
+    const u32x4 lo = *reinterpret_cast<const u32x4 *>(h0 + tile * (16 * ROW) + p0);
+    const u32x4 hi = *reinterpret_cast<const u32x4 *>(h1 + tile * (16 * ROW) + p1);
     return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
                  (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
   };
-  auto frag16 = [&](const uint8_t *rows, int row, f16x8 (&o)[4]) {
+  // token tile j of the block in h0, h1; s: the block's place in its scale buffer
+  auto fetch = [&](int j, const uint8_t *h0, const uint8_t *h1, const uint8_t *s) {
+    xb[j & 1] = frag(h0 + W_BYTES, h1 + W_BYTES, wm * FM + j);
+    sx[j & 1] = *reinterpret_cast<const float *>(s + (wm * FM + j) * 256 + lr * 16);
+  };
+  auto weight_scale = [&](const uint8_t *buf, int slot_, int mat) {
+    return *reinterpret_cast<const float *>(buf + SX_BYTES + wave * G_STAGE + mat * 256 +
+                                            slot_ * 4);
+  };
+  auto codes16 = [](const i32x8 &c, f16x8 (&o)[4]) {
     f16x8 h[2];
-    f8_to_f16(*reinterpret_cast<const u32x4 *>(rows + row * kF8Block + p0), h);
+    f8_to_f16(u32x4{(uint32_t)c[0], (uint32_t)c[1], (uint32_t)c[2], (uint32_t)c[3]}, h);
     o[0] = h[0];
     o[1] = h[1];
-    f8_to_f16(*reinterpret_cast<const u32x4 *>(rows + row * kF8Block + p1), h);
+    f8_to_f16(u32x4{(uint32_t)c[4], (uint32_t)c[5], (uint32_t)c[6], (uint32_t)c[7]}, h);
     o[2] = h[0];
     o[3] = h[1];
   };
-  auto compute = [&](int b, int slot_) {
-    const uint8_t *st = lds + slot_ * C::STAGE;
-    const uint8_t *xt = st + C::W_BYTES;
-    const float *sx = reinterpret_cast<const float *>(xt + C::X_BYTES);
-    const float g0 = sw0[b], g1 = SWIGLU ? sw1[b] : 0.0f;
+  // acc of tile jp += t of that tile times its scales
+  auto join = [&](int f, int jp) {
+    const float sc = SWIGLU && f >= FN / 2 ? sg1 : sg0;
+    const f32x4 v = t[jp & 1][f];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[f][jp][i] = __builtin_fmaf(v[i], sc, acc[f][jp][i]);
+  };
+  // Block i: stage q % 2, scale slot q of buffer s0 (the next four's: s1), its
+  // weights in ab; leaves the next block's in an.  No branch: with one in the
+  // loop the registers no longer suffice.
+  int slot0 = 0, slot1 = HALVES ? 1 : 0;   // of block i
+  auto after = [](int s) {
+    s += HALVES ? 2 : 1;
+    return s < R ? s : s - R;
+  };
+  auto block = [&](int i_, int q, i32x8 (&ab)[4], i32x8 (&an)[4], uint8_t *s0, uint8_t *s1) {
+    const int i = __builtin_amdgcn_readfirstlane(i_);
+    const int qn = (q + 1) % kF8Group;
+    const uint8_t *sb = qn == 0 ? s1 : s0;
+    const int n0_ = after(slot0), n1_ = after(slot1);
+    const uint8_t *x0 = lds + slot0 * SLOT, *x1 = lds + slot1 * SLOT;
+    const uint8_t *y0 = lds + n0_ * SLOT, *y1 = lds + n1_ * SLOT;
+    const uint8_t *st = s0 + q * 4, *sn = sb + qn * 4;
+    f16x8 a16[4][4];
     if constexpr (EXACT) {
-      f16x8 a[C::FN][4];
 #pragma unroll
-      for (int f = 0; f < C::FN; ++f) frag16(st, (wn * C::FN + f) * 16 + lr, a[f]);
+      for (int f = 0; f < FN; ++f) codes16(ab[f], a16[f]);
+    }
 #pragma unroll
-      for (int j = 0; j < C::FM; ++j) {
-        const int row = (wm * C::FM + j) * 16 + lr;
-        f16x8 xb[4];
-        frag16(xt, row, xb);
-        const float s = sx[row];
-        const float s0 = s * g0, s1 = s * g1;
+    for (int j = 0; j < FM; ++j) {
+      if (j == FM - 1) {
+        // this block's operands are in registers, block i + 1 has landed (its
+        // successor, or that one's half, need not)
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(WL + XL) : "memory");
+        if constexpr (HALVES) load_pair(2 * i + R, slot0, slot1);
+        else load(i + R, slot0);
+        if (q == 0) load_scales(i + kF8Group, s1);
+        h0 = weight_scale(sb, qn, 0);
+        if constexpr (SWIGLU) h1 = weight_scale(sb, qn, 1);
 #pragma unroll
-        for (int f = 0; f < C::FN; ++f) {
-          f32x4 t = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int f = 0; f < FN; ++f) an[f] = frag(y0, y1, wn * FN + f);
+        fetch(0, y0, y1, sn);
+      } else {
+        fetch(j + 1, x0, x1, st);
+      }
+      constexpr int kLast = FM - 1;
+      const int jp = j == 0 ? kLast : j - 1;
+      f16x8 x16[4];
+      if constexpr (EXACT) codes16(xb[j & 1], x16);
+#pragma unroll
+      for (int f = 0; f < FN; ++f) {
+        f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
+        if constexpr (EXACT) {
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            t = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[f][q], xb[q], t, 0, 0, 0);
-          const float sc = SWIGLU && f >= C::FN / 2 ? s1 : s0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[f][j][i] = __builtin_fmaf(t[i], sc, acc[f][j][i]);
+            v = __builtin_amdgcn_mfma_f32_16x16x32_f16(a16[f][q], x16[q], v, 0, 0, 0);
+        } else {
+          v = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(ab[f], xb[j & 1], v, 0, 0, 0,
+                                                               0, 0, 0);
         }
+        t[j & 1][f] = v;
+        join(f, jp);
+        __builtin_amdgcn_sched_barrier(0);
       }
-    } else {
-      i32x8 a[C::FN];
-#pragma unroll
-      for (int f = 0; f < C::FN; ++f) a[f] = frag(st, (wn * C::FN + f) * 16 + lr);
-#pragma unroll
-      for (int j = 0; j < C::FM; ++j) {
-        const int row = (wm * C::FM + j) * 16 + lr;
-        const i32x8 xb = frag(xt, row);
-        const float s = sx[row];
-        const float s0 = s * g0, s1 = s * g1;
-#pragma unroll
-        for (int f = 0; f < C::FN; ++f) {
-          const f32x4 t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              a[f], xb, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
-          const float sc = SWIGLU && f >= C::FN / 2 ? s1 : s0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[f][j][i] = __builtin_fmaf(t[i], sc, acc[f][j][i]);
-        }
-      }
+      sg0 = sx[j & 1] * g0;
+      if constexpr (SWIGLU) sg1 = sx[j & 1] * g1;
     }
+    g0 = h0;
+    g1 = h1;
+    slot0 = n0_;
+    slot1 = n1_;
   };
 
-  // ring: blocks b + 1 .. b + S - 1 are in flight while block b is multiplied;
-  // the barrier publishes block b and frees the slot the next loads fill
-  constexpr int S = C::STAGES;
-  constexpr int LOADS = C::W_LOADS + C::X_LOADS;   // (+ 1 in the scale waves)
-#pragma unroll
-  for (int d = 0; d < S - 1; ++d)
-    if (b_begin + d < b_end) load(b_begin + d, d);
-  int slot_r = 0, slot_w = S - 1;
-  for (int b = b_begin; b < b_end; ++b) {
-    // (a wave with a scale load waits for one load more than it must)
-    if (b + S - 2 < b_end) wait_then_barrier<(S - 2) * LOADS>();
-    else wait_then_barrier<0>();
-    if (b + S - 1 < b_end) load(b + S - 1, slot_w);
-    compute(b, slot_r);
-    slot_r = slot_r + 1 == S ? 0 : slot_r + 1;
-    slot_w = slot_w + 1 == S ? 0 : slot_w + 1;
+  load_scales(0, scales);
+  if constexpr (HALVES) {
+    load(0, 0);
+    load_left(0, 0);
+    load_pair(1, 1, 2);
+    load_pair(3, 3, 4);
+  } else {
+    load(0, 0);
+    load(1, 1);
+    load(2, 2);
   }
+  // (block 0 has landed)
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(HALVES ? 3 * (WL + XL) + 1 : 2 * (WL + XL)) : "memory");
+  g0 = weight_scale(scales, 0, 0);
+  if constexpr (SWIGLU) g1 = weight_scale(scales, 0, 1);
+#pragma unroll
+  for (int f = 0; f < FN; ++f) a[0][f] = frag(lds, lds + (HALVES ? SLOT : 0), wn * FN + f);
+  fetch(0, lds, lds + (HALVES ? SLOT : 0), scales);
+  // (a last round's blocks past the end multiply zeros)
+  uint8_t *s0 = scales, *s1 = scales + S_STAGE;
+#pragma unroll 1
+  for (int i = 0; i < nb; i += kF8Group) {
+#pragma unroll
+    for (int q = 0; q < kF8Group; ++q) block(i + q, q, a[q % 2], a[(q + 1) % 2], s0, s1);
+    uint8_t *const s = s0;
+    s0 = s1;
+    s1 = s;
+  }
+#pragma unroll
+  for (int f = 0; f < FN; ++f) join(f, FM - 1);
 
-  // ---- epilogue: lane (lr, lg) holds tokens m0 + .. + lr, columns 4 lg .. + 3
-  if (ks > 1) {
-    const int64_t width = SWIGLU ? 2 * (int64_t)N : N;
+  // ---- epilogue: lane (lr, lg) holds columns 4 lg .. + 3 of tokens lr.  Every
+  // load has landed, then the stages are free.
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  // Sums, or outputs, go through LDS so that a wave stores whole rows of the
+  // tile: PASSES parts of the tokens, lane l columns 4 l .. 4 l + 3.
+  auto store_rows = [&](auto passes) {
+    constexpr int PASSES = decltype(passes)::value;
+    constexpr bool F32 = PASSES == 2;
+    constexpr int RP = BM / PASSES, WR = RP / 2, PITCH = BN * (F32 ? 4 : 2) + 16;
+    static_assert(RP * PITCH <= (int)sizeof(lds), "a part fits");
+    const int c = 4 * lane;
+    const int n = nt * TN + (SWIGLU ? c % TN : c);
+    const int64_t pitch = SWIGLU ? 2 * (int64_t)N : N;
+    const int64_t at = n + (SWIGLU && c >= TN ? N : 0);
+    const bool wide = (N & 3) == 0;
+    char *const out = ks > 1 ? reinterpret_cast<char *>(p.partial + (int64_t)kz * M * pitch)
+                             : static_cast<char *>(p.out);
 #pragma unroll
-    for (int j = 0; j < C::FM; ++j) {
-      const int64_t m = m0 + (wm * C::FM + j) * 16 + lr;
-      if (m >= M) continue;
-      float *row = p.partial + ((int64_t)kz * M + m) * width;
+    for (int h = 0; h < PASSES; ++h) {
+      __syncthreads();
 #pragma unroll
-      for (int f = 0; f < C::FN; ++f) {
-        const int fr = SWIGLU ? f % (C::FN / 2) : f;
-        const int n = n0 + fr * 16 + 4 * lg;
-        const int64_t at = n + (SWIGLU && f >= C::FN / 2 ? N : 0);
+      for (int j = 0; j < FM / PASSES; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (n + i < N) row[at + i] = acc[f][j][i];
-      }
+        for (int f = 0; f < FN; ++f) {
+          const f32x4 v = acc[f][h * (FM / PASSES) + j];
+          const int col = SWIGLU ? f / 2 * TN + wn * 32 + f % 2 * 16 : (wn * FN + f) * 16;
+          uint8_t *to = lds + (wm * WR + j * 16 + lr) * PITCH + (col + 4 * lg) * (F32 ? 4 : 2);
+          if constexpr (F32) {
+            *reinterpret_cast<f32x4 *>(to) = v;
+          } else {
+            *reinterpret_cast<u32x2 *>(to) =
+                u32x2{f32_to_bf16_bits(v[0]) | (f32_to_bf16_bits(v[1]) << 16),
+                      f32_to_bf16_bits(v[2]) | (f32_to_bf16_bits(v[3]) << 16)};
+          }
+        }
+      __syncthreads();
+      if (n < N)
+        for (int r = wave; r < RP; r += kF8Waves) {
+          const int64_t m = m0 + r / WR * (FM * 16) + h * WR + r % WR;
+          if (m >= M) break;
+          const uint8_t *from = lds + r * PITCH + c * (F32 ? 4 : 2);
+          if constexpr (F32) {
+            const f32x4 v = *reinterpret_cast<const f32x4 *>(from);
+            float *o = reinterpret_cast<float *>(out) + m * pitch + at;
+            if (wide) *reinterpret_cast<f32x4 *>(o) = v;
+            else
+              for (int i = 0; i < 4 && n + i < N; ++i) o[i] = reinterpret_cast<const float *>(from)[i];
+          } else {
+            const u32x2 v = *reinterpret_cast<const u32x2 *>(from);
+            uint16_t *o = reinterpret_cast<uint16_t *>(out) + m * pitch + at;
+            if (wide) *reinterpret_cast<u32x2 *>(o) = v;
+            else
+              for (int i = 0; i < 4 && n + i < N; ++i) o[i] = reinterpret_cast<const uint16_t *>(from)[i];
+          }
+        }
     }
-    return;
-  }
-  if constexpr (SWIGLU) {
+  };
+  if (ks > 1 || EXACT) {
+    store_rows(std::integral_constant<int, 2>{});
+  } else if constexpr (!SWIGLU && !EXACT) {
+    store_rows(std::integral_constant<int, 1>{});
+  } else if constexpr (SWIGLU) {
     // h = bf16(silu(g) u), quantised per (token, 128 columns): the tile's 128
     // columns are the block, its maximum joined over the WN waves in LDS
     static_assert(!SWIGLU || TN == kF8Block, "a tile holds one scale block of h");
     float *wmax = reinterpret_cast<float *>(lds);
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < C::FM; ++j) {
+    for (int j = 0; j < FM; ++j) {
       float m = 0.0f;
 #pragma unroll
-      for (int f = 0; f < C::FN / 2; ++f)
+      for (int f = 0; f < FN / 2; ++f)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int n = n0 + f * 16 + 4 * lg + i;
-          float h = silu_mul(acc[f][j][i], acc[f + C::FN / 2][j][i]);
+          float h = silu_mul(acc[f][j][i], acc[f + FN / 2][j][i]);
           h = bf16_bits_to_f32(f32_to_bf16_bits(h));
           h = n < N ? h : 0.0f;
           acc[f][j][i] = h;
           m = fmaxf(m, __builtin_fabsf(h));
         }
       m = f8_rows_max(m);
-      if (lg == 0) wmax[wn * C::BM + (wm * C::FM + j) * 16 + lr] = m;
+      if (lg == 0) wmax[wn * BM + (wm * FM + j) * 16 + lr] = m;
     }
     __syncthreads();
     const int HB = (N + kF8Block - 1) / kF8Block;
 #pragma unroll
-    for (int j = 0; j < C::FM; ++j) {
-      const int r = (wm * C::FM + j) * 16 + lr;
+    for (int j = 0; j < FM; ++j) {
+      const int r = (wm * FM + j) * 16 + lr;
       float m = 0.0f;
 #pragma unroll
-      for (int w = 0; w < C::WN; ++w) m = fmaxf(m, wmax[w * C::BM + r]);
+      for (int w = 0; w < kF8WN; ++w) m = fmaxf(m, wmax[w * BM + r]);
       const float s = f8_scale(m), inv = 1.0f / s;
       if (m0 + r >= M) continue;
       if (wn == 0 && lg == 0) p.hs[(m0 + r) * HB + nt] = s;
 #pragma unroll
-      for (int f = 0; f < C::FN / 2; ++f) {
+      for (int f = 0; f < FN / 2; ++f) {
         const int n = n0 + f * 16 + 4 * lg;
         if (n < N)   // (N % 32 == 0: four columns are in or out together)
           *reinterpret_cast<uint32_t *>(p.hq + (m0 + r) * N + n) =
               f8_pack4(acc[f][j][0] * inv, acc[f][j][1] * inv, acc[f][j][2] * inv,
                        acc[f][j][3] * inv);
-      }
-    }
-  } else {
-    const bool wide = (N & 3) == 0;
-#pragma unroll
-    for (int j = 0; j < C::FM; ++j) {
-      const int64_t m = m0 + (wm * C::FM + j) * 16 + lr;
-      if (m >= M) continue;
-#pragma unroll
-      for (int f = 0; f < C::FN; ++f) {
-        const int n = n0 + f * 16 + 4 * lg;
-        if (n >= N) continue;
-        const f32x4 v = acc[f][j];
-        if (p.out_type == OutType::F32) {
-          float *o = static_cast<float *>(p.out) + m * N + n;
-          if (wide) *reinterpret_cast<f32x4 *>(o) = v;
-          else
-            for (int i = 0; i < 4; ++i)
-              if (n + i < N) o[i] = v[i];
-        } else {
-          uint16_t *o = static_cast<uint16_t *>(p.out) + m * N + n;
-          uint32_t h[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) h[i] = f32_to_bf16_bits(v[i]);
-          if (wide) *reinterpret_cast<u32x2 *>(o) = u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
-          else
-            for (int i = 0; i < 4; ++i)
-              if (n + i < N) o[i] = (uint16_t)h[i];
-        }
       }
     }
   }
@@ -372,38 +475,45 @@ __global__ __launch_bounds__(256) void f8_reduce_swiglu_kernel(const F8GemmArgs 
   if (ok && l == 0) p.hs[m * HB + b] = s;
 }
 
-using CfgBig = F8Cfg<2, 4, 8, 4, 2>;     // 256 x 256
-using CfgMid = F8Cfg<2, 4, 8, 2, 2>;     // 256 x 128
-using CfgExact = F8Cfg<2, 4, 4, 2, 2>;   // 128 x 128
-
-template <class C, bool SWIGLU, bool EXACT>
-hipError_t launch_cfg(const F8GemmArgs &a, hipStream_t s) {
-  constexpr int tn = SWIGLU ? C::BN / 2 : C::BN;
-  int64_t items = (int64_t)((a.N + tn - 1) / tn) * ((a.M + C::BM - 1) / C::BM) * a.ksplit;
+template <int FM, bool SWIGLU, bool EXACT>
+hipError_t launch_tile(const F8GemmArgs &a, hipStream_t s) {
+  constexpr int bm = 32 * FM, tn = SWIGLU ? 128 : 256;
+  int64_t items = (int64_t)((a.N + tn - 1) / tn) * ((a.M + bm - 1) / bm) * a.ksplit;
   items = (items + kXcds - 1) / kXcds * kXcds;
-  launch_kernel((f8_gemm_kernel<C, SWIGLU, EXACT>), dim3((unsigned)items), dim3(64 * C::NW), 0, s,
-                a);
+  launch_kernel((f8_gemm_kernel<FM, SWIGLU, EXACT>), dim3((unsigned)items),
+                dim3(64 * kF8Waves), 0, s, a);
   return hipGetLastError();
 }
 
 }  // namespace
 
+// Tokens of a tile and K parts by an estimate of the time: rounds of tiles over
+// the CUs, each 11 us to start and to store and, per K block, what was measured
+// at M = 512 .. 8192; and the partial sums' way through memory (4 TB/s).  M =
+// 2048, N = 17408, K = 5120: 238 us with 192 tokens (2.9 rounds), 249 with 128
+// (4.25), 320 with 64.  M = 512, N = 5120, K = 17408: 73, 63 and 82.
 F8Plan f8_gemm_plan(bool swiglu, OutType out, int64_t M, int64_t N, int64_t K) {
-  F8Plan pl;
-  pl.exact = !swiglu && out == OutType::F32;
-  const int64_t tn = swiglu || pl.exact ? 128 : 256, nt = (N + tn - 1) / tn;
+  F8Plan best;
+  best.exact = !swiglu && out == OutType::F32;
   const int64_t KB = (K + kF8Block - 1) / kF8Block;
-  pl.bm = !pl.exact && M > 1024 ? 256 : 128;
-  const int64_t tiles = nt * ((M + pl.bm - 1) / pl.bm);
-  int64_t ks = 1;
-  if (tiles < kF8CUs) {
-    ks = kF8CUs / tiles;
-    if (ks > KB / 4) ks = KB / 4;
-    if (ks < 1) ks = 1;
+  const int64_t tn = swiglu ? 128 : 256, nt = (N + tn - 1) / tn;
+  double best_us = 0.0;
+  for (int bm = 64; bm <= (best.exact ? 64 : 192); bm += 64) {
+    const double block_us = best.exact ? 1.2 : bm == 64 ? 0.62 : bm == 128 ? 0.97 : 1.45;
+    const int64_t tiles = nt * ((M + bm - 1) / bm);
+    for (int64_t ks = 1; ks <= 16 && (ks == 1 || ks * 4 <= KB); ++ks) {
+      const int64_t rounds = (tiles * ks + kF8CUs - 1) / kF8CUs;
+      double us = rounds * ((double)((KB + ks - 1) / ks) * block_us + 11.0);
+      if (ks > 1) us += 4.0 + (double)ks * M * N * (swiglu ? 16.0 : 8.0) / 4e6;
+      if (best_us == 0.0 || us < best_us) {
+        best_us = us;
+        best.bm = bm;
+        best.ksplit = (int)ks;
+      }
+    }
   }
-  pl.ksplit = (int)ks;
-  pl.partial_floats = ks > 1 ? (size_t)ks * M * (swiglu ? 2 * N : N) : 0;
-  return pl;
+  best.partial_floats = best.ksplit > 1 ? (size_t)best.ksplit * M * (swiglu ? 2 * N : N) : 0;
+  return best;
 }
 
 hipError_t launch_f8_gemm(bool swiglu, const F8GemmArgs &args, const F8Plan &pl, hipStream_t s) {
@@ -411,12 +521,16 @@ hipError_t launch_f8_gemm(bool swiglu, const F8GemmArgs &args, const F8Plan &pl,
   a.ksplit = pl.ksplit;
   if (a.ksplit > 1 && !a.partial) return hipErrorInvalidValue;
   hipError_t e;
-  if (pl.exact) e = launch_cfg<CfgExact, false, true>(a, s);
+  if (pl.exact)
+    e = launch_tile<2, false, true>(a, s);
   else if (swiglu)
-    e = pl.bm == 256 ? launch_cfg<CfgBig, true, false>(a, s) : launch_cfg<CfgMid, true, false>(a, s);
+    e = pl.bm == 192   ? launch_tile<6, true, false>(a, s)
+        : pl.bm == 128 ? launch_tile<4, true, false>(a, s)
+                       : launch_tile<2, true, false>(a, s);
   else
-    e = pl.bm == 256 ? launch_cfg<CfgBig, false, false>(a, s)
-                     : launch_cfg<CfgMid, false, false>(a, s);
+    e = pl.bm == 192   ? launch_tile<6, false, false>(a, s)
+        : pl.bm == 128 ? launch_tile<4, false, false>(a, s)
+                       : launch_tile<2, false, false>(a, s);
   if (e != hipSuccess || a.ksplit <= 1) return e;
   if (swiglu) {
     const int64_t blocks = a.M * ((a.N + kF8Block - 1) / kF8Block);
