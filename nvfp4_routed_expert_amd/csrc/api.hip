@@ -278,8 +278,8 @@ struct Fp8LinearWs {
 Fp8LinearWs carve_fp8_linear(Carver &c, int64_t M, int64_t N, int64_t K, bool quantised,
                              OutType out) {
   Fp8LinearWs w = {};
-  const bool inside = f8_gemv_supported(M);
-  const bool own = !quantised && !f8_gemv_quantises(M);   // x quantised by a launch of its own
+  const bool inside = f8_gemv_supported(M, K);
+  const bool own = !quantised && !f8_gemv_quantises(M, K);   // x quantised by a launch of its own
   w.xq = c.take<uint8_t>(own ? (size_t)(M * K) : 0);
   w.xs = c.take<float>(own ? (size_t)(M * ((K + 127) / 128)) : 0);
   if (!inside) {
@@ -292,6 +292,8 @@ Fp8LinearWs carve_fp8_linear(Carver &c, int64_t M, int64_t N, int64_t K, bool qu
   return w;
 }
 struct Fp8MlpWs {
+  bool few;             // both products in the form for a few rows
+  bool own_x, own_h;    // x, h quantised by a launch of their own (h: or by the product)
   F8Plan up_plan, down_plan;
   uint8_t *xq, *hq;
   uint16_t *h;    // bf16 h (few rows)
@@ -300,13 +302,15 @@ struct Fp8MlpWs {
 };
 Fp8MlpWs carve_fp8_mlp(Carver &c, int64_t T, int64_t H, int64_t I, OutType out) {
   Fp8MlpWs w = {};
-  const bool few = f8_gemv_supported(T), own = !f8_gemv_quantises(T);
-  w.xq = c.take<uint8_t>(own ? (size_t)(T * H) : 0);
-  w.xs = c.take<float>(own ? (size_t)(T * ((H + 127) / 128)) : 0);
-  w.h = c.take<uint16_t>(few ? (size_t)(T * I) : 0);
-  w.hq = c.take<uint8_t>(own ? (size_t)(T * I) : 0);
-  w.hs = c.take<float>(own ? (size_t)(T * ((I + 127) / 128)) : 0);
-  if (!few) {
+  w.few = f8_gemv_supported(T, H) && f8_gemv_supported(T, I);
+  w.own_x = !w.few || !f8_gemv_quantises(T, H);
+  w.own_h = !w.few || !f8_gemv_quantises(T, I);
+  w.xq = c.take<uint8_t>(w.own_x ? (size_t)(T * H) : 0);
+  w.xs = c.take<float>(w.own_x ? (size_t)(T * ((H + 127) / 128)) : 0);
+  w.h = c.take<uint16_t>(w.few ? (size_t)(T * I) : 0);
+  w.hq = c.take<uint8_t>(w.own_h ? (size_t)(T * I) : 0);
+  w.hs = c.take<float>(w.own_h ? (size_t)(T * ((I + 127) / 128)) : 0);
+  if (!w.few) {
     w.up_plan = f8_gemm_plan(true, OutType::BF16, T, I, H);
     w.down_plan = f8_gemm_plan(false, out, T, H, I);
     const F8Plan other = f8_gemm_plan(
@@ -1471,12 +1475,12 @@ nvfp4_status fp8_block_linear(const void *x, const float *x_scales, int64_t M,
       carve_fp8_linear(c, M, N, K, x_scales != nullptr, out_type(y_dtype));
   const void *xq = x;
   const float *xs = x_scales;
-  if (!x_scales && !f8_gemv_quantises(M)) {
+  if (!x_scales && !f8_gemv_quantises(M, K)) {
     LAUNCH(launch_f8_quantize(x, InType::BF16, M, K, K, 1, ws.xq, ws.xs, stream), "fp8 quantize");
     xq = ws.xq;
     xs = ws.xs;
   }
-  if (f8_gemv_supported(M)) {
+  if (f8_gemv_supported(M, K)) {
     const F8GemvArgs a = {xq, xs, (int)M, {w->codes, nullptr}, {w->scales, nullptr},
                           (int)N, (int)K, y, out_type(y_dtype)};
     LAUNCH(launch_f8_gemv(false, a, stream), "fp8 gemv");
@@ -1531,19 +1535,18 @@ nvfp4_status fp8_block_mlp(const void *x, int64_t T, const fp8_matrix *w_gate,
   if (T == 0) return NVFP4_OK;
   Carver c(workspace);
   const Fp8MlpWs ws = carve_fp8_mlp(c, T, H, I, out_type(y_dtype));
-  const bool inside = f8_gemv_quantises(T);
-  if (!inside)
+  if (ws.own_x)
     LAUNCH(launch_f8_quantize(x, InType::BF16, T, H, H, 1, ws.xq, ws.xs, stream), "fp8 quantize");
-  if (f8_gemv_supported(T)) {
-    const F8GemvArgs g = {inside ? x : ws.xq, inside ? nullptr : ws.xs, (int)T,
+  if (ws.few) {
+    const F8GemvArgs g = {ws.own_x ? ws.xq : x, ws.own_x ? ws.xs : nullptr, (int)T,
                           {w_gate->codes, w_up->codes}, {w_gate->scales, w_up->scales},
                           (int)I, (int)H, ws.h, OutType::BF16};
     LAUNCH(launch_f8_gemv(true, g, stream), "fp8 gate/up");
-    if (!inside)
+    if (ws.own_h)
       LAUNCH(launch_f8_quantize(ws.h, InType::BF16, T, I, I, 1, ws.hq, ws.hs, stream),
              "fp8 quantize");
-    const F8GemvArgs d = {inside ? static_cast<const void *>(ws.h) : ws.hq,
-                          inside ? nullptr : ws.hs, (int)T, {w_down->codes, nullptr},
+    const F8GemvArgs d = {ws.own_h ? static_cast<const void *>(ws.hq) : ws.h,
+                          ws.own_h ? ws.hs : nullptr, (int)T, {w_down->codes, nullptr},
                           {w_down->scales, nullptr}, (int)H, (int)I, y, out_type(y_dtype)};
     LAUNCH(launch_f8_gemv(false, d, stream), "fp8 down");
     return NVFP4_OK;

@@ -72,4 +72,21 @@ __device__ __forceinline__ void f8_to_f16(const u32x4 c, f16x8 (&o)[2]) {
     }
 }
 
+typedef __attribute__((address_space(3))) void *lds_ptr_t;
+constexpr int kOutside = INT32_MIN;   // a byte offset past any buffer bound
+
+// The matrix of `rows` rows of `pitch` bytes from row `row` on; an offset at
+// or past its end (or kOutside) reads zero.  A tile spans less than 2^31 bytes.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t f8_buffer(const void *base, int64_t row,
+                                                            int64_t rows, int64_t pitch) {
+  const int64_t left = row < rows ? (rows - row) * pitch : 0;
+  const uint64_t at = (uint64_t)base + (left > 0 ? row * pitch : 0);
+  // (the 64-bit arithmetic may go through vector registers: back to scalars)
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)at);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
+  const int n = __builtin_amdgcn_readfirstlane((int)(left < 0x7FFFFFFF ? left : 0x7FFFFFFF));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>((uint64_t)hi << 32 | lo), 0, n,
+                                           0x00027000);
+}
+
 }  // namespace nvfp4

@@ -34,8 +34,6 @@ constexpr int kF8Waves = 8;            // kF8WN by 2
 constexpr int kF8WN = 4;
 constexpr int kF8FN = 4;               // 16-row weight tiles of a wave
 constexpr int kF8Group = 4;            // blocks whose scales are loaded together
-constexpr int kOutside = INT32_MIN;   // a byte offset past any buffer bound
-typedef __attribute__((address_space(3))) void *lds_ptr_t;
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
@@ -43,20 +41,6 @@ __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f +
 // read serves together (rows 0-3 and 12-15 of one granule with rows 4-11 of the
 // next, or the reverse) then touch all banks once.
 __device__ __forceinline__ int f8_swizzle(int i) { return (0x1320 >> (4 * i)) & 3; }
-
-// The matrix of `rows` rows of `pitch` bytes from row `row` on; an offset at
-// or past its end (or kOutside) reads zero.  A tile spans less than 2^31 bytes.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t f8_buffer(const void *base, int64_t row,
-                                                            int64_t rows, int64_t pitch) {
-  const int64_t left = row < rows ? (rows - row) * pitch : 0;
-  const uint64_t at = (uint64_t)base + (left > 0 ? row * pitch : 0);
-  // (the 64-bit arithmetic may go through vector registers: back to scalars)
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)at);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
-  const int n = __builtin_amdgcn_readfirstlane((int)(left < 0x7FFFFFFF ? left : 0x7FFFFFFF));
-  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>((uint64_t)hi << 32 | lo), 0, n,
-                                           0x00027000);
-}
 
 // 4 x FM tiles of 16 x 16 per wave: 256 weight rows (SWIGLU: 128 of either
 // matrix) and FM x 32 tokens per workgroup.

@@ -2,45 +2,52 @@
 // weights, shared by every row.
 //
 // Bounded by the weight stream (one byte per element for at most 64 tokens).
-// A workgroup owns 16 R weight rows (R gate and R up tiles in the gate/up
-// form); its eight waves take the 128-column blocks of K in turn, so the
-// workgroup reads eight neighbouring lines of each of its rows at a time, and
-// each wave keeps D blocks of weights in flight in registers.  E4M3 codes
-// become exact fp16 pairs (v_cvt_scalef32_pk_f16_fp8) and a block's sum is
-// four v_mfma_f32_16x16x32_f16 from a zero accumulator: exact products, fp32
-// sums (the fp8 MFMA aligns its products to the largest with about 12 bits,
-// which bf16 outputs hide but fp32 ones do not; here the matrix unit is idle
-// anyway).  The block's results join the fp32 totals by one FMA with s_x s_w.
-// The eight waves' totals are added in wave order in LDS: deterministic.
+// A workgroup owns 16 R weight rows (a gate and an up tile in the gate/up
+// form); its waves take the 128-column blocks of K in turn, so the workgroup
+// reads neighbouring lines of each of its rows at a time.  A wave's blocks
+// arrive in a ring of its own in LDS by direct loads, D ahead, eight whole
+// lines a load: no registers, no barrier.  (A fragment loaded straight into
+// registers touches a line per lane, which takes the address unit 64 cycles
+// instead of 16.)
 //
-// QX: x is bf16 and every wave quantises the block it is about to use (lane
-// group g holds granules g and 4 + g of its token's 128 columns, so a block's
-// maximum is two cross-lane steps).  Each workgroup repeats that for all of
-// x, which costs VALU cycles the stream leaves idle and saves a launch.
+// E4M3 codes become exact fp16 pairs and a block's sum is four
+// v_mfma_f32_16x16x32_f16 from a zero accumulator: exact products, fp32 sums
+// (the fp8 MFMA aligns its products to the largest with about 12 bits, which
+// bf16 outputs hide but fp32 ones do not; here the matrix unit is idle anyway).
+// The block's results join the fp32 totals by one FMA with s_x s_w, and the
+// waves' totals are added in wave order in LDS: deterministic.
+//
+// QX: x is bf16 and each workgroup quantises it into LDS while its first
+// weights are on their way; that saves a launch.  Otherwise x's codes come
+// through the ring with the weights.
 #include "fp8.h"
 #include "kernels.h"
 
 namespace nvfp4 {
 namespace {
 
-constexpr int kGWaves = 8;
+constexpr int kGvMaxKB = 144;          // scale blocks of K: scales are kept in LDS
+constexpr int kGvXBytes = 40 * 1024;   // x's codes and scales of the QX form
 
-__device__ __forceinline__ void unpack_bf16x8(const u32x4 r, float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(r[i] << 16);
-    v[2 * i + 1] = __uint_as_float(r[i] & 0xFFFF0000u);
-  }
+// bytes of LDS for M rows of codes (16 bytes apart from a multiple of the
+// banks) and their scales
+__host__ __device__ constexpr int64_t gv_x_bytes(int64_t M, int64_t KB) {
+  return M * (KB * (kF8Block + 4) + 16);
 }
 
-template <int R, int MT, bool SWIGLU, bool QX>
-__global__ __launch_bounds__(64 * kGWaves, MT == 1 ? 4 : 2)
-void f8_gemv_kernel(const F8GemvArgs p) {
+// XCAP: bytes for x (QX) or its scales.
+template <int MT, int R, bool SWIGLU, bool QX, int NW, int D, int XCAP>
+__global__ __launch_bounds__(64 * NW) void f8_gemv_kernel(const F8GemvArgs p) {
 #pragma clang fp contract(off)
+  static_assert(!QX || MT == 1, "QX: up to 16 rows");
   constexpr int NT = SWIGLU ? 2 * R : R;           // 16-row weight tiles
-  constexpr int D = NT == 1 ? 4 : 2;               // blocks of weights in flight
-  constexpr int XL = QX ? 4 : 2;                   // 16-byte loads of x per token tile
-  __shared__ float red[kGWaves][NT * 16][MT * 16 + 1];
+  constexpr int SLOT = 2048 * (NT + (QX ? 0 : MT));   // a block: 16 x 128 codes a tile
+  constexpr int LS = SLOT / 1024;                  // loads of a block
+  constexpr int RED = NW * NT * 16 * (MT * 16 + 1) * 4;
+  constexpr int RING = NW * D * SLOT > RED ? NW * D * SLOT : RED;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[RING + XCAP + 2 * kGvMaxKB * 4];
+  uint8_t *const xl = lds + RING;
+  float *const swl = reinterpret_cast<float *>(lds + RING + XCAP);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, lg = lane >> 4;
@@ -48,148 +55,164 @@ void f8_gemv_kernel(const F8GemvArgs p) {
   const int KB = (K + kF8Block - 1) / kF8Block;
   const int r0 = blockIdx.x * 16 * R;              // first output column
   const int nb = r0 / kF8Block;                    // (16 R rows lie in one scale block)
-  const int mine = (KB - wave + kGWaves - 1) / kGWaves;   // this wave's blocks
+  const int mine = (KB - wave + NW - 1) / NW;      // this wave's blocks: wave, wave + NW, ...
+  const int xp = KB * kF8Block + 16;               // QX: pitch of a row of codes
+  float *const sxl = reinterpret_cast<float *>(QX ? xl + M * xp : xl);   // [M][KB]
 
-  const uint8_t *wrow[NT];
+  // ---- the ring: a load fills 8 rows of 128 bytes, lane l position l % 8 of
+  // row l / 8, which holds granule (l % 8) ^ (l / 8)
+  __amdgpu_buffer_rsrc_t wbuf[4], xbuf[8];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int row = r0 + (t % R) * 16 + lr;
-    wrow[t] = p.w[t / R] + (int64_t)(row < N ? row : N - 1) * K;
+  for (int h = 0; h < 2 * NT; ++h)
+    wbuf[h] = f8_buffer(p.w[h / 2 / R], r0 + h / 2 % R * 16 + h % 2 * 8, N, K);
+  if constexpr (!QX) {
+#pragma unroll
+    for (int h = 0; h < 2 * MT; ++h) xbuf[h] = f8_buffer(p.x, h * 8, M, K);
   }
-  const uint8_t *xrow[MT];
-  const float *srow[MT];
+  const int gran = (lane & 7) ^ (lane >> 3);
+  const int off_ = (lane >> 3) * K + gran * 16, last = K - gran * 16;
+  uint8_t *const ring = lds + wave * (D * SLOT);
+  auto load = [&](int i, int slot) {
+    const int at = __builtin_amdgcn_readfirstlane((wave + NW * i) * kF8Block);
+    const int off = off_ | (at < last ? 0 : kOutside);   // (granules past K: zero codes)
 #pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    const int m = j * 16 + lr < M ? j * 16 + lr : M - 1;
-    xrow[j] = static_cast<const uint8_t *>(p.x) + (int64_t)m * K * (QX ? 2 : 1);
-    srow[j] = QX ? nullptr : p.xs + (int64_t)m * KB;
+    for (int h = 0; h < LS; ++h)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(h < 2 * NT ? wbuf[h] : xbuf[h - 2 * NT],
+                                               (lds_ptr_t)(ring + slot * SLOT + h * 1024), 16, off,
+                                               at, 0, 0);
+  };
+
+  // ---- x and the scales (their first loads go out before the ring's)
+  constexpr int G = NW * 4, B = 4;                 // QX: groups of 16 lanes, blocks of a batch
+  const int gl = tid & 15;
+  auto x_block = [&](int it) {                     // 8 of the 128 values of block it of [M][KB]
+    const int m = it / KB, k = (it - m * KB) * kF8Block + gl * 8;
+    return it < M * KB && k < K
+               ? *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(p.x) +
+                                                  (int64_t)m * K + k)
+               : u32x4{0u, 0u, 0u, 0u};
+  };
+  u32x4 xr[B];
+  if constexpr (QX) {
+#pragma unroll
+    for (int j = 0; j < B; ++j) xr[j] = x_block(tid / 16 + G * j);
   }
-  const u32x4 zero = u32x4{0u, 0u, 0u, 0u};
-  u32x4 wq[D][NT][2];
-  auto load_w = [&](int i, int d) {
-    const int b = wave + kGWaves * i;
-    const int k0 = b * kF8Block + lg * 16, k1 = k0 + 64;
-    if (b * kF8Block + kF8Block <= K) {   // uniform: a whole block
+  const float *const ws0 = p.ws[0] + (int64_t)nb * KB;
+  const float *const ws1 = SWIGLU ? p.ws[1] + (int64_t)nb * KB : nullptr;
+  float w0 = 0.0f, w1 = 0.0f;
+  if (tid < KB) {                                  // (KB <= kGvMaxKB <= 64 NW)
+    w0 = ws0[tid];
+    if constexpr (SWIGLU) w1 = ws1[tid];
+  }
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        wq[d][t][0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(wrow[t] + k0));
-        wq[d][t][1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(wrow[t] + k1));
-      }
-    } else {                              // granules past K are zero codes
+  for (int d = 0; d < D; ++d) load(d, d);
+  if (tid < KB) {
+    swl[tid] = w0;
+    if constexpr (SWIGLU) swl[kGvMaxKB + tid] = w1;
+  }
+  if constexpr (QX) {
+    for (int it0 = tid / 16; it0 < M * KB; it0 += G * B) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        wq[d][t][0] = k0 < K ? *reinterpret_cast<const u32x4 *>(wrow[t] + k0) : zero;
-        wq[d][t][1] = k1 < K ? *reinterpret_cast<const u32x4 *>(wrow[t] + k1) : zero;
+      for (int j = 0; j < B; ++j) {
+        const int it = it0 + G * j, m = it / KB, b = it - m * KB;
+        float v[8], top = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t w = xr[j][e];
+          v[2 * e] = __uint_as_float(w << 16);
+          v[2 * e + 1] = __uint_as_float(w & 0xFFFF0000u);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, __builtin_fabsf(v[e]));
+        top = f8_row16_max(top);
+        const float s = f8_scale(top), inv = 1.0f / s;
+        if (it < M * KB) {
+          *reinterpret_cast<u32x2 *>(xl + m * xp + b * kF8Block + gl * 8) =
+              u32x2{f8_pack4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                    f8_pack4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv)};
+          if (gl == 0) sxl[it] = s;
+        }
       }
+#pragma unroll
+      for (int j = 0; j < B; ++j) xr[j] = x_block(it0 + G * (B + j));
     }
-  };
-  u32x4 xq[2][MT][XL];
-  float sx[2][MT];
-  auto load_x = [&](int i, int d) {
-    const int b = wave + kGWaves * i;
-    const int k0 = b * kF8Block + lg * 16, k1 = k0 + 64;
-#pragma unroll
-    for (int j = 0; j < MT; ++j) {
-      if constexpr (QX) {
-        const u32x4 *a = reinterpret_cast<const u32x4 *>(xrow[j] + 2 * (int64_t)k0);
-        const u32x4 *c = reinterpret_cast<const u32x4 *>(xrow[j] + 2 * (int64_t)k1);
-        xq[d][j][0] = k0 < K ? a[0] : zero;
-        xq[d][j][1] = k0 < K ? a[1] : zero;
-        xq[d][j][XL - 2] = k1 < K ? c[0] : zero;
-        xq[d][j][XL - 1] = k1 < K ? c[1] : zero;
-      } else {
-        xq[d][j][0] = k0 < K ? *reinterpret_cast<const u32x4 *>(xrow[j] + k0) : zero;
-        xq[d][j][1] = k1 < K ? *reinterpret_cast<const u32x4 *>(xrow[j] + k1) : zero;
-        sx[d][j] = srow[j][b];
-      }
-    }
-  };
+  } else {
+    for (int i = tid; i < M * KB; i += 64 * NW) sxl[i] = p.xs[i];
+  }
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 
   f32x4 acc[NT][MT];
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int j = 0; j < MT; ++j) acc[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  if (mine > 0) load_x(0, 0);
+  const int p0 = lr * kF8Block + (lg ^ (lr & 7)) * 16, p1 = lr * kF8Block + ((lg + 4) ^ (lr & 7)) * 16;
+  int row[4];                                      // token of tile j (repeated past M)
 #pragma unroll
-  for (int d = 0; d < D; ++d)
-    if (d < mine) load_w(d, d);
-
-  for (int i0 = 0; i0 < mine; i0 += D) {
+  for (int j = 0; j < MT; ++j) row[j] = j * 16 + lr < M ? j * 16 + lr : M - 1;
+  int slot = 0;
+#pragma unroll 1
+  for (int i = 0; i < mine; ++i) {
+    const int b = __builtin_amdgcn_readfirstlane(wave + NW * i);
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((D - 1) * LS) : "memory");
+    const uint8_t *st = ring + slot * SLOT;
+    u32x4 wq[4][2], xq[4][2];
 #pragma unroll
-    for (int d = 0; d < D; ++d) {
-      const int i = i0 + d;
-      if (i >= mine) break;   // uniform
-      if (i + 1 < mine) load_x(i + 1, (d + 1) & 1);
-      const int b = wave + kGWaves * i;
-      const float g0 = p.ws[0][(int64_t)nb * KB + b];
-      const float g1 = SWIGLU ? p.ws[1][(int64_t)nb * KB + b] : 0.0f;
-      f16x8 xf[MT][4];
-      float s[MT];
+    for (int t = 0; t < NT; ++t) {
+      wq[t][0] = *reinterpret_cast<const u32x4 *>(st + t * 2048 + p0);
+      wq[t][1] = *reinterpret_cast<const u32x4 *>(st + t * 2048 + p1);
+    }
+    float s[4];
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      const uint8_t *xt = QX ? xl + row[j] * xp + b * kF8Block + lg * 16 : st + (NT + j) * 2048;
+      xq[j][0] = *reinterpret_cast<const u32x4 *>(xt + (QX ? 0 : p0));
+      xq[j][1] = *reinterpret_cast<const u32x4 *>(xt + (QX ? 64 : p1));
+      s[j] = sxl[row[j] * KB + b];
+    }
+    const float g0 = swl[b], g1 = SWIGLU ? swl[kGvMaxKB + b] : 0.0f;
+    // the slot is read: it takes block i + D
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    load(i + D, slot);
+    slot = slot + 1 == D ? 0 : slot + 1;
+    f16x8 xf[4][4];
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        f16x8 o[2];
+        f8_to_f16(xq[j][q], o);
+        xf[j][2 * q] = o[0];
+        xf[j][2 * q + 1] = o[1];
+      }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      f16x8 a[4];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        f16x8 o[2];
+        f8_to_f16(wq[t][q], o);
+        a[2 * q] = o[0];
+        a[2 * q + 1] = o[1];
+      }
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
-        if constexpr (QX) {
-          float v[4][8], m = 0.0f;
+        f32x4 z = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            unpack_bf16x8(xq[d & 1][j][q], v[q]);
+        for (int q = 0; q < 4; ++q)
+          z = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[q], xf[j][q], z, 0, 0, 0);
+        const float sc = s[j] * (t / R ? g1 : g0);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) m = fmaxf(m, __builtin_fabsf(v[q][e]));
-          }
-          m = f8_rows_max(m);
-          s[j] = f8_scale(m);
-          const float inv = 1.0f / s[j];
-#pragma unroll
-          for (int q = 0; q < 4; q += 2) {
-            u32x4 c;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const float *e = &v[q + w / 2][4 * (w & 1)];
-              c[w] = f8_pack4(e[0] * inv, e[1] * inv, e[2] * inv, e[3] * inv);
-            }
-            f16x8 o[2];
-            f8_to_f16(c, o);
-            xf[j][q] = o[0];
-            xf[j][q + 1] = o[1];
-          }
-        } else {
-          s[j] = sx[d & 1][j];
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            f16x8 o[2];
-            f8_to_f16(xq[d & 1][j][q], o);
-            xf[j][2 * q] = o[0];
-            xf[j][2 * q + 1] = o[1];
-          }
-        }
+        for (int e = 0; e < 4; ++e) acc[t][j][e] = __builtin_fmaf(z[e], sc, acc[t][j][e]);
       }
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        f16x8 a[4];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          f16x8 o[2];
-          f8_to_f16(wq[d][t][q], o);
-          a[2 * q] = o[0];
-          a[2 * q + 1] = o[1];
-        }
-#pragma unroll
-        for (int j = 0; j < MT; ++j) {
-          f32x4 z = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            z = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[q], xf[j][q], z, 0, 0, 0);
-          const float sc = s[j] * (t / R ? g1 : g0);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[t][j][e] = __builtin_fmaf(z[e], sc, acc[t][j][e]);
-        }
-      }
-      if (i + D < mine) load_w(i + D, d);
     }
   }
 
-  // totals of the waves, added in wave order
+  // totals of the waves, added in wave order (every load has landed, and every
+  // wave left the ring)
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  float (*red)[NT * 16][MT * 16 + 1] = reinterpret_cast<float (*)[NT * 16][MT * 16 + 1]>(lds);
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -197,17 +220,17 @@ void f8_gemv_kernel(const F8GemvArgs p) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) red[wave][t * 16 + 4 * lg + e][j * 16 + lr] = acc[t][j][e];
   __syncthreads();
-  for (int i = tid; i < 16 * R * M; i += 64 * kGWaves) {
+  for (int i = tid; i < 16 * R * M; i += 64 * NW) {
     const int c = i % (16 * R), m = i / (16 * R);   // consecutive threads: consecutive columns
     const int n = r0 + c;
     if (n >= N) continue;
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kGWaves; ++w) v += red[w][c][m];
+    for (int w = 0; w < NW; ++w) v += red[w][c][m];
     if constexpr (SWIGLU) {
       float u = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kGWaves; ++w) u += red[w][16 * R + c][m];
+      for (int w = 0; w < NW; ++w) u += red[w][16 * R + c][m];
       static_cast<uint16_t *>(p.out)[(int64_t)m * N + n] =
           (uint16_t)f32_to_bf16_bits(v / (1.0f + expf(-v)) * u);
     } else if (p.out_type == OutType::F32) {
@@ -218,36 +241,47 @@ void f8_gemv_kernel(const F8GemvArgs p) {
   }
 }
 
-template <int R, int MT, bool SWIGLU>
-hipError_t launch_gemv_mt(const F8GemvArgs &a, hipStream_t s) {
-  const dim3 grid((unsigned)((a.N + 16 * R - 1) / (16 * R))), block(64 * kGWaves);
-  if (a.xs) launch_kernel((f8_gemv_kernel<R, MT, SWIGLU, false>), grid, block, 0, s, a);
-  else if constexpr (MT == 1)
-    launch_kernel((f8_gemv_kernel<R, MT, SWIGLU, true>), grid, block, 0, s, a);
-  else return hipErrorInvalidValue;
+template <int MT, int R, bool SWIGLU, bool QX, int NW, int D, int XCAP>
+hipError_t launch_gemv(const F8GemvArgs &a, hipStream_t s) {
+  launch_kernel((f8_gemv_kernel<MT, R, SWIGLU, QX, NW, D, XCAP>),
+                dim3((unsigned)((a.N + 16 * R - 1) / (16 * R))), dim3(64 * NW), 0, s, a);
   return hipGetLastError();
 }
 
-template <int R, bool SWIGLU>
-hipError_t launch_gemv_r(const F8GemvArgs &a, hipStream_t s) {
-  switch ((a.M + 15) / 16) {
-    case 1: return launch_gemv_mt<R, 1, SWIGLU>(a, s);
-    case 2: return launch_gemv_mt<R, 2, SWIGLU>(a, s);
-    case 3: return launch_gemv_mt<R, 3, SWIGLU>(a, s);
-    case 4: return launch_gemv_mt<R, 4, SWIGLU>(a, s);
-    default: return hipErrorInvalidValue;
-  }
-}
+// scales of MT x 16 rows
+constexpr int sx_cap(int mt) { return mt * 16 * kGvMaxKB * 4; }
 
 }  // namespace
 
-bool f8_gemv_supported(int64_t M) { return M >= 1 && M <= 64; }
-bool f8_gemv_quantises(int64_t M) { return M >= 1 && M <= 16; }
+bool f8_gemv_supported(int64_t M, int64_t K) {
+  return M >= 1 && M <= 64 && K <= kGvMaxKB * kF8Block;
+}
+bool f8_gemv_quantises(int64_t M, int64_t K) {
+  return f8_gemv_supported(M, K) && M <= 16 &&
+         gv_x_bytes(M, (K + kF8Block - 1) / kF8Block) <= kGvXBytes;
+}
 
 hipError_t launch_f8_gemv(bool swiglu, const F8GemvArgs &a, hipStream_t s) {
-  if (!f8_gemv_supported(a.M) || (!a.xs && !f8_gemv_quantises(a.M))) return hipErrorInvalidValue;
-  if (swiglu) return launch_gemv_r<1, true>(a, s);
-  return a.N >= 32 * 256 ? launch_gemv_r<2, false>(a, s) : launch_gemv_r<1, false>(a, s);
+  if (!f8_gemv_supported(a.M, a.K) || (!a.xs && !f8_gemv_quantises(a.M, a.K)))
+    return hipErrorInvalidValue;
+  if (!a.xs) {
+    const bool small = gv_x_bytes(a.M, (a.K + kF8Block - 1) / kF8Block) <= 10 * 1024;
+    if (swiglu)
+      return small ? launch_gemv<1, 1, true, true, 8, 2, 10 * 1024>(a, s)
+                   : launch_gemv<1, 1, true, true, 8, 2, kGvXBytes>(a, s);
+    return small ? launch_gemv<1, 1, false, true, 8, 4, 10 * 1024>(a, s)
+                 : launch_gemv<1, 1, false, true, 8, 4, kGvXBytes>(a, s);
+  }
+  switch ((a.M + 15) / 16 + (swiglu ? 4 : 0)) {
+    case 1: return launch_gemv<1, 1, false, false, 8, 2, sx_cap(1)>(a, s);
+    case 2: return launch_gemv<2, 1, false, false, 8, 2, sx_cap(2)>(a, s);
+    case 3: return launch_gemv<3, 1, false, false, 4, 3, sx_cap(3)>(a, s);
+    case 4: return launch_gemv<4, 1, false, false, 4, 3, sx_cap(4)>(a, s);
+    case 5: return launch_gemv<1, 1, true, false, 8, 2, sx_cap(1)>(a, s);
+    case 6: return launch_gemv<2, 1, true, false, 8, 2, sx_cap(2)>(a, s);
+    case 7: return launch_gemv<3, 1, true, false, 4, 3, sx_cap(3)>(a, s);
+    default: return launch_gemv<4, 1, true, false, 4, 2, sx_cap(4)>(a, s);
+  }
 }
 
 }  // namespace nvfp4

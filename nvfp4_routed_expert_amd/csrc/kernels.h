@@ -351,8 +351,8 @@ struct F8Plan {
 F8Plan f8_gemm_plan(bool swiglu, OutType out, int64_t M, int64_t N, int64_t K);
 hipError_t launch_f8_gemm(bool swiglu, const F8GemmArgs &a, const F8Plan &pl, hipStream_t s);
 
-// The same product for M <= 64 rows (fp8gemv.hip).  xs null: x is bf16 [M, K]
-// and is quantised inside (M <= 16); otherwise x holds codes.  Gate/up form:
+// The same product for M <= 64 rows of K <= 18432 (fp8gemv.hip).  xs null: x is
+// bf16 [M, K] and is quantised inside (M K up to about 40000); otherwise x holds codes.  Gate/up form:
 // out = h, bf16 [M, N].
 struct F8GemvArgs {
   const void *x;
@@ -364,8 +364,8 @@ struct F8GemvArgs {
   void *out;
   OutType out_type;
 };
-bool f8_gemv_supported(int64_t M);
-bool f8_gemv_quantises(int64_t M);
+bool f8_gemv_supported(int64_t M, int64_t K);
+bool f8_gemv_quantises(int64_t M, int64_t K);
 hipError_t launch_f8_gemv(bool swiglu, const F8GemvArgs &a, hipStream_t s);
 
 // ---- a whole MoE layer for a few tokens (layer.hip) --------------------------------
