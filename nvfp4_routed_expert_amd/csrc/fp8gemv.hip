@@ -2,7 +2,7 @@
 // weights, shared by every row.
 //
 // Bounded by the weight stream (one byte per element for at most 64 tokens).
-// A workgroup owns 16 R weight rows (a gate and an up tile in the gate/up
+// A workgroup owns 16 weight rows (16 gate and 16 up rows in the gate/up
 // form); its waves take the 128-column blocks of K in turn, so the workgroup
 // reads neighbouring lines of each of its rows at a time.  A wave's blocks
 // arrive in a ring of its own in LDS by direct loads, D ahead, eight whole
@@ -14,8 +14,10 @@
 // v_mfma_f32_16x16x32_f16 from a zero accumulator: exact products, fp32 sums
 // (the fp8 MFMA aligns its products to the largest with about 12 bits, which
 // bf16 outputs hide but fp32 ones do not; here the matrix unit is idle anyway).
-// The block's results join the fp32 totals by one FMA with s_x s_w, and the
-// waves' totals are added in wave order in LDS: deterministic.
+// The block's results join the fp32 totals by one FMA with s_x s_w.  Blocks b,
+// b + 8, ... are one stream of sums, and the eight streams are joined in order
+// in LDS: the result depends neither on how many waves share the work nor on
+// where x was quantised.
 //
 // QX: x is bf16 and each workgroup quantises it into LDS while its first
 // weights are on their way; that saves a launch.  Otherwise x's codes come
@@ -26,8 +28,9 @@
 namespace nvfp4 {
 namespace {
 
+constexpr int kGvStreams = 8;          // sums of every 8th block, joined in order
 constexpr int kGvMaxKB = 144;          // scale blocks of K: scales are kept in LDS
-constexpr int kGvXBytes = 40 * 1024;   // x's codes and scales of the QX form
+constexpr int kGvXBytes = 20 * 1024;   // x's codes and scales of the QX form, at most
 
 // bytes of LDS for M rows of codes (16 bytes apart from a multiple of the
 // banks) and their scales
@@ -35,15 +38,16 @@ __host__ __device__ constexpr int64_t gv_x_bytes(int64_t M, int64_t KB) {
   return M * (KB * (kF8Block + 4) + 16);
 }
 
-// XCAP: bytes for x (QX) or its scales.
-template <int MT, int R, bool SWIGLU, bool QX, int NW, int D, int XCAP>
+// XT: groups of 8 rows of x.  XCAP: bytes for x (QX) or its scales.
+template <int XT, bool SWIGLU, bool QX, int NW, int D, int XCAP>
 __global__ __launch_bounds__(64 * NW) void f8_gemv_kernel(const F8GemvArgs p) {
 #pragma clang fp contract(off)
-  static_assert(!QX || MT == 1, "QX: up to 16 rows");
-  constexpr int NT = SWIGLU ? 2 * R : R;           // 16-row weight tiles
-  constexpr int SLOT = 2048 * (NT + (QX ? 0 : MT));   // a block: 16 x 128 codes a tile
+  static_assert(!QX || XT <= 2, "QX: up to 16 rows");
+  constexpr int NT = SWIGLU ? 2 : 1, MT = (XT + 1) / 2;   // tiles of 16 rows of w, x
+  constexpr int SLOT = 2048 * NT + (QX ? 0 : 1024 * XT);  // a block: 1 KB for 8 rows
   constexpr int LS = SLOT / 1024;                  // loads of a block
-  constexpr int RED = NW * NT * 16 * (MT * 16 + 1) * 4;
+  constexpr int V = kGvStreams / NW;               // streams of a wave
+  constexpr int RED = kGvStreams * NT * 16 * (MT * 16 + 1) * 4;
   constexpr int RING = NW * D * SLOT > RED ? NW * D * SLOT : RED;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[RING + XCAP + 2 * kGvMaxKB * 4];
   uint8_t *const xl = lds + RING;
@@ -53,8 +57,8 @@ __global__ __launch_bounds__(64 * NW) void f8_gemv_kernel(const F8GemvArgs p) {
   const int lr = lane & 15, lg = lane >> 4;
   const int K = p.K, N = p.N, M = p.M;
   const int KB = (K + kF8Block - 1) / kF8Block;
-  const int r0 = blockIdx.x * 16 * R;              // first output column
-  const int nb = r0 / kF8Block;                    // (16 R rows lie in one scale block)
+  const int r0 = blockIdx.x * 16;                  // first output column
+  const int nb = r0 / kF8Block;                    // (16 rows lie in one scale block)
   const int mine = (KB - wave + NW - 1) / NW;      // this wave's blocks: wave, wave + NW, ...
   const int xp = KB * kF8Block + 16;               // QX: pitch of a row of codes
   float *const sxl = reinterpret_cast<float *>(QX ? xl + M * xp : xl);   // [M][KB]
@@ -64,10 +68,10 @@ __global__ __launch_bounds__(64 * NW) void f8_gemv_kernel(const F8GemvArgs p) {
   __amdgpu_buffer_rsrc_t wbuf[4], xbuf[8];
 #pragma unroll
   for (int h = 0; h < 2 * NT; ++h)
-    wbuf[h] = f8_buffer(p.w[h / 2 / R], r0 + h / 2 % R * 16 + h % 2 * 8, N, K);
+    wbuf[h] = f8_buffer(p.w[h / 2], r0 + h % 2 * 8, N, K);
   if constexpr (!QX) {
 #pragma unroll
-    for (int h = 0; h < 2 * MT; ++h) xbuf[h] = f8_buffer(p.x, h * 8, M, K);
+    for (int h = 0; h < XT; ++h) xbuf[h] = f8_buffer(p.x, h * 8, M, K);
   }
   const int gran = (lane & 7) ^ (lane >> 3);
   const int off_ = (lane >> 3) * K + gran * 16, last = K - gran * 16;
@@ -141,19 +145,24 @@ __global__ __launch_bounds__(64 * NW) void f8_gemv_kernel(const F8GemvArgs p) {
   }
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 
-  f32x4 acc[NT][MT];
+  f32x4 acc[2][2][4];
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
+  for (int c = 0; c < V; ++c)
 #pragma unroll
-    for (int j = 0; j < MT; ++j) acc[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int j = 0; j < MT; ++j) acc[c][t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int p0 = lr * kF8Block + (lg ^ (lr & 7)) * 16, p1 = lr * kF8Block + ((lg + 4) ^ (lr & 7)) * 16;
+  // (8 rows: read twice)
+  const int xr0 = XT == 1 ? p0 - (lr & 8) * kF8Block : p0, xr1 = XT == 1 ? p1 - (lr & 8) * kF8Block : p1;
   int row[4];                                      // token of tile j (repeated past M)
 #pragma unroll
   for (int j = 0; j < MT; ++j) row[j] = j * 16 + lr < M ? j * 16 + lr : M - 1;
   int slot = 0;
-#pragma unroll 1
-  for (int i = 0; i < mine; ++i) {
+  auto block = [&](int i, int c) {
     const int b = __builtin_amdgcn_readfirstlane(wave + NW * i);
+    const bool in = V == 1 || b < KB;              // (past the end: zeros times zero)
+    const int bs = in ? b : KB - 1;
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"((D - 1) * LS) : "memory");
     const uint8_t *st = ring + slot * SLOT;
     u32x4 wq[4][2], xq[4][2];
@@ -165,12 +174,12 @@ __global__ __launch_bounds__(64 * NW) void f8_gemv_kernel(const F8GemvArgs p) {
     float s[4];
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
-      const uint8_t *xt = QX ? xl + row[j] * xp + b * kF8Block + lg * 16 : st + (NT + j) * 2048;
-      xq[j][0] = *reinterpret_cast<const u32x4 *>(xt + (QX ? 0 : p0));
-      xq[j][1] = *reinterpret_cast<const u32x4 *>(xt + (QX ? 64 : p1));
-      s[j] = sxl[row[j] * KB + b];
+      const uint8_t *xt = QX ? xl + row[j] * xp + bs * kF8Block + lg * 16 : st + (NT + j) * 2048;
+      xq[j][0] = *reinterpret_cast<const u32x4 *>(xt + (QX ? 0 : xr0));
+      xq[j][1] = *reinterpret_cast<const u32x4 *>(xt + (QX ? 64 : xr1));
+      s[j] = in ? sxl[row[j] * KB + bs] : 0.0f;
     }
-    const float g0 = swl[b], g1 = SWIGLU ? swl[kGvMaxKB + b] : 0.0f;
+    const float g0 = swl[bs], g1 = SWIGLU ? swl[kGvMaxKB + bs] : 0.0f;
     // the slot is read: it takes block i + D
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     load(i + D, slot);
@@ -201,36 +210,44 @@ __global__ __launch_bounds__(64 * NW) void f8_gemv_kernel(const F8GemvArgs p) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           z = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[q], xf[j][q], z, 0, 0, 0);
-        const float sc = s[j] * (t / R ? g1 : g0);
+        const float sc = s[j] * (t ? g1 : g0);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[t][j][e] = __builtin_fmaf(z[e], sc, acc[t][j][e]);
+        for (int e = 0; e < 4; ++e) acc[c][t][j][e] = __builtin_fmaf(z[e], sc, acc[c][t][j][e]);
       }
     }
+  };
+#pragma unroll 1
+  for (int i = 0; i < mine; i += V) {
+#pragma unroll
+    for (int c = 0; c < V; ++c) block(i + c, c);
   }
 
-  // totals of the waves, added in wave order (every load has landed, and every
+  // the streams' totals, added in their order (every load has landed, and every
   // wave left the ring)
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
   float (*red)[NT * 16][MT * 16 + 1] = reinterpret_cast<float (*)[NT * 16][MT * 16 + 1]>(lds);
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
+  for (int c = 0; c < V; ++c)
 #pragma unroll
-    for (int j = 0; j < MT; ++j)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) red[wave][t * 16 + 4 * lg + e][j * 16 + lr] = acc[t][j][e];
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          red[wave + NW * c][t * 16 + 4 * lg + e][j * 16 + lr] = acc[c][t][j][e];
   __syncthreads();
-  for (int i = tid; i < 16 * R * M; i += 64 * NW) {
-    const int c = i % (16 * R), m = i / (16 * R);   // consecutive threads: consecutive columns
+  for (int i = tid; i < 16 * M; i += 64 * NW) {
+    const int c = i % 16, m = i / 16;   // consecutive threads: consecutive columns
     const int n = r0 + c;
     if (n >= N) continue;
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) v += red[w][c][m];
+    for (int w = 0; w < kGvStreams; ++w) v += red[w][c][m];
     if constexpr (SWIGLU) {
       float u = 0.0f;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) u += red[w][16 * R + c][m];
+      for (int w = 0; w < kGvStreams; ++w) u += red[w][16 + c][m];
       static_cast<uint16_t *>(p.out)[(int64_t)m * N + n] =
           (uint16_t)f32_to_bf16_bits(v / (1.0f + expf(-v)) * u);
     } else if (p.out_type == OutType::F32) {
@@ -241,15 +258,12 @@ __global__ __launch_bounds__(64 * NW) void f8_gemv_kernel(const F8GemvArgs p) {
   }
 }
 
-template <int MT, int R, bool SWIGLU, bool QX, int NW, int D, int XCAP>
+template <int XT, bool SWIGLU, bool QX, int NW, int D, int XCAP = XT * 8 * kGvMaxKB * 4>
 hipError_t launch_gemv(const F8GemvArgs &a, hipStream_t s) {
-  launch_kernel((f8_gemv_kernel<MT, R, SWIGLU, QX, NW, D, XCAP>),
-                dim3((unsigned)((a.N + 16 * R - 1) / (16 * R))), dim3(64 * NW), 0, s, a);
+  launch_kernel((f8_gemv_kernel<XT, SWIGLU, QX, NW, D, XCAP>), dim3((unsigned)((a.N + 15) / 16)),
+                dim3(64 * NW), 0, s, a);
   return hipGetLastError();
 }
-
-// scales of MT x 16 rows
-constexpr int sx_cap(int mt) { return mt * 16 * kGvMaxKB * 4; }
 
 }  // namespace
 
@@ -264,23 +278,28 @@ bool f8_gemv_quantises(int64_t M, int64_t K) {
 hipError_t launch_f8_gemv(bool swiglu, const F8GemvArgs &a, hipStream_t s) {
   if (!f8_gemv_supported(a.M, a.K) || (!a.xs && !f8_gemv_quantises(a.M, a.K)))
     return hipErrorInvalidValue;
+  // LDS decides how many workgroups share a CU and how much is in flight: the
+  // least that holds x is taken, and rings of 16 to 36 KB per 4 waves
   if (!a.xs) {
     const bool small = gv_x_bytes(a.M, (a.K + kF8Block - 1) / kF8Block) <= 10 * 1024;
     if (swiglu)
-      return small ? launch_gemv<1, 1, true, true, 8, 2, 10 * 1024>(a, s)
-                   : launch_gemv<1, 1, true, true, 8, 2, kGvXBytes>(a, s);
-    return small ? launch_gemv<1, 1, false, true, 8, 4, 10 * 1024>(a, s)
-                 : launch_gemv<1, 1, false, true, 8, 4, kGvXBytes>(a, s);
+      return small ? launch_gemv<2, true, true, 4, 4, 10 * 1024>(a, s)
+                   : launch_gemv<2, true, true, 4, 3, kGvXBytes>(a, s);
+    return small ? launch_gemv<2, false, true, 4, 4, 10 * 1024>(a, s)
+                 : launch_gemv<2, false, true, 8, 2, kGvXBytes>(a, s);
   }
+  if (a.M <= 8)
+    return swiglu ? launch_gemv<1, true, false, 4, 3>(a, s)
+                  : launch_gemv<1, false, false, 8, 3>(a, s);
   switch ((a.M + 15) / 16 + (swiglu ? 4 : 0)) {
-    case 1: return launch_gemv<1, 1, false, false, 8, 2, sx_cap(1)>(a, s);
-    case 2: return launch_gemv<2, 1, false, false, 8, 2, sx_cap(2)>(a, s);
-    case 3: return launch_gemv<3, 1, false, false, 4, 3, sx_cap(3)>(a, s);
-    case 4: return launch_gemv<4, 1, false, false, 4, 3, sx_cap(4)>(a, s);
-    case 5: return launch_gemv<1, 1, true, false, 8, 2, sx_cap(1)>(a, s);
-    case 6: return launch_gemv<2, 1, true, false, 8, 2, sx_cap(2)>(a, s);
-    case 7: return launch_gemv<3, 1, true, false, 4, 3, sx_cap(3)>(a, s);
-    default: return launch_gemv<4, 1, true, false, 4, 2, sx_cap(4)>(a, s);
+    case 1: return launch_gemv<2, false, false, 8, 2>(a, s);
+    case 2: return launch_gemv<4, false, false, 8, 2>(a, s);
+    case 3: return launch_gemv<6, false, false, 4, 3>(a, s);
+    case 4: return launch_gemv<8, false, false, 4, 3>(a, s);
+    case 5: return launch_gemv<2, true, false, 8, 2>(a, s);
+    case 6: return launch_gemv<4, true, false, 8, 2>(a, s);
+    case 7: return launch_gemv<6, true, false, 4, 3>(a, s);
+    default: return launch_gemv<8, true, false, 4, 2>(a, s);
   }
 }
 

@@ -352,7 +352,7 @@ F8Plan f8_gemm_plan(bool swiglu, OutType out, int64_t M, int64_t N, int64_t K);
 hipError_t launch_f8_gemm(bool swiglu, const F8GemmArgs &a, const F8Plan &pl, hipStream_t s);
 
 // The same product for M <= 64 rows of K <= 18432 (fp8gemv.hip).  xs null: x is
-// bf16 [M, K] and is quantised inside (M K up to about 40000); otherwise x holds codes.  Gate/up form:
+// bf16 [M, K] and is quantised inside (up to about 20000 elements); otherwise x holds codes.  Gate/up form:
 // out = h, bf16 [M, N].
 struct F8GemvArgs {
   const void *x;
