@@ -75,6 +75,11 @@ __device__ __forceinline__ void f8_to_f16(const u32x4 c, f16x8 (&o)[2]) {
 typedef __attribute__((address_space(3))) void *lds_ptr_t;
 constexpr int kOutside = INT32_MIN;   // a byte offset past any buffer bound
 
+// Where granule 0 of 64-byte rows 4 i .. 4 i + 3 lies: the 16 lanes that an LDS
+// read serves together (rows 0-3 and 12-15 of one granule with rows 4-11 of the
+// next, or the reverse) then touch all banks once.
+__device__ __forceinline__ int f8_swizzle(int i) { return (0x1320 >> (4 * i)) & 3; }
+
 // The matrix of `rows` rows of `pitch` bytes from row `row` on; an offset at
 // or past its end (or kOutside) reads zero.  A tile spans less than 2^31 bytes.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t f8_buffer(const void *base, int64_t row,
@@ -84,7 +89,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t f8_buffer(const void *base, in
   // (the 64-bit arithmetic may go through vector registers: back to scalars)
   const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)at);
   const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
-  const int n = __builtin_amdgcn_readfirstlane((int)(left < 0x7FFFFFFF ? left : 0x7FFFFFFF));
+  const int n = __builtin_amdgcn_readfirstlane((int)(left < 0x80000000ll ? left : 0x80000000ll));
   return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>((uint64_t)hi << 32 | lo), 0, n,
                                            0x00027000);
 }

@@ -37,11 +37,6 @@ constexpr int kF8Group = 4;            // blocks whose scales are loaded togethe
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
-// Where granule 0 of 64-byte rows 4 i .. 4 i + 3 lies: the 16 lanes that an LDS
-// read serves together (rows 0-3 and 12-15 of one granule with rows 4-11 of the
-// next, or the reverse) then touch all banks once.
-__device__ __forceinline__ int f8_swizzle(int i) { return (0x1320 >> (4 * i)) & 3; }
-
 // 4 x FM tiles of 16 x 16 per wave: 256 weight rows (SWIGLU: 128 of either
 // matrix) and FM x 32 tokens per workgroup.
 //

@@ -53,7 +53,7 @@ namespace {
 
 constexpr int kSegTokens = 4;              // most tokens of one segment
 constexpr int kChunk = 128;                // K of one matrix instruction
-constexpr int kLMaxT = 64, kLMaxP = 512, kLMaxE = 1024, kLMaxK = 32;
+constexpr int kLMaxT = 64, kLMaxP = 512, kLMaxE = 1024, kLMaxK = 32, kLMaxH = 8192;
 
 template <typename T>
 __device__ __forceinline__ T dev_load(const T *p) {
@@ -94,6 +94,11 @@ __device__ __forceinline__ bool wait_for(uint32_t *ctl, const uint32_t *p, uint3
 // this wave's stores have reached the coherence point
 __device__ __forceinline__ void stores_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
+// a barrier for LDS alone: global loads stay in flight
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 __device__ __forceinline__ int wave_index() {   // in a scalar register
   return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
 }
@@ -106,14 +111,12 @@ __device__ __forceinline__ uint16_t swiglu_bf16(float g, float u) {
 // activation pieces
 // ---------------------------------------------------------------------------
 
-// Chunks of weights in flight per wave (a body): a segment of one token has
-// the registers for twice as many.
-constexpr int kMaxDepth = 8;
-__host__ __device__ constexpr int ffn_depth(int nt) { return nt == 1 ? kMaxDepth : 4; }
+constexpr int kBody = 4;   // chunks of a gate and an up block in flight per wave
 constexpr int kFfnWaves = 8, kFfnThreads = 64 * kFfnWaves;
-// chunks of a row of H, padded to whole bodies (x is zero there)
+// chunks of a row of H, padded to whole bodies, two at least (x is zero there)
 __host__ __device__ inline int layer_chunks(int H) {
-  return (H + kMaxDepth * kChunk - 1) / (kMaxDepth * kChunk) * kMaxDepth;
+  const int n = (H + kBody * kChunk - 1) / (kBody * kChunk) * kBody;
+  return n > 2 * kBody ? n : 2 * kBody;
 }
 
 // Power of two that brings a row's largest magnitude into [128, 256), and the
@@ -600,15 +603,9 @@ __device__ __forceinline__ f32x4 scales4(uint32_t s) {
   const f32x2_t hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(s, 1.0f, true);
   return f32x4{lo[0], lo[1], hi[0], hi[1]};
 }
-// A lane's codes of chunk c of a row of K elements, and the eight block scales
-// of a chunk.  AL: K is a multiple of 128; otherwise the last chunk's missing
-// elements read valid bytes (the operand is zero there) and scales go two
-// bytes at a time.
-template <bool AL>
-__device__ __forceinline__ u32x4 load_codes(const uint8_t *m, uint32_t row_off, int K, int c, int g) {
-  const uint32_t k = AL ? (uint32_t)(c * 64 + g * 16) : (uint32_t)min(c * 64 + g * 16, K / 2 - 16);
-  return __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(m + (row_off + k)));
-}
+// The eight block scales of chunk c of a row of K elements.  AL: K is a multiple
+// of 128; otherwise the last chunk's missing ones read valid bytes (the operand
+// is zero there) and scales go two bytes at a time.
 template <bool AL>
 __device__ __forceinline__ u32x2 load_scales(const uint8_t *m, uint32_t row_off, int K, int c) {
   if constexpr (AL) {
@@ -631,32 +628,39 @@ __device__ __forceinline__ float group_sum(float v) {
   return v + o;
 }
 
-constexpr int kScaleRow = 8 * kMaxDepth + 8;   // LDS bytes of a row's scales of a body, padded
+constexpr int kScaleRow = 16 * kBody + 16;   // LDS bytes of a row's scales (gate and up) of a body, padded
+// (One variable: between several, the compiler attributes alias scopes, and
+// then makes LDS reads wait for every direct load that may alias.)
+template <int NTMAX, int SW>
 struct FfnLds {
+  // per wave, 8 loads of 16 rows by 64 bytes
+  __attribute__((aligned(1024))) uint8_t ring[kFfnWaves][8 * 1024];
   RouteLds route;
   union {
-    __attribute__((aligned(16))) uint8_t scales[kFfnWaves][2][16 * kScaleRow];
+    __attribute__((aligned(16))) uint8_t scales[kFfnWaves][16 * kScaleRow];
     f32x4 sums[4][kCombine / 4];
   };
   uint32_t item;
+  __attribute__((aligned(16))) uint8_t h_pieces[NTMAX * 2 * SW];
+  __attribute__((aligned(16))) uint8_t x_pieces[NTMAX * 2 * kLMaxH];   // of a segment
 };
 
 // One slice of one segment.  Wave w takes the gate and up rows of the slice's
 // 16-column blocks w, w + 8, .., then every eighth batch of down rows.
 // xp: the tokens' x pieces, [NT][2][HP]; hp: [NT][2][SW].
 //
-// A body is kDepth chunks of a gate and an up block: their codes are loaded
-// two chunks at a time (the two halves of each row's 128-byte lines together)
-// as the previous body's registers fall free; the body's scales come in one
-// or two 8-byte loads per lane (each a chunk's) and go through the wave's own
-// LDS, where a lane finds its four for each chunk.  (One 4-byte load per lane
-// and chunk fetched the scales' lines again and again: 16 rows a load, far
-// more lines in use than the L1 holds.)
-template <int NT, int SW, bool AL>
-__device__ __forceinline__ void segment_slice(const LayerArgs &p, FfnLds &lds, int c, uint8_t *xp,
-                                              uint8_t *hp) {
+// Codes come through a ring of the wave's own in LDS by direct loads of 16 rows
+// by 64 bytes, four lanes to a row (a fragment loaded straight into registers
+// touches a line per lane: the address unit takes 64 cycles or more for it, and
+// four times fewer for this), their granules placed by f8_swizzle.  A chunk's
+// operands are read while the chunk before it is multiplied, and its slot is
+// loaded again at once.  The scales of four chunks come in one 8-byte load per
+// lane and matrix and go through the wave's own LDS, where a lane finds its
+// four for each chunk.
+template <int NT, int NTMAX, int SW, bool AL>
+__device__ __forceinline__ void segment_slice(const LayerArgs &p, FfnLds<NTMAX, SW> &lds, int c) {
+  uint8_t *const xp = lds.x_pieces, *const hp = lds.h_pieces;
   constexpr int NW = kFfnWaves, TW = SW / 16 / NW;   // blocks per wave
-  constexpr int kDepth = ffn_depth(NT), SH = kDepth / 4;   // (SH: chunks' scales a lane loads)
   RouteLds &l = lds.route;
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
   const int lr = lane & 15, g = lane >> 4;
@@ -683,32 +687,37 @@ __device__ __forceinline__ void segment_slice(const LayerArgs &p, FfnLds &lds, i
 #pragma unroll
   for (int t = 0; t < NT; ++t) xs[t] = p.x_shift[pr[t] / p.k];
 
-  const int64_t code_e = (int64_t)p.I * (H / 2), scale_e = (int64_t)p.I * (H / 16);
-  const uint8_t *const gc[2] = {p.codes[0] + e * code_e, p.codes[1] + e * code_e};
+  uint8_t *const ring = lds.ring[wave];
+  const int rd = lr * 64 + (g ^ f8_swizzle(lr >> 2)) * 16;   // this lane's operand in a slot
+  const int drow = lane >> 2, dgran = (lane & 3) ^ f8_swizzle(lane >> 4);   // what it loads
+  const __amdgpu_buffer_rsrc_t wbuf[2] = {
+      f8_buffer(p.codes[0] + e * ((int64_t)p.I * (H / 2)), c0, p.I, H / 2),
+      f8_buffer(p.codes[1] + e * ((int64_t)p.I * (H / 2)), c0, p.I, H / 2)};
+  const int64_t scale_e = (int64_t)p.I * (H / 16);
   const uint8_t *const gs[2] = {p.scales[0] + e * scale_e, p.scales[1] + e * scale_e};
-  uint32_t crow, srow;
-  auto set_row = [&](int i) {   // block i of this wave
-    const uint32_t row = (uint32_t)(c0 + min(16 * (wave + NW * i) + lr, cols - 1));
-    crow = row * ((uint32_t)H / 2);
-    srow = row * ((uint32_t)H / 16);
-  };
-  u32x4 cq[kDepth][2];
-  u32x2 sq[2][SH];
-  auto load = [&](int d, int ch) {   // (chunks past H: the last one again, x is zero)
-#pragma unroll
-    for (int m = 0; m < 2; ++m) cq[d][m] = load_codes<AL>(gc[m], crow, H, min(ch, last_ch), g);
-  };
-  auto load_s = [&](int ch) {
+  // block i of this wave: rows c0 + 16 (wave + NW i) ..; the stream is nch
+  // chunks of each (granules past H and blocks past the last: zero codes)
+  auto row_at = [&](int i) { return i < TW ? min(16 * (wave + NW * i) + drow, cols - 1) : -1; };
+  int row = row_at(0), row_n = row_at(1);
+  auto load = [&](int slot, int ch) {   // (ch >= nch: the next block's)
+    const int r = ch < nch ? row : row_n, k = (ch < nch ? ch : ch - nch) * 64 + dgran * 16;
+    const int off = r >= 0 && k < H / 2 ? r * (H / 2) + k : kOutside;
 #pragma unroll
     for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int q = 0; q < SH; ++q)
-        sq[m][q] = load_scales<AL>(gs[m], srow, H, min(ch + SH * g + q, last_ch));
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          wbuf[m], (lds_ptr_t)(ring + (2 * slot + m) * 1024), 16, off, 0, 0, 2);
   };
-  set_row(0);
-  load_s(0);
+  u32x2 sq[2];
+  auto load_s = [&](int ch) {           // (chunks past H: the last one again, x is zero)
+    const int r = max(ch < nch ? row : row_n, 0), c_ = (ch < nch ? ch : ch - nch) + (lane & 3);
 #pragma unroll
-  for (int d = 0; d < kDepth; ++d) load(d, d);
+    for (int m = 0; m < 2; ++m)
+      sq[m] = load_scales<AL>(gs[m], (uint32_t)(c0 + r) * ((uint32_t)H / 16), H, min(c_, last_ch));
+  };
+  load_s(0);
+  asm volatile("" ::: "memory");
+#pragma unroll
+  for (int d = 0; d < kBody; ++d) load(d, d);
   const float gg = p.glob[0][e], gu = p.glob[1][e], gd = p.glob[2][e];
 
   if (tid < kSegTokens) l.hmax[tid] = 0u;
@@ -719,55 +728,60 @@ __device__ __forceinline__ void segment_slice(const LayerArgs &p, FfnLds &lds, i
       *reinterpret_cast<u32x4 *>(xp + 2 * t * HP + k) = *reinterpret_cast<const u32x4 *>(
           p.x_pieces + (int64_t)(pr[t] / p.k) * 2 * HP + k);
   }
-  __syncthreads();
+  lds_barrier();
 
   // ---- gate and up: h = bf16(silu(gate) up).  After the group sums every
   // lane group has the totals of row lr; group g keeps token g.
   const PieceLane xl = piece_lane(lane, HP);
   const float lane_f = g >= 2 ? 0.0625f : 1.0f;   // the second pieces are 16 times too large
-  uint8_t *const sw = lds.scales[wave][0] + lr * kScaleRow;   // this lane's row (gate; up behind)
-  constexpr int kUp = 16 * kScaleRow;
+  // (read as whole vectors: single words here are taken for possible targets of
+  // the direct loads, and every one would wait for all of those)
+  uint8_t *const sl = lds.scales[wave];
+  auto store_s = [&]() {
+    *reinterpret_cast<u32x4 *>(sl + drow * kScaleRow + 16 * (lane & 3)) =
+        u32x4{sq[0][0], sq[0][1], sq[1][0], sq[1][1]};
+  };
+  u32x4 cq[2][2];      // a chunk's codes (gate, up) and scales: this one's, the next one's
+  u32x4 cs[2];
+  // Reads slot d into set q, then loads chunk ch into it.  (The loads since the
+  // slot's own: three slots', and scales.)
+  auto turn = [&](int d, int q, int ch) {
+    asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+      cq[q][m] = *reinterpret_cast<const u32x4 *>(ring + (2 * d + m) * 1024 + rd);
+    cs[q] = *reinterpret_cast<const u32x4 *>(sl + lr * kScaleRow + 16 * d);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    load(d, ch);
+  };
   float acc[2][NT], hv[TW];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) acc[0][t] = acc[1][t] = 0.0f;
+  store_s();
+  load_s(kBody);
+  turn(0, 0, kBody);
   int i = 0, ch0 = 0;
 #pragma unroll 1
   while (i < TW) {
-    if (ch0 == 0)
 #pragma unroll
-      for (int t = 0; t < NT; ++t) acc[0][t] = acc[1][t] = 0.0f;
-    const bool end = ch0 + kDepth >= nch;   // uniform: the block's last body
-    const int next = end ? 0 : ch0 + kDepth;
-    // (the wave's own LDS: its reads of the last body are done, in order)
-#pragma unroll
-    for (int q = 0; q < SH; ++q) {
-      *reinterpret_cast<u32x2 *>(sw + 8 * (SH * g + q)) = sq[0][q];
-      *reinterpret_cast<u32x2 *>(sw + kUp + 8 * (SH * g + q)) = sq[1][q];
-    }
-    if (end) {
-      set_row(min(i + 1, TW - 1));
-      if (i + 1 == TW) crow = srow = 0u;    // nothing follows: one line, not used
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    load_s(next);
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d) {
-      const f32x4 s0 = scales4(*reinterpret_cast<const uint32_t *>(sw + 8 * d + 4 * (g & 1)));
-      const f32x4 s1 = scales4(*reinterpret_cast<const uint32_t *>(sw + kUp + 8 * d + 4 * (g & 1)));
+    for (int d = 0; d < kBody; ++d) {
+      const int q = d & 1;
+      if (d == kBody - 1) {   // (the body's scales are read)
+        store_s();
+        load_s(ch0 + 2 * kBody);
+      }
+      turn((d + 1) % kBody, q ^ 1, ch0 + d + 1 + kBody);
+      const f32x4 s0 = scales4((g & 1) ? cs[q][1] : cs[q][0]);
+      const f32x4 s1 = scales4((g & 1) ? cs[q][3] : cs[q][2]);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const i32x8 a = piece_operand(xp + 2 * t * HP, xl, ch0 + d);
-        acc[0][t] = chunk_dot(a, cq[d][0], s0, acc[0][t]);
-        acc[1][t] = chunk_dot(a, cq[d][1], s1, acc[1][t]);
-      }
-      // (loaded only once the registers are free: a load issued earlier would
-      // go to others, and the copies back at the loop's end wait for it)
-      __builtin_amdgcn_sched_barrier(0);
-      if (d & 1) {
-        load(d - 1, next + d - 1);
-        load(d, next + d);
-        __builtin_amdgcn_sched_barrier(0);
+        acc[0][t] = chunk_dot(a, cq[q][0], s0, acc[0][t]);
+        acc[1][t] = chunk_dot(a, cq[q][1], s1, acc[1][t]);
       }
     }
-    if (end) {
+    ch0 += kBody;
+    if (ch0 == nch) {   // the block's last body
       float v = 0.0f;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
@@ -775,43 +789,66 @@ __device__ __forceinline__ void segment_slice(const LayerArgs &p, FfnLds &lds, i
         const float U = __builtin_ldexpf(group_sum(acc[1][t] * lane_f), -xs[t]) * gu;
         const float w = bf16_bits_to_f32(swiglu_bf16(G, U));
         v = g == t ? w : v;
+        acc[0][t] = acc[1][t] = 0.0f;
       }
       if (16 * (wave + NW * i) + lr >= cols) v = 0.0f;
 #pragma unroll
       for (int q = 0; q < TW; ++q) hv[q] = q == i ? v : hv[q];
       ++i;
+      row = row_n;
+      row_n = row_at(i + 1);
+      ch0 = 0;
     }
-    ch0 = next;
   }
 
-  // ---- the first down loads, independent of h
-  constexpr int NC = SW / kChunk;           // chunks of a down row's slice
-  constexpr int TILES = 8 / NC;             // 16-row tiles of a batch (8 code loads)
-  constexpr int BROWS = 16 * TILES;
-  const uint8_t *const dc = p.codes[2] + (int64_t)e * H * (p.I / 2);
-  const uint8_t *const ds = p.scales[2] + (int64_t)e * H * (p.I / 16);
-  const int nb = (H + BROWS - 1) / BROWS;
-  const int ic = c0 / kChunk, last_ic = (p.I - 1) / kChunk;   // first chunk of the slice, last of a row
-  u32x4 dq[8];
-  u32x2 dsq[8];
-  auto load_d = [&](int u, int b) {         // load u of batch b: tile u / NC, chunk u % NC
-    // (b < 0: nothing follows; every lane reads the first row, not used)
-    const uint32_t r = b < 0 ? 0u : (uint32_t)min(b * BROWS + (u / NC) * 16 + lr, H - 1);
-    const int ch = min(ic + u % NC, last_ic);
-    dq[u] = load_codes<AL>(dc, __umul24(r, (uint32_t)p.I / 2), p.I, ch, g);
-    dsq[u] = load_scales<AL>(ds, __umul24(r, (uint32_t)p.I / 16), p.I, ch);
-  };
-#pragma unroll
-  for (int u = 0; u < 8; ++u) load_d(u, min(wave, nb - 1));
-
-  // ---- h pieces
   if (g < NT) {
     uint32_t m = 0u;
 #pragma unroll
     for (int q = 0; q < TW; ++q) m = max(m, __float_as_uint(hv[q]) & 0x7FFFFFFFu);
     atomicMax(&l.hmax[g], m);
   }
-  __syncthreads();
+
+  // ---- the first down loads, independent of h
+  constexpr int NC = SW / kChunk;           // chunks of a down row's slice
+  constexpr int TILES = 8 / NC;             // 16-row tiles of a batch (8 code loads)
+  constexpr int BROWS = 16 * TILES;
+  const __amdgpu_buffer_rsrc_t dbuf = f8_buffer(p.codes[2] + (int64_t)e * H * (p.I / 2), 0, H, p.I / 2);
+  const uint8_t *const ds = p.scales[2] + (int64_t)e * H * (p.I / 16);
+  const int nb = (H + BROWS - 1) / BROWS;
+  const int ic = c0 / kChunk, last_ic = (p.I - 1) / kChunk;   // first chunk of the slice, last of a row
+  auto load_d = [&](int u, int b) {         // load u of batch b: tile u / NC, chunk u % NC
+    // (past H, I or the last batch: zero codes)
+    const uint32_t r = (uint32_t)(b * BROWS + (u / NC) * 16 + drow);
+    const uint32_t k = (uint32_t)((ic + u % NC) * 64 + dgran * 16);
+    const uint32_t off = r < (uint32_t)H && k < (uint32_t)p.I / 2 ? r * ((uint32_t)p.I / 2) + k
+                                                                  : (uint32_t)kOutside;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(dbuf, (lds_ptr_t)(ring + u * 1024), 16, (int)off, 0, 0,
+                                             2);
+  };
+  // a batch's scales: lane l has row l's chunks (SW = 128: rows l and 64 + l)
+  u32x2 dsq[2];
+  auto load_ds = [&](int b) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const uint32_t r = (uint32_t)min(b * BROWS + (NC == 2 ? lane : 64 * q + lane), H - 1);
+      dsq[q] = load_scales<AL>(ds, r * ((uint32_t)p.I / 16), p.I, min(ic + (NC == 2 ? q : 0), last_ic));
+    }
+  };
+  auto store_ds = [&]() {                   // [row][chunk], 8 bytes each
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      *reinterpret_cast<u32x2 *>(sl + (NC == 2 ? 16 * lane + 8 * q : 512 * q + 8 * lane)) = dsq[q];
+  };
+  // (the gate and up loads past the end have landed before their slots are
+  // used again)
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  load_ds(wave);
+  asm volatile("" ::: "memory");
+#pragma unroll
+  for (int u = 0; u < 8; ++u) load_d(u, wave);
+
+  // ---- h pieces
+  lds_barrier();
   int hs[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) hs[t] = piece_shift(l.hmax[t]);
@@ -826,13 +863,27 @@ __device__ __forceinline__ void segment_slice(const LayerArgs &p, FfnLds &lds, i
       at[SW] = (uint8_t)piece_lo2(a, 0.0f, h);
     }
   }
-  __syncthreads();
+  lds_barrier();
 
   // ---- down
-  PieceLane hl = piece_lane(lane, SW);
+  const PieceLane hl = piece_lane(lane, SW);
   float wt[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) wt[t] = __builtin_ldexpf(l.wts[pr[t]] * gd * lane_f, -hs[t]);
+  u32x4 dq[2];
+  u32x2 dsc[2];
+  auto turn_d = [&](int u, int q, int b) {   // reads slot u into set q, then loads it for batch b
+    asm volatile("s_waitcnt vmcnt(7)" ::: "memory");
+    dq[q] = *reinterpret_cast<const u32x4 *>(ring + u * 1024 + rd);
+    dsc[q] = *reinterpret_cast<const u32x2 *>(sl + ((u / NC) * 16 + lr) * (8 * NC) + 8 * (u % NC));
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    load_d(u, b);
+  };
+  if (wave < nb) {
+    store_ds();
+    load_ds(wave + NW);
+    turn_d(0, 0, wave + NW);
+  }
 #pragma unroll 1
   for (int b = wave; b < nb; b += NW) {
     float s[NT][TILES];
@@ -840,23 +891,20 @@ __device__ __forceinline__ void segment_slice(const LayerArgs &p, FfnLds &lds, i
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int q = 0; q < TILES; ++q) s[t][q] = 0.0f;
-    const int next = b + NW < nb ? b + NW : -1;
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      // (several tokens' operands are read again for every load: kept, they
-      // would spill)
-      if (NT > 1) asm volatile("" : "+v"(hl.off));
-      const f32x4 sc = scales4((g & 1) ? dsq[u][1] : dsq[u][0]);
+      if (u == 7) {
+        store_ds();
+        load_ds(b + 2 * NW);
+        turn_d(0, 0, b + 2 * NW);
+      } else {
+        turn_d(u + 1, (u + 1) & 1, b + NW);
+      }
+      const f32x4 sc = scales4((g & 1) ? dsc[u & 1][1] : dsc[u & 1][0]);
 #pragma unroll
       for (int t = 0; t < NT; ++t)
-        s[t][u / NC] = chunk_dot(piece_operand(hp + 2 * t * SW, hl, u % NC), dq[u], sc,
+        s[t][u / NC] = chunk_dot(piece_operand(hp + 2 * t * SW, hl, u % NC), dq[u & 1], sc,
                                  s[t][u / NC]);
-      __builtin_amdgcn_sched_barrier(0);
-      if (u & 1) {
-        load_d(u - 1, next);
-        load_d(u, next);
-        __builtin_amdgcn_sched_barrier(0);
-      }
     }
     // four tiles' totals at a time: lane group g ends with tile g
 #pragma unroll
@@ -876,13 +924,12 @@ __device__ __forceinline__ void segment_slice(const LayerArgs &p, FfnLds &lds, i
           dev_store(p.part + ((int64_t)pr[t] * p.n_c + c) * H + r, v0);
       }
   }
+  // (the caller waits for every store, and so for the loads past the end)
 }
 
 template <int SW, bool AL, int NTMAX>
 __global__ __launch_bounds__(kFfnThreads, 2) void layer_ffn_kernel(const LayerArgs p) {
-  extern __shared__ __attribute__((aligned(16))) uint8_t pieces[];   // x pieces of a segment
-  __shared__ FfnLds lds;
-  __shared__ __attribute__((aligned(16))) uint8_t h_pieces[NTMAX * 2 * SW];
+  __shared__ FfnLds<NTMAX, SW> lds;
   RouteLds &l = lds.route;
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
   uint32_t claimed = 0;
@@ -907,11 +954,11 @@ __global__ __launch_bounds__(kFfnThreads, 2) void layer_ffn_kernel(const LayerAr
       if (tid == 0) claimed = dev_add(p.ctl + kCtlClaim, 1u);
       __syncthreads();
       if (NTMAX == 1 || __builtin_amdgcn_readfirstlane(l.pair[1]) < 0)
-        segment_slice<1, SW, AL>(p, lds, c, pieces, h_pieces);
+        segment_slice<1, NTMAX, SW, AL>(p, lds, c);
       else if (NTMAX == 2 || __builtin_amdgcn_readfirstlane(l.pair[2]) < 0)
-        segment_slice<NTMAX == 1 ? 1 : 2, SW, AL>(p, lds, c, pieces, h_pieces);
+        segment_slice<NTMAX == 1 ? 1 : 2, NTMAX, SW, AL>(p, lds, c);
       else
-        segment_slice<NTMAX, SW, AL>(p, lds, c, pieces, h_pieces);
+        segment_slice<NTMAX, NTMAX, SW, AL>(p, lds, c);
       stores_done();
       __syncthreads();
       if (tid < NTMAX && l.pair[tid] >= 0) dev_add(p.ctl + kCtlDone + l.pair[tid] / p.k, 1u);
@@ -982,10 +1029,9 @@ hipError_t launch_layer(const LayerArgs &args, hipStream_t s) {
   // has under one pair per two experts, and the kernel for two keeps more
   // registers free.
   const int nt = a.T == 1 ? 1 : 2 * P <= a.E || a.T == 2 ? 2 : 4;
-  const uint32_t lds = (uint32_t)(nt * 2 * layer_chunks(a.H) * kChunk);
   const bool al = a.H % kChunk == 0 && a.I % kChunk == 0;
 #define NVFP4_LAYER(SW, AL, NT) \
-  launch_kernel((layer_ffn_kernel<SW, AL, NT>), grid, block, lds, s, a)
+  launch_kernel((layer_ffn_kernel<SW, AL, NT>), grid, block, 0, s, a)
 #define NVFP4_LAYER_NT(SW, AL)                \
   do {                                        \
     if (nt == 1) NVFP4_LAYER(SW, AL, 1);      \
