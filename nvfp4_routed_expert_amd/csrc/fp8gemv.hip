@@ -30,7 +30,8 @@ namespace {
 
 constexpr int kGvStreams = 8;          // sums of every 8th block, joined in order
 constexpr int kGvMaxKB = 144;          // scale blocks of K: scales are kept in LDS
-constexpr int kGvXBytes = 20 * 1024;   // x's codes and scales of the QX form, at most
+constexpr int kGvXBytes = 20 * 1024;   // x's codes and scales of the QX form, at most,
+constexpr int kGvXBytesFew = 52 * 1024;   // and with at most a workgroup per CU
 
 // bytes of LDS for M rows of codes (16 bytes apart from a multiple of the
 // banks) and their scales
@@ -42,7 +43,7 @@ __host__ __device__ constexpr int64_t gv_x_bytes(int64_t M, int64_t KB) {
 template <int XT, bool SWIGLU, bool QX, int NW, int D, int XCAP>
 __global__ __launch_bounds__(64 * NW) void f8_gemv_kernel(const F8GemvArgs p) {
 #pragma clang fp contract(off)
-  static_assert(!QX || XT <= 2, "QX: up to 16 rows");
+  static_assert(!QX || XT <= 4, "QX: up to 32 rows");
   constexpr int NT = SWIGLU ? 2 : 1, MT = (XT + 1) / 2;   // tiles of 16 rows of w, x
   constexpr int SLOT = 2048 * NT + (QX ? 0 : 1024 * XT);  // a block: 1 KB for 8 rows
   constexpr int LS = SLOT / 1024;                  // loads of a block
@@ -270,18 +271,26 @@ hipError_t launch_gemv(const F8GemvArgs &a, hipStream_t s) {
 bool f8_gemv_supported(int64_t M, int64_t K) {
   return M >= 1 && M <= 64 && K <= kGvMaxKB * kF8Block;
 }
-bool f8_gemv_quantises(int64_t M, int64_t K) {
-  return f8_gemv_supported(M, K) && M <= 16 &&
-         gv_x_bytes(M, (K + kF8Block - 1) / kF8Block) <= kGvXBytes;
+// A workgroup per CU has the LDS to itself, and a launch costs more than its
+// quantising (24 tokens, 2048 / 1056: 25.7 us with launches for x and h).
+bool f8_gemv_quantises(int64_t M, int64_t N, int64_t K) {
+  const int64_t bytes = gv_x_bytes(M, (K + kF8Block - 1) / kF8Block);
+  return f8_gemv_supported(M, K) &&
+         ((M <= 16 && bytes <= kGvXBytes) ||
+          (M <= 32 && bytes <= kGvXBytesFew && N <= 16 * 256));
 }
 
 hipError_t launch_f8_gemv(bool swiglu, const F8GemvArgs &a, hipStream_t s) {
-  if (!f8_gemv_supported(a.M, a.K) || (!a.xs && !f8_gemv_quantises(a.M, a.K)))
+  if (!f8_gemv_supported(a.M, a.K) || (!a.xs && !f8_gemv_quantises(a.M, a.N, a.K)))
     return hipErrorInvalidValue;
   // LDS decides how many workgroups share a CU and how much is in flight: the
   // least that holds x is taken, and rings of 16 to 36 KB per 4 waves
   if (!a.xs) {
-    const bool small = gv_x_bytes(a.M, (a.K + kF8Block - 1) / kF8Block) <= 10 * 1024;
+    const int64_t bytes = gv_x_bytes(a.M, (a.K + kF8Block - 1) / kF8Block);
+    const bool small = bytes <= 10 * 1024;
+    if (a.M > 16 || bytes > kGvXBytes)
+      return swiglu ? launch_gemv<4, true, true, 8, 2, kGvXBytesFew>(a, s)
+                    : launch_gemv<4, false, true, 8, 4, kGvXBytesFew>(a, s);
     if (swiglu)
       return small ? launch_gemv<2, true, true, 4, 4, 10 * 1024>(a, s)
                    : launch_gemv<2, true, true, 4, 3, kGvXBytes>(a, s);
