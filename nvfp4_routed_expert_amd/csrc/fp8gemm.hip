@@ -88,9 +88,11 @@ __global__ __launch_bounds__(64 * kF8Waves, 2) void f8_gemm_kernel(const F8GemmA
   const int gm = m_tiles - gi * 8 < 8 ? m_tiles - gi * 8 : 8;
   const int nt = gr / gm;
   const int64_t m0 = (int64_t)(gi * 8 + gr - nt * gm) * BM;
-  // (64-bit divisions run on the vector unit: back to scalars)
-  const int b_begin = __builtin_amdgcn_readfirstlane((int)((int64_t)KB * kz / ks));
-  const int nb = __builtin_amdgcn_readfirstlane((int)((int64_t)KB * (kz + 1) / ks)) - b_begin;
+  // parts of whole groups of four blocks (the loop's step)
+  const int KG = (KB + kF8Group - 1) / kF8Group;
+  const int b_begin = __builtin_amdgcn_readfirstlane(kF8Group * (KG * kz / ks));
+  const int b_end = __builtin_amdgcn_readfirstlane(kF8Group * (KG * (kz + 1) / ks));
+  const int nb = (b_end < KB ? b_end : KB) - b_begin;
   const int n0 = nt * TN + wn * (TN / kF8WN);   // first output column of this wave
 
   // ---- loader: a load fills 1 KB, 8 (16) rows of a slot.  Granule g of row r
@@ -474,15 +476,15 @@ hipError_t launch_tile(const F8GemmArgs &a, hipStream_t s) {
 F8Plan f8_gemm_plan(bool swiglu, OutType out, int64_t M, int64_t N, int64_t K) {
   F8Plan best;
   best.exact = !swiglu && out == OutType::F32;
-  const int64_t KB = (K + kF8Block - 1) / kF8Block;
+  const int64_t KG = (K + kF8Group * kF8Block - 1) / (kF8Group * kF8Block);
   const int64_t tn = swiglu ? 128 : 256, nt = (N + tn - 1) / tn;
   double best_us = 0.0;
   for (int bm = 64; bm <= (best.exact ? 64 : 192); bm += 64) {
     const double block_us = best.exact ? 1.2 : bm == 64 ? 0.62 : bm == 128 ? 0.97 : 1.45;
     const int64_t tiles = nt * ((M + bm - 1) / bm);
-    for (int64_t ks = 1; ks <= 16 && (ks == 1 || ks * 4 <= KB); ++ks) {
+    for (int64_t ks = 1; ks <= 16 && ks <= KG; ++ks) {
       const int64_t rounds = (tiles * ks + kF8CUs - 1) / kF8CUs;
-      double us = rounds * ((double)((KB + ks - 1) / ks) * block_us + 11.0);
+      double us = rounds * ((double)(kF8Group * ((KG + ks - 1) / ks)) * block_us + 11.0);
       if (ks > 1) us += 4.0 + (double)ks * M * N * (swiglu ? 16.0 : 8.0) / 4e6;
       if (best_us == 0.0 || us < best_us) {
         best_us = us;
