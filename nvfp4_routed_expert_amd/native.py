@@ -573,6 +573,14 @@ def _stream_of(dev):
     return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
+def _scratch(nbytes, dev, workspace):
+    """(keep-alive, address, bytes) of a workspace of nbytes; none for 0."""
+    if workspace is None and nbytes == 0:
+        return None, None, 0
+    ws = _workspace(nbytes, dev, workspace)
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def _expect(name, t, shape, dtype):
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
@@ -589,7 +597,8 @@ def _fp8_matrix(name, codes, scales):
     if codes.dim() != 2:
         raise ValueError(f"{name} codes must be [rows, cols], got {tuple(codes.shape)}")
     n, k = codes.shape
-    _expect(f"{name} codes", codes, (n, k), torch.uint8)
+    if codes.dtype is not torch.uint8:
+        raise TypeError(f"{name} codes is {codes.dtype}, expected torch.uint8")
     _expect(f"{name} scales", scales, (_fp8_blocks(n), _fp8_blocks(k)), torch.float32)
     return Fp8Matrix(codes.data_ptr(), scales.data_ptr(), n, k)
 
@@ -638,14 +647,17 @@ def fp8_block_linear(x, codes, scales, x_scales=None, out_dtype=torch.bfloat16, 
         _expect("x_scales", x_scales, (M, _fp8_blocks(K)), torch.float32)
     dev = _device_of(x, rows=x, codes=codes, scales=scales, x_scales=x_scales, out=out,
                      workspace=workspace)
-    y = out if out is not None else torch.empty((M, m.rows), dtype=out_dtype, device=dev)
-    _expect("out", y, (M, m.rows), y.dtype)
+    if out is None:
+        y = torch.empty((M, m.rows), dtype=out_dtype, device=dev)
+    else:
+        _expect("out", out, (M, m.rows), out.dtype)
+        y = out
     L = lib()
+    ws = _scratch(L.fp8_block_linear_workspace_size(M, m.rows, K, x_scales is not None), dev,
+                  workspace)
     with _on(dev):
-        ws = _workspace(L.fp8_block_linear_workspace_size(M, m.rows, K, x_scales is not None), dev,
-                        workspace)
-        _check(L.fp8_block_linear(_ptr(x), _ptr(x_scales), M, ctypes.byref(m), _ptr(y),
-                                  _dt(y.dtype), _ptr(ws), ws.numel() * ws.element_size(),
+        _check(L.fp8_block_linear(x.data_ptr(), None if x_scales is None else x_scales.data_ptr(),
+                                  M, ctypes.byref(m), y.data_ptr(), _dt(y.dtype), ws[1], ws[2],
                                   _stream_of(dev)))
     return y
 
@@ -665,10 +677,10 @@ def fp8_block_mlp(x, gate, up, down, out_dtype=torch.bfloat16, workspace=None, o
     y = out if out is not None else torch.empty((T, H), dtype=out_dtype, device=dev)
     _expect("out", y, (T, H), y.dtype)
     L = lib()
+    ws = _scratch(L.fp8_block_mlp_workspace_size(T, H, I), dev, workspace)
     with _on(dev):
-        ws = _workspace(L.fp8_block_mlp_workspace_size(T, H, I), dev, workspace)
-        _check(L.fp8_block_mlp(_ptr(x), T, *(ctypes.byref(m) for m in mats.values()), _ptr(y),
-                               _dt(y.dtype), _ptr(ws), ws.numel() * ws.element_size(), _stream_of(dev)))
+        _check(L.fp8_block_mlp(x.data_ptr(), T, *(ctypes.byref(m) for m in mats.values()),
+                               y.data_ptr(), _dt(y.dtype), ws[1], ws[2], _stream_of(dev)))
     return y
 
 
