@@ -54,6 +54,7 @@ namespace {
 constexpr int kSegTokens = 4;              // most tokens of one segment
 constexpr int kChunk = 128;                // K of one matrix instruction
 constexpr int kLMaxT = 64, kLMaxP = 512, kLMaxE = 1024, kLMaxK = 32, kLMaxH = 8192;
+constexpr int kLMaxH4 = 4096;   // of segments of four tokens
 
 template <typename T>
 __device__ __forceinline__ T dev_load(const T *p) {
@@ -111,7 +112,8 @@ __device__ __forceinline__ uint16_t swiglu_bf16(float g, float u) {
 // activation pieces
 // ---------------------------------------------------------------------------
 
-constexpr int kBody = 4;   // chunks of a gate and an up block in flight per wave
+constexpr int kBody = 4;   // chunks whose scales are loaded together
+constexpr int kRing = 3, kPair = 4096;   // pairs of chunks in flight per wave; bytes of one (gate, up)
 constexpr int kFfnWaves = 8, kFfnThreads = 64 * kFfnWaves;
 // chunks of a row of H, padded to whole bodies, two at least (x is zero there)
 __host__ __device__ inline int layer_chunks(int H) {
@@ -633,8 +635,8 @@ constexpr int kScaleRow = 16 * kBody + 16;   // LDS bytes of a row's scales (gat
 // then makes LDS reads wait for every direct load that may alias.)
 template <int NTMAX, int SW>
 struct FfnLds {
-  // per wave, 8 loads of 16 rows by 64 bytes
-  __attribute__((aligned(1024))) uint8_t ring[kFfnWaves][8 * 1024];
+  // per wave, three pairs of chunks of a gate and an up block
+  __attribute__((aligned(1024))) uint8_t ring[kFfnWaves][kRing * kPair];
   RouteLds route;
   union {
     __attribute__((aligned(16))) uint8_t scales[kFfnWaves][16 * kScaleRow];
@@ -642,21 +644,21 @@ struct FfnLds {
   };
   uint32_t item;
   __attribute__((aligned(16))) uint8_t h_pieces[NTMAX * 2 * SW];
-  __attribute__((aligned(16))) uint8_t x_pieces[NTMAX * 2 * kLMaxH];   // of a segment
+  __attribute__((aligned(16))) uint8_t x_pieces[NTMAX == 4 ? 8 * kLMaxH4 : NTMAX * 2 * kLMaxH];   // of a segment
 };
 
 // One slice of one segment.  Wave w takes the gate and up rows of the slice's
 // 16-column blocks w, w + 8, .., then every eighth batch of down rows.
 // xp: the tokens' x pieces, [NT][2][HP]; hp: [NT][2][SW].
 //
-// Codes come through a ring of the wave's own in LDS by direct loads of 16 rows
-// by 64 bytes, four lanes to a row (a fragment loaded straight into registers
-// touches a line per lane: the address unit takes 64 cycles or more for it, and
-// four times fewer for this), their granules placed by f8_swizzle.  A chunk's
-// operands are read while the chunk before it is multiplied, and its slot is
-// loaded again at once.  The scales of four chunks come in one 8-byte load per
-// lane and matrix and go through the wave's own LDS, where a lane finds its
-// four for each chunk.
+// Codes come through a ring of the wave's own in LDS by direct loads of 8 rows
+// by 128 bytes (two chunks), whole cache lines; a fragment loaded straight into
+// registers touches a line per lane, which takes the address unit 64 cycles or
+// more instead of 16.  Granules are XOR-swizzled by the row.  A chunk's operands
+// are read while the chunk before it is multiplied, and a pair of chunks' slot
+// is loaded again once both are read.  The scales of four chunks come in one
+// 8-byte load per lane and matrix and go through the wave's own LDS, where a
+// lane finds its four for each chunk.
 template <int NT, int NTMAX, int SW, bool AL>
 __device__ __forceinline__ void segment_slice(const LayerArgs &p, FfnLds<NTMAX, SW> &lds, int c) {
   uint8_t *const xp = lds.x_pieces, *const hp = lds.h_pieces;
@@ -688,8 +690,10 @@ __device__ __forceinline__ void segment_slice(const LayerArgs &p, FfnLds<NTMAX, 
   for (int t = 0; t < NT; ++t) xs[t] = p.x_shift[pr[t] / p.k];
 
   uint8_t *const ring = lds.ring[wave];
-  const int rd = lr * 64 + (g ^ f8_swizzle(lr >> 2)) * 16;   // this lane's operand in a slot
-  const int drow = lane >> 2, dgran = (lane & 3) ^ f8_swizzle(lane >> 4);   // what it loads
+  // this lane's operands of a pair, and what it loads (rows lrow and 8 + lrow)
+  const int rd0 = lr * 128 + (g ^ (lr & 7)) * 16, rd1 = lr * 128 + ((4 + g) ^ (lr & 7)) * 16;
+  const int lrow = lane >> 3, lgran = (lane & 7) ^ lrow;
+  const int drow = lane >> 2;   // the row whose scales it loads
   const __amdgpu_buffer_rsrc_t wbuf[2] = {
       f8_buffer(p.codes[0] + e * ((int64_t)p.I * (H / 2)), c0, p.I, H / 2),
       f8_buffer(p.codes[1] + e * ((int64_t)p.I * (H / 2)), c0, p.I, H / 2)};
@@ -697,19 +701,27 @@ __device__ __forceinline__ void segment_slice(const LayerArgs &p, FfnLds<NTMAX, 
   const uint8_t *const gs[2] = {p.scales[0] + e * scale_e, p.scales[1] + e * scale_e};
   // block i of this wave: rows c0 + 16 (wave + NW i) ..; the stream is nch
   // chunks of each (granules past H and blocks past the last: zero codes)
-  auto row_at = [&](int i) { return i < TW ? min(16 * (wave + NW * i) + drow, cols - 1) : -1; };
-  int row = row_at(0), row_n = row_at(1);
-  auto load = [&](int slot, int ch) {   // (ch >= nch: the next block's)
-    const int r = ch < nch ? row : row_n, k = (ch < nch ? ch : ch - nch) * 64 + dgran * 16;
-    const int off = r >= 0 && k < H / 2 ? r * (H / 2) + k : kOutside;
+  // row r of block i (no block: outside the matrix)
+  auto row_at = [&](int i, int r) {
+    return i < TW ? min(16 * (wave + NW * i) + r, cols - 1) : INT32_MIN / 2;
+  };
+  int blk = 0;   // the block multiplied
+  auto load = [&](int slot, int ch) {   // chunks ch, ch + 1 (ch >= nch: the next block's)
+    const int i = ch < nch ? blk : blk + 1, k = (ch < nch ? ch : ch - nch) * 64 + lgran * 16;
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          wbuf[m], (lds_ptr_t)(ring + (2 * slot + m) * 1024), 16, off, 0, 0, 2);
+    for (int h = 0; h < 2; ++h) {
+      const int r = row_at(i, 8 * h + lrow);
+      const int off = r >= 0 && k < H / 2 ? r * (H / 2) + k : kOutside;
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            wbuf[m], (lds_ptr_t)(ring + slot * kPair + m * (kPair / 2) + h * 1024), 16, off, 0, 0, 2);
+    }
   };
   u32x2 sq[2];
   auto load_s = [&](int ch) {           // (chunks past H: the last one again, x is zero)
-    const int r = max(ch < nch ? row : row_n, 0), c_ = (ch < nch ? ch : ch - nch) + (lane & 3);
+    const int r = max(row_at(ch < nch ? blk : blk + 1, drow), 0);
+    const int c_ = (ch < nch ? ch : ch - nch) + (lane & 3);
 #pragma unroll
     for (int m = 0; m < 2; ++m)
       sq[m] = load_scales<AL>(gs[m], (uint32_t)(c0 + r) * ((uint32_t)H / 16), H, min(c_, last_ch));
@@ -717,7 +729,7 @@ __device__ __forceinline__ void segment_slice(const LayerArgs &p, FfnLds<NTMAX, 
   load_s(0);
   asm volatile("" ::: "memory");
 #pragma unroll
-  for (int d = 0; d < kBody; ++d) load(d, d);
+  for (int d = 0; d < kRing; ++d) load(d, 2 * d);
   const float gg = p.glob[0][e], gu = p.glob[1][e], gd = p.glob[2][e];
 
   if (tid < kSegTokens) l.hmax[tid] = 0u;
@@ -743,34 +755,41 @@ __device__ __forceinline__ void segment_slice(const LayerArgs &p, FfnLds<NTMAX, 
   };
   u32x4 cq[2][2];      // a chunk's codes (gate, up) and scales: this one's, the next one's
   u32x4 cs[2];
-  // Reads slot d into set q, then loads chunk ch into it.  (The loads since the
-  // slot's own: three slots', and scales.)
-  auto turn = [&](int d, int q, int ch) {
-    asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
+  // Reads chunk c (0, 1) of a pair, the body's chunk d, into set q.  The first
+  // waits for the pair (newer: two pairs', and scales); after the second, the
+  // slot takes chunks ch, ch + 1.
+  auto turn = [&](int slot, int c, int d, int q, int ch) {
+    if (c == 0) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+    const uint8_t *from = ring + slot * kPair + (c ? rd1 : rd0);
 #pragma unroll
     for (int m = 0; m < 2; ++m)
-      cq[q][m] = *reinterpret_cast<const u32x4 *>(ring + (2 * d + m) * 1024 + rd);
+      cq[q][m] = *reinterpret_cast<const u32x4 *>(from + m * (kPair / 2));
     cs[q] = *reinterpret_cast<const u32x4 *>(sl + lr * kScaleRow + 16 * d);
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    load(d, ch);
+    if (c == 1) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      load(slot, ch);
+    }
   };
   float acc[2][NT], hv[TW];
 #pragma unroll
   for (int t = 0; t < NT; ++t) acc[0][t] = acc[1][t] = 0.0f;
   store_s();
   load_s(kBody);
-  turn(0, 0, kBody);
-  int i = 0, ch0 = 0;
+  turn(0, 0, 0, 0, 0);
+  int ch0 = 0, sa = 0, sb = 1, sc = 2;   // the body's first chunk; slots of its pairs and the next
 #pragma unroll 1
-  while (i < TW) {
+  while (blk < TW) {
 #pragma unroll
     for (int d = 0; d < kBody; ++d) {
       const int q = d & 1;
-      if (d == kBody - 1) {   // (the body's scales are read)
+      if (d == 0) turn(sa, 1, 1, 1, ch0 + 2 * kRing);
+      if (d == 1) turn(sb, 0, 2, 0, 0);
+      if (d == 2) turn(sb, 1, 3, 1, ch0 + 2 + 2 * kRing);
+      if (d == 3) {   // (the body's scales are read)
         store_s();
         load_s(ch0 + 2 * kBody);
+        turn(sc, 0, 0, 0, 0);
       }
-      turn((d + 1) % kBody, q ^ 1, ch0 + d + 1 + kBody);
       const f32x4 s0 = scales4((g & 1) ? cs[q][1] : cs[q][0]);
       const f32x4 s1 = scales4((g & 1) ? cs[q][3] : cs[q][2]);
 #pragma unroll
@@ -781,6 +800,10 @@ __device__ __forceinline__ void segment_slice(const LayerArgs &p, FfnLds<NTMAX, 
       }
     }
     ch0 += kBody;
+    const int last_a = sa;
+    sa = sc;
+    sc = sb;
+    sb = last_a;
     if (ch0 == nch) {   // the block's last body
       float v = 0.0f;
 #pragma unroll
@@ -791,12 +814,10 @@ __device__ __forceinline__ void segment_slice(const LayerArgs &p, FfnLds<NTMAX, 
         v = g == t ? w : v;
         acc[0][t] = acc[1][t] = 0.0f;
       }
-      if (16 * (wave + NW * i) + lr >= cols) v = 0.0f;
+      if (16 * (wave + NW * blk) + lr >= cols) v = 0.0f;
 #pragma unroll
-      for (int q = 0; q < TW; ++q) hv[q] = q == i ? v : hv[q];
-      ++i;
-      row = row_n;
-      row_n = row_at(i + 1);
+      for (int q = 0; q < TW; ++q) hv[q] = q == blk ? v : hv[q];
+      ++blk;
       ch0 = 0;
     }
   }
@@ -816,14 +837,22 @@ __device__ __forceinline__ void segment_slice(const LayerArgs &p, FfnLds<NTMAX, 
   const uint8_t *const ds = p.scales[2] + (int64_t)e * H * (p.I / 16);
   const int nb = (H + BROWS - 1) / BROWS;
   const int ic = c0 / kChunk, last_ic = (p.I - 1) / kChunk;   // first chunk of the slice, last of a row
-  auto load_d = [&](int u, int b) {         // load u of batch b: tile u / NC, chunk u % NC
-    // (past H, I or the last batch: zero codes)
-    const uint32_t r = (uint32_t)(b * BROWS + (u / NC) * 16 + drow);
-    const uint32_t k = (uint32_t)((ic + u % NC) * 64 + dgran * 16);
-    const uint32_t off = r < (uint32_t)H && k < (uint32_t)p.I / 2 ? r * ((uint32_t)p.I / 2) + k
-                                                                  : (uint32_t)kOutside;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(dbuf, (lds_ptr_t)(ring + u * 1024), 16, (int)off, 0, 0,
-                                             2);
+  // (past H, I or the last batch: zero codes)
+  auto load_1k = [&](int to, int row, int k) {
+    const uint32_t r = (uint32_t)row, off = r < (uint32_t)H && k < p.I / 2
+                                                ? r * ((uint32_t)p.I / 2) + (uint32_t)k
+                                                : (uint32_t)kOutside;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(dbuf, (lds_ptr_t)(ring + to), 16, (int)off, 0, 0, 2);
+  };
+  auto load_d = [&](int q, int b) {         // tile q of batch b
+    const int r = b * BROWS + q * 16;
+    if constexpr (NC == 2) {                // 128 bytes a row
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        load_1k(q * 2048 + h * 1024, r + 8 * h + lrow, ic * 64 + lgran * 16);
+    } else {                                // 64 bytes a row
+      load_1k(q * 1024, r + drow, ic * 64 + ((lane & 3) ^ f8_swizzle(lane >> 4)) * 16);
+    }
   };
   // a batch's scales: lane l has row l's chunks (SW = 128: rows l and 64 + l)
   u32x2 dsq[2];
@@ -845,7 +874,7 @@ __device__ __forceinline__ void segment_slice(const LayerArgs &p, FfnLds<NTMAX, 
   load_ds(wave);
   asm volatile("" ::: "memory");
 #pragma unroll
-  for (int u = 0; u < 8; ++u) load_d(u, wave);
+  for (int q = 0; q < TILES; ++q) load_d(q, wave);
 
   // ---- h pieces
   lds_barrier();
@@ -872,12 +901,19 @@ __device__ __forceinline__ void segment_slice(const LayerArgs &p, FfnLds<NTMAX, 
   for (int t = 0; t < NT; ++t) wt[t] = __builtin_ldexpf(l.wts[pr[t]] * gd * lane_f, -hs[t]);
   u32x4 dq[2];
   u32x2 dsc[2];
-  auto turn_d = [&](int u, int q, int b) {   // reads slot u into set q, then loads it for batch b
-    asm volatile("s_waitcnt vmcnt(7)" ::: "memory");
-    dq[q] = *reinterpret_cast<const u32x4 *>(ring + u * 1024 + rd);
-    dsc[q] = *reinterpret_cast<const u32x2 *>(sl + ((u / NC) * 16 + lr) * (8 * NC) + 8 * (u % NC));
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    load_d(u, b);
+  const int rd = lr * 64 + (g ^ f8_swizzle(lr >> 2)) * 16;   // (64 bytes a row)
+  // reads tile u / NC, chunk u % NC into set q; the tile's last read loads it
+  // for batch b
+  auto turn_d = [&](int u, int q, int b) {
+    const int tile = u / NC, c = u % NC;
+    if (c == 0) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(8 - NC) : "memory");
+    dq[q] = *reinterpret_cast<const u32x4 *>(ring + (NC == 2 ? tile * 2048 + (c ? rd1 : rd0)
+                                                             : tile * 1024 + rd));
+    dsc[q] = *reinterpret_cast<const u32x2 *>(sl + (tile * 16 + lr) * (8 * NC) + 8 * c);
+    if (c == NC - 1) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      load_d(tile, b);
+    }
   };
   if (wave < nb) {
     store_ds();
@@ -896,7 +932,7 @@ __device__ __forceinline__ void segment_slice(const LayerArgs &p, FfnLds<NTMAX, 
       if (u == 7) {
         store_ds();
         load_ds(b + 2 * NW);
-        turn_d(0, 0, b + 2 * NW);
+        turn_d(0, 0, b + 2 * NW);   // (tile 0 of the next batch)
       } else {
         turn_d(u + 1, (u + 1) & 1, b + NW);
       }
@@ -1028,7 +1064,7 @@ hipError_t launch_layer(const LayerArgs &args, hipStream_t s) {
   // Most tokens of a segment: few experts have more than two where the batch
   // has under one pair per two experts, and the kernel for two keeps more
   // registers free.
-  const int nt = a.T == 1 ? 1 : 2 * P <= a.E || a.T == 2 ? 2 : 4;
+  const int nt = a.T == 1 ? 1 : 2 * P <= a.E || a.T == 2 || a.H > kLMaxH4 ? 2 : 4;
   const bool al = a.H % kChunk == 0 && a.I % kChunk == 0;
 #define NVFP4_LAYER(SW, AL, NT) \
   launch_kernel((layer_ffn_kernel<SW, AL, NT>), grid, block, 0, s, a)
