@@ -292,8 +292,8 @@ Fp8LinearWs carve_fp8_linear(Carver &c, int64_t M, int64_t N, int64_t K, bool qu
   return w;
 }
 struct Fp8MlpWs {
-  bool few;             // both products in the form for a few rows
-  bool own_x, own_h;    // x, h quantised by a launch of their own (h: or by the product)
+  bool few_up, few_down;   // products in the form for a few rows
+  bool own_x, own_h;       // x, h quantised by a launch of their own (h: or by the product)
   F8Plan up_plan, down_plan;
   uint8_t *xq, *hq;
   uint16_t *h;    // bf16 h (few rows)
@@ -302,24 +302,28 @@ struct Fp8MlpWs {
 };
 Fp8MlpWs carve_fp8_mlp(Carver &c, int64_t T, int64_t H, int64_t I, OutType out) {
   Fp8MlpWs w = {};
-  w.few = f8_gemv_supported(T, H) && f8_gemv_supported(T, I);
-  w.own_x = !w.few || !f8_gemv_quantises(T, I, H);
-  w.own_h = !w.few || !f8_gemv_quantises(T, H, I);
+  w.few_up = f8_gemv_supported(T, H);
+  w.few_down = f8_gemv_supported(T, I);
+  w.own_x = !w.few_up || !f8_gemv_quantises(T, I, H);
+  w.own_h = !w.few_up || !w.few_down || !f8_gemv_quantises(T, H, I);
   w.xq = c.take<uint8_t>(w.own_x ? (size_t)(T * H) : 0);
   w.xs = c.take<float>(w.own_x ? (size_t)(T * ((H + 127) / 128)) : 0);
-  w.h = c.take<uint16_t>(w.few ? (size_t)(T * I) : 0);
+  w.h = c.take<uint16_t>(w.few_up ? (size_t)(T * I) : 0);
   w.hq = c.take<uint8_t>(w.own_h ? (size_t)(T * I) : 0);
   w.hs = c.take<float>(w.own_h ? (size_t)(T * ((I + 127) / 128)) : 0);
-  if (!w.few) {
+  size_t n = 0;
+  if (!w.few_up) {
     w.up_plan = f8_gemm_plan(true, OutType::BF16, T, I, H);
+    n = w.up_plan.partial_floats;
+  }
+  if (!w.few_down) {
     w.down_plan = f8_gemm_plan(false, out, T, H, I);
     const F8Plan other = f8_gemm_plan(
         false, out == OutType::F32 ? OutType::BF16 : OutType::F32, T, H, I);
-    size_t n = w.up_plan.partial_floats;
     if (w.down_plan.partial_floats > n) n = w.down_plan.partial_floats;
     if (other.partial_floats > n) n = other.partial_floats;
-    w.split = c.take<float>(n);
   }
+  w.split = c.take<float>(n);
   return w;
 }
 OutType out_type(nvfp4_dtype t) { return t == NVFP4_DT_F32 ? OutType::F32 : OutType::BF16; }
@@ -1537,7 +1541,7 @@ nvfp4_status fp8_block_mlp(const void *x, int64_t T, const fp8_matrix *w_gate,
   const Fp8MlpWs ws = carve_fp8_mlp(c, T, H, I, out_type(y_dtype));
   if (ws.own_x)
     LAUNCH(launch_f8_quantize(x, InType::BF16, T, H, H, 1, ws.xq, ws.xs, stream), "fp8 quantize");
-  if (ws.few) {
+  if (ws.few_up) {
     const F8GemvArgs g = {ws.own_x ? ws.xq : x, ws.own_x ? ws.xs : nullptr, (int)T,
                           {w_gate->codes, w_up->codes}, {w_gate->scales, w_up->scales},
                           (int)I, (int)H, ws.h, OutType::BF16};
@@ -1545,26 +1549,29 @@ nvfp4_status fp8_block_mlp(const void *x, int64_t T, const fp8_matrix *w_gate,
     if (ws.own_h)
       LAUNCH(launch_f8_quantize(ws.h, InType::BF16, T, I, I, 1, ws.hq, ws.hs, stream),
              "fp8 quantize");
+  } else {
+    F8GemmArgs a = {};
+    a.x = ws.xq;
+    a.xs = ws.xs;
+    a.M = T;
+    a.w[0] = w_gate->codes;
+    a.ws[0] = w_gate->scales;
+    a.w[1] = w_up->codes;
+    a.ws[1] = w_up->scales;
+    a.N = (int)I;
+    a.K = (int)H;
+    a.hq = ws.hq;
+    a.hs = ws.hs;
+    a.partial = ws.split;
+    LAUNCH(launch_f8_gemm(true, a, ws.up_plan, stream), "fp8 gate/up");
+  }
+  if (ws.few_down) {
     const F8GemvArgs d = {ws.own_h ? static_cast<const void *>(ws.hq) : ws.h,
                           ws.own_h ? ws.hs : nullptr, (int)T, {w_down->codes, nullptr},
                           {w_down->scales, nullptr}, (int)H, (int)I, y, out_type(y_dtype)};
     LAUNCH(launch_f8_gemv(false, d, stream), "fp8 down");
     return NVFP4_OK;
   }
-  F8GemmArgs a = {};
-  a.x = ws.xq;
-  a.xs = ws.xs;
-  a.M = T;
-  a.w[0] = w_gate->codes;
-  a.ws[0] = w_gate->scales;
-  a.w[1] = w_up->codes;
-  a.ws[1] = w_up->scales;
-  a.N = (int)I;
-  a.K = (int)H;
-  a.hq = ws.hq;
-  a.hs = ws.hs;
-  a.partial = ws.split;
-  LAUNCH(launch_f8_gemm(true, a, ws.up_plan, stream), "fp8 gate/up");
   F8GemmArgs d = {};
   d.x = ws.hq;
   d.xs = ws.hs;

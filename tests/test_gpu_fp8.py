@@ -316,3 +316,62 @@ def test_linear_and_mlp_in_a_graph(T):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want_y) and torch.equal(z, want_z)
+
+
+# ---- where the forms change ---------------------------------------------------------
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 33, 18432), (4, 70, 4864), (4, 70, 5120), (9, 30, 18432),
+                                   (24, 4096, 1024), (24, 4112, 1024), (32, 48, 1536),
+                                   (32, 48, 1568), (64, 31, 18432), (65, 257, 160),
+                                   (129, 1003, 640), (193, 515, 4224), (385, 130, 512)])
+def test_linear_at_the_rules(M, N, K):
+    """Either side of the rules: x quantised inside (small, large, a workgroup
+    per CU) or by a launch, few rows or a batch, odd columns, K parts that are
+    not whole groups of blocks."""
+    test_linear(M, N, K)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 40, 18464), (33, 130, 18560)])
+def test_linear_of_few_rows_with_a_long_k(M, N, K):
+    """Past the few-row form's K the batch form runs, exact for either type."""
+    test_linear(M, N, K)
+
+
+@pytest.mark.parametrize("T,H,I", [(2, 64, 18464), (2, 18464, 32), (8, 1024, 1056), (17, 2048, 96),
+                                   (32, 1568, 160)])
+def test_mlp_at_the_rules(T, H, I):
+    test_mlp(T, H, I)
+
+
+def test_row_of_infinite_scale_stays_alone():
+    """A token with non-finite values: its own row is not finite, the others
+    are as without it."""
+    say("linear infinite row")
+    for M in (3, 20, 100):
+        w, ws = weight(96, 640, 5)
+        x = acts(M, 640, M).to(DEV)
+        clean = native.fp8_block_linear(x, w, ws, out_dtype=torch.float32)
+        x[1, 7] = float("inf")
+        y = native.fp8_block_linear(x, w, ws, out_dtype=torch.float32)
+        keep = torch.ones(M, dtype=torch.bool, device=DEV)
+        keep[1] = False
+        assert torch.equal(y[keep], clean[keep])
+        assert not torch.isfinite(y[1]).any()
+
+
+def test_linear_on_two_streams_at_once():
+    say("linear two streams")
+    w, ws = weight(1000, 2080, 8)
+    xs_ = [acts(77, 2080, s).to(DEV) for s in (1, 2)]
+    want = [native.fp8_block_linear(x, w, ws, out_dtype=torch.float32) for x in xs_]
+    streams = [torch.cuda.Stream() for _ in xs_]
+    got = []
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, x in zip(streams, xs_):
+            with torch.cuda.stream(s):
+                got.append(native.fp8_block_linear(x, w, ws, out_dtype=torch.float32))
+    torch.cuda.synchronize()
+    for i, y in enumerate(got):
+        assert torch.equal(y, want[i % 2])

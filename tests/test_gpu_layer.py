@@ -266,3 +266,14 @@ def test_decode_block_with_fp8_projections():
     codes, s = native.fp8_block_quantize(x0)
     assert torch.equal(a, native.fp8_block_linear(codes, *ws[0], x_scales=s))
     assert torch.isfinite(z.float()).all() and z.shape == (T, H)
+
+
+@pytest.mark.parametrize("T,H,I,E,k,Is,gate,bias,renorm",
+                         [(9, 8192, 160, 3, 2, 0, False, False, True),
+                          (12, 4096, 288, 3, 2, 64, True, False, True),
+                          (12, 4128, 288, 3, 2, 64, True, False, True),
+                          (5, 544, 512, 4, 2, 0, False, True, True),
+                          (64, 1024, 1024, 2, 1, 0, False, False, True)])
+def test_layer_of_crowded_experts(T, H, I, E, k, Is, gate, bias, renorm):
+    """Several segments per expert, of up to four tokens or (H > 4096) two."""
+    test_layer(T, H, I, E, k, Is, gate, bias, renorm)
