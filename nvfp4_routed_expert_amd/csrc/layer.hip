@@ -149,13 +149,12 @@ __device__ __forceinline__ uint32_t piece_lo2(float a, float b, uint32_t hi) {
 
 // A tile of 16 bf16 weight rows (NM matrices) against every token:
 // v_mfma_f32_16x16x32_bf16 (exact products, fp32 sums).  The waves take the
-// 32-wide steps of K in turn, kTileBatch of them in flight; acc[m][j]: rows
+// 32-wide steps of K in turn, B of them in flight; acc[m][j]: rows
 // 4 lg + i of matrix m, token 16 j + lr.
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-constexpr int kTileBatch = 4;
 constexpr int kTT = kLMaxT / 16;
 
-template <int NM>
+template <int NM, int B>
 __device__ __forceinline__ void tile_dot(const uint16_t *const (&w)[NM], const uint16_t *x,
                                          int64_t x_ld, int T, int K, int wave, int waves,
                                          f32x4 (&acc)[NM][kTT]) {
@@ -169,10 +168,10 @@ __device__ __forceinline__ void tile_dot(const uint16_t *const (&w)[NM], const u
   const uint16_t *xr[kTT];
 #pragma unroll
   for (int j = 0; j < kTT; ++j) xr[j] = x + (int64_t)min(j * 16 + lr, T - 1) * x_ld + 8 * lg;
-  for (int s0 = wave; s0 < steps; s0 += waves * kTileBatch) {
-    u32x4 wv[NM][kTileBatch];
+  for (int s0 = wave; s0 < steps; s0 += waves * B) {
+    u32x4 wv[NM][B];
 #pragma unroll
-    for (int b = 0; b < kTileBatch; ++b) {
+    for (int b = 0; b < B; ++b) {
       const int s = s0 + b * waves;
 #pragma unroll
       for (int m = 0; m < NM; ++m)
@@ -181,12 +180,12 @@ __device__ __forceinline__ void tile_dot(const uint16_t *const (&w)[NM], const u
 #pragma unroll
     for (int j = 0; j < kTT; ++j) {
       if (j >= tt) break;   // uniform
-      u32x4 xv[kTileBatch];
+      u32x4 xv[B];
 #pragma unroll
-      for (int b = 0; b < kTileBatch; ++b)
+      for (int b = 0; b < B; ++b)
         xv[b] = *reinterpret_cast<const u32x4 *>(xr[j] + 32 * min(s0 + b * waves, steps - 1));
 #pragma unroll
-      for (int b = 0; b < kTileBatch; ++b) {
+      for (int b = 0; b < B; ++b) {
         if (s0 + b * waves >= steps) break;   // uniform
 #pragma unroll
         for (int m = 0; m < NM; ++m)
@@ -255,7 +254,8 @@ __global__ __launch_bounds__(kFrontThreads) void layer_front_kernel(const LayerA
                         : p.sgate ? p.sgate
                                   : p.router + (int64_t)(p.E - 1) * p.H;
     f32x4 one[1][kTT];
-    tile_dot<1>({w}, p.x, p.H, p.T, p.H, wave, kFrontWaves, one);
+    if (p.H <= 32 * 4 * kFrontWaves) tile_dot<1, 4>({w}, p.x, p.H, p.T, p.H, wave, kFrontWaves, one);
+    else tile_dot<1, 8>({w}, p.x, p.H, p.T, p.H, wave, kFrontWaves, one);
 #pragma unroll
     for (int j = 0; j < kTT; ++j) {
       acc[0][j] = one[0][j];
@@ -264,7 +264,7 @@ __global__ __launch_bounds__(kFrontThreads) void layer_front_kernel(const LayerA
   } else {
     tile = blockIdx.x - p.n_router;
     const int64_t row = min(tile * 16 + lr, p.Is - 1);
-    tile_dot<2>({p.sw[0] + row * p.H, p.sw[1] + row * p.H}, p.x, p.H, p.T, p.H, wave, kFrontWaves,
+    tile_dot<2, 4>({p.sw[0] + row * p.H, p.sw[1] + row * p.H}, p.x, p.H, p.T, p.H, wave, kFrontWaves,
                 acc);
   }
   // (two rounds of eight waves: half the LDS; the sums stay in wave order)
@@ -668,7 +668,8 @@ struct FfnLds {
 // 8-byte load per lane and matrix and go through the wave's own LDS, where a
 // lane finds its four for each chunk.
 template <int NT, int NTMAX, int SW, bool AL>
-__device__ __forceinline__ void segment_slice(const LayerArgs &p, FfnLds<NTMAX, SW> &lds, int c) {
+__device__ __forceinline__ void segment_slice(const LayerArgs &p, FfnLds<NTMAX, SW> &lds, int c,
+                                              uint32_t &claimed) {
   uint8_t *const xp = lds.x_pieces, *const hp = lds.h_pieces;
   constexpr int NW = kFfnWaves, TW = SW / 16 / NW;   // blocks per wave
   RouteLds &l = lds.route;
@@ -883,6 +884,9 @@ __device__ __forceinline__ void segment_slice(const LayerArgs &p, FfnLds<NTMAX, 
   asm volatile("" ::: "memory");
 #pragma unroll
   for (int q = 0; q < TILES; ++q) load_d(q, wave);
+  // (the next item: late, so that the workgroups that are first through take
+  // what is left, early enough to be back at the end)
+  if (tid == 0) claimed = dev_add(p.ctl + kCtlClaim, 1u);
 
   // ---- h pieces
   lds_barrier();
@@ -995,14 +999,13 @@ __global__ __launch_bounds__(kFfnThreads, 2) void layer_ffn_kernel(const LayerAr
     if (item < iSD) {
       const int seg = (int)item / p.n_c, c = (int)item - seg * p.n_c;
       find_segment<NTMAX>(p, l, first, seg);
-      if (tid == 0) claimed = dev_add(p.ctl + kCtlClaim, 1u);
       __syncthreads();
       if (NTMAX == 1 || __builtin_amdgcn_readfirstlane(l.pair[1]) < 0)
-        segment_slice<1, NTMAX, SW, AL>(p, lds, c);
+        segment_slice<1, NTMAX, SW, AL>(p, lds, c, claimed);
       else if (NTMAX == 2 || __builtin_amdgcn_readfirstlane(l.pair[2]) < 0)
-        segment_slice<NTMAX == 1 ? 1 : 2, NTMAX, SW, AL>(p, lds, c);
+        segment_slice<NTMAX == 1 ? 1 : 2, NTMAX, SW, AL>(p, lds, c, claimed);
       else
-        segment_slice<NTMAX, NTMAX, SW, AL>(p, lds, c);
+        segment_slice<NTMAX, NTMAX, SW, AL>(p, lds, c, claimed);
       stores_done();
       __syncthreads();
       if (tid < NTMAX && l.pair[tid] >= 0) dev_add(p.ctl + kCtlDone + l.pair[tid] / p.k, 1u);
@@ -1013,7 +1016,7 @@ __global__ __launch_bounds__(kFfnThreads, 2) void layer_ffn_kernel(const LayerAr
       const int r0 = ((int)(item - iSD) * kFfnWaves + wave) * 16;
       if (r0 < p.H) {   // (H is a multiple of 32: whole tiles)
         f32x4 acc[1][kTT];
-        tile_dot<1>({p.sw[2] + (int64_t)(r0 + lr) * p.Is}, p.sh, p.sh_ld, p.T, p.Is, 0, 1, acc);
+        tile_dot<1, 8>({p.sw[2] + (int64_t)(r0 + lr) * p.Is}, p.sh, p.sh_ld, p.T, p.Is, 0, 1, acc);
 #pragma unroll
         for (int j = 0; j < kTT; ++j) {
           const int t = 16 * j + lr;
