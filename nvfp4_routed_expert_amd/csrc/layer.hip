@@ -154,20 +154,20 @@ __device__ __forceinline__ uint32_t piece_lo2(float a, float b, uint32_t hi) {
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 constexpr int kTT = kLMaxT / 16;
 
-template <int NM, int B>
+template <int NM, int B, int TT>
 __device__ __forceinline__ void tile_dot(const uint16_t *const (&w)[NM], const uint16_t *x,
                                          int64_t x_ld, int T, int K, int wave, int waves,
-                                         f32x4 (&acc)[NM][kTT]) {
+                                         f32x4 (&acc)[NM][TT]) {
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
   const int tt = (T + 15) / 16;
 #pragma unroll
   for (int m = 0; m < NM; ++m)
 #pragma unroll
-    for (int j = 0; j < kTT; ++j) acc[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < TT; ++j) acc[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int steps = K / 32;
-  const uint16_t *xr[kTT];
+  const uint16_t *xr[TT];
 #pragma unroll
-  for (int j = 0; j < kTT; ++j) xr[j] = x + (int64_t)min(j * 16 + lr, T - 1) * x_ld + 8 * lg;
+  for (int j = 0; j < TT; ++j) xr[j] = x + (int64_t)min(j * 16 + lr, T - 1) * x_ld + 8 * lg;
   for (int s0 = wave; s0 < steps; s0 += waves * B) {
     u32x4 wv[NM][B];
 #pragma unroll
@@ -178,7 +178,7 @@ __device__ __forceinline__ void tile_dot(const uint16_t *const (&w)[NM], const u
         wv[m][b] = *reinterpret_cast<const u32x4 *>(w[m] + 32 * min(s, steps - 1) + 8 * lg);
     }
 #pragma unroll
-    for (int j = 0; j < kTT; ++j) {
+    for (int j = 0; j < TT; ++j) {
       if (j >= tt) break;   // uniform
       u32x4 xv[B];
 #pragma unroll
@@ -197,22 +197,24 @@ __device__ __forceinline__ void tile_dot(const uint16_t *const (&w)[NM], const u
   }
 }
 
-// The first launch: workgroups of 16 waves, each a tile of 16 rows (K split
-// over the waves, their sums added in wave order in LDS), so all of a tile's
-// loads are in flight at once.  Tiles: the router rows (experts, then the
+// The first launch: workgroups of 16 waves, each a tile of 16 rows and 16 tokens
+// (K split over the waves, their sums added in wave order in LDS), so all of a
+// tile's loads are in flight at once.  (A tile for every token: 17 us at 32
+// tokens, H = 4096, where only eight workgroups had rows of the router.)  Tiles: the router rows (experts, then the
 // shared gate's row) and the shared expert's gate/up rows; then a workgroup
 // per token for its x pieces.
 constexpr int kFrontWaves = 16;
 constexpr int kFrontThreads = 64 * kFrontWaves;
 
 __global__ __launch_bounds__(kFrontThreads) void layer_front_kernel(const LayerArgs p) {
-  __shared__ float red[kFrontWaves / 2][2][16][kLMaxT];
+  __shared__ float red[kFrontWaves][2][16][17];
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < kCtlWords; i += kFrontThreads) p.ctl[i] = 0u;
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
-  if ((int)blockIdx.x >= p.n_router + p.n_su) {   // x pieces of one token
+  const int n_tiles = (p.n_router + p.n_su) * ((p.T + 15) / 16);
+  if ((int)blockIdx.x >= n_tiles) {   // x pieces of one token
     uint32_t *wmax = reinterpret_cast<uint32_t *>(red);
-    const int t = (int)blockIdx.x - p.n_router - p.n_su, HP = layer_chunks(p.H) * kChunk;
+    const int t = (int)blockIdx.x - n_tiles, HP = layer_chunks(p.H) * kChunk;
     const int k = 8 * tid;   // (H <= 8192: one piece of eight per thread)
     u32x4 v = u32x4{0u, 0u, 0u, 0u};
     if (k < p.H) v = *reinterpret_cast<const u32x4 *>(p.x + (int64_t)t * p.H + k);
@@ -242,59 +244,43 @@ __global__ __launch_bounds__(kFrontThreads) void layer_front_kernel(const LayerA
     return;
   }
   const int lr = lane & 15, lg = lane >> 4;
-  const int tt = (p.T + 15) / 16;
-  const bool router = (int)blockIdx.x < p.n_router;   // uniform
+  const int groups = (p.T + 15) / 16, t0 = (int)blockIdx.x % groups * 16;
+  const int idx = (int)blockIdx.x / groups, T = min(p.T - t0, 16);
+  const uint16_t *const x = p.x + (int64_t)t0 * p.H;
+  const bool router = idx < p.n_router;   // uniform
   const int ER = p.E + (p.sgate ? 1 : 0);
-  f32x4 acc[2][kTT];
-  int tile;
+  const int tile = router ? idx : idx - p.n_router;
+  f32x4 acc[2][1];
   if (router) {
-    tile = blockIdx.x;
     const int row = tile * 16 + lr;
     const uint16_t *w = row < p.E ? p.router + (int64_t)row * p.H
                         : p.sgate ? p.sgate
                                   : p.router + (int64_t)(p.E - 1) * p.H;
-    f32x4 one[1][kTT];
-    if (p.H <= 32 * 4 * kFrontWaves) tile_dot<1, 4>({w}, p.x, p.H, p.T, p.H, wave, kFrontWaves, one);
-    else tile_dot<1, 8>({w}, p.x, p.H, p.T, p.H, wave, kFrontWaves, one);
-#pragma unroll
-    for (int j = 0; j < kTT; ++j) {
-      acc[0][j] = one[0][j];
-      acc[1][j] = one[0][j];
-    }
+    f32x4 one[1][1];
+    if (p.H <= 32 * 4 * kFrontWaves)
+      tile_dot<1, 4, 1>({w}, x, p.H, T, p.H, wave, kFrontWaves, one);
+    else
+      tile_dot<1, 8, 1>({w}, x, p.H, T, p.H, wave, kFrontWaves, one);
+    acc[0][0] = acc[1][0] = one[0][0];
   } else {
-    tile = blockIdx.x - p.n_router;
     const int64_t row = min(tile * 16 + lr, p.Is - 1);
-    tile_dot<2, 4>({p.sw[0] + row * p.H, p.sw[1] + row * p.H}, p.x, p.H, p.T, p.H, wave, kFrontWaves,
-                acc);
+    tile_dot<2, 4, 1>({p.sw[0] + row * p.H, p.sw[1] + row * p.H}, x, p.H, T, p.H, wave, kFrontWaves,
+                      acc);
   }
-  // (two rounds of eight waves: half the LDS; the sums stay in wave order)
-  constexpr int HALF = kFrontWaves / 2;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    red[wave][0][4 * lg + i][lr] = acc[0][0][i];
+    if (!router) red[wave][1][4 * lg + i][lr] = acc[1][0][i];
+  }
+  __syncthreads();
+  const int r = tid & 15, tl = tid >> 4, t = t0 + tl, row = tile * 16 + r;   // 16 rows x 16 tokens
+  if (tl >= T) return;
   float sum0 = 0.0f, sum1 = 0.0f;
-  for (int round = 0; round < 2; ++round) {
-    if (wave / HALF == round) {
 #pragma unroll
-      for (int j = 0; j < kTT; ++j)
-        if (j < tt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            red[wave % HALF][0][4 * lg + i][j * 16 + lr] = acc[0][j][i];
-            if (!router) red[wave % HALF][1][4 * lg + i][j * 16 + lr] = acc[1][j][i];
-          }
-    }
-    __syncthreads();
-    {
-      const int r = tid & 15, t = tid >> 4;   // 16 rows x 64 tokens
-      if (t < p.T) {
-        for (int w = 0; w < HALF; ++w) {
-          sum0 += red[w][0][r][t];
-          if (!router) sum1 += red[w][1][r][t];
-        }
-      }
-    }
-    __syncthreads();
+  for (int w = 0; w < kFrontWaves; ++w) {
+    sum0 += red[w][0][r][tl];
+    if (!router) sum1 += red[w][1][r][tl];
   }
-  const int r = tid & 15, t = tid >> 4, row = tile * 16 + r;
-  if (t >= p.T) return;
   if (router) {
     if (row >= ER) return;
     float v = sum0;
@@ -1016,7 +1002,7 @@ __global__ __launch_bounds__(kFfnThreads, 2) void layer_ffn_kernel(const LayerAr
       const int r0 = ((int)(item - iSD) * kFfnWaves + wave) * 16;
       if (r0 < p.H) {   // (H is a multiple of 32: whole tiles)
         f32x4 acc[1][kTT];
-        tile_dot<1, 8>({p.sw[2] + (int64_t)(r0 + lr) * p.Is}, p.sh, p.sh_ld, p.T, p.Is, 0, 1, acc);
+        tile_dot<1, 8, kTT>({p.sw[2] + (int64_t)(r0 + lr) * p.Is}, p.sh, p.sh_ld, p.T, p.Is, 0, 1, acc);
 #pragma unroll
         for (int j = 0; j < kTT; ++j) {
           const int t = 16 * j + lr;
@@ -1065,7 +1051,7 @@ hipError_t launch_layer(const LayerArgs &args, hipStream_t s) {
   a.n_router = groups(a.E + (a.sgate ? 1 : 0), 16);
   a.n_sd = a.Is ? groups(a.H, 16 * kFfnWaves) : 0;
   a.n_su = a.Is ? groups(a.Is, 16) : 0;
-  launch_kernel(layer_front_kernel, dim3((unsigned)(a.n_router + a.n_su + a.T)),
+  launch_kernel(layer_front_kernel, dim3((unsigned)((a.n_router + a.n_su) * ((a.T + 15) / 16) + a.T)),
                 dim3(kFrontThreads), 0, s, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
