@@ -184,6 +184,7 @@ __device__ __forceinline__ void tile_dot(const uint16_t *const (&w)[NM], const u
 #pragma unroll
       for (int b = 0; b < B; ++b)
         xv[b] = *reinterpret_cast<const u32x4 *>(xr[j] + 32 * min(s0 + b * waves, steps - 1));
+      __builtin_amdgcn_sched_barrier(0);   // (all loads, then the products)
 #pragma unroll
       for (int b = 0; b < B; ++b) {
         if (s0 + b * waves >= steps) break;   // uniform
