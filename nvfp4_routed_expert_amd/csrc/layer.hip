@@ -47,10 +47,10 @@
 // block sums, scales and K add up in fp32.
 //
 // Measured (both launches): one token, H = 2048, I = shared I = 512, E = 512,
-// k = 8 33.7 us, a chain of latencies (front 7.7, routing 4, x 4, the slice 14,
-// combine 4); 16 tokens of it 65.9 us, of which the stream of 210 MB takes 38
-// at 5.6 TB/s; 32 tokens, H = 4096, I = 1536, E = 128, k = 8 277 us (1.19 GB,
-// 4.3 TB/s over all: 2.7 rounds of slices on 256 CUs).
+// k = 8 32.9 us, a chain of latencies (front 7.8, routing 4.5, x 4, the slice 12,
+// combine 4); 16 tokens of it 63 us (211 MB: 17 us of front and routing, then a
+// round of slices of 27 to 45 us); 32 tokens, H = 4096, I = 1536, E = 128, k = 8
+// 268 us (1.19 GB, 4.4 TB/s over all: 2.7 rounds of slices on 256 CUs).
 #include "fp8.h"
 #include "kernels.h"
 #include "rowdot.h"
