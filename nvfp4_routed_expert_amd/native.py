@@ -566,7 +566,7 @@ _STAY = contextlib.nullcontext()
 
 def _on(dev):
     """Makes dev the current device (nothing to do, 3 us less, where it is)."""
-    return _STAY if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    return _STAY if torch._C._cuda_getDevice() == dev.index else torch.cuda.device(dev)
 
 
 def _stream_of(dev):
@@ -611,21 +611,24 @@ def fp8_block_quantize(x, block_rows=1, out=None):
     if x.dim() != 2:
         raise ValueError(f"x must be [rows, cols], got {tuple(x.shape)}")
     rows, cols = x.shape
-    if cols > 1 and x.stride(1) != 1:
+    ld, step = x.stride()
+    if cols > 1 and step != 1:
         raise ValueError("x must have unit column stride")
     if block_rows not in (1, 128):
         raise ValueError(f"block_rows must be 1 or 128, got {block_rows}")
     shape = (rows if block_rows == 1 else _fp8_blocks(rows), _fp8_blocks(cols))
     if out is None:
-        codes = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
-        scales = torch.empty(shape, dtype=torch.float32, device=x.device)
+        dev = _device_of(x)
+        codes = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
+        scales = torch.empty(shape, dtype=torch.float32, device=dev)
     else:
         codes, scales = out
         _expect("codes", codes, (rows, cols), torch.uint8)
         _expect("scales", scales, shape, torch.float32)
-    dev = _device_of(x, codes=codes, scales=scales)
+        dev = _device_of(x, codes=codes, scales=scales)
+    if rows <= 1:
+        ld = _round_up(cols, 8)
     with _on(dev):
-        ld = x.stride(0) if rows > 1 else _round_up(cols, 8)
         _check(lib().fp8_block_quantize(x.data_ptr(), _dt(x.dtype), rows, cols, ld, block_rows,
                                         codes.data_ptr(), scales.data_ptr(), _stream_of(dev)))
     return codes, scales
