@@ -568,7 +568,8 @@ size_t fp8_block_linear_workspace_size(int64_t M, int64_t N, int64_t K, int quan
  *   h_t = bf16_rne( silu(x_t Wg^T) * (x_t Wu^T) )
  *   y_t = h_t Wd^T
  * both products as fp8_block_linear computes them, gate and up as for bf16 y
- * (and through the FP8 matrix unit for H > 18432 too; x and h are quantised
+ * (and through the FP8 matrix unit too for H > 18432, and for T > 32 with
+ * H * I >= 32 * 10^6; x and h are quantised
  * online per row and 128 columns, and an element of h at a rounding boundary
  * may fall either way where that unit is used).  y [T, H] bf16 or f32.  Requires H % 32 == 0,
  * I % 32 == 0, T, H, I <= 2^24.  workspace: fp8_block_mlp_workspace_size

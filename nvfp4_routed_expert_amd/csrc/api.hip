@@ -278,8 +278,8 @@ struct Fp8LinearWs {
 Fp8LinearWs carve_fp8_linear(Carver &c, int64_t M, int64_t N, int64_t K, bool quantised,
                              OutType out) {
   Fp8LinearWs w = {};
-  const bool inside = f8_gemv_supported(M, K);
-  const bool own = !quantised && !f8_gemv_quantises(M, N, K);   // x quantised by a launch of its own
+  const bool inside = f8_gemv_supported(false, M, N, K);
+  const bool own = !quantised && !f8_gemv_quantises(false, M, N, K);   // x quantised by a launch of its own
   w.xq = c.take<uint8_t>(own ? (size_t)(M * K) : 0);
   w.xs = c.take<float>(own ? (size_t)(M * ((K + 127) / 128)) : 0);
   if (!inside) {
@@ -302,10 +302,10 @@ struct Fp8MlpWs {
 };
 Fp8MlpWs carve_fp8_mlp(Carver &c, int64_t T, int64_t H, int64_t I, OutType out) {
   Fp8MlpWs w = {};
-  w.few_up = f8_gemv_supported(T, H);
-  w.few_down = f8_gemv_supported(T, I);
-  w.own_x = !w.few_up || !f8_gemv_quantises(T, I, H);
-  w.own_h = !w.few_up || !w.few_down || !f8_gemv_quantises(T, H, I);
+  w.few_up = f8_gemv_supported(true, T, I, H);
+  w.few_down = f8_gemv_supported(false, T, H, I);
+  w.own_x = !w.few_up || !f8_gemv_quantises(true, T, I, H);
+  w.own_h = !w.few_up || !w.few_down || !f8_gemv_quantises(false, T, H, I);
   w.xq = c.take<uint8_t>(w.own_x ? (size_t)(T * H) : 0);
   w.xs = c.take<float>(w.own_x ? (size_t)(T * ((H + 127) / 128)) : 0);
   w.h = c.take<uint16_t>(w.few_up ? (size_t)(T * I) : 0);
@@ -1479,12 +1479,12 @@ nvfp4_status fp8_block_linear(const void *x, const float *x_scales, int64_t M,
       carve_fp8_linear(c, M, N, K, x_scales != nullptr, out_type(y_dtype));
   const void *xq = x;
   const float *xs = x_scales;
-  if (!x_scales && !f8_gemv_quantises(M, N, K)) {
+  if (!x_scales && !f8_gemv_quantises(false, M, N, K)) {
     LAUNCH(launch_f8_quantize(x, InType::BF16, M, K, K, 1, ws.xq, ws.xs, stream), "fp8 quantize");
     xq = ws.xq;
     xs = ws.xs;
   }
-  if (f8_gemv_supported(M, K)) {
+  if (f8_gemv_supported(false, M, N, K)) {
     const F8GemvArgs a = {xq, xs, (int)M, {w->codes, nullptr}, {w->scales, nullptr},
                           (int)N, (int)K, y, out_type(y_dtype)};
     LAUNCH(launch_f8_gemv(false, a, stream), "fp8 gemv");

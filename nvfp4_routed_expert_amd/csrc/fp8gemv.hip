@@ -274,20 +274,28 @@ hipError_t launch_gemv(const F8GemvArgs &a, hipStream_t s) {
 
 }  // namespace
 
-bool f8_gemv_supported(int64_t M, int64_t K) {
-  return M >= 1 && M <= 64 && K <= kGvMaxKB * kF8Block;
+// Where every workgroup's stream of x outweighs its 16 rows of weights, the
+// batch form's 256 rows are better.  17408 x 5120, this form and that: 17 rows
+// 36 and 32 us, 32 rows 39 and 31, 64 rows 58 and 35; 4096 x 4096: 9 and 14,
+// 9 and 15, 12 and 17.  A whole gated MLP with its gate/up product in this form
+// and that, 5120 / 17408: 33 tokens 101 and 80 us, 64 tokens 120 and 85; 4096 /
+// 4096: 27 and 28, 32 and 31 (up to 32 tokens its products stay exact).
+bool f8_gemv_supported(bool swiglu, int64_t M, int64_t N, int64_t K) {
+  return M >= 1 && M <= 64 && K <= kGvMaxKB * kF8Block &&
+         (M <= (swiglu ? 32 : 16) || N * K < (M <= 32 ? 48 : 32) * 1000000);
 }
 // A workgroup per CU has the LDS to itself, and a launch costs more than its
 // quantising (24 tokens, 2048 / 1056: 25.7 us with launches for x and h).
-bool f8_gemv_quantises(int64_t M, int64_t N, int64_t K) {
+bool f8_gemv_quantises(bool swiglu, int64_t M, int64_t N, int64_t K) {
   const int64_t bytes = gv_x_bytes(M, (K + kF8Block - 1) / kF8Block);
-  return f8_gemv_supported(M, K) &&
+  return f8_gemv_supported(swiglu, M, N, K) &&
          ((M <= 16 && bytes <= kGvXBytes) ||
           (M <= 32 && bytes <= kGvXBytesFew && N <= 16 * 256));
 }
 
 hipError_t launch_f8_gemv(bool swiglu, const F8GemvArgs &a, hipStream_t s) {
-  if (!f8_gemv_supported(a.M, a.K) || (!a.xs && !f8_gemv_quantises(a.M, a.N, a.K)))
+  if (!f8_gemv_supported(swiglu, a.M, a.N, a.K) ||
+      (!a.xs && !f8_gemv_quantises(swiglu, a.M, a.N, a.K)))
     return hipErrorInvalidValue;
   // LDS decides how many workgroups share a CU and how much is in flight.  One
   // row, 17408 x 5120: 4 waves, 4 blocks each 18.8 us; 8 waves, 4 blocks 23.3;

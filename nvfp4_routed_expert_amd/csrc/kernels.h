@@ -364,8 +364,8 @@ struct F8GemvArgs {
   void *out;
   OutType out_type;
 };
-bool f8_gemv_supported(int64_t M, int64_t K);
-bool f8_gemv_quantises(int64_t M, int64_t N, int64_t K);
+bool f8_gemv_supported(bool swiglu, int64_t M, int64_t N, int64_t K);
+bool f8_gemv_quantises(bool swiglu, int64_t M, int64_t N, int64_t K);
 hipError_t launch_f8_gemv(bool swiglu, const F8GemvArgs &a, hipStream_t s);
 
 // ---- a whole MoE layer for a few tokens (layer.hip) --------------------------------

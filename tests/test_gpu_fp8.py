@@ -332,9 +332,11 @@ def test_linear_at_the_rules(M, N, K):
     test_linear(M, N, K)
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 40, 18464), (33, 130, 18560)])
+@pytest.mark.parametrize("M,N,K", [(1, 40, 18464), (33, 130, 18560), (17, 8192, 5888),
+                                   (33, 8192, 3936)])
 def test_linear_of_few_rows_with_a_long_k(M, N, K):
-    """Past the few-row form's K the batch form runs, exact for either type."""
+    """Past the few-row form's K, and with large weights, the batch form runs,
+    exact for either type."""
     test_linear(M, N, K)
 
 
