@@ -553,7 +553,7 @@ nvfp4_status fp8_block_quantize(const void *x, nvfp4_dtype x_dtype, int64_t rows
  * contiguous, quantised online exactly as fp8_block_quantize with
  * block_rows = 1.  x_scales set: x holds E4M3 codes [M, K] with x_scales
  * [M, ceil(K / 128)] (quantised once for several projections).
- * Requires K % 32 == 0, M, N <= 2^24.
+ * Requires K % 32 == 0, K <= 2^27, M, N <= 2^24, M * ceil(K / 128) <= 2^27.
  * workspace: fp8_block_linear_workspace_size bytes (device, 16-byte
  * aligned), scratch only; quantised: x_scales is set.
  */
@@ -572,7 +572,7 @@ size_t fp8_block_linear_workspace_size(int64_t M, int64_t N, int64_t K, int quan
  * H * I >= 32 * 10^6; x and h are quantised
  * online per row and 128 columns, and an element of h at a rounding boundary
  * may fall either way where that unit is used).  y [T, H] bf16 or f32.  Requires H % 32 == 0,
- * I % 32 == 0, T, H, I <= 2^24.  workspace: fp8_block_mlp_workspace_size
+ * I % 32 == 0, T, H, I <= 2^24, T * ceil(H / 128) and T * ceil(I / 128) <= 2^27.  workspace: fp8_block_mlp_workspace_size
  * bytes (device, 16-byte aligned), scratch only.
  */
 nvfp4_status fp8_block_mlp(const void *x, int64_t T, const fp8_matrix *w_gate,

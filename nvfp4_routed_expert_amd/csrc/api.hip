@@ -267,7 +267,7 @@ SharedWs carve_shared(Carver &c, int64_t T, int64_t H, int64_t I) {
   return w;
 }
 
-constexpr int64_t kFp8MaxRows = (int64_t)1 << 24;
+constexpr int64_t kFp8MaxRows = (int64_t)1 << 24, kFp8MaxCols = (int64_t)1 << 27;
 struct Fp8LinearWs {
   F8Plan plan;
   uint8_t *xq;
@@ -1411,9 +1411,19 @@ static nvfp4_status check_fp8_matrix(const fp8_matrix *w, const char *name) {
   if (w->rows > kFp8MaxRows)
     return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s->rows exceeds 2^24", name);
   TRY(check_k(w->cols, name));
+  if (w->cols > kFp8MaxCols)   // (sixteen rows within 31 bits of byte offset)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s->cols exceeds 2^27", name);
   if (!aligned16(w->codes) || !aligned16(w->scales))
     return fail(NVFP4_ERR_MISALIGNED, "%s->%s is not 16-byte aligned", name,
                 aligned16(w->codes) ? "scales" : "codes");
+  return NVFP4_OK;
+}
+
+// Rows that a call quantises: the quantiser's own limit.
+static nvfp4_status check_fp8_batch(int64_t M, int64_t K) {
+  if (M * ((K + 127) / 128) > (int64_t)1 << 27)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%lld rows of %lld have more than 2^27 scales",
+                (long long)M, (long long)K);
   return NVFP4_OK;
 }
 
@@ -1471,6 +1481,7 @@ nvfp4_status fp8_block_linear(const void *x, const float *x_scales, int64_t M,
   CHECK_ALIGN(x_scales);
   CHECK_ALIGN(y);
   const int64_t K = w->cols, N = w->rows;
+  TRY(check_fp8_batch(M, K));
   TRY(check_workspace(workspace, workspace_bytes,
                       fp8_block_linear_workspace_size(M, N, K, x_scales != nullptr)));
   if (M == 0) return NVFP4_OK;
@@ -1535,6 +1546,8 @@ nvfp4_status fp8_block_mlp(const void *x, int64_t T, const fp8_matrix *w_gate,
     return fail(NVFP4_ERR_INVALID_ARGUMENT, "y_dtype %d is not BF16 or F32", (int)y_dtype);
   CHECK_ALIGN(x);
   CHECK_ALIGN(y);
+  TRY(check_fp8_batch(T, H));
+  TRY(check_fp8_batch(T, I));
   TRY(check_workspace(workspace, workspace_bytes, fp8_block_mlp_workspace_size(T, H, I)));
   if (T == 0) return NVFP4_OK;
   Carver c(workspace);

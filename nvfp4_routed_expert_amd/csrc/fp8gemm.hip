@@ -147,7 +147,8 @@ __global__ __launch_bounds__(64 * kF8Waves, 2) void f8_gemm_kernel(const F8GemmA
     load_left(wave >= 4 ? u : u + 1, wave >= 4 ? s : s2);
     load(u + 1, s2);
   };
-  // Scales of the four blocks from i on: s_x as [row][block]; then, per wave, its rows' s_w (64 values a matrix: the four, repeated).
+  // Scales of the four blocks from i on: s_x as [row][block]; then, per wave,
+  // its rows' s_w (64 values a matrix: the four, repeated).
   const int g_row = n0 / kF8Block, g_rows = (N + kF8Block - 1) / kF8Block;
   const __amdgpu_buffer_rsrc_t gb0 = f8_buffer(p.ws[0], g_row, g_rows, KB * 4);
   const __amdgpu_buffer_rsrc_t gb1 = f8_buffer(p.ws[SWIGLU ? 1 : 0], g_row, g_rows, KB * 4);
@@ -165,8 +166,7 @@ __global__ __launch_bounds__(64 * kF8Waves, 2) void f8_gemm_kernel(const F8GemmA
     uint8_t *g = st + SX_BYTES + wave * G_STAGE;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(gb0, (lds_ptr_t)g, 4, goff, at, 0, 0);
     if constexpr (SWIGLU)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(gb1, (lds_ptr_t)(g + 256), 4,
-                                               goff, at, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(gb1, (lds_ptr_t)(g + 256), 4, goff, at, 0, 0);
   };
 
   f32x4 acc[4][8], t[2][4];
@@ -213,14 +213,14 @@ __global__ __launch_bounds__(64 * kF8Waves, 2) void f8_gemm_kernel(const F8GemmA
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[f][jp][i] = __builtin_fmaf(v[i], sc, acc[f][jp][i]);
   };
-  // Block i: stage q % 2, scale slot q of buffer s0 (the next four's: s1), its
-  // weights in ab; leaves the next block's in an.  No branch: with one in the
-  // loop the registers no longer suffice.
   int slot0 = 0, slot1 = HALVES ? 1 : 0;   // of block i
   auto after = [](int s) {
     s += HALVES ? 2 : 1;
     return s < R ? s : s - R;
   };
+  // Block i: scales in place q of buffer s0 (the next four blocks': s1), weights
+  // in ab; leaves the next block's in an.  No branch: with one in the loop the
+  // registers no longer suffice.
   auto block = [&](int i_, int q, i32x8 (&ab)[4], i32x8 (&an)[4], uint8_t *s0, uint8_t *s1) {
     const int i = __builtin_amdgcn_readfirstlane(i_);
     const int qn = (q + 1) % kF8Group;
@@ -291,7 +291,9 @@ __global__ __launch_bounds__(64 * kF8Waves, 2) void f8_gemm_kernel(const F8GemmA
     load(2, 2);
   }
   // (block 0 has landed)
-  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(HALVES ? 3 * (WL + XL) + 1 : 2 * (WL + XL)) : "memory");
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(HALVES ? 3 * (WL + XL) + 1
+                                                               : 2 * (WL + XL))
+               : "memory");
   g0 = weight_scale(scales, 0, 0);
   if constexpr (SWIGLU) g1 = weight_scale(scales, 0, 1);
 #pragma unroll

@@ -343,17 +343,17 @@ struct F8GemmArgs {
 // Tokens of a tile and K parts for a problem; a split needs partial_floats
 // floats of workspace.
 struct F8Plan {
-  int bm = 256;
-  bool exact = false;   // fp32 sums of exact products (fp32 outputs)
+  int bm = 0;           // 64, 128 or 192
+  bool exact = false;   // fp32 sums of exact products
   int ksplit = 1;
   size_t partial_floats = 0;
 };
 F8Plan f8_gemm_plan(bool swiglu, OutType out, int64_t M, int64_t N, int64_t K);
 hipError_t launch_f8_gemm(bool swiglu, const F8GemmArgs &a, const F8Plan &pl, hipStream_t s);
 
-// The same product for M <= 64 rows of K <= 18432 (fp8gemv.hip).  xs null: x is
-// bf16 [M, K] and is quantised inside (up to about 20000 elements); otherwise x holds codes.  Gate/up form:
-// out = h, bf16 [M, N].
+// The same product for a few rows (fp8gemv.hip), where _supported says so.  xs
+// null: x is bf16 [M, K] and is quantised inside (where _quantises says so);
+// otherwise x holds codes.  Gate/up form: out = h, bf16 [M, N].
 struct F8GemvArgs {
   const void *x;
   const float *xs;

@@ -115,3 +115,20 @@ def test_binding_refusals():
                                 x_scales=torch.ones((4, 2)))
     with pytest.raises(TypeError, match="uint8"):
         native.fp8_block_mlp(x, (w.int(), ws), (w, ws), (w, ws))
+
+
+def test_sizes_past_the_kernels_ranges():
+    """Offsets of sixteen rows, and scales of a batch, past what the kernels
+    index: refused before anything else is looked at."""
+    L = native.lib()
+    big = 1 << 50
+    lin = lambda M, N, K: L.fp8_block_linear(
+        FAKE, None, M, ctypes.byref(native.Fp8Matrix(FAKE.value, FAKE.value, N, K)), FAKE, 0, FAKE,
+        big, None)
+    assert lin(1, 1, (1 << 27) + 32) == 2 and "2^27" in _last()
+    assert lin(1 << 20, 1, 128 * 129) == 2 and "2^27" in _last()
+    m = lambda n, k: ctypes.byref(native.Fp8Matrix(FAKE.value, FAKE.value, n, k))
+    assert L.fp8_block_mlp(FAKE, 1 << 20, m(32, 128 * 129), m(32, 128 * 129), m(128 * 129, 32), FAKE, 0,
+                           FAKE, big, None) == 2 and "2^27" in _last()
+    assert L.fp8_block_mlp(FAKE, 1 << 20, m(128 * 129, 32), m(128 * 129, 32), m(32, 128 * 129), FAKE, 0,
+                           FAKE, big, None) == 2 and "2^27" in _last()
