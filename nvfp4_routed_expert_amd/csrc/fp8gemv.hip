@@ -25,7 +25,7 @@
 //
 // Measured: N = 17408, K = 5120, one row 16.5 us (5.4 TB/s); N = 5120, K = 17408,
 // 8 rows 22 us with the quantiser's launch (4.0 TB/s; 320 workgroups on 256
-// CUs); a gated MLP of one token, 5120 / 17408, 57.5 us (4.65 TB/s).  With
+// CUs); a gated MLP of one token, 5120 / 17408, 53.3 us (5.0 TB/s).  With
 // fragments loaded straight into registers and x quantised by every wave:
 // 31.7, 47.7 and 94.5 us.
 #include "fp8.h"
@@ -45,8 +45,8 @@ __host__ __device__ constexpr int64_t gv_x_bytes(int64_t M, int64_t KB) {
   return M * (KB * (kF8Block + 4) + 16);
 }
 
-// XT: groups of 8 rows of x.  XCAP: bytes for x (QX) or its scales.
-template <int XT, bool SWIGLU, bool QX, int NW, int D, int XCAP>
+// STREAM: the weights are loaded as used once.  XT: groups of 8 rows of x.  XCAP: bytes for x (QX) or its scales.
+template <int XT, bool SWIGLU, bool QX, int NW, int D, int XCAP, bool STREAM>
 __global__ __launch_bounds__(64 * NW) void f8_gemv_kernel(const F8GemvArgs p) {
 #pragma clang fp contract(off)
   static_assert(!QX || XT <= 4, "QX: up to 32 rows");
@@ -88,9 +88,12 @@ __global__ __launch_bounds__(64 * NW) void f8_gemv_kernel(const F8GemvArgs p) {
     const int off = off_ | (at < last ? 0 : kOutside);   // (granules past K: zero codes)
 #pragma unroll
     for (int h = 0; h < LS; ++h)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(h < 2 * NT ? wbuf[h] : xbuf[h - 2 * NT],
-                                               (lds_ptr_t)(ring + slot * SLOT + h * 1024), 16, off,
-                                               at, 0, 0);
+      if (h < 2 * NT)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            wbuf[h], (lds_ptr_t)(ring + slot * SLOT + h * 1024), 16, off, at, 0, STREAM ? 2 : 0);
+      else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            xbuf[h - 2 * NT], (lds_ptr_t)(ring + slot * SLOT + h * 1024), 16, off, at, 0, 0);
   };
 
   // ---- x and the scales (their first loads go out before the ring's)
@@ -267,8 +270,15 @@ __global__ __launch_bounds__(64 * NW) void f8_gemv_kernel(const F8GemvArgs p) {
 
 template <int XT, bool SWIGLU, bool QX, int NW, int D, int XCAP = XT * 8 * kGvMaxKB * 4>
 hipError_t launch_gemv(const F8GemvArgs &a, hipStream_t s) {
-  launch_kernel((f8_gemv_kernel<XT, SWIGLU, QX, NW, D, XCAP>), dim3((unsigned)((a.N + 15) / 16)),
-                dim3(64 * NW), 0, s, a);
+  const dim3 grid((unsigned)((a.N + 15) / 16)), block(64 * NW);
+  // Weights past half of the 256 MB cache behind the L2s will not be there at
+  // the next call: gate and up of 5120 / 17408, one token, 57.6 us for the MLP
+  // without the hint and 54 with it.  Smaller ones may be (17408 x 5120, the
+  // matrices of three calls in turn: 16.7 us without and 17.2 with it).
+  if ((int64_t)a.N * a.K * (SWIGLU ? 2 : 1) > 128000000)
+    launch_kernel((f8_gemv_kernel<XT, SWIGLU, QX, NW, D, XCAP, true>), grid, block, 0, s, a);
+  else
+    launch_kernel((f8_gemv_kernel<XT, SWIGLU, QX, NW, D, XCAP, false>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 

@@ -377,3 +377,27 @@ def test_linear_on_two_streams_at_once():
     torch.cuda.synchronize()
     for i, y in enumerate(got):
         assert torch.equal(y, want[i % 2])
+
+
+@pytest.mark.parametrize("M", [1, 6])
+def test_large_weights_equal_their_parts(M):
+    """Weights past the size from which they are loaded as used once: rows of W,
+    and columns of h, as with the parts alone (bit for bit)."""
+    H, I, part = 5120, 13056, 384
+    say("large weights", M)
+    gen = torch.Generator(device=DEV).manual_seed(M)
+    quant = lambda r, c: native.fp8_block_quantize(
+        0.02 * torch.randn(r, c, generator=gen, device=DEV), 128)
+    x = acts(M, H, 3).to(DEV)
+    w, ws = quant(2 * I, H)
+    y = native.fp8_block_linear(x, w, ws)
+    assert torch.equal(y[:, -part:], native.fp8_block_linear(x, w[-part:].contiguous(),
+                                                             ws[-part // 128:].contiguous()))
+    gate, up = (w[:I], ws[:I // 128]), (w[I:], ws[I // 128:])
+    d, ds = quant(H, I)
+    d[:, part:] = 0
+    whole = native.fp8_block_mlp(x, gate, up, (d, ds))
+    cut = lambda m: (m[0][:part].contiguous(), m[1][:part // 128].contiguous())
+    alone = native.fp8_block_mlp(x, cut(gate), cut(up), (d[:, :part].contiguous(),
+                                                         ds[:, :part // 128].contiguous()))
+    assert torch.equal(whole, alone)
