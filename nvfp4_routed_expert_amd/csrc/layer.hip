@@ -47,8 +47,8 @@
 // block sums, scales and K add up in fp32.
 //
 // Measured (both launches): one token, H = 2048, I = shared I = 512, E = 512,
-// k = 8 32.9 us, a chain of latencies (front 7.8, routing 4.5, x 4, the slice 12,
-// combine 4); 16 tokens of it 63 us (211 MB: 17 us of front and routing, then a
+// k = 8 27.8 us, a chain of latencies (front 7.8, routing 4.5, x 4, the slice 8,
+// combine 4); 16 tokens of it 65 us (211 MB: 17 us of front and routing, then a
 // round of slices of 27 to 45 us); 32 tokens, H = 4096, I = 1536, E = 128, k = 8
 // 268 us (1.19 GB, 4.4 TB/s over all: 2.7 rounds of slices on 256 CUs).
 #include "fp8.h"
@@ -654,7 +654,7 @@ struct FfnLds {
 // is loaded again once both are read.  The scales of four chunks come in one
 // 8-byte load per lane and matrix and go through the wave's own LDS, where a
 // lane finds its four for each chunk.
-template <int NT, int NTMAX, int SW, bool AL>
+template <int NT, int NTMAX, int SW, bool AL, int HINT>
 __device__ __forceinline__ void segment_slice(const LayerArgs &p, FfnLds<NTMAX, SW> &lds, int c,
                                               uint32_t &claimed) {
   uint8_t *const xp = lds.x_pieces, *const hp = lds.h_pieces;
@@ -711,7 +711,8 @@ __device__ __forceinline__ void segment_slice(const LayerArgs &p, FfnLds<NTMAX, 
 #pragma unroll
       for (int m = 0; m < 2; ++m)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            wbuf[m], (lds_ptr_t)(ring + slot * kPair + m * (kPair / 2) + h * 1024), 16, off, 0, 0, 2);
+            wbuf[m], (lds_ptr_t)(ring + slot * kPair + m * (kPair / 2) + h * 1024), 16, off, 0, 0,
+            HINT);
     }
   };
   u32x2 sq[2];
@@ -838,7 +839,8 @@ __device__ __forceinline__ void segment_slice(const LayerArgs &p, FfnLds<NTMAX, 
     const uint32_t r = (uint32_t)row, off = r < (uint32_t)H && k < p.I / 2
                                                 ? r * ((uint32_t)p.I / 2) + (uint32_t)k
                                                 : (uint32_t)kOutside;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(dbuf, (lds_ptr_t)(ring + to), 16, (int)off, 0, 0, 2);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(dbuf, (lds_ptr_t)(ring + to), 16, (int)off, 0, 0,
+                                             HINT);
   };
   auto load_d = [&](int q, int b) {         // tile q of batch b
     const int r = b * BROWS + q * 16;
@@ -962,7 +964,7 @@ __device__ __forceinline__ void segment_slice(const LayerArgs &p, FfnLds<NTMAX, 
   // (the caller waits for every store, and so for the loads past the end)
 }
 
-template <int SW, bool AL, int NTMAX>
+template <int SW, bool AL, int NTMAX, int HINT>
 __global__ __launch_bounds__(kFfnThreads, 2) void layer_ffn_kernel(const LayerArgs p) {
   __shared__ FfnLds<NTMAX, SW> lds;
   RouteLds &l = lds.route;
@@ -988,11 +990,11 @@ __global__ __launch_bounds__(kFfnThreads, 2) void layer_ffn_kernel(const LayerAr
       find_segment<NTMAX>(p, l, first, seg);
       __syncthreads();
       if (NTMAX == 1 || __builtin_amdgcn_readfirstlane(l.pair[1]) < 0)
-        segment_slice<1, NTMAX, SW, AL>(p, lds, c, claimed);
+        segment_slice<1, NTMAX, SW, AL, HINT>(p, lds, c, claimed);
       else if (NTMAX == 2 || __builtin_amdgcn_readfirstlane(l.pair[2]) < 0)
-        segment_slice<NTMAX == 1 ? 1 : 2, NTMAX, SW, AL>(p, lds, c, claimed);
+        segment_slice<NTMAX == 1 ? 1 : 2, NTMAX, SW, AL, HINT>(p, lds, c, claimed);
       else
-        segment_slice<NTMAX, NTMAX, SW, AL>(p, lds, c, claimed);
+        segment_slice<NTMAX, NTMAX, SW, AL, HINT>(p, lds, c, claimed);
       stores_done();
       __syncthreads();
       if (tid < NTMAX && l.pair[tid] >= 0) dev_add(p.ctl + kCtlDone + l.pair[tid] / p.k, 1u);
@@ -1064,8 +1066,16 @@ hipError_t launch_layer(const LayerArgs &args, hipStream_t s) {
   // registers free.
   const int nt = a.T == 1 ? 1 : 2 * P <= a.E || a.T == 2 || a.H > kLMaxH4 ? 2 : 4;
   const bool al = a.H % kChunk == 0 && a.I % kChunk == 0;
-#define NVFP4_LAYER(SW, AL, NT) \
-  launch_kernel((layer_ffn_kernel<SW, AL, NT>), grid, block, 0, s, a)
+  // Codes past half of the 256 MB cache behind the L2s are loaded as used once
+  // (hint 2): they will not be there at the next call, and what else the call
+  // reads may.  One token of 512 experts (14 MB, four calls' weights in turn)
+  // 33.6 us with the hint and 29.0 without, 16 tokens (200 MB) 67 and 71.
+  const bool once = P * 3 * a.H * a.I * 9 / 16 > 128000000;
+#define NVFP4_LAYER(SW, AL, NT)                                                          \
+  do {                                                                                   \
+    if (once) launch_kernel((layer_ffn_kernel<SW, AL, NT, 2>), grid, block, 0, s, a);    \
+    else launch_kernel((layer_ffn_kernel<SW, AL, NT, 0>), grid, block, 0, s, a);         \
+  } while (0)
 #define NVFP4_LAYER_NT(SW, AL)                \
   do {                                        \
     if (nt == 1) NVFP4_LAYER(SW, AL, 1);      \

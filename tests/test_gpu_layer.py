@@ -277,3 +277,28 @@ def test_decode_block_with_fp8_projections():
 def test_layer_of_crowded_experts(T, H, I, E, k, Is, gate, bias, renorm):
     """Several segments per expert, of up to four tokens or (H > 4096) two."""
     test_layer(T, H, I, E, k, Is, gate, bias, renorm)
+
+
+@pytest.mark.parametrize("T,H,I,E,k,Is,gate,bias,renorm",
+                         [(1, 4160, 2336, 8, 8, 0, False, False, True),
+                          (20, 8192, 288, 4, 4, 0, False, False, True),
+                          (33, 2080, 1056, 8, 8, 32, True, False, True)])
+def test_layer_of_large_experts(T, H, I, E, k, Is, gate, bias, renorm):
+    """Codes past the size from which they are loaded as used once.  The bf16
+    outputs are the f32 ones rounded, element by element.  (Their Frobenius
+    distance to the rounded oracle is no bound of its own: an f32 deviation d,
+    here the roundings of h that fall the other way, moves a fraction d / u of
+    the elements by a step u, sqrt(d u) together; d = 3e-4, a third of the f32
+    limit, and u = 2^-7.5 give 1.3e-3.)"""
+    say("layer", T, H, I, E, k, Is, gate, bias, renorm)
+    L = Layer(T, H, I, E, k, Is, gate, bias, seed=T + H)
+    ref, ids, wts, gaps = L.ref(renorm)
+    y32, (gids, gw) = L.run(renormalize=renorm, out_dtype=torch.float32)
+    ok = clear_gaps(ids, gaps)
+    assert ok.mean() > 0.9
+    assert np.array_equal(gids.cpu().numpy()[ok], ids[ok])
+    np.testing.assert_allclose(gw.cpu().numpy()[ok], wts[ok], rtol=1e-5)
+    print("rel_frob, max/rms:", assert_close_f32(y32.cpu().numpy()[ok], ref[ok], "large experts"),
+          flush=True)
+    y16, _ = L.run(renormalize=renorm)
+    assert torch.equal(y16, y32.to(torch.bfloat16))
