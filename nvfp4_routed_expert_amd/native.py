@@ -718,6 +718,8 @@ def moe_layer_decode(x, router_w, weights: ExpertWeights, k, renormalize=True, b
         _expect("bias", bias, (E,), torch.float32)
     Is = 0
     if shared is not None:
+        if len(shared) != 3:
+            raise ValueError(f"shared must be (w_gate, w_up, w_down), got {len(shared)} tensors")
         Is = shared[0].shape[0]
         for n, t, s in zip(("shared gate", "shared up", "shared down"), shared,
                            ((Is, H), (Is, H), (H, Is))):

@@ -96,3 +96,15 @@ def test_binding_refusals():
     s = torch.zeros((32, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="shared down"):
         native.moe_layer_decode(x, r, w, 2, shared=(s, s, s))
+
+
+@pytest.mark.parametrize("n", [0, 1, 2, 4])
+def test_shared_expert_is_three_matrices(n):
+    """With two of them and a shared gate, the gate's [H] vector would be taken
+    for the [H, shared_I] down projection and read past its end."""
+    w = weights.empty_experts(4, 64, 32, "cpu")
+    x = torch.zeros((2, 64), dtype=torch.bfloat16)
+    r = torch.zeros((4, 64), dtype=torch.bfloat16)
+    s, d = torch.zeros((32, 64), dtype=torch.bfloat16), torch.zeros((64, 32), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="shared must be"):
+        native.moe_layer_decode(x, r, w, 2, shared=(s, s, d, d)[:n], shared_gate=x[0])
