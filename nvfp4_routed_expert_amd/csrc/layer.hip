@@ -296,9 +296,12 @@ __global__ __launch_bounds__(kFrontThreads) void layer_front_kernel(const LayerA
 // routing of the batch
 // ---------------------------------------------------------------------------
 
+// (at least 1: the NaN of all one bits must still count as a candidate, or a
+// token of such logits would have fewer than k and leave ids unwritten)
 __device__ __forceinline__ uint32_t order_key(float v) {
   const uint32_t b = __float_as_uint(v + 0.0f);   // -0 -> +0
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  const uint32_t key = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  return key > 1u ? key : 1u;
 }
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_u32(uint32_t x) {

@@ -302,3 +302,25 @@ def test_layer_of_large_experts(T, H, I, E, k, Is, gate, bias, renorm):
           flush=True)
     y16, _ = L.run(renormalize=renorm)
     assert torch.equal(y16, y32.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("E,k", [(5, 5), (40, 6), (600, 8)])
+def test_logits_of_any_bits_choose_valid_experts(E, k):
+    """Biases that turn every logit into the NaN of all one bits (the lowest
+    order key): k different experts all the same, since ids address weights.
+    The values are unspecified."""
+    say("nan logits", E, k)
+    L = Layer(3, 256, 32, E, k, seed=2, bias=True)
+    L.bias.view(torch.int32).fill_(-1)
+    y, (ids, _) = L.run()
+    torch.cuda.synchronize()
+    for row in ids.tolist():
+        assert len(set(row)) == k and min(row) >= 0 and max(row) < E
+    # one expert alone: it ranks last
+    L.bias.zero_()
+    L.bias.view(torch.int32)[1] = -1
+    _, (ids, _) = L.run()
+    torch.cuda.synchronize()
+    for row in ids.tolist():
+        assert len(set(row)) == k and min(row) >= 0 and max(row) < E
+        assert (1 in row) == (k == E) and (k < E or row[-1] == 1)
