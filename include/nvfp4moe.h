@@ -535,7 +535,7 @@ typedef struct {
  *   a = amax |x|;  s = a > 0 ? max(a / 448, 2^-126) : 1;  i = 1 / s;
  *   code = E4M3_rne_saturate(x * i).
  * Requires cols % 32 == 0, ld_x >= cols, ld_x % 8 == 0, block_rows 1 or 128
- * and rows * ceil(cols / 128) <= 2^27.
+ * and rows * ceil(cols / 128) <= 2^27 (f32 with block_rows 1: 2^27 - 8).
  */
 nvfp4_status fp8_block_quantize(const void *x, nvfp4_dtype x_dtype, int64_t rows, int64_t cols,
                                 int64_t ld_x, int32_t block_rows, uint8_t *codes, float *scales,

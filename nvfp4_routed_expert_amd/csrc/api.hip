@@ -1445,8 +1445,11 @@ nvfp4_status fp8_block_quantize(const void *x, nvfp4_dtype x_dtype, int64_t rows
   if (ld_x < cols || ld_x % 8 != 0)
     return fail(NVFP4_ERR_INVALID_ARGUMENT, "ld_x = %lld must be >= cols and a multiple of 8",
                 (long long)ld_x);
-  if (rows > ((int64_t)1 << 27) / ((cols + 127) / 128))
-    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "rows * ceil(cols / 128) exceeds 2^27");
+  // (a launch has less than 2^32 work-items: 32 for a 1 x 128 block of f32)
+  const bool wide = x_dtype == NVFP4_DT_F32 && block_rows == 1;
+  if (rows > (((int64_t)1 << 27) - (wide ? 8 : 0)) / ((cols + 127) / 128))
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "rows * ceil(cols / 128) exceeds 2^27%s",
+                wide ? " - 8 (f32, block_rows 1)" : "");
   CHECK_ALIGN(x);
   CHECK_ALIGN(codes);
   CHECK_ALIGN(scales);

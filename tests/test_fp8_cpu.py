@@ -132,3 +132,14 @@ def test_sizes_past_the_kernels_ranges():
                            FAKE, big, None) == 2 and "2^27" in _last()
     assert L.fp8_block_mlp(FAKE, 1 << 20, m(128 * 129, 32), m(128 * 129, 32), m(32, 128 * 129), FAKE, 0,
                            FAKE, big, None) == 2 and "2^27" in _last()
+
+
+def test_quantize_refuses_what_one_launch_cannot_hold():
+    """f32 rows of 1 x 128 blocks go eight to a workgroup of 256: past 2^27 - 8
+    of them a launch has 2^32 work-items or more."""
+    L = native.lib()
+    q = lambda dt, rows, br: L.fp8_block_quantize(FAKE, dt, rows, 128, 128, br, FAKE, FAKE, None)
+    for rows in ((1 << 27) - 7, 1 << 27):
+        assert q(native.DT_F32, rows, 1) == 2 and "2^27 - 8" in _last()
+    assert q(native.DT_BF16, (1 << 27) + 1, 1) == 2 and "2^27" in _last()
+    assert q(native.DT_F32, (1 << 27) + 1, 128) == 2 and "2^27" in _last()
