@@ -467,7 +467,8 @@ typedef struct {
  * shared_I multiples of 32 with H <= 2^13, I and shared_I <= 2^20 and
  * H * I <= 2^32.
  * workspace: moe_layer_decode_workspace_size bytes (device, 16-byte
- * aligned), scratch only (no state between calls).  The second launch waits
+ * aligned; enough for every smaller T too), scratch only (no state between
+ * calls).  The second launch waits
  * on words of it that it counts up itself, so calls or graph replays that may
  * run at the same time need separate workspaces; two that share one all the
  * same end within seconds, with NaN or wrong values in y.

@@ -1608,9 +1608,13 @@ nvfp4_status fp8_block_mlp(const void *x, int64_t T, const fp8_matrix *w_gate,
 size_t moe_layer_decode_workspace_size(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k,
                                        int64_t shared_I) {
   if (T < 1 || H < 1 || I < 1 || E < 1 || k < 1 || shared_I < 0) return 0;
-  Carver c(nullptr);
+  // (fewer tokens may take narrower slices, and so more partial rows each: the
+  // size is the largest of any batch up to T)
+  Carver c(nullptr), n(nullptr);
   carve_layer(c, T, H, I, E, k, shared_I);
-  return c.used;
+  const int64_t narrow = layer_narrow_tokens(I, k);
+  if (narrow < T) carve_layer(n, narrow, H, I, E, k, shared_I);
+  return c.used > n.used ? c.used : n.used;
 }
 
 nvfp4_status moe_layer_decode(const void *x, int64_t T, const moe_layer *layer, int renormalize,
@@ -1679,7 +1683,7 @@ nvfp4_status moe_layer_decode(const void *x, int64_t T, const moe_layer *layer, 
                       moe_layer_decode_workspace_size(T, l.H, l.I, l.E, l.k, l.shared_I)));
   if (T == 0) return NVFP4_OK;
   Carver c(workspace);
-  const LayerWs ws = carve_layer(c, T, l.H, l.I, l.E, l.k, l.shared_I);
+  const LayerWs ws = carve_layer(c, T, l.H, l.I, l.E, l.k, l.shared_I);   // (within the size checked)
   LayerArgs a = {};
   a.x = static_cast<const uint16_t *>(x);
   a.T = (int)T;

@@ -399,6 +399,7 @@ struct LayerArgs {
 bool layer_supported(int64_t T, int E, int k);
 size_t layer_ctl_bytes();
 int layer_slice(int64_t T, int64_t I, int64_t k);   // columns of I per slice
+int64_t layer_narrow_tokens(int64_t I, int64_t k);  // most tokens that take the narrower one
 size_t layer_x_bytes(int64_t T, int64_t H);          // x_pieces
 hipError_t launch_layer(const LayerArgs &a, hipStream_t s);
 

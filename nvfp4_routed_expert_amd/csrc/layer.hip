@@ -1045,8 +1045,11 @@ bool layer_supported(int64_t T, int E, int k) {
 // Columns of I per slice: whole 128-byte pieces of the down rows (256) where
 // the slices of the batch's pairs fill the GPU, else 128.
 int layer_slice(int64_t T, int64_t I, int64_t k) {
-  return T * k * ((I + 255) / 256) >= 256 ? 256 : 128;
+  return T > layer_narrow_tokens(I, k) ? 256 : 128;
 }
+// Most tokens whose slices are 128 columns (may be 0): fewer than 256 wide
+// slices in T * k pairs.
+int64_t layer_narrow_tokens(int64_t I, int64_t k) { return 255 / (k * ((I + 255) / 256)); }
 
 hipError_t launch_layer(const LayerArgs &args, hipStream_t s) {
   LayerArgs a = args;

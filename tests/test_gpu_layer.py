@@ -324,3 +324,16 @@ def test_logits_of_any_bits_choose_valid_experts(E, k):
     for row in ids.tolist():
         assert len(set(row)) == k and min(row) >= 0 and max(row) < E
         assert (1 in row) == (k == E) and (k < E or row[-1] == 1)
+
+
+def test_workspace_of_the_largest_batch():
+    """One workspace of the size of 16 tokens (slices of 256 columns) for fewer
+    (of 128, with more partial rows), each as on a workspace of its own."""
+    say("workspace of the largest batch")
+    L = Layer(16, 256, 512, 24, 8, 32, gate=True, seed=14)
+    ws = L.workspace()
+    for T in (16, 15, 3, 16, 14, 1):
+        x = L.x[:T].contiguous()
+        y, (i, w) = L.run(x=x, workspace=ws, out_dtype=torch.float32)
+        y2, (i2, w2) = L.run(x=x, workspace=L.workspace(T), out_dtype=torch.float32)
+        assert torch.equal(y, y2) and torch.equal(i, i2) and torch.equal(w, w2)

@@ -108,3 +108,14 @@ def test_shared_expert_is_three_matrices(n):
     s, d = torch.zeros((32, 64), dtype=torch.bfloat16), torch.zeros((64, 32), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="shared must be"):
         native.moe_layer_decode(x, r, w, 2, shared=(s, s, d, d)[:n], shared_gate=x[0])
+
+
+@pytest.mark.parametrize("H,I,E,k,Is", [(2048, 512, 512, 8, 512), (4096, 1536, 128, 8, 0),
+                                        (256, 2080, 6, 2, 32), (1024, 8192, 64, 1, 0),
+                                        (512, 96, 1024, 32, 544)])
+def test_workspace_of_a_batch_serves_smaller_ones(H, I, E, k, Is):
+    """A decode loop allocates once, for its largest batch: also where fewer
+    tokens take narrower slices, and so more partial rows each."""
+    size = native.lib().moe_layer_decode_workspace_size
+    sizes = [size(T, H, I, E, k, Is) for T in range(65)]
+    assert sizes == sorted(sizes) and sizes[1] > 0
