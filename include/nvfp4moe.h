@@ -33,7 +33,9 @@
  *     host structs holding device pointers; they are read during the call
  *     only.  The library allocates nothing, frees nothing and keeps no
  *     pointer after returning; scratch memory comes from `workspace`, at
- *     least the size the matching *_workspace_size query returns.
+ *     least the size the matching *_workspace_size query returns.  A query
+ *     answers for the sizes it is given, and a smaller batch may need more,
+ *     unless the call's description says otherwise.
  *   - All work is enqueued on `stream` (0 = the null stream).  No call
  *     synchronises or copies between host and device, so buffers must stay
  *     valid until the stream's work completes.
@@ -556,7 +558,8 @@ nvfp4_status fp8_block_quantize(const void *x, nvfp4_dtype x_dtype, int64_t rows
  * [M, ceil(K / 128)] (quantised once for several projections).
  * Requires K % 32 == 0, K <= 2^27, M, N <= 2^24, M * ceil(K / 128) <= 2^27.
  * workspace: fp8_block_linear_workspace_size bytes (device, 16-byte
- * aligned), scratch only; quantised: x_scales is set.
+ * aligned; enough for every smaller M too), scratch only; quantised: x_scales
+ * is set.
  */
 nvfp4_status fp8_block_linear(const void *x, const float *x_scales, int64_t M,
                               const fp8_matrix *w, void *y, nvfp4_dtype y_dtype, void *workspace,
@@ -573,8 +576,9 @@ size_t fp8_block_linear_workspace_size(int64_t M, int64_t N, int64_t K, int quan
  * H * I >= 32 * 10^6; x and h are quantised
  * online per row and 128 columns, and an element of h at a rounding boundary
  * may fall either way where that unit is used).  y [T, H] bf16 or f32.  Requires H % 32 == 0,
- * I % 32 == 0, T, H, I <= 2^24, T * ceil(H / 128) and T * ceil(I / 128) <= 2^27.  workspace: fp8_block_mlp_workspace_size
- * bytes (device, 16-byte aligned), scratch only.
+ * I % 32 == 0, T, H, I <= 2^24, T * ceil(H / 128) and T * ceil(I / 128) <= 2^27.
+ * workspace: fp8_block_mlp_workspace_size bytes (device, 16-byte aligned;
+ * enough for every smaller T too), scratch only.
  */
 nvfp4_status fp8_block_mlp(const void *x, int64_t T, const fp8_matrix *w_gate,
                            const fp8_matrix *w_up, const fp8_matrix *w_down, void *y,

@@ -269,26 +269,20 @@ SharedWs carve_shared(Carver &c, int64_t T, int64_t H, int64_t I) {
 
 constexpr int64_t kFp8MaxRows = (int64_t)1 << 24, kFp8MaxCols = (int64_t)1 << 27;
 struct Fp8LinearWs {
-  F8Plan plan;
   uint8_t *xq;
   float *xs;
   float *split;   // partial sums of a K split
 };
-// (sized for either output type: the workspace query does not take it)
+// A call's layout; partial: floats for its parts' sums (the plan's own, or, to
+// size a workspace, enough for every batch up to M).
 Fp8LinearWs carve_fp8_linear(Carver &c, int64_t M, int64_t N, int64_t K, bool quantised,
-                             OutType out) {
+                             size_t partial) {
   Fp8LinearWs w = {};
-  const bool inside = f8_gemv_supported(false, M, N, K);
-  const bool own = !quantised && !f8_gemv_quantises(false, M, N, K);   // x quantised by a launch of its own
+  // (once more rows need a launch of their own to quantise x, all larger batches do)
+  const bool own = !quantised && !f8_gemv_quantises(false, M, N, K);
   w.xq = c.take<uint8_t>(own ? (size_t)(M * K) : 0);
   w.xs = c.take<float>(own ? (size_t)(M * ((K + 127) / 128)) : 0);
-  if (!inside) {
-    w.plan = f8_gemm_plan(false, out, M, N, K);
-    const F8Plan other = f8_gemm_plan(
-        false, out == OutType::F32 ? OutType::BF16 : OutType::F32, M, N, K);
-    w.split = c.take<float>(w.plan.partial_floats > other.partial_floats ? w.plan.partial_floats
-                                                                         : other.partial_floats);
-  }
+  w.split = c.take<float>(partial);
   return w;
 }
 struct Fp8MlpWs {
@@ -300,7 +294,9 @@ struct Fp8MlpWs {
   float *xs, *hs;
   float *split;
 };
-Fp8MlpWs carve_fp8_mlp(Carver &c, int64_t T, int64_t H, int64_t I, OutType out) {
+// h_rows: tokens of bf16 h; partial as above.
+Fp8MlpWs carve_fp8_mlp(Carver &c, int64_t T, int64_t H, int64_t I, int64_t h_rows,
+                       size_t partial) {
   Fp8MlpWs w = {};
   w.few_up = f8_gemv_supported(true, T, I, H);
   w.few_down = f8_gemv_supported(false, T, H, I);
@@ -308,23 +304,30 @@ Fp8MlpWs carve_fp8_mlp(Carver &c, int64_t T, int64_t H, int64_t I, OutType out) 
   w.own_h = !w.few_up || !w.few_down || !f8_gemv_quantises(false, T, H, I);
   w.xq = c.take<uint8_t>(w.own_x ? (size_t)(T * H) : 0);
   w.xs = c.take<float>(w.own_x ? (size_t)(T * ((H + 127) / 128)) : 0);
-  w.h = c.take<uint16_t>(w.few_up ? (size_t)(T * I) : 0);
+  w.h = c.take<uint16_t>((size_t)(h_rows * I));
   w.hq = c.take<uint8_t>(w.own_h ? (size_t)(T * I) : 0);
   w.hs = c.take<float>(w.own_h ? (size_t)(T * ((I + 127) / 128)) : 0);
-  size_t n = 0;
-  if (!w.few_up) {
-    w.up_plan = f8_gemm_plan(true, OutType::BF16, T, I, H);
-    n = w.up_plan.partial_floats;
-  }
-  if (!w.few_down) {
-    w.down_plan = f8_gemm_plan(false, out, T, H, I);
-    const F8Plan other = f8_gemm_plan(
-        false, out == OutType::F32 ? OutType::BF16 : OutType::F32, T, H, I);
-    if (w.down_plan.partial_floats > n) n = w.down_plan.partial_floats;
-    if (other.partial_floats > n) n = other.partial_floats;
-  }
-  w.split = c.take<float>(n);
+  w.split = c.take<float>(partial);
   return w;
+}
+Fp8MlpWs plan_fp8_mlp(Carver &c, int64_t T, int64_t H, int64_t I, OutType out) {
+  const bool few_up = f8_gemv_supported(true, T, I, H);
+  const bool few_down = f8_gemv_supported(false, T, H, I);
+  const F8Plan up = few_up ? F8Plan() : f8_gemm_plan(true, OutType::BF16, T, I, H);
+  const F8Plan down = few_down ? F8Plan() : f8_gemm_plan(false, out, T, H, I);
+  Fp8MlpWs w = carve_fp8_mlp(c, T, H, I, few_up ? T : 0,
+                             up.partial_floats > down.partial_floats ? up.partial_floats
+                                                                     : down.partial_floats);
+  w.up_plan = up;
+  w.down_plan = down;
+  return w;
+}
+// Fewest rows, at most M, that the form for a few rows does not take (M + 1:
+// none): it ends at 0, 16, 32 or 64 rows.
+int64_t fp8_batch_rows(bool swiglu, int64_t M, int64_t N, int64_t K) {
+  for (int64_t m : {1, 17, 33, 65})
+    if (m <= M && !f8_gemv_supported(swiglu, m, N, K)) return m;
+  return M + 1;
 }
 OutType out_type(nvfp4_dtype t) { return t == NVFP4_DT_F32 ? OutType::F32 : OutType::BF16; }
 
@@ -1463,7 +1466,8 @@ nvfp4_status fp8_block_quantize(const void *x, nvfp4_dtype x_dtype, int64_t rows
 size_t fp8_block_linear_workspace_size(int64_t M, int64_t N, int64_t K, int quantised) {
   if (M < 1 || N < 1 || K < 1) return 0;
   Carver c(nullptr);
-  carve_fp8_linear(c, M, N, K, quantised != 0, OutType::BF16);
+  carve_fp8_linear(c, M, N, K, quantised != 0,
+                   f8_gemm_max_partial(false, fp8_batch_rows(false, M, N, K), M, N, K));
   return c.used;
 }
 
@@ -1485,12 +1489,14 @@ nvfp4_status fp8_block_linear(const void *x, const float *x_scales, int64_t M,
   CHECK_ALIGN(y);
   const int64_t K = w->cols, N = w->rows;
   TRY(check_fp8_batch(M, K));
-  TRY(check_workspace(workspace, workspace_bytes,
-                      fp8_block_linear_workspace_size(M, N, K, x_scales != nullptr)));
-  if (M == 0) return NVFP4_OK;
+  const bool few = f8_gemv_supported(false, M, N, K);
+  const F8Plan plan =
+      M == 0 || few ? F8Plan() : f8_gemm_plan(false, out_type(y_dtype), M, N, K);
   Carver c(workspace);
   const Fp8LinearWs ws =
-      carve_fp8_linear(c, M, N, K, x_scales != nullptr, out_type(y_dtype));
+      M == 0 ? Fp8LinearWs() : carve_fp8_linear(c, M, N, K, x_scales != nullptr, plan.partial_floats);
+  TRY(check_workspace(workspace, workspace_bytes, c.used));
+  if (M == 0) return NVFP4_OK;
   const void *xq = x;
   const float *xs = x_scales;
   if (!x_scales && !f8_gemv_quantises(false, M, N, K)) {
@@ -1498,7 +1504,7 @@ nvfp4_status fp8_block_linear(const void *x, const float *x_scales, int64_t M,
     xq = ws.xq;
     xs = ws.xs;
   }
-  if (f8_gemv_supported(false, M, N, K)) {
+  if (few) {
     const F8GemvArgs a = {xq, xs, (int)M, {w->codes, nullptr}, {w->scales, nullptr},
                           (int)N, (int)K, y, out_type(y_dtype)};
     LAUNCH(launch_f8_gemv(false, a, stream), "fp8 gemv");
@@ -1515,14 +1521,18 @@ nvfp4_status fp8_block_linear(const void *x, const float *x_scales, int64_t M,
   a.out = y;
   a.out_type = out_type(y_dtype);
   a.partial = ws.split;
-  LAUNCH(launch_f8_gemm(false, a, ws.plan, stream), "fp8 gemm");
+  LAUNCH(launch_f8_gemm(false, a, plan, stream), "fp8 gemm");
   return NVFP4_OK;
 }
 
 size_t fp8_block_mlp_workspace_size(int64_t T, int64_t H, int64_t I) {
   if (T < 1 || H < 1 || I < 1) return 0;
+  const int64_t up = fp8_batch_rows(true, T, I, H), down = fp8_batch_rows(false, T, H, I);
+  const size_t up_floats = f8_gemm_max_partial(true, up, T, I, H);
+  const size_t down_floats = f8_gemm_max_partial(false, down, T, H, I);
   Carver c(nullptr);
-  carve_fp8_mlp(c, T, H, I, OutType::BF16);
+  carve_fp8_mlp(c, T, H, I, up - 1 < T ? up - 1 : T,
+                up_floats > down_floats ? up_floats : down_floats);
   return c.used;
 }
 
@@ -1551,10 +1561,10 @@ nvfp4_status fp8_block_mlp(const void *x, int64_t T, const fp8_matrix *w_gate,
   CHECK_ALIGN(y);
   TRY(check_fp8_batch(T, H));
   TRY(check_fp8_batch(T, I));
-  TRY(check_workspace(workspace, workspace_bytes, fp8_block_mlp_workspace_size(T, H, I)));
-  if (T == 0) return NVFP4_OK;
   Carver c(workspace);
-  const Fp8MlpWs ws = carve_fp8_mlp(c, T, H, I, out_type(y_dtype));
+  const Fp8MlpWs ws = T == 0 ? Fp8MlpWs() : plan_fp8_mlp(c, T, H, I, out_type(y_dtype));
+  TRY(check_workspace(workspace, workspace_bytes, c.used));
+  if (T == 0) return NVFP4_OK;
   if (ws.own_x)
     LAUNCH(launch_f8_quantize(x, InType::BF16, T, H, H, 1, ws.xq, ws.xs, stream), "fp8 quantize");
   if (ws.few_up) {

@@ -33,6 +33,7 @@
 #include "fp8.h"
 #include "kernels.h"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace nvfp4 {
@@ -507,6 +508,35 @@ F8Plan f8_gemm_plan(bool swiglu, OutType out, int64_t M, int64_t N, int64_t K) {
   }
   best.partial_floats = best.ksplit > 1 ? (size_t)best.ksplit * M * (swiglu ? 2 * N : N) : 0;
   return best;
+}
+
+// Within 64 rows that end at a multiple of 64 the numbers of tiles stay, so the
+// estimates are lines over M whose slope is the number of parts, and the least
+// one's number of parts falls with M: that of the first row bounds all.  A split
+// saves less than one round's blocks (rounds * blocks of a round are at least
+// tiles / 256 * blocks with any number of parts, and less than one round more
+// with one), so the parts' way through memory has to cost less than that: past
+// `last` rows not even two parts do.  Past kExactRows that bound is used itself.
+size_t f8_gemm_max_partial(bool swiglu, int64_t first, int64_t M, int64_t N, int64_t K) {
+  constexpr int64_t kExactRows = 2048;
+  const int64_t KG = (K + kF8Group * kF8Block - 1) / (kF8Group * kF8Block);
+  if (KG < 2) return 0;
+  const int64_t width = swiglu ? 2 * N : N;                  // floats of a row
+  const double most = kF8Group * KG * 1.5 * 4e6 / 8.0;       // floats of all parts (1.45 us a block)
+  const double last = most / 2.0 / (double)width;
+  if (last < (double)M) M = (int64_t)last;
+  size_t floats = 0;
+  for (int64_t m = first, end; m <= M && m <= kExactRows; m = end + 1) {
+    end = (m + 63) / 64 * 64;
+    int parts = f8_gemm_plan(swiglu, OutType::BF16, m, N, K).ksplit;
+    if (!swiglu) parts = std::max(parts, f8_gemm_plan(false, OutType::F32, m, N, K).ksplit);
+    if (parts > 1) floats = std::max(floats, (size_t)parts * (end < M ? end : M) * width);
+  }
+  if (M > kExactRows) {
+    const double bound = std::min(most, 16.0 * (double)M * (double)width);
+    floats = std::max(floats, (size_t)bound);
+  }
+  return floats;
 }
 
 hipError_t launch_f8_gemm(bool swiglu, const F8GemmArgs &args, const F8Plan &pl, hipStream_t s) {

@@ -349,6 +349,8 @@ struct F8Plan {
   size_t partial_floats = 0;
 };
 F8Plan f8_gemm_plan(bool swiglu, OutType out, int64_t M, int64_t N, int64_t K);
+// At least the partial_floats of first .. M rows (0: none), for either output type.
+size_t f8_gemm_max_partial(bool swiglu, int64_t first, int64_t M, int64_t N, int64_t K);
 hipError_t launch_f8_gemm(bool swiglu, const F8GemmArgs &a, const F8Plan &pl, hipStream_t s);
 
 // The same product for a few rows (fp8gemv.hip), where _supported says so.  xs

@@ -143,3 +143,21 @@ def test_quantize_refuses_what_one_launch_cannot_hold():
         assert q(native.DT_F32, rows, 1) == 2 and "2^27 - 8" in _last()
     assert q(native.DT_BF16, (1 << 27) + 1, 1) == 2 and "2^27" in _last()
     assert q(native.DT_F32, (1 << 27) + 1, 128) == 2 and "2^27" in _last()
+
+
+MONOTONE = [(5120, 17408), (17408, 5120), (5120, 5120), (4096, 4096), (2048, 1056), (300, 2080),
+            (17, 32), (32, 18464), (4112, 1024), (8192, 3936)]
+
+
+@pytest.mark.parametrize("N,K", MONOTONE)
+def test_workspace_of_a_batch_serves_smaller_ones(N, K):
+    """A workspace allocated once, for the largest batch: also where fewer rows
+    split K further, or change their form."""
+    L = native.lib()
+    rows = list(range(260)) + [*range(260, 2600, 13), 2048, 2049, 1 << 13, 1 << 16, 1 << 20, 1 << 24]
+    rows.sort()
+    for size in (lambda m: L.fp8_block_linear_workspace_size(m, N, K, 0),
+                 lambda m: L.fp8_block_linear_workspace_size(m, N, K, 1),
+                 lambda m: L.fp8_block_mlp_workspace_size(m, K, (N + 31) // 32 * 32)):
+        sizes = [size(m) for m in rows]
+        assert sizes == sorted(sizes)

@@ -401,3 +401,37 @@ def test_large_weights_equal_their_parts(M):
     alone = native.fp8_block_mlp(x, cut(gate), cut(up), (d[:, :part].contiguous(),
                                                          ds[:, :part // 128].contiguous()))
     assert torch.equal(whole, alone)
+
+
+@pytest.mark.parametrize("N,K,rows", [(640, 4096, (455, 384, 385, 130, 65, 64, 20, 1)),
+                                      (130, 18560, (150, 64, 65, 33, 2))])
+@pytest.mark.parametrize("pre", [False, True])
+def test_workspace_of_the_largest_batch(N, K, rows, pre):
+    """One workspace, of the first batch's size, for the smaller ones (whose K
+    is split further, or whose form is another): the results of a call that
+    makes its own."""
+    say("workspace linear", N, K, pre)
+    w, ws = weight(N, K, 41)
+    size = native.lib().fp8_block_linear_workspace_size
+    space = torch.empty(size(rows[0], N, K, pre), dtype=torch.uint8, device=DEV)
+    x = acts(rows[0], K, 42).to(DEV)
+    q, s = native.fp8_block_quantize(x)
+    for M in rows:
+        for dt in (torch.float32, torch.bfloat16):
+            a = (q[:M], w, ws, s[:M].contiguous()) if pre else (x[:M], w, ws)
+            got = native.fp8_block_linear(*a, out_dtype=dt, workspace=space)
+            assert torch.equal(got, native.fp8_block_linear(*a, out_dtype=dt))
+
+
+@pytest.mark.parametrize("H,I,rows", [(512, 2080, (260, 200, 70, 65, 64, 33, 32, 1)),
+                                      (2080, 544, (130, 66, 40, 17, 5))])
+def test_mlp_workspace_of_the_largest_batch(H, I, rows):
+    say("workspace mlp", H, I)
+    mats = [weight(I, H, 51), weight(I, H, 52), weight(H, I, 53)]
+    space = torch.empty(native.lib().fp8_block_mlp_workspace_size(rows[0], H, I),
+                        dtype=torch.uint8, device=DEV)
+    x = acts(rows[0], H, 54).to(DEV)
+    for T in rows:
+        for dt in (torch.float32, torch.bfloat16):
+            got = native.fp8_block_mlp(x[:T], *mats, out_dtype=dt, workspace=space)
+            assert torch.equal(got, native.fp8_block_mlp(x[:T], *mats, out_dtype=dt))
