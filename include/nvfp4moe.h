@@ -587,6 +587,17 @@ nvfp4_status fp8_block_mlp(const void *x, int64_t T, const fp8_matrix *w_gate,
 size_t fp8_block_mlp_workspace_size(int64_t T, int64_t H, int64_t I);
 
 /*
+ * fp8_block_debug_plan: a test aid (not part of the computation).  How the
+ * FP8 product of M rows with a W [N, K] runs (gate_up: the gate and up
+ * products of fp8_block_mlp, N = I and K = H, where y_dtype is unused):
+ * returns the rows of a tile of the batch form (64, 128 or 192) and sets
+ * *parts to the parts that K is split into; 0 and 0 for the form for a few
+ * rows.
+ */
+int fp8_block_debug_plan(int gate_up, int64_t M, int64_t N, int64_t K, nvfp4_dtype y_dtype,
+                         int32_t *parts);
+
+/*
  * moe_grouped_nvfp4_ffn_debug_h: a test aid (not part of the computation)
  * for checking h element by element where it decides an integer: its bf16
  * rounding and, in W4A4, its NVFP4 codes (Qwen3.8-Flash-Next-NVFP4-SSD-

@@ -1613,6 +1613,15 @@ nvfp4_status fp8_block_mlp(const void *x, int64_t T, const fp8_matrix *w_gate,
   return NVFP4_OK;
 }
 
+int fp8_block_debug_plan(int gate_up, int64_t M, int64_t N, int64_t K, nvfp4_dtype y_dtype,
+                         int32_t *parts) {
+  *parts = 0;
+  if (f8_gemv_supported(gate_up != 0, M, N, K)) return 0;
+  const F8Plan p = f8_gemm_plan(gate_up != 0, out_type(y_dtype), M, N, K);
+  *parts = p.ksplit;
+  return p.bm;
+}
+
 // ---- moe_layer_decode --------------------------------------------------------------------
 
 size_t moe_layer_decode_workspace_size(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k,

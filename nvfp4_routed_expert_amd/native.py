@@ -116,6 +116,8 @@ def lib():
                                      ctypes.POINTER(Fp8Matrix), ctypes.POINTER(Fp8Matrix), _vp,
                                      _i32, _vp, _sz, _vp]),
             "fp8_block_mlp_workspace_size": (_sz, [_i64, _i64, _i64]),
+            "fp8_block_debug_plan": (ctypes.c_int, [ctypes.c_int, _i64, _i64, _i64, _i32,
+                                                    ctypes.POINTER(_i32)]),
             "moe_layer_decode": (_i32, [_vp, _i64, ctypes.POINTER(MoeLayerC), ctypes.c_int, _vp,
                                         _vp, _vp, _i32, _vp, _sz, _vp]),
             "moe_layer_decode_workspace_size": (_sz, [_i64, _i64, _i64, _i32, _i32, _i64]),
@@ -149,7 +151,7 @@ def exported_symbols():
             "moe_route_ffn_decode", "moe_route_ffn_decode_workspace_size",
             "moe_grouped_nvfp4_ffn_static", "moe_grouped_nvfp4_ffn_static_max_bytes",
             "fp8_block_quantize", "fp8_block_linear", "fp8_block_linear_workspace_size",
-            "fp8_block_mlp", "fp8_block_mlp_workspace_size",
+            "fp8_block_mlp", "fp8_block_mlp_workspace_size", "fp8_block_debug_plan",
             "moe_layer_decode", "moe_layer_decode_workspace_size",
             "nvfp4_set_ffn_stage_events",
             "nvfp4_set_ffn_separate_h_quant", "nvfp4_read_probe",
@@ -685,6 +687,14 @@ def fp8_block_mlp(x, gate, up, down, out_dtype=torch.bfloat16, workspace=None, o
         _check(L.fp8_block_mlp(x.data_ptr(), T, *(ctypes.byref(m) for m in mats.values()),
                                y.data_ptr(), _dt(y.dtype), ws[1], ws[2], _stream_of(dev)))
     return y
+
+
+def fp8_debug_plan(M, N, K, dtype=torch.bfloat16, gate_up=False):
+    """(rows of a tile, parts of K) of an FP8 product, (0, 0) where the form for
+    a few rows takes it."""
+    parts = _i32()
+    rows = lib().fp8_block_debug_plan(int(gate_up), M, N, K, _dt(dtype), ctypes.byref(parts))
+    return rows, parts.value
 
 
 # ---- a whole MoE layer for a few tokens ------------------------------------------

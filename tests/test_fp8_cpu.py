@@ -161,3 +161,18 @@ def test_workspace_of_a_batch_serves_smaller_ones(N, K):
                  lambda m: L.fp8_block_mlp_workspace_size(m, K, (N + 31) // 32 * 32)):
         sizes = [size(m) for m in rows]
         assert sizes == sorted(sizes)
+
+
+def test_the_shapes_of_the_gpu_tests_take_the_tiles_they_name():
+    """The plan is host code: a changed rule shows here, before the GPU tests of
+    the larger tiles lose what they are for."""
+    from test_gpu_fp8 import MLP_TILE_SHAPES, TILE_SHAPES
+    for M, N, K, rows, parts in TILE_SHAPES:
+        assert native.fp8_debug_plan(M, N, K) == (rows, parts), (M, N, K)
+    for T, H, I, rows, parts in MLP_TILE_SHAPES:
+        assert native.fp8_debug_plan(T, I, H, gate_up=True) == (rows, parts), (T, H, I)
+    for shapes in (TILE_SHAPES, MLP_TILE_SHAPES):
+        assert {(s[3], s[4] > 1) for s in shapes} == {(128, False), (128, True), (192, False),
+                                                      (192, True)}
+    assert native.fp8_debug_plan(64, 4096, 4096) == (0, 0)
+    assert native.fp8_debug_plan(32, 4096, 4096, gate_up=True) == (0, 0)

@@ -435,3 +435,47 @@ def test_mlp_workspace_of_the_largest_batch(H, I, rows):
         for dt in (torch.float32, torch.bfloat16):
             got = native.fp8_block_mlp(x[:T], *mats, out_dtype=dt, workspace=space)
             assert torch.equal(got, native.fp8_block_mlp(x[:T], *mats, out_dtype=dt))
+
+
+# ---- the larger tiles ---------------------------------------------------------------
+
+# bf16 products whose tiles have 128 and 192 rows, with K whole and in parts:
+# (M, N, K, rows of a tile, parts).  Last tiles of one row and of all but one,
+# odd N, K with a last block of 32, 96 and 128 columns, odd and even numbers of
+# blocks, parts of different lengths.
+TILE_SHAPES = [(257, 13777, 160, 128, 1), (383, 10787, 416, 128, 1), (257, 13777, 1056, 128, 1),
+               (300, 17408, 128, 128, 1), (385, 16399, 160, 192, 1), (575, 13349, 416, 192, 1),
+               (577, 13351, 288, 192, 1), (385, 17301, 736, 192, 1), (512, 17408, 512, 192, 1),
+               (2057, 34, 3968, 128, 8), (1602, 34, 4640, 128, 10), (645, 3841, 12192, 192, 4),
+               (2719, 33, 6048, 192, 12)]
+# (T, H, I, rows of a tile, parts) of the gate and up products
+MLP_TILE_SHAPES = [(65, 160, 16416, 128, 1), (191, 1056, 11008, 128, 1), (129, 32, 16416, 192, 1),
+                   (385, 160, 8224, 192, 1), (191, 96, 16416, 192, 1), (67, 4640, 5504, 128, 5),
+                   (65, 5312, 5664, 128, 4), (1345, 12160, 928, 192, 4)]
+
+
+@pytest.mark.parametrize("M,N,K,rows,parts", TILE_SHAPES)
+def test_linear_of_larger_tiles(M, N, K, rows, parts):
+    assert native.fp8_debug_plan(M, N, K) == (rows, parts)
+    test_linear(M, N, K)
+
+
+@pytest.mark.parametrize("T,H,I,rows,parts", MLP_TILE_SHAPES)
+def test_mlp_of_larger_tiles(T, H, I, rows, parts):
+    assert native.fp8_debug_plan(T, I, H, gate_up=True) == (rows, parts)
+    test_mlp(T, H, I)
+
+
+def test_rows_behind_a_larger_tile_are_left():
+    """A last tile of one row stores that row alone, bf16 and f32 parts."""
+    for M, N, K, rows, parts in ((257, 13777, 160, 128, 1), (385, 16399, 160, 192, 1),
+                                 (1345, 34, 4640, 64, 10)):
+        say("rows behind", M, N, K)
+        assert native.fp8_debug_plan(M, N, K) == (rows, parts)
+        w, ws = weight(N, K, 61)
+        x = acts(M, K, 62).to(DEV)
+        base = torch.full((M + 64, N), 7.0, dtype=torch.bfloat16, device=DEV)
+        out = base[:M]
+        native.fp8_block_linear(x, w, ws, out=out)
+        assert torch.all(base[M:] == 7.0)
+        assert torch.equal(out, native.fp8_block_linear(x, w, ws))
