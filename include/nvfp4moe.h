@@ -598,6 +598,15 @@ int fp8_block_debug_plan(int gate_up, int64_t M, int64_t N, int64_t K, nvfp4_dty
                          int32_t *parts);
 
 /*
+ * moe_layer_debug_plan: a test aid (not part of the computation).  How the
+ * routed experts of a moe_layer_decode call run: returns the columns of I of
+ * a slice (128 or 256); *tokens: the most tokens of one pass over an expert's
+ * weights (1, 2 or 4); *once: whether their codes are loaded as used once.
+ */
+int moe_layer_debug_plan(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k, int32_t *tokens,
+                         int32_t *once);
+
+/*
  * moe_grouped_nvfp4_ffn_debug_h: a test aid (not part of the computation)
  * for checking h element by element where it decides an integer: its bf16
  * rounding and, in W4A4, its NVFP4 codes (Qwen3.8-Flash-Next-NVFP4-SSD-

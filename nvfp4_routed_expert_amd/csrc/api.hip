@@ -1636,6 +1636,14 @@ size_t moe_layer_decode_workspace_size(int64_t T, int64_t H, int64_t I, int32_t 
   return c.used > n.used ? c.used : n.used;
 }
 
+int moe_layer_debug_plan(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k, int32_t *tokens,
+                         int32_t *once) {
+  const LayerPlan p = layer_plan(T, H, I, E, k);
+  *tokens = p.tokens;
+  *once = p.once;
+  return p.slice;
+}
+
 nvfp4_status moe_layer_decode(const void *x, int64_t T, const moe_layer *layer, int renormalize,
                               int32_t *topk_ids, float *topk_weights, void *y,
                               nvfp4_dtype y_dtype, void *workspace, size_t workspace_bytes,

@@ -403,6 +403,13 @@ size_t layer_ctl_bytes();
 int layer_slice(int64_t T, int64_t I, int64_t k);   // columns of I per slice
 int64_t layer_narrow_tokens(int64_t I, int64_t k);  // most tokens that take the narrower one
 size_t layer_x_bytes(int64_t T, int64_t H);          // x_pieces
+// The kernel for a batch: columns of I per slice, most tokens of a segment, H and
+// I multiples of 128, codes loaded as used once.
+struct LayerPlan {
+  int slice, tokens;
+  bool aligned, once;
+};
+LayerPlan layer_plan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k);
 hipError_t launch_layer(const LayerArgs &a, hipStream_t s);
 
 // ---- measurement aid (probe.hip) ---------------------------------------------------

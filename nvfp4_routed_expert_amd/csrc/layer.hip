@@ -1051,12 +1051,30 @@ int layer_slice(int64_t T, int64_t I, int64_t k) {
 // slices in T * k pairs.
 int64_t layer_narrow_tokens(int64_t I, int64_t k) { return 255 / (k * ((I + 255) / 256)); }
 
+LayerPlan layer_plan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k) {
+  const int64_t P = T * k;
+  LayerPlan pl;
+  pl.slice = layer_slice(T, I, k);
+  // Most tokens of a segment: few experts have more than two where the batch
+  // has under one pair per two experts, and the kernel for two keeps more
+  // registers free.
+  pl.tokens = T == 1 ? 1 : 2 * P <= E || T == 2 || H > kLMaxH4 ? 2 : 4;
+  pl.aligned = H % kChunk == 0 && I % kChunk == 0;
+  // Codes past half of the 256 MB cache behind the L2s are loaded as used once
+  // (hint 2): they will not be there at the next call, and what else the call
+  // reads may.  One token of 512 experts (14 MB, four calls' weights in turn)
+  // 33.6 us with the hint and 29.0 without, 16 tokens (200 MB) 67 and 71.
+  // (Counted per pair: an expert that several pairs chose counts each time.)
+  pl.once = P * 3 * H * I * 9 / 16 > 128000000;
+  return pl;
+}
+
 hipError_t launch_layer(const LayerArgs &args, hipStream_t s) {
   LayerArgs a = args;
   const int64_t P = (int64_t)a.T * a.k;
   auto groups = [](int rows, int per) { return (rows + per - 1) / per; };
-  const int sw = layer_slice(a.T, a.I, a.k);
-  a.n_c = groups(a.I, sw);
+  const LayerPlan pl = layer_plan(a.T, a.H, a.I, a.E, a.k);
+  a.n_c = groups(a.I, pl.slice);
   a.n_router = groups(a.E + (a.sgate ? 1 : 0), 16);
   a.n_sd = a.Is ? groups(a.H, 16 * kFfnWaves) : 0;
   a.n_su = a.Is ? groups(a.Is, 16) : 0;
@@ -1067,32 +1085,22 @@ hipError_t launch_layer(const LayerArgs &args, hipStream_t s) {
   // one workgroup per CU (256 VGPRs per wave)
   const int64_t items = a.n_sd + P * a.n_c + (int64_t)a.T * groups(a.H, kCombine);
   const dim3 grid((unsigned)(items < 256 ? items : 256)), block(kFfnThreads);
-  // Most tokens of a segment: few experts have more than two where the batch
-  // has under one pair per two experts, and the kernel for two keeps more
-  // registers free.
-  const int nt = a.T == 1 ? 1 : 2 * P <= a.E || a.T == 2 || a.H > kLMaxH4 ? 2 : 4;
-  const bool al = a.H % kChunk == 0 && a.I % kChunk == 0;
-  // Codes past half of the 256 MB cache behind the L2s are loaded as used once
-  // (hint 2): they will not be there at the next call, and what else the call
-  // reads may.  One token of 512 experts (14 MB, four calls' weights in turn)
-  // 33.6 us with the hint and 29.0 without, 16 tokens (200 MB) 67 and 71.
-  const bool once = P * 3 * a.H * a.I * 9 / 16 > 128000000;
 #define NVFP4_LAYER(SW, AL, NT)                                                          \
   do {                                                                                   \
-    if (once) launch_kernel((layer_ffn_kernel<SW, AL, NT, 2>), grid, block, 0, s, a);    \
+    if (pl.once) launch_kernel((layer_ffn_kernel<SW, AL, NT, 2>), grid, block, 0, s, a); \
     else launch_kernel((layer_ffn_kernel<SW, AL, NT, 0>), grid, block, 0, s, a);         \
   } while (0)
-#define NVFP4_LAYER_NT(SW, AL)                \
-  do {                                        \
-    if (nt == 1) NVFP4_LAYER(SW, AL, 1);      \
-    else if (nt == 2) NVFP4_LAYER(SW, AL, 2); \
-    else NVFP4_LAYER(SW, AL, 4);              \
+#define NVFP4_LAYER_NT(SW, AL)                       \
+  do {                                               \
+    if (pl.tokens == 1) NVFP4_LAYER(SW, AL, 1);      \
+    else if (pl.tokens == 2) NVFP4_LAYER(SW, AL, 2); \
+    else NVFP4_LAYER(SW, AL, 4);                     \
   } while (0)
-  if (sw == 256) {
-    if (al) NVFP4_LAYER_NT(256, true);
+  if (pl.slice == 256) {
+    if (pl.aligned) NVFP4_LAYER_NT(256, true);
     else NVFP4_LAYER_NT(256, false);
   } else {
-    if (al) NVFP4_LAYER_NT(128, true);
+    if (pl.aligned) NVFP4_LAYER_NT(128, true);
     else NVFP4_LAYER_NT(128, false);
   }
 #undef NVFP4_LAYER_NT

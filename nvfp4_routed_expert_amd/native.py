@@ -121,6 +121,8 @@ def lib():
             "moe_layer_decode": (_i32, [_vp, _i64, ctypes.POINTER(MoeLayerC), ctypes.c_int, _vp,
                                         _vp, _vp, _i32, _vp, _sz, _vp]),
             "moe_layer_decode_workspace_size": (_sz, [_i64, _i64, _i64, _i32, _i32, _i64]),
+            "moe_layer_debug_plan": (ctypes.c_int, [_i64, _i64, _i64, _i32, _i32,
+                                                    ctypes.POINTER(_i32), ctypes.POINTER(_i32)]),
             "nvfp4_set_ffn_stage_events": (None, [_vp]),
             "nvfp4_set_ffn_separate_h_quant": (None, [ctypes.c_int]),
             "nvfp4_read_probe": (_i32, [_vp, _sz, _vp, _vp]),
@@ -152,7 +154,7 @@ def exported_symbols():
             "moe_grouped_nvfp4_ffn_static", "moe_grouped_nvfp4_ffn_static_max_bytes",
             "fp8_block_quantize", "fp8_block_linear", "fp8_block_linear_workspace_size",
             "fp8_block_mlp", "fp8_block_mlp_workspace_size", "fp8_block_debug_plan",
-            "moe_layer_decode", "moe_layer_decode_workspace_size",
+            "moe_layer_decode", "moe_layer_decode_workspace_size", "moe_layer_debug_plan",
             "nvfp4_set_ffn_stage_events",
             "nvfp4_set_ffn_separate_h_quant", "nvfp4_read_probe",
             "nvfp4_status_string", "nvfp4_last_error"]
@@ -760,6 +762,14 @@ def moe_layer_decode(x, router_w, weights: ExpertWeights, k, renormalize=True, b
                                   _ptr(route_out[0]), _ptr(route_out[1]), _ptr(y), _dt(y.dtype),
                                   _ptr(ws), ws.numel() * ws.element_size(), _stream_of(dev)))
     return y, route_out
+
+
+def layer_debug_plan(T, H, I, E, k):
+    """(columns of a slice of I, most tokens of one pass over an expert's weights,
+    codes loaded as used once) of a moe_layer_decode call."""
+    tokens, once = _i32(), _i32()
+    cols = lib().moe_layer_debug_plan(T, H, I, E, k, ctypes.byref(tokens), ctypes.byref(once))
+    return cols, tokens.value, bool(once.value)
 
 
 def ffn_debug_h(workspace, T, H, I, E, k, act=W4A16, given=False):

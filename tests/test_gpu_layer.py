@@ -337,3 +337,122 @@ def test_workspace_of_the_largest_batch():
         y, (i, w) = L.run(x=x, workspace=ws, out_dtype=torch.float32)
         y2, (i2, w2) = L.run(x=x, workspace=L.workspace(T), out_dtype=torch.float32)
         assert torch.equal(y, y2) and torch.equal(i, i2) and torch.equal(w, w2)
+
+
+# ---- every compiled kernel ---------------------------------------------------------
+
+# A case for each kernel that CASES and the tests above leave out: (T, H, I, E, k,
+# Is, gate, bias, renorm) and what it takes: columns of a slice, H and I multiples
+# of 128, tokens of a pass over an expert's weights, codes loaded as used once.
+KERNEL_CASES = [((5, 512, 256, 5, 2, 0, False, False, True), (128, True, 4, False)),
+                ((1, 320, 96, 5, 5, 32, True, False, True), (128, False, 1, False)),
+                ((1, 4096, 2432, 8, 8, 0, False, False, True), (128, True, 1, True)),
+                ((2, 4096, 1280, 16, 8, 0, False, True, True), (128, True, 2, True)),
+                ((15, 1280, 512, 8, 8, 0, False, False, False), (128, True, 4, True)),
+                ((15, 1376, 480, 8, 8, 96, False, False, True), (128, False, 4, True)),
+                ((1, 256, 2048, 32, 32, 64, False, False, True), (256, True, 1, False)),
+                ((1, 288, 2080, 32, 32, 0, False, False, True), (256, False, 1, False)),
+                ((1, 1280, 8192, 8, 8, 0, False, False, True), (256, True, 1, True)),
+                ((1, 1312, 8224, 8, 8, 0, False, True, True), (256, False, 1, True)),
+                ((16, 256, 512, 256, 8, 512, True, False, True), (256, True, 2, False)),
+                ((2, 1312, 1056, 33, 32, 0, False, False, False), (256, False, 2, True)),
+                ((16, 1280, 512, 256, 8, 0, False, False, True), (256, True, 2, True))]
+
+
+@pytest.mark.parametrize("case,plan", KERNEL_CASES)
+def test_every_kernel(case, plan):
+    T, H, I, E, k = case[:5]
+    cols, tokens, once = native.layer_debug_plan(T, H, I, E, k)
+    assert (cols, H % 128 == 0 and I % 128 == 0, tokens, once) == plan
+    test_layer_of_large_experts(*case)
+
+
+# ---- activations of very different magnitude ---------------------------------------
+
+
+def integer_stack(e, n, k, seed, clear_first):
+    """e NVFP4 matrices of random codes, block scales 0.5, 1 or 2 and global
+    scale 2^-4: sums of their products with small integers times a power of two
+    are exact in fp32.  clear_first: column 0 is zero."""
+    r = np.random.default_rng(seed)
+    codes = r.integers(0, 256, (e, n, k // 2), np.uint8)
+    if clear_first:
+        codes[:, :, 0] &= 0xF0
+    scales = r.choice(np.array([0x30, 0x38, 0x40], np.uint8), (e, n, k // 16))
+    put = lambda a: torch.from_numpy(a).to(DEV)
+    return put(codes), put(scales), torch.full((e,), 2.0 ** -4, device=DEV)
+
+
+@pytest.mark.parametrize("T,H,I,E,k", [(9, 320, 96, 1, 1), (10, 1056, 288, 2, 2),
+                                       (2, 4128, 128, 2, 1), (6, 512, 256, 3, 2)])
+def test_tokens_of_different_magnitudes(T, H, I, E, k):
+    """x is used as two pieces by way of a power of two per token, h of one per
+    token and slice.  Tokens from 2^-20 to 2^20 in one segment, one that is all
+    zero, and one whose channel 0 is 2^20 times the rest (with zero weights in
+    that channel: the rest, at the bottom of the pieces' range, must count in
+    full).  x is small integers, gate and up are exact, so h is known up to expf;
+    the down sums may be off by the pieces' 2^-21 of the largest h, 2^-12 of a
+    block's largest product (16 products aligned to it with about 17 bits, twice
+    for the two pieces) and the roundings of fp32.  Row by row."""
+    say("magnitudes", T, H, I, E, k)
+    r = np.random.default_rng(T)
+    exps = np.array([0, -20, 20, 7, 0, -9, 14, 0, 3, -14])[:T]
+    base = r.integers(-3, 4, (T, H)).astype(np.float64)
+    base[:, 1] = 3.0
+    base[min(7, T - 1)] = 0.0
+    x = base * 2.0 ** exps[:, None]
+    outlier = 4 if T > 4 else 0
+    x[outlier, 0] = 2.0 ** 20
+    L = Layer(T, H, I, E, k, seed=3)
+    L.mats = [integer_stack(E, I, H, 1, True), integer_stack(E, I, H, 2, True),
+              integer_stack(E, H, I, 3, False)]
+    L.w = native.ExpertWeights(*L.mats[0], *L.mats[1], *L.mats[2])
+    y, (ids, wts) = L.run(x=torch.from_numpy(x).to(torch.bfloat16).to(DEV), out_dtype=torch.float32)
+    y, ids, wts = y.double().cpu().numpy(), ids.cpu().numpy(), wts.double().cpu().numpy()
+    ref, bound = np.zeros((T, H)), np.zeros((T, H))
+    for e in np.unique(ids):
+        t, j = np.nonzero(ids == e)
+        gw, uw, dw = (nvfp4_values(*m, e) for m in L.mats)
+        g, u = x[t] @ gw.T, x[t] @ uw.T
+        with np.errstate(over="ignore"):
+            h64 = g / (1 + np.exp(-g)) * u
+        dh = np.abs(h64) * 2.0 ** -20                # expf, a division and a product in fp32
+        lo, hi, h = bf16(h64 - dh), bf16(h64 + dh), bf16(h64)
+        off = np.abs(hi - lo) + np.abs(h).max(1, keepdims=True) * 2.0 ** -21
+        prod = np.abs(h[:, None, :] * dw[None])      # [tokens, H, I]
+        blocks = prod.reshape(len(t), H, I // 16, 16).max(3).sum(2) * 2.0 ** -12
+        err = blocks + prod.sum(2) * (I + 8) * 2.0 ** -24 + off @ np.abs(dw).T
+        w = wts[t, j][:, None]
+        ref[t] += w * (h @ dw.T)
+        bound[t] += w * err
+    bound += np.abs(ref) * 2.0 ** -20                # weights, combine
+    assert np.all(np.abs(y - ref) <= bound), np.abs(y - ref).max(1) / bound.max(1)
+    assert np.all(y[min(7, T - 1)] == 0.0)
+
+
+def test_decode_block_against_the_host():
+    """The same chain as above, every step against its 64-bit form on the
+    previous step's device output: the projection within its fp32 sums and one
+    bf16 rounding, the MLP within 2^-8 in the Frobenius norm (a bf16 rounding
+    of every element is at most that, typically a third of it, which leaves
+    room for the few h whose rounding the fp32 sums decide)."""
+    import test_gpu_fp8 as f8
+    say("block against the host")
+    T, H, I = 6, 512, 640
+    L = Layer(T, H, 256, 16, 4, 128, gate=True, seed=12)
+    g = torch.Generator().manual_seed(5)
+    ws = [native.fp8_block_quantize((torch.randn(*s, generator=g) * 0.05).to(DEV), 128)
+          for s in ((H, H), (I, H), (I, H), (H, I))]
+    a = native.fp8_block_linear(L.x, *ws[0])
+    y, _ = L.run(x=a)
+    z = native.fp8_block_mlp(y, *ws[1:])
+    q, s = f8.quantize_ref(L.x.float().cpu().numpy(), 1)
+    ref, mag = f8.linear_ref(q * f8.spread(s, T, H, 1), f8.values(*ws[0], 128))
+    f8.check_out(a, ref, f8.sum_bound(mag, H), "projection")
+    q, s = f8.quantize_ref(y.float().cpu().numpy(), 1)
+    gate, up, down = (f8.values(*w, 128) for w in ws[1:])
+    xv = q * f8.spread(s, T, H, 1)
+    gt, ut = xv @ gate.T, xv @ up.T
+    q, s = f8.quantize_ref(bf16(gt / (1 + np.exp(-gt)) * ut).astype(np.float32), 1)
+    ref = (q * f8.spread(s, T, I, 1)) @ down.T
+    assert np.linalg.norm(z.double().cpu().numpy() - ref) <= 2.0 ** -8 * np.linalg.norm(ref)

@@ -119,3 +119,23 @@ def test_workspace_of_a_batch_serves_smaller_ones(H, I, E, k, Is):
     size = native.lib().moe_layer_decode_workspace_size
     sizes = [size(T, H, I, E, k, Is) for T in range(65)]
     assert sizes == sorted(sizes) and sizes[1] > 0
+
+
+def test_the_gpu_tests_reach_every_kernel():
+    """The rule that picks a kernel is host code: a changed one shows here, before
+    the GPU tests lose what they are for."""
+    import test_gpu_layer as g
+    reached = set()
+    cases = [c for c, _ in g.KERNEL_CASES]
+    for f in (g.test_layer, g.test_layer_of_crowded_experts, g.test_layer_of_large_experts):
+        for m in f.pytestmark:
+            if m.name == "parametrize":
+                cases += m.args[1]
+    for T, H, I, E, k, *_ in cases:
+        cols, tokens, once = native.layer_debug_plan(T, H, I, E, k)
+        reached.add((cols, H % 128 == 0 and I % 128 == 0, tokens, once))
+    assert reached == {(c, a, t, o) for c in (128, 256) for a in (False, True)
+                       for t in (1, 2, 4) for o in (False, True)}
+    for (T, H, I, E, k, *_), plan in g.KERNEL_CASES:
+        cols, tokens, once = native.layer_debug_plan(T, H, I, E, k)
+        assert (cols, H % 128 == 0 and I % 128 == 0, tokens, once) == plan
