@@ -1627,6 +1627,7 @@ int fp8_block_debug_plan(int gate_up, int64_t M, int64_t N, int64_t K, nvfp4_dty
 size_t moe_layer_decode_workspace_size(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k,
                                        int64_t shared_I) {
   if (T < 1 || H < 1 || I < 1 || E < 1 || k < 1 || shared_I < 0) return 0;
+  T = layer_max_tokens(k) < T ? layer_max_tokens(k) : T;   // (larger batches are refused)
   // (fewer tokens may take narrower slices, and so more partial rows each: the
   // size is the largest of any batch up to T)
   Carver c(nullptr), n(nullptr);

@@ -398,6 +398,7 @@ struct LayerArgs {
   // down items
   int n_router, n_su, n_c, n_sd;
 };
+int64_t layer_max_tokens(int k);
 bool layer_supported(int64_t T, int E, int k);
 size_t layer_ctl_bytes();
 int layer_slice(int64_t T, int64_t I, int64_t k);   // columns of I per slice

@@ -1038,9 +1038,10 @@ __global__ __launch_bounds__(kFfnThreads, 2) void layer_ffn_kernel(const LayerAr
 
 size_t layer_x_bytes(int64_t T, int64_t H) { return (size_t)T * 2 * layer_chunks((int)H) * kChunk; }
 size_t layer_ctl_bytes() { return kCtlWords * sizeof(uint32_t); }
+int64_t layer_max_tokens(int k) { return kLMaxP / k < kLMaxT ? kLMaxP / k : kLMaxT; }
 bool layer_supported(int64_t T, int E, int k) {
-  return T >= 0 && T <= kLMaxT && E >= 1 && E <= kLMaxE && k >= 1 && k <= kLMaxK && k <= E &&
-         T * k <= kLMaxP;
+  return E >= 1 && E <= kLMaxE && k >= 1 && k <= kLMaxK && k <= E && T >= 0 &&
+         T <= layer_max_tokens(k);
 }
 // Columns of I per slice: whole 128-byte pieces of the down rows (256) where
 // the slices of the batch's pairs fill the GPU, else 128.

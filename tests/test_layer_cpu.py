@@ -139,3 +139,12 @@ def test_the_gpu_tests_reach_every_kernel():
     for (T, H, I, E, k, *_), plan in g.KERNEL_CASES:
         cols, tokens, once = native.layer_debug_plan(T, H, I, E, k)
         assert (cols, H % 128 == 0 and I % 128 == 0, tokens, once) == plan
+
+
+def test_workspace_of_a_batch_that_is_refused():
+    """A batch past the call's limits is not made to allocate for its size before
+    it is refused: the query answers for the largest one that is not."""
+    size = native.lib().moe_layer_decode_workspace_size
+    assert size(1 << 16, 4096, 1536, 128, 8, 0) == size(64, 4096, 1536, 128, 8, 0)
+    assert size(65, 256, 64, 64, 32, 32) == size(16, 256, 64, 64, 32, 32)
+    assert size(1 << 40, 256, 64, 8, 2, 32) == size(64, 256, 64, 8, 2, 32)
