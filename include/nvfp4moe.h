@@ -556,7 +556,8 @@ nvfp4_status fp8_block_quantize(const void *x, nvfp4_dtype x_dtype, int64_t rows
  * contiguous, quantised online exactly as fp8_block_quantize with
  * block_rows = 1.  x_scales set: x holds E4M3 codes [M, K] with x_scales
  * [M, ceil(K / 128)] (quantised once for several projections).
- * Requires K % 32 == 0, K <= 2^27, M, N <= 2^24, M * ceil(K / 128) <= 2^27.
+ * Requires K % 32 == 0, K <= 2^27, M, N <= 2^24, M * ceil(K / 128) <= 2^27;
+ * y must not overlap x.
  * workspace: fp8_block_linear_workspace_size bytes (device, 16-byte
  * aligned; enough for every smaller M too), scratch only; quantised: x_scales
  * is set.

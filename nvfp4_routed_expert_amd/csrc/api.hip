@@ -1404,6 +1404,11 @@ nvfp4_status moe_grouped_nvfp4_ffn_static(const void *x, int64_t T, int64_t H, i
                                ws, need > 0 ? kStaticScratchBytes : 0, stream);
 }
 
+static bool ranges_overlap(const void *a, size_t na, const void *b, size_t nb) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return p < q + nb && q < p + na;
+}
+
 // ---- FP8 block-scaled operators ---------------------------------------------------------
 
 static nvfp4_status check_fp8_matrix(const fp8_matrix *w, const char *name) {
@@ -1499,7 +1504,11 @@ nvfp4_status fp8_block_linear(const void *x, const float *x_scales, int64_t M,
   if (M == 0) return NVFP4_OK;
   const void *xq = x;
   const float *xs = x_scales;
-  if (!x_scales && !f8_gemv_quantises(false, M, N, K)) {
+  const bool reads_x = x_scales || f8_gemv_quantises(false, M, N, K);   // the product itself
+  if (reads_x && ranges_overlap(x, (size_t)(M * K) * (x_scales ? 1 : 2), y,
+                                (size_t)(M * N) * (y_dtype == NVFP4_DT_F32 ? 4 : 2)))
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "y overlaps x");
+  if (!reads_x) {
     LAUNCH(launch_f8_quantize(x, InType::BF16, M, K, K, 1, ws.xq, ws.xs, stream), "fp8 quantize");
     xq = ws.xq;
     xs = ws.xs;

@@ -642,7 +642,8 @@ def fp8_block_linear(x, codes, scales, x_scales=None, out_dtype=torch.bfloat16, 
                      out=None):
     """y [M, N] = x [M, K] . W [N, K]^T for FP8 W (codes, scales from
     fp8_block_quantize(w, 128)).  x: bf16, quantised online per row and 128
-    columns; or with x_scales, the codes of fp8_block_quantize(x)."""
+    columns; or with x_scales, the codes of fp8_block_quantize(x).  out must
+    not overlap x."""
     if x.dim() != 2 or x.shape[1] != codes.shape[-1]:
         raise ValueError(f"x {tuple(x.shape)} does not match W {tuple(codes.shape)}")
     M, K = x.shape

@@ -176,3 +176,17 @@ def test_the_shapes_of_the_gpu_tests_take_the_tiles_they_name():
                                                       (192, True)}
     assert native.fp8_debug_plan(64, 4096, 4096) == (0, 0)
     assert native.fp8_debug_plan(32, 4096, 4096, gate_up=True) == (0, 0)
+
+
+def test_linear_refuses_an_output_over_its_input():
+    """Where the product reads x itself, workgroups that are done would overwrite
+    what others still quantise."""
+    L = native.lib()
+    m = native.Fp8Matrix(1 << 30, 1 << 29, 256, 256)
+    lin = lambda x, y, xs=None, M=4, dt=0: L.fp8_block_linear(
+        x, xs, M, ctypes.byref(m), y, dt, None, 0, None)
+    row = 512                                                   # bytes of a bf16 row
+    for y in (1 << 20, (1 << 20) + 3 * row, (1 << 20) - 3 * row):
+        assert lin(1 << 20, y) == 1 and "overlap" in _last()
+    for y in ((1 << 20) + 3 * 256, (1 << 20) - 7 * 512):        # codes in, f32 out
+        assert lin(1 << 20, y, xs=1 << 25, dt=1) == 1 and "overlap" in _last()
