@@ -460,11 +460,18 @@ typedef struct {
  * with shared the BF16 expert of moe_shared_expert_ffn (its h rounded to
  * bf16) and c_t = 1, or sigmoid(x_t . shared_gate).  Sums are fp32, except
  * that the routed products of 16 elements sharing a weight scale are summed
- * by the matrix unit with about 17 bits and use x and h to 2^-22 of their
+ * by the matrix unit with about 17 bits and use x and h to 2^-21 of their
  * row's (h: slice's) largest magnitude; y [T, H] is rounded once (bf16
  * round-to-nearest-even, or f32).  Logits are summed in
  * this call's own order: ids equal moe_router_topk's except where two logits
  * differ by less than the sums' rounding.  Calls are deterministic.
+ * An expert's weights are read once for every four of its tokens (two where
+ * H > 4096 or 2 T k <= E).  The separate calls, moe_router_topk,
+ * moe_grouped_nvfp4_ffn and moe_shared_expert_ffn, can be faster, so measure
+ * from about ten tokens on: with H = 2048, I = 512, k = 8 and a shared expert of
+ * E = 512 experts one token takes 28 us here and 48 there, 8 tokens 53 and 55,
+ * 12 tokens 71 and 59, 32 tokens 107 and 99, 64 tokens 162 and 241; 64 tokens
+ * of E = 8, k = 2 without one 70 and 42 (H = 4096, I = 1536: 114 and 173).
  * Requires T <= 64, T * k <= 512, 1 <= k <= 32, k <= E <= 1024, and H, I,
  * shared_I multiples of 32 with H <= 2^13, I and shared_I <= 2^20 and
  * H * I <= 2^32.
@@ -552,7 +559,7 @@ nvfp4_status fp8_block_quantize(const void *x, nvfp4_dtype x_dtype, int64_t rows
  * rows the products go through the FP8 matrix unit, which aligns the 128 of a
  * block to the largest with about 12 bits: off by up to 2^-10 of that
  * product per block, 1.5e-5 of y in the Frobenius norm on Gaussian data (a
- * bf16 rounding is 2^-9 of an element).  x_scales NULL: x is bf16 [M, K],
+ * bf16 rounding is up to 2^-8 of an element).  x_scales NULL: x is bf16 [M, K],
  * contiguous, quantised online exactly as fp8_block_quantize with
  * block_rows = 1.  x_scales set: x holds E4M3 codes [M, K] with x_scales
  * [M, ceil(K / 128)] (quantised once for several projections).
@@ -572,12 +579,14 @@ size_t fp8_block_linear_workspace_size(int64_t M, int64_t N, int64_t K, int quan
  * w_up [I, H], w_down [H, I]:
  *   h_t = bf16_rne( silu(x_t Wg^T) * (x_t Wu^T) )
  *   y_t = h_t Wd^T
- * both products as fp8_block_linear computes them, gate and up as for bf16 y
- * (and through the FP8 matrix unit too for H > 18432, and for T > 32 with
- * H * I >= 32 * 10^6; x and h are quantised
- * online per row and 128 columns, and an element of h at a rounding boundary
- * may fall either way where that unit is used).  y [T, H] bf16 or f32.  Requires H % 32 == 0,
- * I % 32 == 0, T, H, I <= 2^24, T * ceil(H / 128) and T * ceil(I / 128) <= 2^27.
+ * both products as fp8_block_linear computes them, gate and up as for bf16 y,
+ * also where y is f32 (and through the FP8 matrix unit too for H > 18432, and
+ * for T > 32 with H * I >= 32 * 10^6); x and h are quantised online per row and
+ * 128 columns, and where that unit is used an element of h at a rounding
+ * boundary may fall either way, by one E4M3 step (512 tokens, 5120 / 17408: y
+ * 2.2e-3 off the formula in the Frobenius norm, 1.7e-3 with fp32 sums, both
+ * with bf16 y).  y [T, H] bf16 or f32.  Requires H % 32 == 0, I % 32 == 0,
+ * T, H, I <= 2^24, T * ceil(H / 128) and T * ceil(I / 128) <= 2^27.
  * workspace: fp8_block_mlp_workspace_size bytes (device, 16-byte aligned;
  * enough for every smaller T too), scratch only.
  */

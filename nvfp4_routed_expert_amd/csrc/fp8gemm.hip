@@ -21,8 +21,9 @@
 // g takes granules g and g + 4.  Rows past a matrix, granules past K and blocks
 // past a part's end lie behind a buffer's bound, where loads return zeros.
 //
-// Measured: M = 2048, N = 17408, K = 5120 207 to 213 us, 1.71 to 1.76 PFLOP/s
-// (a library product of the same size with one scale per matrix: 207 us);
+// Measured: M = 2048, N = 17408, K = 5120 206 us, 1.77 PFLOP/s, over many calls
+// in a row (the first 30 after idling take 214 to 240; a library product of the
+// same size with one scale per matrix: 207 us);
 // 8192 x 8192 x 8192 582 to 600 us, 1.84 to 1.89 PFLOP/s.  With the loads taken
 // out the loop alone runs at 2.1 to 2.5 PFLOP/s: issue of the FMAs and LDS reads
 // beside the MFMAs, then L2 misses, then 11 us a round of tiles to start and
@@ -51,11 +52,12 @@ __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f +
 // 4 x FM tiles of 16 x 16 per wave: 256 weight rows (SWIGLU: 128 of either
 // matrix) and FM x 32 tokens per workgroup.
 //
-// EXACT (fp32 outputs, and few rows of a K too long for the few-row form): the fp8 matrix instruction aligns the products of a
-// sum to the largest with about 12 bits (measured: errors up to 2^-10.9 of the
-// largest product, 1.5e-5 of the result in the Frobenius norm on Gaussian
-// data, the same for the 32- and the 128-wide form), far below a bf16
-// output's rounding (2^-9) but not below an fp32 one's.  The exact form turns
+// EXACT (fp32 outputs, and up to 64 rows whose K is too long or whose weights
+// are too large for the few-row form): the fp8 matrix instruction aligns the
+// products of a sum to the largest with about 12 bits (measured: errors up to
+// 2^-10.9 of the largest product, 1.5e-5 of the result in the Frobenius norm on
+// Gaussian data, the same for the 32- and the 128-wide form), far below a bf16
+// output's rounding (up to 2^-8) but not below an fp32 one's.  The exact form turns
 // the codes into fp16 (exactly) and multiplies them on the fp16 unit, with
 // exact products and fp32 sums, at half the rate.
 template <int FM, bool SWIGLU, bool EXACT>

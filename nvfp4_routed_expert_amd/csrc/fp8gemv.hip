@@ -45,7 +45,8 @@ __host__ __device__ constexpr int64_t gv_x_bytes(int64_t M, int64_t KB) {
   return M * (KB * (kF8Block + 4) + 16);
 }
 
-// STREAM: the weights are loaded as used once.  XT: groups of 8 rows of x.  XCAP: bytes for x (QX) or its scales.
+// STREAM: the weights are loaded as used once.  XT: groups of 8 rows of x.
+// XCAP: bytes for x (QX) or its scales.
 template <int XT, bool SWIGLU, bool QX, int NW, int D, int XCAP, bool STREAM>
 __global__ __launch_bounds__(64 * NW) void f8_gemv_kernel(const F8GemvArgs p) {
 #pragma clang fp contract(off)

@@ -389,7 +389,7 @@ struct LayerArgs {
   // workspace
   uint32_t *ctl;                // control words
   float *logits;                // [T, E (+ 1)]
-  uint8_t *x_pieces;            // [T][2][H padded to 1024] E4M3 pieces of x
+  uint8_t *x_pieces;            // [T][2][H padded to 512, 1024 at least] E4M3 pieces of x
   int32_t *x_shift;             // [T]
   uint16_t *sh;                 // [T][sh_ld] the shared expert's h
   int sh_ld;

@@ -39,7 +39,8 @@
 // row's four E4M3 scales in four FMAs.  The operand's other
 // eight rows carry a second piece of the activations: with a power-of-two
 // scale per token, x = hi + lo / 16 with hi and lo E4M3 represents a bf16 x
-// to 2^-22 of the token's largest |x|.  Per KiB of codes that is one MFMA and
+// to 2^-21 of the token's largest |x| (exactly, but for elements below 2^-13 of
+// it).  Per KiB of codes that is one MFMA and
 // a dozen VALU instructions for each token (unpacking to bf16 pairs and
 // v_dot2 takes 45, which bound the kernel), so a batch's tokens cost little
 // beside the stream.  The unit's sums of 16 products keep about 17 bits
@@ -201,9 +202,9 @@ __device__ __forceinline__ void tile_dot(const uint16_t *const (&w)[NM], const u
 // The first launch: workgroups of 16 waves, each a tile of 16 rows and 16 tokens
 // (K split over the waves, their sums added in wave order in LDS), so all of a
 // tile's loads are in flight at once.  (A tile for every token: 17 us at 32
-// tokens, H = 4096, where only eight workgroups had rows of the router.)  Tiles: the router rows (experts, then the
-// shared gate's row) and the shared expert's gate/up rows; then a workgroup
-// per token for its x pieces.
+// tokens, H = 4096, where only eight workgroups had rows of the router.)
+// Tiles: the router rows (experts, then the shared gate's row) and the shared
+// expert's gate/up rows; then a workgroup per token for its x pieces.
 constexpr int kFrontWaves = 16;
 constexpr int kFrontThreads = 64 * kFrontWaves;
 
@@ -641,7 +642,8 @@ struct FfnLds {
   };
   uint32_t item;
   __attribute__((aligned(16))) uint8_t h_pieces[NTMAX * 2 * SW];
-  __attribute__((aligned(16))) uint8_t x_pieces[NTMAX == 4 ? 8 * kLMaxH4 : NTMAX * 2 * kLMaxH];   // of a segment
+  // of a segment
+  __attribute__((aligned(16))) uint8_t x_pieces[NTMAX == 4 ? 8 * kLMaxH4 : NTMAX * 2 * kLMaxH];
 };
 
 // One slice of one segment.  Wave w takes the gate and up rows of the slice's
@@ -652,8 +654,8 @@ struct FfnLds {
 // by 128 bytes (two chunks), whole cache lines (64-byte rows, the two halves of
 // a line a chunk apart: 341 us against 277 for 32 tokens of 128 experts); a
 // fragment loaded straight into registers touches a line per lane, which takes
-// the address unit 64 cycles or more instead of 16 (348 us).  Granules are XOR-swizzled by the row.  A chunk's operands
-// are read while the chunk before it is multiplied, and a pair of chunks' slot
+// the address unit 64 cycles or more instead of 16 (348 us).  Granules are
+// XOR-swizzled by the row.  A chunk's operands are read while the chunk before it is multiplied, and a pair of chunks' slot
 // is loaded again once both are read.  The scales of four chunks come in one
 // 8-byte load per lane and matrix and go through the wave's own LDS, where a
 // lane finds its four for each chunk.
