@@ -35,7 +35,8 @@
  *     pointer after returning; scratch memory comes from `workspace`, at
  *     least the size the matching *_workspace_size query returns.  A query
  *     answers for the sizes it is given, and a smaller batch may need more,
- *     unless the call's description says otherwise.
+ *     unless the call's description says otherwise.  Calls that may run at
+ *     the same time need workspaces of their own.
  *   - All work is enqueued on `stream` (0 = the null stream).  No call
  *     synchronises or copies between host and device, so buffers must stay
  *     valid until the stream's work completes.
@@ -602,7 +603,7 @@ size_t fp8_block_mlp_workspace_size(int64_t T, int64_t H, int64_t I);
  * products of fp8_block_mlp, N = I and K = H, where y_dtype is unused):
  * returns the rows of a tile of the batch form (64, 128 or 192) and sets
  * *parts to the parts that K is split into; 0 and 0 for the form for a few
- * rows.
+ * rows, and for sizes below 1.  parts may be NULL.
  */
 int fp8_block_debug_plan(int gate_up, int64_t M, int64_t N, int64_t K, nvfp4_dtype y_dtype,
                          int32_t *parts);
@@ -612,6 +613,7 @@ int fp8_block_debug_plan(int gate_up, int64_t M, int64_t N, int64_t K, nvfp4_dty
  * routed experts of a moe_layer_decode call run: returns the columns of I of
  * a slice (128 or 256); *tokens: the most tokens of one pass over an expert's
  * weights (1, 2 or 4); *once: whether their codes are loaded as used once.
+ * All 0 for sizes below 1; either pointer may be NULL.
  */
 int moe_layer_debug_plan(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k, int32_t *tokens,
                          int32_t *once);

@@ -1624,10 +1624,10 @@ nvfp4_status fp8_block_mlp(const void *x, int64_t T, const fp8_matrix *w_gate,
 
 int fp8_block_debug_plan(int gate_up, int64_t M, int64_t N, int64_t K, nvfp4_dtype y_dtype,
                          int32_t *parts) {
-  *parts = 0;
-  if (f8_gemv_supported(gate_up != 0, M, N, K)) return 0;
-  const F8Plan p = f8_gemm_plan(gate_up != 0, out_type(y_dtype), M, N, K);
-  *parts = p.ksplit;
+  const bool batch = M >= 1 && N >= 1 && K >= 1 && !f8_gemv_supported(gate_up != 0, M, N, K);
+  F8Plan p;
+  if (batch) p = f8_gemm_plan(gate_up != 0, out_type(y_dtype), M, N, K);
+  if (parts) *parts = batch ? p.ksplit : 0;
   return p.bm;
 }
 
@@ -1648,9 +1648,10 @@ size_t moe_layer_decode_workspace_size(int64_t T, int64_t H, int64_t I, int32_t 
 
 int moe_layer_debug_plan(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k, int32_t *tokens,
                          int32_t *once) {
-  const LayerPlan p = layer_plan(T, H, I, E, k);
-  *tokens = p.tokens;
-  *once = p.once;
+  LayerPlan p = {0, 0, false, false};
+  if (T >= 1 && H >= 1 && I >= 1 && E >= 1 && k >= 1) p = layer_plan(T, H, I, E, k);
+  if (tokens) *tokens = p.tokens;
+  if (once) *once = p.once;
   return p.slice;
 }
 

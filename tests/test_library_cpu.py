@@ -351,3 +351,16 @@ def test_bench_and_entry_reference_only_defined_names():
         used = {n.id for n in ast.walk(tree) if isinstance(n, ast.Name) and isinstance(n.ctx, ast.Load)}
         assert not (used - bound), (fname, sorted(used - bound))
 
+
+
+def test_debug_plans_of_nonsense_sizes():
+    """The test aids answer 0 for sizes that no call takes, and take NULL."""
+    L = native.lib()
+    a, b = ctypes.c_int32(7), ctypes.c_int32(7)
+    for T, H, I, E, k in ((1, 256, 64, 8, 0), (1, 256, 0, 8, 2), (0, 256, 64, 8, 2), (1, 0, 64, 8, 2)):
+        assert L.moe_layer_debug_plan(T, H, I, E, k, ctypes.byref(a), ctypes.byref(b)) == 0
+        assert a.value == 0 and b.value == 0
+    assert L.moe_layer_debug_plan(1, 256, 64, 8, 2, None, None) == 128
+    for M, N, K in ((0, 64, 64), (100, 0, 64), (100, 64, 0)):
+        assert L.fp8_block_debug_plan(0, M, N, K, 0, ctypes.byref(a)) == 0 and a.value == 0
+    assert L.fp8_block_debug_plan(1, 100, 64, 64, 0, None) == 64
