@@ -609,6 +609,112 @@ int fp8_block_debug_plan(int gate_up, int64_t M, int64_t N, int64_t K, nvfp4_dty
                          int32_t *parts);
 
 /*
+ * int8 operators: dense projections kept in 8-bit integers beside NVFP4 and
+ * FP8.  An int8 matrix X [R, C] is
+ *   codes  int8 [R, C]  row-major, two's complement;
+ *   scales float [R]    one per row: a token of activations, an output
+ *          channel of a weight;
+ *   and X[r][c] = code * scale[r].  Scales must be finite.  C must be a
+ * multiple of 32, R is any number of rows.
+ */
+typedef struct {
+  const int8_t *codes;     /* [rows, cols]                                  */
+  const float *scales;     /* [rows]                                        */
+  int64_t rows, cols;
+} int8_matrix;
+
+/*
+ * int8_quantize: quantise x [rows, cols] (row stride ld_x elements, bf16 or
+ * f32) to int8 codes [rows, cols] and one scale per row.  Per row, every step
+ * an fp32 operation rounded to nearest-even:
+ *   a = amax |x|;  s = a > 0 ? max(a / 127, 2^-126) : 1;  i = 1 / s;
+ *   code = rint(x * i)   (-127 .. 127).
+ * codes and scales must not overlap x or each other.  Requires cols % 32 == 0,
+ * cols <= 2^27, rows <= 2^24, ld_x >= cols, ld_x % 8 == 0, ld_x <= 2^31.
+ */
+nvfp4_status int8_quantize(const void *x, nvfp4_dtype x_dtype, int64_t rows, int64_t cols,
+                           int64_t ld_x, int8_t *codes, float *scales, hipStream_t stream);
+
+/*
+ * int8_linear: y [M, N] = x [M, K] . W^T for an int8 W [N, K]:
+ *   y[m][n] = (fp32(sum_k xq[m][k] wq[n][k]) * s_x[m]) * s_w[n]
+ * with the sum exact in 32-bit integers and each of the three fp32 steps
+ * rounded to nearest-even; y is bf16 (a fourth rounding) or f32.  The result
+ * is the same bits whatever M, and however the sum is split.
+ * x_scales NULL: x is bf16 [M, K], contiguous, quantised online exactly as
+ * int8_quantize.  x_scales set: x holds int8 codes [M, K] with x_scales [M]
+ * (quantised once for several projections, or by rms_norm_quantize).
+ * Requires K % 32 == 0, K <= 131040 (the sum of codes -128 stays below 2^31),
+ * M, N <= 2^24, M * N <= 2^36; y must not overlap x, x_scales or the
+ * workspace.
+ * workspace: int8_linear_workspace_size bytes (device, 16-byte aligned;
+ * enough for every smaller M too), scratch only; quantised: x_scales is set.
+ */
+nvfp4_status int8_linear(const void *x, const float *x_scales, int64_t M, const int8_matrix *w,
+                         void *y, nvfp4_dtype y_dtype, void *workspace, size_t workspace_bytes,
+                         hipStream_t stream);
+size_t int8_linear_workspace_size(int64_t M, int64_t N, int64_t K, int quantised);
+
+/*
+ * int8_mlp: the gated MLP with int8 weights, x [T, H], w_gate and w_up [I, H],
+ * w_down [H, I]:
+ *   h_t = bf16_rne( silu(x_t Wg^T) * (x_t Wu^T) )
+ *   y_t = h_t Wd^T
+ * both products as int8_linear computes them (gate and up in fp32), h
+ * quantised per token as int8_quantize does.  x as in int8_linear: bf16 with
+ * x_scales NULL, or codes and their scales.  y [T, H] bf16 or f32.  Requires
+ * H % 32 == 0, I % 32 == 0, H, I <= 131040, T <= 2^24, T * H and T * I <= 2^36;
+ * y must not overlap x, x_scales or the workspace.
+ * workspace: int8_mlp_workspace_size bytes (device, 16-byte aligned; enough
+ * for every smaller T too), scratch only.
+ */
+nvfp4_status int8_mlp(const void *x, const float *x_scales, int64_t T, const int8_matrix *w_gate,
+                      const int8_matrix *w_up, const int8_matrix *w_down, void *y,
+                      nvfp4_dtype y_dtype, void *workspace, size_t workspace_bytes,
+                      hipStream_t stream);
+size_t int8_mlp_workspace_size(int64_t T, int64_t H, int64_t I, int quantised);
+
+/*
+ * rms_norm_quantize: the front of a block.  Per token t of T, over H columns:
+ *   v = x, or round(x + residual) to the residual's type, stored in
+ *       residual_out;
+ *   r = fp32(1 / sqrt(sum_c v[c]^2 / H + eps))   (sum, quotients and root in
+ *       64 bits);
+ *   n[c] = (v[c] * r) * weight[c]   (two fp32 products);
+ *   y = n rounded to y's type; codes and scales = n quantised, without a
+ *       rounding to y's type before, as fp8_block_quantize with block_rows = 1
+ *       (RMS_NORM_FP8: E4M3 codes [T, H], scales [T, ceil(H / 128)]) or as
+ *       int8_quantize (RMS_NORM_INT8: codes [T, H], scales [T]) does.
+ * Any of y and the codes may be left out, not both.  x, residual and
+ * residual_out have row strides (elements, >= H, multiples of 8, <= 2^31); y,
+ * codes and scales are contiguous.  residual_out may be residual itself (same
+ * stride), or x (same stride and type).  Apart from that, no output's span of
+ * memory (first to last element) may overlap that of an input or another
+ * output.  Requires H % 32 == 0, H <= 2^27, T <= 2^24, 2^-126 <= eps < 2^126.
+ */
+typedef enum { RMS_NORM_NO_CODES = 0, RMS_NORM_FP8 = 1, RMS_NORM_INT8 = 2 } rms_norm_codes;
+typedef struct {
+  const void *x;
+  nvfp4_dtype x_dtype;
+  int64_t ld_x;
+  const void *residual;          /* NULL: none                              */
+  nvfp4_dtype residual_dtype;    /* of residual_out too                     */
+  int64_t ld_residual;
+  void *residual_out;            /* NULL without a residual                 */
+  int64_t ld_residual_out;
+  const void *weight;            /* [H]                                     */
+  nvfp4_dtype weight_dtype;
+  double eps;
+  void *y;                       /* NULL: none                              */
+  nvfp4_dtype y_dtype;
+  rms_norm_codes format;
+  void *codes;                   /* NULL for RMS_NORM_NO_CODES              */
+  float *scales;
+} rms_norm_args;
+nvfp4_status rms_norm_quantize(const rms_norm_args *args, int64_t T, int64_t H,
+                               hipStream_t stream);
+
+/*
  * moe_layer_debug_plan: a test aid (not part of the computation).  How the
  * routed experts of a moe_layer_decode call run: returns the columns of I of
  * a slice (128 or 256); *tokens: the most tokens of one pass over an expert's

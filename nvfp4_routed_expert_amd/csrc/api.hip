@@ -331,6 +331,34 @@ int64_t fp8_batch_rows(bool swiglu, int64_t M, int64_t N, int64_t K) {
 }
 OutType out_type(nvfp4_dtype t) { return t == NVFP4_DT_F32 ? OutType::F32 : OutType::BF16; }
 
+constexpr int64_t kInt8MaxRows = (int64_t)1 << 24, kInt8MaxCols = 131040;
+constexpr int64_t kInt8MaxOutputs = (int64_t)1 << 36;
+constexpr int64_t kRowMaxCols = (int64_t)1 << 27, kRowMaxStride = (int64_t)1 << 31;
+struct Int8LinearWs {
+  int8_t *xq;
+  float *xs;
+};
+Int8LinearWs carve_int8_linear(Carver &c, int64_t M, int64_t K, bool quantised) {
+  Int8LinearWs w = {};
+  w.xq = c.take<int8_t>(quantised ? 0 : (size_t)(M * K));
+  w.xs = c.take<float>(quantised ? 0 : (size_t)M);
+  return w;
+}
+struct Int8MlpWs {
+  int8_t *xq, *hq;
+  uint16_t *h;
+  float *xs, *hs;
+};
+Int8MlpWs carve_int8_mlp(Carver &c, int64_t T, int64_t H, int64_t I, bool quantised) {
+  Int8MlpWs w = {};
+  w.xq = c.take<int8_t>(quantised ? 0 : (size_t)(T * H));
+  w.xs = c.take<float>(quantised ? 0 : (size_t)T);
+  w.h = c.take<uint16_t>((size_t)(T * I));
+  w.hq = c.take<int8_t>((size_t)(T * I));
+  w.hs = c.take<float>((size_t)T);
+  return w;
+}
+
 struct LayerWs {
   uint32_t *ctl;
   float *logits;
@@ -1629,6 +1657,307 @@ int fp8_block_debug_plan(int gate_up, int64_t M, int64_t N, int64_t K, nvfp4_dty
   if (batch) p = f8_gemm_plan(gate_up != 0, out_type(y_dtype), M, N, K);
   if (parts) *parts = batch ? p.ksplit : 0;
   return p.bm;
+}
+
+// ---- int8 operators, RMS norm ----------------------------------------------------------
+
+static bool is_dtype(nvfp4_dtype t) { return t == NVFP4_DT_BF16 || t == NVFP4_DT_F32; }
+static size_t dtype_size(nvfp4_dtype t) { return t == NVFP4_DT_F32 ? 4 : 2; }
+static InType in_type(nvfp4_dtype t) { return t == NVFP4_DT_F32 ? InType::F32 : InType::BF16; }
+
+static nvfp4_status check_stride(int64_t ld, int64_t cols, const char *name) {
+  if (ld < cols || ld % 8 != 0)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "%s = %lld must be >= the columns and a multiple of 8",
+                name, (long long)ld);
+  if (ld > kRowMaxStride)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s = %lld exceeds 2^31", name, (long long)ld);
+  return NVFP4_OK;
+}
+static nvfp4_status check_rows(int64_t rows, int64_t cols, const char *rows_name,
+                               const char *cols_name) {
+  if (rows < 0)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "%s = %lld < 0", rows_name, (long long)rows);
+  if (rows > kInt8MaxRows)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s exceeds 2^24", rows_name);
+  TRY(check_k(cols, cols_name));
+  if (cols > kRowMaxCols)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s exceeds 2^27", cols_name);
+  return NVFP4_OK;
+}
+
+nvfp4_status int8_quantize(const void *x, nvfp4_dtype x_dtype, int64_t rows, int64_t cols,
+                           int64_t ld_x, int8_t *codes, float *scales, hipStream_t stream) {
+  g_last_error[0] = 0;
+  if (rows > 0) {   // (an empty batch may pass NULL for its empty arrays)
+    CHECK_NULL(x);
+    CHECK_NULL(codes);
+    CHECK_NULL(scales);
+  }
+  if (!is_dtype(x_dtype))
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "x_dtype %d is not BF16 or F32", (int)x_dtype);
+  TRY(check_rows(rows, cols, "rows", "cols"));
+  TRY(check_stride(ld_x, cols, "ld_x"));
+  CHECK_ALIGN(x);
+  CHECK_ALIGN(codes);
+  CHECK_ALIGN(scales);
+  if (rows == 0) return NVFP4_OK;
+  const size_t nx = (size_t)((rows - 1) * ld_x + cols) * dtype_size(x_dtype);
+  const size_t nc = (size_t)(rows * cols), ns = (size_t)rows * 4;
+  if (ranges_overlap(codes, nc, x, nx) || ranges_overlap(scales, ns, x, nx) ||
+      ranges_overlap(codes, nc, scales, ns))
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "codes or scales overlap x or each other");
+  LAUNCH(launch_i8_quantize(x, in_type(x_dtype), rows, cols, ld_x, codes, scales, stream),
+         "int8 quantize");
+  return NVFP4_OK;
+}
+
+static nvfp4_status check_int8_matrix(const int8_matrix *w, const char *name) {
+  if (!w) return fail(NVFP4_ERR_INVALID_ARGUMENT, "%s is NULL", name);
+  if (!w->codes || !w->scales)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "%s->%s is NULL", name, w->codes ? "scales" : "codes");
+  if (w->rows < 1) return fail(NVFP4_ERR_INVALID_ARGUMENT, "%s->rows < 1", name);
+  if (w->rows > kInt8MaxRows)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s->rows exceeds 2^24", name);
+  TRY(check_k(w->cols, name));
+  if (w->cols > kInt8MaxCols)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s->cols exceeds 131040 (32-bit sums)", name);
+  if (!aligned16(w->codes) || !aligned16(w->scales))
+    return fail(NVFP4_ERR_MISALIGNED, "%s->%s is not 16-byte aligned", name,
+                aligned16(w->codes) ? "scales" : "codes");
+  return NVFP4_OK;
+}
+// The batch of an int8 product: M rows of K columns (codes, or bf16) and
+// outputs of the width of y, or of anything the call keeps per row.
+static nvfp4_status check_int8_batch(int64_t M, int64_t width, const char *name) {
+  if (M < 0) return fail(NVFP4_ERR_INVALID_ARGUMENT, "%s = %lld < 0", name, (long long)M);
+  if (M > kInt8MaxRows) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s exceeds 2^24", name);
+  if (M * width > kInt8MaxOutputs)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%lld rows of %lld exceed 2^36", (long long)M,
+                (long long)width);
+  return NVFP4_OK;
+}
+// y may lie over nothing that the call reads or keeps.
+static nvfp4_status check_int8_output(const void *y, size_t ny, const void *x, size_t nx,
+                                      const float *xs, size_t ns, const void *ws, size_t nw) {
+  if (ranges_overlap(y, ny, x, nx)) return fail(NVFP4_ERR_INVALID_ARGUMENT, "y overlaps x");
+  if (xs && ranges_overlap(y, ny, xs, ns))
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "y overlaps x_scales");
+  if (nw > 0 && ranges_overlap(y, ny, ws, nw))
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "y overlaps the workspace");
+  return NVFP4_OK;
+}
+
+size_t int8_linear_workspace_size(int64_t M, int64_t N, int64_t K, int quantised) {
+  if (M < 1 || N < 1 || K < 1 || M > kInt8MaxRows || N > kInt8MaxRows || K > kInt8MaxCols) return 0;
+  Carver c(nullptr);
+  carve_int8_linear(c, M, K, quantised != 0);
+  return c.used;
+}
+
+nvfp4_status int8_linear(const void *x, const float *x_scales, int64_t M, const int8_matrix *w,
+                         void *y, nvfp4_dtype y_dtype, void *workspace, size_t workspace_bytes,
+                         hipStream_t stream) {
+  g_last_error[0] = 0;
+  if (M > 0) {
+    CHECK_NULL(x);
+    CHECK_NULL(y);
+  }
+  TRY(check_int8_matrix(w, "w"));
+  const int64_t K = w->cols, N = w->rows;
+  TRY(check_int8_batch(M, N, "M"));
+  if (!is_dtype(y_dtype))
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "y_dtype %d is not BF16 or F32", (int)y_dtype);
+  CHECK_ALIGN(x);
+  CHECK_ALIGN(x_scales);
+  CHECK_ALIGN(y);
+  Carver c(workspace);
+  const Int8LinearWs ws =
+      M == 0 ? Int8LinearWs() : carve_int8_linear(c, M, K, x_scales != nullptr);
+  TRY(check_workspace(workspace, workspace_bytes, c.used));
+  if (M == 0) return NVFP4_OK;
+  TRY(check_int8_output(y, (size_t)(M * N) * dtype_size(y_dtype), x,
+                        (size_t)(M * K) * (x_scales ? 1 : 2), x_scales, (size_t)M * 4, workspace,
+                        c.used));
+  I8GemmArgs a = {};
+  a.x = static_cast<const int8_t *>(x);
+  a.xs = x_scales;
+  if (!x_scales) {
+    LAUNCH(launch_i8_quantize(x, InType::BF16, M, K, K, ws.xq, ws.xs, stream), "int8 quantize");
+    a.x = ws.xq;
+    a.xs = ws.xs;
+  }
+  a.M = M;
+  a.w[0] = w->codes;
+  a.ws[0] = w->scales;
+  a.N = (int)N;
+  a.K = (int)K;
+  a.out = y;
+  a.out_type = out_type(y_dtype);
+  LAUNCH(launch_i8_gemm(false, a, stream), "int8 gemm");
+  return NVFP4_OK;
+}
+
+size_t int8_mlp_workspace_size(int64_t T, int64_t H, int64_t I, int quantised) {
+  if (T < 1 || H < 1 || I < 1 || T > kInt8MaxRows || H > kInt8MaxCols || I > kInt8MaxCols) return 0;
+  Carver c(nullptr);
+  carve_int8_mlp(c, T, H, I, quantised != 0);
+  return c.used;
+}
+
+nvfp4_status int8_mlp(const void *x, const float *x_scales, int64_t T, const int8_matrix *w_gate,
+                      const int8_matrix *w_up, const int8_matrix *w_down, void *y,
+                      nvfp4_dtype y_dtype, void *workspace, size_t workspace_bytes,
+                      hipStream_t stream) {
+  g_last_error[0] = 0;
+  if (T > 0) {
+    CHECK_NULL(x);
+    CHECK_NULL(y);
+  }
+  TRY(check_int8_matrix(w_gate, "w_gate"));
+  TRY(check_int8_matrix(w_up, "w_up"));
+  TRY(check_int8_matrix(w_down, "w_down"));
+  const int64_t H = w_gate->cols, I = w_gate->rows;
+  if (w_up->rows != I || w_up->cols != H || w_down->rows != H || w_down->cols != I)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT,
+                "w_up is not [%lld, %lld] or w_down not [%lld, %lld] (from w_gate)", (long long)I,
+                (long long)H, (long long)H, (long long)I);
+  TRY(check_int8_batch(T, H > I ? H : I, "T"));
+  if (!is_dtype(y_dtype))
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "y_dtype %d is not BF16 or F32", (int)y_dtype);
+  CHECK_ALIGN(x);
+  CHECK_ALIGN(x_scales);
+  CHECK_ALIGN(y);
+  Carver c(workspace);
+  const Int8MlpWs ws = T == 0 ? Int8MlpWs() : carve_int8_mlp(c, T, H, I, x_scales != nullptr);
+  TRY(check_workspace(workspace, workspace_bytes, c.used));
+  if (T == 0) return NVFP4_OK;
+  TRY(check_int8_output(y, (size_t)(T * H) * dtype_size(y_dtype), x,
+                        (size_t)(T * H) * (x_scales ? 1 : 2), x_scales, (size_t)T * 4, workspace,
+                        c.used));
+  I8GemmArgs a = {};
+  a.x = static_cast<const int8_t *>(x);
+  a.xs = x_scales;
+  if (!x_scales) {
+    LAUNCH(launch_i8_quantize(x, InType::BF16, T, H, H, ws.xq, ws.xs, stream), "int8 quantize");
+    a.x = ws.xq;
+    a.xs = ws.xs;
+  }
+  a.M = T;
+  a.w[0] = w_gate->codes;
+  a.ws[0] = w_gate->scales;
+  a.w[1] = w_up->codes;
+  a.ws[1] = w_up->scales;
+  a.N = (int)I;
+  a.K = (int)H;
+  a.out = ws.h;
+  a.out_type = OutType::BF16;
+  LAUNCH(launch_i8_gemm(true, a, stream), "int8 gate/up");
+  LAUNCH(launch_i8_quantize(ws.h, InType::BF16, T, I, I, ws.hq, ws.hs, stream), "int8 quantize");
+  I8GemmArgs d = {};
+  d.x = ws.hq;
+  d.xs = ws.hs;
+  d.M = T;
+  d.w[0] = w_down->codes;
+  d.ws[0] = w_down->scales;
+  d.N = (int)H;
+  d.K = (int)I;
+  d.out = y;
+  d.out_type = out_type(y_dtype);
+  LAUNCH(launch_i8_gemm(false, d, stream), "int8 down");
+  return NVFP4_OK;
+}
+
+nvfp4_status rms_norm_quantize(const rms_norm_args *a, int64_t T, int64_t H, hipStream_t stream) {
+  g_last_error[0] = 0;
+  if (!a) return fail(NVFP4_ERR_INVALID_ARGUMENT, "args is NULL");
+  if (a->format != RMS_NORM_NO_CODES && a->format != RMS_NORM_FP8 && a->format != RMS_NORM_INT8)
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "format %d is not a rms_norm_codes", (int)a->format);
+  const bool codes = a->format != RMS_NORM_NO_CODES, res = a->residual != nullptr;
+  if (!is_dtype(a->x_dtype) || !is_dtype(a->weight_dtype) || (res && !is_dtype(a->residual_dtype)) ||
+      (a->y && !is_dtype(a->y_dtype)))
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "a dtype is not BF16 or F32");
+  TRY(check_rows(T, H, "T", "H"));
+  if (T > 0) {
+    if (!a->x) return fail(NVFP4_ERR_INVALID_ARGUMENT, "x is NULL");
+    if (!a->y && !codes)
+      return fail(NVFP4_ERR_INVALID_ARGUMENT, "y is NULL and no codes are asked for");
+    if (codes != (a->codes != nullptr) || codes != (a->scales != nullptr))
+      return fail(NVFP4_ERR_INVALID_ARGUMENT, "codes and scales do not go with format %d",
+                  (int)a->format);
+    if (res != (a->residual_out != nullptr))
+      return fail(NVFP4_ERR_INVALID_ARGUMENT, "residual and residual_out go together");
+  }
+  if (!a->weight) return fail(NVFP4_ERR_INVALID_ARGUMENT, "weight is NULL");
+  if (!(a->eps >= 0x1p-126 && a->eps < 0x1p126))
+    return fail(NVFP4_ERR_INVALID_ARGUMENT, "eps = %g is not in [2^-126, 2^126)", a->eps);
+  TRY(check_stride(a->ld_x, H, "ld_x"));
+  if (res) {
+    TRY(check_stride(a->ld_residual, H, "ld_residual"));
+    TRY(check_stride(a->ld_residual_out, H, "ld_residual_out"));
+  }
+  const struct {
+    const void *at;
+    const char *name;
+  } all[] = {{a->x, "x"},         {a->residual, "residual"}, {a->residual_out, "residual_out"},
+             {a->weight, "weight"}, {a->y, "y"},             {a->codes, "codes"},
+             {a->scales, "scales"}};
+  for (const auto &e : all)
+    if (!aligned16(e.at))
+      return fail(NVFP4_ERR_MISALIGNED, "%s is not 16-byte aligned", e.name);
+  if (T == 0) return NVFP4_OK;
+
+  // spans: three inputs, then four outputs (0 bytes: not there)
+  const size_t cb = (size_t)((H + 127) / 128), n = (size_t)(T * H);
+  auto span = [&](int64_t ld, nvfp4_dtype t) {
+    return (size_t)((T - 1) * ld + H) * dtype_size(t);
+  };
+  const struct {
+    const void *at;
+    size_t bytes;
+    const char *name;
+  } mem[] = {{a->x, span(a->ld_x, a->x_dtype), "x"},
+             {a->residual, res ? span(a->ld_residual, a->residual_dtype) : 0, "residual"},
+             {a->weight, (size_t)H * dtype_size(a->weight_dtype), "weight"},
+             {a->residual_out, res ? span(a->ld_residual_out, a->residual_dtype) : 0,
+              "residual_out"},
+             {a->y, a->y ? n * dtype_size(a->y_dtype) : 0, "y"},
+             {a->codes, codes ? n : 0, "codes"},
+             {a->scales, (a->format == RMS_NORM_FP8 ? cb : codes ? 1 : 0) * (size_t)T * 4,
+              "scales"}};
+  const bool over_res = res && a->residual_out == a->residual && a->ld_residual_out == a->ld_residual;
+  const bool over_x = res && a->residual_out == a->x && a->ld_residual_out == a->ld_x &&
+                      a->residual_dtype == a->x_dtype;
+  for (int o = 3; o < 7; ++o)
+    for (int i = 0; i < o; ++i) {
+      if (mem[o].bytes == 0 || mem[i].bytes == 0) continue;
+      if (o == 3 && ((i == 0 && over_x) || (i == 1 && over_res))) continue;
+      if (ranges_overlap(mem[o].at, mem[o].bytes, mem[i].at, mem[i].bytes))
+        return fail(NVFP4_ERR_INVALID_ARGUMENT, "%s overlaps %s", mem[o].name, mem[i].name);
+    }
+  RowArgs r = {};
+  r.x = a->x;
+  r.ld_x = a->ld_x;
+  r.res = a->residual;
+  r.ld_res = a->ld_residual;
+  r.res_out = a->residual_out;
+  r.ld_out = a->ld_residual_out;
+  r.w = a->weight;
+  r.eps = a->eps;
+  r.y = a->y;
+  r.codes = static_cast<uint8_t *>(a->codes);
+  r.scales = a->scales;
+  r.rows = T;
+  r.cols = (int)H;
+  r.x_f32 = a->x_dtype == NVFP4_DT_F32;
+  r.res_f32 = a->residual_dtype == NVFP4_DT_F32;
+  r.w_f32 = a->weight_dtype == NVFP4_DT_F32;
+  r.y_f32 = a->y_dtype == NVFP4_DT_F32;
+  LAUNCH(launch_rms_norm(r, a->format == RMS_NORM_FP8    ? RowCodes::FP8
+                            : a->format == RMS_NORM_INT8 ? RowCodes::INT8
+                                                         : RowCodes::NONE,
+                         stream),
+         "rms norm");
+  return NVFP4_OK;
 }
 
 // ---- moe_layer_decode --------------------------------------------------------------------

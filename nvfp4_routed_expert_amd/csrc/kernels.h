@@ -370,6 +370,43 @@ bool f8_gemv_supported(bool swiglu, int64_t M, int64_t N, int64_t K);
 bool f8_gemv_quantises(bool swiglu, int64_t M, int64_t N, int64_t K);
 hipError_t launch_f8_gemv(bool swiglu, const F8GemvArgs &a, hipStream_t s);
 
+// ---- row operators and int8 products (rowquant.hip, int8gemm.hip) ------------------------
+
+enum class RowCodes : int { NONE = 0, FP8 = 1, INT8 = 2 };
+struct RowArgs {
+  const void *x;
+  int64_t ld_x;
+  const void *res;        // null: none
+  int64_t ld_res;
+  void *res_out;          // may be res or x
+  int64_t ld_out;
+  const void *w;          // [cols]
+  double eps;
+  void *y;                // [rows, cols] or null
+  uint8_t *codes;         // [rows, cols]
+  float *scales;
+  int64_t rows;
+  int cols;
+  int waves;              // of a row (set by the launcher)
+  bool x_f32, res_f32, w_f32, y_f32;
+};
+hipError_t launch_rms_norm(const RowArgs &a, RowCodes codes, hipStream_t s);
+// x [rows, cols] (row stride ld) -> int8 codes [rows, cols] and a scale per row.
+hipError_t launch_i8_quantize(const void *x, InType t, int64_t rows, int64_t cols, int64_t ld,
+                              int8_t *codes, float *scales, hipStream_t s);
+
+struct I8GemmArgs {
+  const int8_t *x;        // codes [M, K]
+  const float *xs;        // [M]
+  int64_t M;
+  const int8_t *w[2];     // codes [N, K]; matrix 1 is `up` in the gate/up form
+  const float *ws[2];     // [N]
+  int N, K;
+  void *out;              // [M, N]; gate/up form: h, bf16
+  OutType out_type;
+};
+hipError_t launch_i8_gemm(bool swiglu, const I8GemmArgs &a, hipStream_t s);
+
 // ---- a whole MoE layer for a few tokens (layer.hip) --------------------------------
 
 struct LayerArgs {

@@ -10,6 +10,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -40,6 +41,18 @@ class Matrix(ctypes.Structure):
 
 class Fp8Matrix(ctypes.Structure):
     _fields_ = [("codes", _vp), ("scales", _vp), ("rows", _i64), ("cols", _i64)]
+
+
+class Int8Matrix(ctypes.Structure):
+    _fields_ = [("codes", _vp), ("scales", _vp), ("rows", _i64), ("cols", _i64)]
+
+
+class RmsNormArgs(ctypes.Structure):
+    _fields_ = [("x", _vp), ("x_dtype", _i32), ("ld_x", _i64), ("residual", _vp),
+                ("residual_dtype", _i32), ("ld_residual", _i64), ("residual_out", _vp),
+                ("ld_residual_out", _i64), ("weight", _vp), ("weight_dtype", _i32),
+                ("eps", ctypes.c_double), ("y", _vp), ("y_dtype", _i32), ("format", _i32),
+                ("codes", _vp), ("scales", _vp)]
 
 
 class ExpertWeightsC(ctypes.Structure):
@@ -118,6 +131,15 @@ def lib():
             "fp8_block_mlp_workspace_size": (_sz, [_i64, _i64, _i64]),
             "fp8_block_debug_plan": (ctypes.c_int, [ctypes.c_int, _i64, _i64, _i64, _i32,
                                                     ctypes.POINTER(_i32)]),
+            "int8_quantize": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp]),
+            "int8_linear": (_i32, [_vp, _vp, _i64, ctypes.POINTER(Int8Matrix), _vp, _i32, _vp, _sz,
+                                   _vp]),
+            "int8_linear_workspace_size": (_sz, [_i64, _i64, _i64, ctypes.c_int]),
+            "int8_mlp": (_i32, [_vp, _vp, _i64, ctypes.POINTER(Int8Matrix),
+                                ctypes.POINTER(Int8Matrix), ctypes.POINTER(Int8Matrix), _vp, _i32,
+                                _vp, _sz, _vp]),
+            "int8_mlp_workspace_size": (_sz, [_i64, _i64, _i64, ctypes.c_int]),
+            "rms_norm_quantize": (_i32, [ctypes.POINTER(RmsNormArgs), _i64, _i64, _vp]),
             "moe_layer_decode": (_i32, [_vp, _i64, ctypes.POINTER(MoeLayerC), ctypes.c_int, _vp,
                                         _vp, _vp, _i32, _vp, _sz, _vp]),
             "moe_layer_decode_workspace_size": (_sz, [_i64, _i64, _i64, _i32, _i32, _i64]),
@@ -154,6 +176,8 @@ def exported_symbols():
             "moe_grouped_nvfp4_ffn_static", "moe_grouped_nvfp4_ffn_static_max_bytes",
             "fp8_block_quantize", "fp8_block_linear", "fp8_block_linear_workspace_size",
             "fp8_block_mlp", "fp8_block_mlp_workspace_size", "fp8_block_debug_plan",
+            "int8_quantize", "int8_linear", "int8_linear_workspace_size", "int8_mlp",
+            "int8_mlp_workspace_size", "rms_norm_quantize",
             "moe_layer_decode", "moe_layer_decode_workspace_size", "moe_layer_debug_plan",
             "nvfp4_set_ffn_stage_events",
             "nvfp4_set_ffn_separate_h_quant", "nvfp4_read_probe",
@@ -698,6 +722,174 @@ def fp8_debug_plan(M, N, K, dtype=torch.bfloat16, gate_up=False):
     parts = _i32()
     rows = lib().fp8_block_debug_plan(int(gate_up), M, N, K, _dt(dtype), ctypes.byref(parts))
     return rows, parts.value
+
+
+# ---- int8 operators, RMS norm ------------------------------------------------------
+
+
+def _int8_matrix(name, codes, scales):
+    """The C view of int8 codes [N, K] and their scales [N]."""
+    if codes.dim() != 2:
+        raise ValueError(f"{name} codes must be [rows, cols], got {tuple(codes.shape)}")
+    n, k = codes.shape
+    if codes.dtype is not torch.int8:
+        raise TypeError(f"{name} codes is {codes.dtype}, expected torch.int8")
+    _expect(f"{name} scales", scales, (n,), torch.float32)
+    return Int8Matrix(codes.data_ptr(), scales.data_ptr(), n, k)
+
+
+def _rows_stride(name, x, dev=None):
+    """Row stride of a matrix of rows (unit column stride, on dev)."""
+    if dev is not None and x.device != dev:
+        raise ValueError(f"{name} is on {x.device}, x on {dev}")
+    rows, cols = x.shape
+    ld, step = x.stride()
+    if cols > 1 and step != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return ld if rows > 1 else _round_up(cols, 8)
+
+
+def int8_quantize(x, out=None):
+    """Quantise x [rows, cols] (bf16/f32, cuda, unit column stride) to int8
+    with one fp32 scale per row (a token, or an output channel of a weight).
+    Returns (codes int8 [rows, cols], scales [rows])."""
+    if x.dim() != 2:
+        raise ValueError(f"x must be [rows, cols], got {tuple(x.shape)}")
+    rows, cols = x.shape
+    ld = _rows_stride("x", x)
+    if out is None:
+        dev = _device_of(x)
+        codes = torch.empty((rows, cols), dtype=torch.int8, device=dev)
+        scales = torch.empty(rows, dtype=torch.float32, device=dev)
+    else:
+        codes, scales = out
+        _expect("codes", codes, (rows, cols), torch.int8)
+        _expect("scales", scales, (rows,), torch.float32)
+        dev = _device_of(x, codes=codes, scales=scales)
+    with _on(dev):
+        _check(lib().int8_quantize(x.data_ptr(), _dt(x.dtype), rows, cols, ld, codes.data_ptr(),
+                                   scales.data_ptr(), _stream_of(dev)))
+    return codes, scales
+
+
+def _int8_rows(x, x_scales, cols):
+    """Checks the left operand of an int8 product."""
+    if x.dim() != 2 or x.shape[1] != cols:
+        raise ValueError(f"x {tuple(x.shape)} does not match a weight of {cols} columns")
+    if x_scales is None:
+        _expect("x", x, x.shape, torch.bfloat16)
+    else:
+        _expect("x", x, x.shape, torch.int8)
+        _expect("x_scales", x_scales, (x.shape[0],), torch.float32)
+
+
+def int8_linear(x, codes, scales, x_scales=None, out_dtype=torch.bfloat16, workspace=None,
+                out=None):
+    """y [M, N] = x [M, K] . W [N, K]^T for int8 W (codes, scales from
+    int8_quantize(w)).  x: bf16, quantised online per row; or with x_scales, the
+    codes of int8_quantize(x) or rms_norm_quantize(codes="int8").  out must not
+    overlap x."""
+    m = _int8_matrix("W", codes, scales)
+    _int8_rows(x, x_scales, m.cols)
+    M, K = x.shape
+    dev = _device_of(x, rows=x, codes=codes, scales=scales, x_scales=x_scales, out=out,
+                     workspace=workspace)
+    if out is None:
+        y = torch.empty((M, m.rows), dtype=out_dtype, device=dev)
+    else:
+        _expect("out", out, (M, m.rows), out.dtype)
+        y = out
+    L = lib()
+    ws = _scratch(L.int8_linear_workspace_size(M, m.rows, K, x_scales is not None), dev, workspace)
+    with _on(dev):
+        _check(L.int8_linear(x.data_ptr(), None if x_scales is None else x_scales.data_ptr(), M,
+                             ctypes.byref(m), y.data_ptr(), _dt(y.dtype), ws[1], ws[2],
+                             _stream_of(dev)))
+    return y
+
+
+def int8_mlp(x, gate, up, down, x_scales=None, out_dtype=torch.bfloat16, workspace=None, out=None):
+    """y [T, H] = down(silu(x Wg^T) * (x Wu^T)) with int8 weights: gate, up
+    ([I, H]) and down ([H, I]) are (codes, scales) pairs from int8_quantize(w).
+    x [T, H] bf16, or codes with their x_scales; h is quantised per token."""
+    mats = {n: _int8_matrix(n, *p) for n, p in (("gate", gate), ("up", up), ("down", down))}
+    I, H = mats["gate"].rows, mats["gate"].cols
+    _int8_rows(x, x_scales, H)
+    T = x.shape[0]
+    dev = _device_of(x, rows=x, gate=gate[0], up=up[0], down=down[0], gate_scales=gate[1],
+                     up_scales=up[1], down_scales=down[1], x_scales=x_scales, out=out,
+                     workspace=workspace)
+    y = out if out is not None else torch.empty((T, H), dtype=out_dtype, device=dev)
+    _expect("out", y, (T, H), y.dtype)
+    L = lib()
+    ws = _scratch(L.int8_mlp_workspace_size(T, H, I, x_scales is not None), dev, workspace)
+    with _on(dev):
+        _check(L.int8_mlp(x.data_ptr(), None if x_scales is None else x_scales.data_ptr(), T,
+                          *(ctypes.byref(m) for m in mats.values()), y.data_ptr(), _dt(y.dtype),
+                          ws[1], ws[2], _stream_of(dev)))
+    return y
+
+
+class RmsNorm(NamedTuple):
+    """What rms_norm_quantize returns; None for what was not asked for."""
+    y: Optional[torch.Tensor]
+    codes: Optional[torch.Tensor]
+    scales: Optional[torch.Tensor]
+    residual: Optional[torch.Tensor]
+
+
+_NORM_CODES = {None: (0, None), "fp8": (1, torch.uint8), "int8": (2, torch.int8)}
+
+
+def rms_norm_quantize(x, weight, residual=None, eps=1e-6, codes=None, y_dtype=None, out=None):
+    """RMS norm of x [T, H], or of x + residual, times weight [H]: as codes
+    ("fp8": E4M3 with a scale per 128 columns, for fp8_block_linear's x_scales;
+    "int8": a scale per token, for int8_linear and int8_mlp), as y (y_dtype
+    bf16 or f32), or both.  x, residual and weight are bf16 or f32; rows of x
+    and of the residual may be strided.  Returns RmsNorm(y, codes, scales,
+    residual), where residual is the rounded sum.  out: an RmsNorm of tensors to
+    write (None: allocated); its residual may be the residual itself, or x."""
+    if codes not in _NORM_CODES:
+        raise ValueError(f'codes must be None, "fp8" or "int8", got {codes!r}')
+    if codes is None and y_dtype is None:
+        raise ValueError("nothing to compute: give codes, y_dtype or both")
+    if x.dim() != 2:
+        raise ValueError(f"x must be [T, H], got {tuple(x.shape)}")
+    T, H = x.shape
+    fmt, code_t = _NORM_CODES[codes]
+    o = out if out is not None else RmsNorm(None, None, None, None)
+    dev = _device_of(x, weight=weight, y=o.y, codes=o.codes, scales=o.scales)
+    _expect("weight", weight, (H,), weight.dtype)
+    a = RmsNormArgs()
+    a.x, a.x_dtype, a.ld_x = x.data_ptr(), _dt(x.dtype), _rows_stride("x", x)
+    a.weight, a.weight_dtype, a.eps = weight.data_ptr(), _dt(weight.dtype), eps
+    total = None
+    if residual is not None:
+        _expect("residual", residual, (T, H), residual.dtype)
+        a.residual, a.residual_dtype = residual.data_ptr(), _dt(residual.dtype)
+        a.ld_residual = _rows_stride("residual", residual, dev)
+        total = o.residual
+        if total is None:
+            total = torch.empty((T, H), dtype=residual.dtype, device=dev)
+        _expect("out.residual", total, (T, H), residual.dtype)
+        a.residual_out = total.data_ptr()
+        a.ld_residual_out = _rows_stride("out.residual", total, dev)
+    y = q = s = None
+    if y_dtype is not None:
+        y = torch.empty((T, H), dtype=y_dtype, device=dev) if o.y is None else o.y
+        _expect("y", y, (T, H), y_dtype)
+        a.y, a.y_dtype = y.data_ptr(), _dt(y_dtype)
+    if fmt:
+        shape = (T, _fp8_blocks(H)) if fmt == 1 else (T,)
+        q = torch.empty((T, H), dtype=code_t, device=dev) if o.codes is None else o.codes
+        s = torch.empty(shape, dtype=torch.float32, device=dev) if o.scales is None else o.scales
+        _expect("codes", q, (T, H), code_t)
+        _expect("scales", s, shape, torch.float32)
+        a.codes, a.scales = q.data_ptr(), s.data_ptr()
+    a.format = fmt
+    with _on(dev):
+        _check(lib().rms_norm_quantize(ctypes.byref(a), T, H, _stream_of(dev)))
+    return RmsNorm(y, q, s, total)
 
 
 # ---- a whole MoE layer for a few tokens ------------------------------------------
