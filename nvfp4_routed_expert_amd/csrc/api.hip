@@ -338,10 +338,11 @@ struct Int8LinearWs {
   int8_t *xq;
   float *xs;
 };
-Int8LinearWs carve_int8_linear(Carver &c, int64_t M, int64_t K, bool quantised) {
+Int8LinearWs carve_int8_linear(Carver &c, int64_t M, int64_t N, int64_t K, bool quantised) {
   Int8LinearWs w = {};
-  w.xq = c.take<int8_t>(quantised ? 0 : (size_t)(M * K));
-  w.xs = c.take<float>(quantised ? 0 : (size_t)M);
+  if (quantised || i8_gemv_quantises(false, M, N, K)) return w;
+  w.xq = c.take<int8_t>((size_t)(M * K));
+  w.xs = c.take<float>((size_t)M);
   return w;
 }
 struct Int8MlpWs {
@@ -351,11 +352,15 @@ struct Int8MlpWs {
 };
 Int8MlpWs carve_int8_mlp(Carver &c, int64_t T, int64_t H, int64_t I, bool quantised) {
   Int8MlpWs w = {};
-  w.xq = c.take<int8_t>(quantised ? 0 : (size_t)(T * H));
-  w.xs = c.take<float>(quantised ? 0 : (size_t)T);
+  if (!quantised && !i8_gemv_quantises(true, T, I, H)) {
+    w.xq = c.take<int8_t>((size_t)(T * H));
+    w.xs = c.take<float>((size_t)T);
+  }
   w.h = c.take<uint16_t>((size_t)(T * I));
-  w.hq = c.take<int8_t>((size_t)(T * I));
-  w.hs = c.take<float>((size_t)T);
+  if (!i8_gemv_quantises(false, T, H, I)) {
+    w.hq = c.take<int8_t>((size_t)(T * I));
+    w.hs = c.take<float>((size_t)T);
+  }
   return w;
 }
 
@@ -1747,10 +1752,41 @@ static nvfp4_status check_int8_output(const void *y, size_t ny, const void *x, s
   return NVFP4_OK;
 }
 
+// One product: x codes with their scales, or bf16 with xs null where the form
+// for a few rows quantises it.  w_up: the gate/up form.
+static nvfp4_status int8_product(const void *x, const float *xs, int64_t M, const int8_matrix *w,
+                                 const int8_matrix *w_up, void *out, OutType type,
+                                 hipStream_t stream) {
+  const bool swiglu = w_up != nullptr;
+  const int64_t N = w->rows, K = w->cols;
+  if (i8_gemv_supported(swiglu, M, N, K)) {
+    const I8GemvArgs a = {x, xs, (int)M, {w->codes, swiglu ? w_up->codes : nullptr},
+                          {w->scales, swiglu ? w_up->scales : nullptr}, (int)N, (int)K, out, type};
+    LAUNCH(launch_i8_gemv(swiglu, a, stream), "int8 gemv");
+    return NVFP4_OK;
+  }
+  I8GemmArgs a = {};
+  a.x = static_cast<const int8_t *>(x);
+  a.xs = xs;
+  a.M = M;
+  a.w[0] = w->codes;
+  a.ws[0] = w->scales;
+  if (swiglu) {
+    a.w[1] = w_up->codes;
+    a.ws[1] = w_up->scales;
+  }
+  a.N = (int)N;
+  a.K = (int)K;
+  a.out = out;
+  a.out_type = type;
+  LAUNCH(launch_i8_gemm(swiglu, a, i8_gemm_plan(swiglu, M, N, K), stream), "int8 gemm");
+  return NVFP4_OK;
+}
+
 size_t int8_linear_workspace_size(int64_t M, int64_t N, int64_t K, int quantised) {
   if (M < 1 || N < 1 || K < 1 || M > kInt8MaxRows || N > kInt8MaxRows || K > kInt8MaxCols) return 0;
   Carver c(nullptr);
-  carve_int8_linear(c, M, K, quantised != 0);
+  carve_int8_linear(c, M, N, K, quantised != 0);
   return c.used;
 }
 
@@ -1772,28 +1808,20 @@ nvfp4_status int8_linear(const void *x, const float *x_scales, int64_t M, const 
   CHECK_ALIGN(y);
   Carver c(workspace);
   const Int8LinearWs ws =
-      M == 0 ? Int8LinearWs() : carve_int8_linear(c, M, K, x_scales != nullptr);
+      M == 0 ? Int8LinearWs() : carve_int8_linear(c, M, N, K, x_scales != nullptr);
   TRY(check_workspace(workspace, workspace_bytes, c.used));
   if (M == 0) return NVFP4_OK;
   TRY(check_int8_output(y, (size_t)(M * N) * dtype_size(y_dtype), x,
                         (size_t)(M * K) * (x_scales ? 1 : 2), x_scales, (size_t)M * 4, workspace,
                         c.used));
-  I8GemmArgs a = {};
-  a.x = static_cast<const int8_t *>(x);
-  a.xs = x_scales;
-  if (!x_scales) {
+  const void *xq = x;
+  const float *xs = x_scales;
+  if (ws.xq) {
     LAUNCH(launch_i8_quantize(x, InType::BF16, M, K, K, ws.xq, ws.xs, stream), "int8 quantize");
-    a.x = ws.xq;
-    a.xs = ws.xs;
+    xq = ws.xq;
+    xs = ws.xs;
   }
-  a.M = M;
-  a.w[0] = w->codes;
-  a.ws[0] = w->scales;
-  a.N = (int)N;
-  a.K = (int)K;
-  a.out = y;
-  a.out_type = out_type(y_dtype);
-  LAUNCH(launch_i8_gemm(false, a, stream), "int8 gemm");
+  TRY(int8_product(xq, xs, M, w, nullptr, y, out_type(y_dtype), stream));
   return NVFP4_OK;
 }
 
@@ -1834,36 +1862,20 @@ nvfp4_status int8_mlp(const void *x, const float *x_scales, int64_t T, const int
   TRY(check_int8_output(y, (size_t)(T * H) * dtype_size(y_dtype), x,
                         (size_t)(T * H) * (x_scales ? 1 : 2), x_scales, (size_t)T * 4, workspace,
                         c.used));
-  I8GemmArgs a = {};
-  a.x = static_cast<const int8_t *>(x);
-  a.xs = x_scales;
-  if (!x_scales) {
+  const void *xq = x, *hq = ws.h;
+  const float *xs = x_scales, *hs = nullptr;
+  if (ws.xq) {
     LAUNCH(launch_i8_quantize(x, InType::BF16, T, H, H, ws.xq, ws.xs, stream), "int8 quantize");
-    a.x = ws.xq;
-    a.xs = ws.xs;
+    xq = ws.xq;
+    xs = ws.xs;
   }
-  a.M = T;
-  a.w[0] = w_gate->codes;
-  a.ws[0] = w_gate->scales;
-  a.w[1] = w_up->codes;
-  a.ws[1] = w_up->scales;
-  a.N = (int)I;
-  a.K = (int)H;
-  a.out = ws.h;
-  a.out_type = OutType::BF16;
-  LAUNCH(launch_i8_gemm(true, a, stream), "int8 gate/up");
-  LAUNCH(launch_i8_quantize(ws.h, InType::BF16, T, I, I, ws.hq, ws.hs, stream), "int8 quantize");
-  I8GemmArgs d = {};
-  d.x = ws.hq;
-  d.xs = ws.hs;
-  d.M = T;
-  d.w[0] = w_down->codes;
-  d.ws[0] = w_down->scales;
-  d.N = (int)H;
-  d.K = (int)I;
-  d.out = y;
-  d.out_type = out_type(y_dtype);
-  LAUNCH(launch_i8_gemm(false, d, stream), "int8 down");
+  TRY(int8_product(xq, xs, T, w_gate, w_up, ws.h, OutType::BF16, stream));
+  if (ws.hq) {
+    LAUNCH(launch_i8_quantize(ws.h, InType::BF16, T, I, I, ws.hq, ws.hs, stream), "int8 quantize");
+    hq = ws.hq;
+    hs = ws.hs;
+  }
+  TRY(int8_product(hq, hs, T, w_down, nullptr, y, out_type(y_dtype), stream));
   return NVFP4_OK;
 }
 

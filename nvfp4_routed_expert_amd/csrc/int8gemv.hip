@@ -1,0 +1,259 @@
+// int8 matrix product with a scale per token and per output channel, for a few
+// rows (M <= 64): one stream of the weights, shared by every row.
+//
+// Bounded by the weight stream (one byte per element for at most 64 tokens).
+// A workgroup owns 16 weight rows (16 gate and 16 up rows in the gate/up
+// form); its waves take the 128-column blocks of K in turn, so the workgroup
+// reads neighbouring lines of each of its rows at a time.  A wave's blocks
+// arrive in a ring of its own in LDS by direct loads, D ahead, eight whole
+// lines a load: no registers, no barrier.  A block is two
+// v_mfma_i32_16x16x64_i8 per 16 tokens; the sums are integers, so how the waves
+// share K changes no bit of the result.
+//
+// QX: x is bf16 and each workgroup quantises it into LDS while its first
+// weights are on their way; that saves a launch.  Otherwise x's codes come
+// through the ring with the weights.
+#include "int8.h"
+#include "kernels.h"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kI8Line = 128;             // columns of a block
+constexpr int kI8XBytes = 20 * 1024;     // x's codes in LDS of the QX form, at most
+
+// bytes of LDS for M rows of codes: 16 bytes apart from a multiple of the banks
+__host__ __device__ constexpr int64_t i8_x_bytes(int64_t M, int64_t K) {
+  return M * ((K + kI8Line - 1) / kI8Line * kI8Line + 16);
+}
+
+// STREAM: the weights are loaded as used once.  XT: groups of 8 rows of x.
+// XCAP: bytes for x's codes (QX).
+template <int XT, bool SWIGLU, bool QX, int NW, int D, int XCAP, bool STREAM>
+__global__ __launch_bounds__(64 * NW) void i8_gemv_kernel(const I8GemvArgs p) {
+#pragma clang fp contract(off)
+  constexpr int NT = SWIGLU ? 2 : 1, MT = (XT + 1) / 2;   // tiles of 16 rows of w, x
+  constexpr int SLOT = 2048 * NT + (QX ? 0 : 1024 * XT);  // a block: 1 KB for 8 rows
+  constexpr int LS = SLOT / 1024;                  // loads of a block
+  constexpr int RED = NW * NT * 16 * (MT * 16 + 1) * 4;
+  constexpr int RING = NW * D * SLOT > RED ? NW * D * SLOT : RED;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[RING + XCAP + MT * 16 * 4];
+  uint8_t *const xl = lds + RING;
+  uint32_t *const top = reinterpret_cast<uint32_t *>(lds + RING + XCAP);   // QX: maxima of rows
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = lane & 15, lg = lane >> 4;
+  const int K = p.K, N = p.N, M = p.M;
+  const int KB = (K + kI8Line - 1) / kI8Line;
+  const int r0 = blockIdx.x * 16;                  // first output column
+  const int mine = (KB - wave + NW - 1) / NW;      // this wave's blocks: wave, wave + NW, ...
+  const int xp = KB * kI8Line + 16;                // QX: pitch of a row of codes
+
+  // ---- the ring: a load fills 8 rows of 128 bytes, lane l position l % 8 of
+  // row l / 8, which holds granule (l % 8) ^ (l / 8)
+  __amdgpu_buffer_rsrc_t wbuf[4], xbuf[8];
+#pragma unroll
+  for (int h = 0; h < 2 * NT; ++h) wbuf[h] = f8_buffer(p.w[h / 2], r0 + h % 2 * 8, N, K);
+  if constexpr (!QX) {
+#pragma unroll
+    for (int h = 0; h < XT; ++h) xbuf[h] = f8_buffer(p.x, h * 8, M, K);
+  }
+  const int gran = (lane & 7) ^ (lane >> 3);
+  const int off_ = (lane >> 3) * K + gran * 16, last = K - gran * 16;
+  uint8_t *const ring = lds + wave * (D * SLOT);
+  auto load = [&](int i, int slot) {
+    const int at = __builtin_amdgcn_readfirstlane((wave + NW * i) * kI8Line);
+    const int off = off_ | (at < last ? 0 : kOutside);   // (granules past K: zero codes)
+#pragma unroll
+    for (int h = 0; h < LS; ++h)
+      if (h < 2 * NT)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            wbuf[h], (lds_ptr_t)(ring + slot * SLOT + h * 1024), 16, off, at, 0, STREAM ? 2 : 0);
+      else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            xbuf[h - 2 * NT], (lds_ptr_t)(ring + slot * SLOT + h * 1024), 16, off, at, 0, 0);
+  };
+
+  // ---- QX: a wave takes pieces of 512 columns of the rows in turn; a row's
+  // maximum is joined by an integer maximum in LDS.  The first B pieces stay in
+  // registers for their conversion, later ones are read again.
+  constexpr int B = 4;
+  const int pieces = (K + 511) / 512;
+  auto x_piece = [&](int it) {
+    const int m = it / pieces, k = (it - m * pieces) * 512 + lane * 8;
+    return it < M * pieces && k < K
+               ? *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(p.x) +
+                                                  (int64_t)m * K + k)
+               : u32x4{0u, 0u, 0u, 0u};
+  };
+  u32x4 xr[B];
+  if constexpr (QX) {
+#pragma unroll
+    for (int j = 0; j < B; ++j) xr[j] = x_piece(wave + NW * j);
+    if (tid < MT * 16) top[tid] = 0u;
+  }
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(d, d);
+  if constexpr (QX) {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    auto piece_top = [&](const u32x4 &r, int it) {
+      uint32_t m = 0u;   // bf16 magnitudes order as integers
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t lo = (r[e] << 16) & 0x7FFFFFFFu, hi = r[e] & 0x7FFF0000u;
+        m = m > lo ? m : lo;
+        m = m > hi ? m : hi;
+      }
+      const float f = i8_wave_max(__uint_as_float(m));
+      if (lane == 0 && it < M * pieces) atomicMax(&top[it / pieces], __float_as_uint(f));
+    };
+#pragma unroll
+    for (int j = 0; j < B; ++j) piece_top(xr[j], wave + NW * j);
+    for (int it = wave + NW * B; it < M * pieces; it += NW) piece_top(x_piece(it), it);
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    auto convert = [&](const u32x4 &r, int it) {
+      const int m = it / pieces, k = (it - m * pieces) * 512 + lane * 8;
+      if (it >= M * pieces || k >= KB * kI8Line) return;
+      const float inv = 1.0f / i8_scale(__uint_as_float(top[m]));
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[2 * e] = __uint_as_float(r[e] << 16) * inv;
+        v[2 * e + 1] = __uint_as_float(r[e] & 0xFFFF0000u) * inv;
+      }
+      *reinterpret_cast<u32x2 *>(xl + m * xp + k) =
+          u32x2{i8_pack4(v[0], v[1], v[2], v[3]), i8_pack4(v[4], v[5], v[6], v[7])};
+    };
+#pragma unroll
+    for (int j = 0; j < B; ++j) convert(xr[j], wave + NW * j);
+    for (int it = wave + NW * B; it < M * pieces; it += NW) convert(x_piece(it), it);
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  }
+
+  i32x4 acc[NT][MT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) acc[t][j] = i32x4{0, 0, 0, 0};
+  const int p0 = lr * kI8Line + (lg ^ (lr & 7)) * 16, p1 = lr * kI8Line + ((lg + 4) ^ (lr & 7)) * 16;
+  // (an odd number of groups: the last one is read twice)
+  const int x0 = p0 - (lr & 8) * kI8Line, x1 = p1 - (lr & 8) * kI8Line;
+  int row[MT];                                     // QX: token of tile j (repeated past M)
+#pragma unroll
+  for (int j = 0; j < MT; ++j) row[j] = j * 16 + lr < M ? j * 16 + lr : M - 1;
+  int slot = 0;
+#pragma unroll 1
+  for (int i = 0; i < mine; ++i) {
+    const int b = __builtin_amdgcn_readfirstlane(wave + NW * i);
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((D - 1) * LS) : "memory");
+    const uint8_t *st = ring + slot * SLOT;
+    i32x4 wq[NT][2], xq[MT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      wq[t][0] = *reinterpret_cast<const i32x4 *>(st + t * 2048 + p0);
+      wq[t][1] = *reinterpret_cast<const i32x4 *>(st + t * 2048 + p1);
+    }
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      if constexpr (QX) {
+        const uint8_t *xt = xl + row[j] * xp + b * kI8Line + lg * 16;
+        xq[j][0] = *reinterpret_cast<const i32x4 *>(xt);
+        xq[j][1] = *reinterpret_cast<const i32x4 *>(xt + 64);
+      } else {
+        const uint8_t *xt = st + (NT + j) * 2048;
+        const bool odd = XT % 2 == 1 && j == MT - 1;
+        xq[j][0] = *reinterpret_cast<const i32x4 *>(xt + (odd ? x0 : p0));
+        xq[j][1] = *reinterpret_cast<const i32x4 *>(xt + (odd ? x1 : p1));
+      }
+    }
+    // the slot is read: it takes block i + D
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    load(i + D, slot);
+    slot = slot + 1 == D ? 0 : slot + 1;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          acc[t][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wq[t][q], xq[j][q], acc[t][j], 0, 0, 0);
+  }
+
+  // the waves' totals (every load has landed, and every wave left the ring)
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  int (*red)[NT * 16][MT * 16 + 1] = reinterpret_cast<int (*)[NT * 16][MT * 16 + 1]>(lds);
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) red[wave][t * 16 + 4 * lg + e][j * 16 + lr] = acc[t][j][e];
+  __syncthreads();
+  for (int i = tid; i < 16 * M; i += 64 * NW) {
+    const int c = i % 16, m = i / 16;   // consecutive threads: consecutive columns
+    const int n = r0 + c;
+    if (n >= N) continue;
+    const float sx = QX ? i8_scale(__uint_as_float(top[m])) : p.xs[m];
+    int g = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) g += red[w][c][m];
+    float v = i8_value(g, sx, p.ws[0][n]);
+    if constexpr (SWIGLU) {
+      int u = 0;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) u += red[w][16 + c][m];
+      v = v / (1.0f + expf(-v)) * i8_value(u, sx, p.ws[1][n]);
+    }
+    if (p.out_type == OutType::F32) static_cast<float *>(p.out)[(int64_t)m * N + n] = v;
+    else static_cast<uint16_t *>(p.out)[(int64_t)m * N + n] = (uint16_t)f32_to_bf16_bits(v);
+  }
+}
+
+template <int XT, bool SWIGLU, bool QX, int NW, int D, int XCAP = 0>
+hipError_t launch_gemv(const I8GemvArgs &a, hipStream_t s) {
+  const dim3 grid((unsigned)((a.N + 15) / 16)), block(64 * NW);
+  if ((int64_t)a.N * a.K * (SWIGLU ? 2 : 1) > 128000000)
+    launch_kernel((i8_gemv_kernel<XT, SWIGLU, QX, NW, D, XCAP, true>), grid, block, 0, s, a);
+  else
+    launch_kernel((i8_gemv_kernel<XT, SWIGLU, QX, NW, D, XCAP, false>), grid, block, 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+bool i8_gemv_supported(bool swiglu, int64_t M, int64_t N, int64_t K) {
+  return M >= 1 && M <= 64 && (M <= (swiglu ? 32 : 16) || N * K < (M <= 32 ? 48 : 32) * 1000000);
+}
+bool i8_gemv_quantises(bool swiglu, int64_t M, int64_t N, int64_t K) {
+  return i8_gemv_supported(swiglu, M, N, K) && M <= 16 && i8_x_bytes(M, K) <= kI8XBytes;
+}
+
+hipError_t launch_i8_gemv(bool swiglu, const I8GemvArgs &a, hipStream_t s) {
+  if (!i8_gemv_supported(swiglu, a.M, a.N, a.K) ||
+      (!a.xs && !i8_gemv_quantises(swiglu, a.M, a.N, a.K)))
+    return hipErrorInvalidValue;
+  if (!a.xs) {
+    const bool small = i8_x_bytes(a.M, a.K) <= 10 * 1024;
+    if (swiglu)
+      return small ? launch_gemv<2, true, true, 4, 4, 10 * 1024>(a, s)
+                   : launch_gemv<2, true, true, 4, 3, kI8XBytes>(a, s);
+    return small ? launch_gemv<2, false, true, 4, 4, 10 * 1024>(a, s)
+                 : launch_gemv<2, false, true, 8, 2, kI8XBytes>(a, s);
+  }
+  if (a.M <= 8)
+    return swiglu ? launch_gemv<1, true, false, 4, 3>(a, s)
+                  : launch_gemv<1, false, false, 8, 3>(a, s);
+  switch ((a.M + 15) / 16 + (swiglu ? 4 : 0)) {
+    case 1: return launch_gemv<2, false, false, 8, 2>(a, s);
+    case 2: return launch_gemv<4, false, false, 8, 2>(a, s);
+    case 3: return launch_gemv<6, false, false, 4, 3>(a, s);
+    case 4: return launch_gemv<8, false, false, 4, 3>(a, s);
+    case 5: return launch_gemv<2, true, false, 8, 2>(a, s);
+    case 6: return launch_gemv<4, true, false, 8, 2>(a, s);
+    case 7: return launch_gemv<6, true, false, 4, 3>(a, s);
+    default: return launch_gemv<8, true, false, 4, 2>(a, s);
+  }
+}
+
+}  // namespace nvfp4

@@ -370,7 +370,7 @@ bool f8_gemv_supported(bool swiglu, int64_t M, int64_t N, int64_t K);
 bool f8_gemv_quantises(bool swiglu, int64_t M, int64_t N, int64_t K);
 hipError_t launch_f8_gemv(bool swiglu, const F8GemvArgs &a, hipStream_t s);
 
-// ---- row operators and int8 products (rowquant.hip, int8gemm.hip) ------------------------
+// ---- row operators and int8 products (rowquant.hip, int8gemm.hip, int8gemv.hip) ------------------------
 
 enum class RowCodes : int { NONE = 0, FP8 = 1, INT8 = 2 };
 struct RowArgs {
@@ -404,8 +404,35 @@ struct I8GemmArgs {
   int N, K;
   void *out;              // [M, N]; gate/up form: h, bf16
   OutType out_type;
+  int ksplit;
+  int32_t *partial;       // [ksplit][M][N, or 2 N: gate then up sums]
 };
-hipError_t launch_i8_gemm(bool swiglu, const I8GemmArgs &a, hipStream_t s);
+// Tokens of a tile and K parts for a problem; a split needs partial_ints words
+// of workspace.
+struct I8Plan {
+  int bm = 0;
+  int ksplit = 1;
+  size_t partial_ints = 0;
+};
+I8Plan i8_gemm_plan(bool swiglu, int64_t M, int64_t N, int64_t K);
+hipError_t launch_i8_gemm(bool swiglu, const I8GemmArgs &a, const I8Plan &pl, hipStream_t s);
+
+// The same product for a few rows (int8gemv.hip), where _supported says so.  xs
+// null: x is bf16 [M, K] and is quantised inside (where _quantises says so);
+// otherwise x holds codes.  Gate/up form: out = h, bf16 [M, N].
+struct I8GemvArgs {
+  const void *x;
+  const float *xs;
+  int M;
+  const int8_t *w[2];
+  const float *ws[2];
+  int N, K;
+  void *out;
+  OutType out_type;
+};
+bool i8_gemv_supported(bool swiglu, int64_t M, int64_t N, int64_t K);
+bool i8_gemv_quantises(bool swiglu, int64_t M, int64_t N, int64_t K);
+hipError_t launch_i8_gemv(bool swiglu, const I8GemvArgs &a, hipStream_t s);
 
 // ---- a whole MoE layer for a few tokens (layer.hip) --------------------------------
 
