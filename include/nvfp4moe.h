@@ -675,6 +675,17 @@ nvfp4_status int8_mlp(const void *x, const float *x_scales, int64_t T, const int
 size_t int8_mlp_workspace_size(int64_t T, int64_t H, int64_t I, int quantised);
 
 /*
+ * int8_debug_plan: a test aid (not part of the computation).  How the product
+ * of M rows with an int8 W [N, K] runs (gate_up: the gate and up products of
+ * int8_mlp, N = I and K = H): returns the rows of x of a tile of the batch
+ * form (64, 128, 192 or 256), sets *columns to its rows of W (gate and up
+ * together) and *parts to the parts that K is split into; 0, 0 and 0 for the
+ * form for a few rows, and for sizes below 1.  Either pointer may be NULL.
+ */
+int int8_debug_plan(int gate_up, int64_t M, int64_t N, int64_t K, int32_t *columns,
+                    int32_t *parts);
+
+/*
  * rms_norm_quantize: the front of a block.  Per token t of T, over H columns:
  *   v = x, or round(x + residual) to the residual's type, stored in
  *       residual_out;

@@ -337,20 +337,28 @@ constexpr int64_t kRowMaxCols = (int64_t)1 << 27, kRowMaxStride = (int64_t)1 << 
 struct Int8LinearWs {
   int8_t *xq;
   float *xs;
+  int32_t *split;   // partial sums of a K split
 };
-Int8LinearWs carve_int8_linear(Carver &c, int64_t M, int64_t N, int64_t K, bool quantised) {
+// A call's layout; partial: words for its parts' sums (the plan's own, or, to
+// size a workspace, enough for every batch up to M).
+Int8LinearWs carve_int8_linear(Carver &c, int64_t M, int64_t N, int64_t K, bool quantised,
+                               size_t partial) {
   Int8LinearWs w = {};
-  if (quantised || i8_gemv_quantises(false, M, N, K)) return w;
-  w.xq = c.take<int8_t>((size_t)(M * K));
-  w.xs = c.take<float>((size_t)M);
+  if (!quantised && !i8_gemv_quantises(false, M, N, K)) {
+    w.xq = c.take<int8_t>((size_t)(M * K));
+    w.xs = c.take<float>((size_t)M);
+  }
+  w.split = c.take<int32_t>(partial);
   return w;
 }
 struct Int8MlpWs {
   int8_t *xq, *hq;
   uint16_t *h;
   float *xs, *hs;
+  int32_t *split;
 };
-Int8MlpWs carve_int8_mlp(Carver &c, int64_t T, int64_t H, int64_t I, bool quantised) {
+Int8MlpWs carve_int8_mlp(Carver &c, int64_t T, int64_t H, int64_t I, bool quantised,
+                         size_t partial) {
   Int8MlpWs w = {};
   if (!quantised && !i8_gemv_quantises(true, T, I, H)) {
     w.xq = c.take<int8_t>((size_t)(T * H));
@@ -361,7 +369,18 @@ Int8MlpWs carve_int8_mlp(Carver &c, int64_t T, int64_t H, int64_t I, bool quanti
     w.hq = c.take<int8_t>((size_t)(T * I));
     w.hs = c.take<float>((size_t)T);
   }
+  w.split = c.take<int32_t>(partial);
   return w;
+}
+// Words of the parts' sums of one product: of this call, or at least those of
+// any batch up to M.
+size_t int8_partial(bool swiglu, int64_t M, int64_t N, int64_t K, bool any) {
+  if (i8_gemv_supported(swiglu, M, N, K)) return 0;   // (nor do fewer rows)
+  return any ? i8_gemm_max_partial(swiglu, M, N, K) : i8_gemm_plan(swiglu, M, N, K).partial_ints;
+}
+size_t int8_mlp_partial(int64_t T, int64_t H, int64_t I, bool any) {
+  const size_t up = int8_partial(true, T, I, H, any), down = int8_partial(false, T, H, I, any);
+  return up > down ? up : down;
 }
 
 struct LayerWs {
@@ -1755,7 +1774,7 @@ static nvfp4_status check_int8_output(const void *y, size_t ny, const void *x, s
 // One product: x codes with their scales, or bf16 with xs null where the form
 // for a few rows quantises it.  w_up: the gate/up form.
 static nvfp4_status int8_product(const void *x, const float *xs, int64_t M, const int8_matrix *w,
-                                 const int8_matrix *w_up, void *out, OutType type,
+                                 const int8_matrix *w_up, void *out, OutType type, int32_t *split,
                                  hipStream_t stream) {
   const bool swiglu = w_up != nullptr;
   const int64_t N = w->rows, K = w->cols;
@@ -1779,6 +1798,7 @@ static nvfp4_status int8_product(const void *x, const float *xs, int64_t M, cons
   a.K = (int)K;
   a.out = out;
   a.out_type = type;
+  a.partial = split;
   LAUNCH(launch_i8_gemm(swiglu, a, i8_gemm_plan(swiglu, M, N, K), stream), "int8 gemm");
   return NVFP4_OK;
 }
@@ -1786,7 +1806,7 @@ static nvfp4_status int8_product(const void *x, const float *xs, int64_t M, cons
 size_t int8_linear_workspace_size(int64_t M, int64_t N, int64_t K, int quantised) {
   if (M < 1 || N < 1 || K < 1 || M > kInt8MaxRows || N > kInt8MaxRows || K > kInt8MaxCols) return 0;
   Carver c(nullptr);
-  carve_int8_linear(c, M, N, K, quantised != 0);
+  carve_int8_linear(c, M, N, K, quantised != 0, int8_partial(false, M, N, K, true));
   return c.used;
 }
 
@@ -1808,7 +1828,8 @@ nvfp4_status int8_linear(const void *x, const float *x_scales, int64_t M, const 
   CHECK_ALIGN(y);
   Carver c(workspace);
   const Int8LinearWs ws =
-      M == 0 ? Int8LinearWs() : carve_int8_linear(c, M, N, K, x_scales != nullptr);
+      M == 0 ? Int8LinearWs() : carve_int8_linear(c, M, N, K, x_scales != nullptr,
+                                              int8_partial(false, M, N, K, false));
   TRY(check_workspace(workspace, workspace_bytes, c.used));
   if (M == 0) return NVFP4_OK;
   TRY(check_int8_output(y, (size_t)(M * N) * dtype_size(y_dtype), x,
@@ -1821,14 +1842,14 @@ nvfp4_status int8_linear(const void *x, const float *x_scales, int64_t M, const 
     xq = ws.xq;
     xs = ws.xs;
   }
-  TRY(int8_product(xq, xs, M, w, nullptr, y, out_type(y_dtype), stream));
+  TRY(int8_product(xq, xs, M, w, nullptr, y, out_type(y_dtype), ws.split, stream));
   return NVFP4_OK;
 }
 
 size_t int8_mlp_workspace_size(int64_t T, int64_t H, int64_t I, int quantised) {
   if (T < 1 || H < 1 || I < 1 || T > kInt8MaxRows || H > kInt8MaxCols || I > kInt8MaxCols) return 0;
   Carver c(nullptr);
-  carve_int8_mlp(c, T, H, I, quantised != 0);
+  carve_int8_mlp(c, T, H, I, quantised != 0, int8_mlp_partial(T, H, I, true));
   return c.used;
 }
 
@@ -1856,7 +1877,8 @@ nvfp4_status int8_mlp(const void *x, const float *x_scales, int64_t T, const int
   CHECK_ALIGN(x_scales);
   CHECK_ALIGN(y);
   Carver c(workspace);
-  const Int8MlpWs ws = T == 0 ? Int8MlpWs() : carve_int8_mlp(c, T, H, I, x_scales != nullptr);
+  const Int8MlpWs ws = T == 0 ? Int8MlpWs() : carve_int8_mlp(c, T, H, I, x_scales != nullptr,
+                                       int8_mlp_partial(T, H, I, false));
   TRY(check_workspace(workspace, workspace_bytes, c.used));
   if (T == 0) return NVFP4_OK;
   TRY(check_int8_output(y, (size_t)(T * H) * dtype_size(y_dtype), x,
@@ -1869,14 +1891,24 @@ nvfp4_status int8_mlp(const void *x, const float *x_scales, int64_t T, const int
     xq = ws.xq;
     xs = ws.xs;
   }
-  TRY(int8_product(xq, xs, T, w_gate, w_up, ws.h, OutType::BF16, stream));
+  TRY(int8_product(xq, xs, T, w_gate, w_up, ws.h, OutType::BF16, ws.split, stream));
   if (ws.hq) {
     LAUNCH(launch_i8_quantize(ws.h, InType::BF16, T, I, I, ws.hq, ws.hs, stream), "int8 quantize");
     hq = ws.hq;
     hs = ws.hs;
   }
-  TRY(int8_product(hq, hs, T, w_down, nullptr, y, out_type(y_dtype), stream));
+  TRY(int8_product(hq, hs, T, w_down, nullptr, y, out_type(y_dtype), ws.split, stream));
   return NVFP4_OK;
+}
+
+int int8_debug_plan(int gate_up, int64_t M, int64_t N, int64_t K, int32_t *columns,
+                    int32_t *parts) {
+  const bool batch = M >= 1 && N >= 1 && K >= 1 && !i8_gemv_supported(gate_up != 0, M, N, K);
+  I8Plan p;
+  if (batch) p = i8_gemm_plan(gate_up != 0, M, N, K);
+  if (columns) *columns = 64 * p.fn;
+  if (parts) *parts = batch ? p.ksplit : 0;
+  return 64 * p.fm;
 }
 
 nvfp4_status rms_norm_quantize(const rms_norm_args *a, int64_t T, int64_t H, hipStream_t stream) {

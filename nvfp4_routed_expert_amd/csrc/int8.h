@@ -42,6 +42,13 @@ __device__ __forceinline__ float i8_value(int sum, float sx, float sw) {
   return ((float)sum * sx) * sw;
 }
 
+// Two fp32 values -> two bf16 codes, round to nearest even, a in the low half.
+__device__ __forceinline__ uint32_t i8_pack_bf16(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+}
+
 // Maximum over a wave, in every lane.
 __device__ __forceinline__ float i8_wave_max(float v) {
   v = f8_row16_max(v);

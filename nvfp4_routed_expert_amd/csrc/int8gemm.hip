@@ -15,24 +15,20 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kI8Xcds = 8;
+constexpr int kI8CUs = 256;
 constexpr int kI8Block = 128;          // columns of a step of the ring: a cache line of codes
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
 // A workgroup of four waves, one per SIMD, two by two: FN tiles of 32 weight
 // rows by FM tiles of 32 tokens each.
-template <int FN, int FM, int R, int G, bool SWIGLU>
-__global__ __launch_bounds__(256, 1) void i8_gemm_kernel(const I8GemmArgs p) {
+template <int FN, int FM, int R, int G, int PER_CU, bool SWIGLU>
+__global__ __launch_bounds__(256, PER_CU) void i8_gemm_kernel(const I8GemmArgs p) {
   static_assert(FN % G == 0 && (!SWIGLU || FN % 2 == 0), "groups of whole tiles");
   constexpr int BN = 64 * FN, BM = 64 * FM;
   constexpr int TN = SWIGLU ? BN / 2 : BN;       // output columns of a tile
   constexpr int AG = FN / G, BT = (FM + G - 1) / G;   // weight, token tiles of a group
-  constexpr int W_BYTES = BN * kI8Block, SLOT = W_BYTES + BM * kI8Block;
-  constexpr int PITCH16 = TN * 2 + 16, PITCH32 = BN * 4 + 16;
-  constexpr int P32 = FM == 1 ? 1 : 2;           // passes of 32-bit outputs
-  constexpr int OUT16 = BM * PITCH16, OUT32 = BM / P32 * PITCH32;
-  constexpr int OUT = OUT16 > OUT32 ? OUT16 : OUT32;
-  constexpr int RING = R * SLOT > OUT ? R * SLOT : OUT;
+  constexpr int W_BYTES = BN * kI8Block, SLOT = W_BYTES + BM * kI8Block, RING = R * SLOT;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[RING + (BN + BM) * 4];
   float *const swl = reinterpret_cast<float *>(lds + RING), *const sxl = swl + BN;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -50,13 +46,13 @@ __global__ __launch_bounds__(256, 1) void i8_gemm_kernel(const I8GemmArgs p) {
   const int slot_ = blockIdx.x / kI8Xcds;
   const int item = (blockIdx.x % kI8Xcds) * per + slot_;
   if (slot_ >= per || item >= n_items) return;
-  // up to eight token tiles side by side, then the next weight rows: the tiles
+  // up to four token tiles side by side, then the next weight rows: the tiles
   // that run together on an XCD share both operands in its L2
   const int kz = item / (n_tiles * m_tiles), tile = item - kz * (n_tiles * m_tiles);
-  const int gi = tile / (8 * n_tiles), gr = tile - gi * 8 * n_tiles;
-  const int gm = m_tiles - gi * 8 < 8 ? m_tiles - gi * 8 : 8;
+  const int gi = tile / (4 * n_tiles), gr = tile - gi * 4 * n_tiles;
+  const int gm = m_tiles - gi * 4 < 4 ? m_tiles - gi * 4 : 4;
   const int nt = gr / gm;
-  const int64_t m0 = (int64_t)(gi * 8 + gr - nt * gm) * BM;
+  const int64_t m0 = (int64_t)(gi * 4 + gr - nt * gm) * BM;
   const int b_begin = __builtin_amdgcn_readfirstlane((int)((int64_t)KB * kz / ks));
   const int nb = __builtin_amdgcn_readfirstlane((int)((int64_t)KB * (kz + 1) / ks)) - b_begin;
   const int k0 = b_begin * kI8Block;
@@ -67,14 +63,13 @@ __global__ __launch_bounds__(256, 1) void i8_gemm_kernel(const I8GemmArgs p) {
   // likewise.  Granule g (16 bytes) of row r lies at position g ^ (r / 2 % 8):
   // the 16 lanes that an LDS read serves together then touch all banks once.
   // A wave loads 16 rows of each pair of tiles, 8 whole lines a load.
-  __amdgpu_buffer_rsrc_t wbuf[FN], xbuf[FM];
+  __amdgpu_buffer_rsrc_t wbuf[4], xbuf[4];
   const int part = (wave & 1) * 16;
 #pragma unroll
   for (int f = 0; f < FN; ++f) {
-    if constexpr (SWIGLU)
-      wbuf[f] = f8_buffer(p.w[f / (FN / 2)],
-                          nt * TN + wm * (TN / 2) + f % (FN / 2) * 32 + part, N, K);
-    else wbuf[f] = f8_buffer(p.w[0], nt * TN + wm * (TN / 2) + f * 32 + part, N, K);
+    const int c = nt * TN + wm * (TN / 2) + part;
+    if constexpr (SWIGLU) wbuf[f] = f8_buffer(p.w[f / (FN / 2)], c + f % (FN / 2) * 32, N, K);
+    else wbuf[f] = f8_buffer(p.w[0], c + f * 32, N, K);
   }
 #pragma unroll
   for (int t = 0; t < FM; ++t) xbuf[t] = f8_buffer(p.x, m0 + (wm * FM + t) * 32 + part, M, K);
@@ -117,19 +112,15 @@ __global__ __launch_bounds__(256, 1) void i8_gemm_kernel(const I8GemmArgs p) {
   };
 
   // scales of the tile's rows, in the order of its rows in a slot
-  {
-    const __amdgpu_buffer_rsrc_t sb = f8_buffer(p.xs, m0, M, 4);
-    for (int q = wave; q < FN; q += 4) {
-      const int f = q, c = lane >> 5;
-      const int n = nt * TN + c * (TN / 2) + (SWIGLU ? f % (FN / 2) : f) * 32 + lr;
-      const __amdgpu_buffer_rsrc_t wb =
-          f8_buffer(p.ws[SWIGLU ? (f >= FN / 2 ? 1 : 0) : 0], 0, N, 4);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(wb, (lds_ptr_t)(swl + q * 64), 4, n * 4, 0, 0, 0);
-    }
-    for (int q = wave; q < FM; q += 4)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(sb, (lds_ptr_t)(sxl + q * 64), 4,
-                                               (q * 64 + lane) * 4, 0, 0, 0);
+  for (int f = wave; f < FN; f += 4) {
+    const int n = nt * TN + lh * (TN / 2) + (SWIGLU ? f % (FN / 2) : f) * 32 + lr;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        f8_buffer(p.ws[SWIGLU ? f / (FN / 2) : 0], 0, N, 4), (lds_ptr_t)(swl + f * 64), 4, n * 4, 0,
+        0, 0);
   }
+  for (int t = wave; t < FM; t += 4)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(f8_buffer(p.xs, m0, M, 4), (lds_ptr_t)(sxl + t * 64), 4,
+                                             (t * 64 + lane) * 4, 0, 0, 0);
 
   // ---- steps.  Step g of block i multiplies the weight tiles of group g with
   // all token tiles; while it does, the weight tiles of the next step and the
@@ -166,13 +157,13 @@ __global__ __launch_bounds__(256, 1) void i8_gemm_kernel(const I8GemmArgs p) {
   };
 
   int sl = 0, sn = R > 1 ? SLOT : 0;   // slots of block i and of the next
-  auto step = [&](auto g_, int i, i32x4 (&ac)[AG][4], i32x4 (&an)[AG][4], i32x4 (&bc)[FM][4],
-                  i32x4 (&bn)[FM][4]) {
+  // w_at, x_at: columns that the step loads of weights and of tokens
+  auto step = [&](auto g_, int w_at, int x_at, i32x4 (&ac)[AG][4], i32x4 (&an)[AG][4],
+                  i32x4 (&bc)[FM][4], i32x4 (&bn)[FM][4]) {
     constexpr int g = decltype(g_)::value;
     constexpr int NM = AG * FM * 4, ND = 4 * AG + 4 * nx(g), NL = loads(g);
     constexpr int PER = (ND + NL + NM - 1) / NM;
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(in_flight(g)) : "memory");
-    const int w_at = k_of(i + R), x_at = g == 0 ? w_at : k_of(i + 1 + R);
     const int x_slot = g == 0 ? sl : sn;
     auto item = [&](int e) {
       if (e < 4 * AG) {
@@ -203,11 +194,12 @@ __global__ __launch_bounds__(256, 1) void i8_gemm_kernel(const I8GemmArgs p) {
   auto block = [&](int i_, auto parity, i32x4 (&bc)[FM][4], i32x4 (&bn)[FM][4]) {
     const int i = __builtin_amdgcn_readfirstlane(i_);
     constexpr int P = G % 2 ? decltype(parity)::value : 0;
-    step(std::integral_constant<int, 0>{}, i, a[P], a[1 - P], bc, bn);
-    if constexpr (G > 1) step(std::integral_constant<int, 1>{}, i, a[1 - P], a[P], bc, bn);
+    const int at0 = k_of(i + R), at1 = at0 + kI8Block;   // (tokens run one step behind: a block on)
+    step(std::integral_constant<int, 0>{}, at0, at0, a[P], a[1 - P], bc, bn);
+    if constexpr (G > 1) step(std::integral_constant<int, 1>{}, at0, at1, a[1 - P], a[P], bc, bn);
     if constexpr (G > 2) {
-      step(std::integral_constant<int, 2>{}, i, a[P], a[1 - P], bc, bn);
-      step(std::integral_constant<int, 3>{}, i, a[1 - P], a[P], bc, bn);
+      step(std::integral_constant<int, 2>{}, at0, at1, a[P], a[1 - P], bc, bn);
+      step(std::integral_constant<int, 3>{}, at0, at1, a[1 - P], a[P], bc, bn);
     }
     sl = sn;
     sn = sn + SLOT == R * SLOT ? 0 : sn + SLOT;
@@ -228,12 +220,12 @@ __global__ __launch_bounds__(256, 1) void i8_gemm_kernel(const I8GemmArgs p) {
     const int xb = (v + G - 1) / G;
     load_group(v % G, v / G * SLOT, k_of(v / G), xb % R * SLOT, k_of(xb), 0, 64);
   }
-  constexpr auto first_wait = [](auto in, auto ld) {   // loads after those of virtual step - R G
+  constexpr auto first_wait = [](auto ld) {   // loads after those of virtual step - R G
     int n = 0;
     for (int v = 1; v <= (R - 1) * G; ++v) n += ld(v % G);
     return n;
   };
-  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(first_wait(in_flight, loads)) : "memory");
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(first_wait(loads)) : "memory");
 #pragma unroll
   for (int t = 0; t < FM; ++t)
 #pragma unroll
@@ -258,99 +250,110 @@ __global__ __launch_bounds__(256, 1) void i8_gemm_kernel(const I8GemmArgs p) {
   if (i < nb) block(i, std::integral_constant<int, 0>{}, b[0], b[1]);
 
   // ---- epilogue: lane (lr, lh) holds, of token lr of a tile, columns 8 q + 4 lh
-  // + 0 .. 3 of each weight tile.  Every load has landed, then the ring is free;
-  // outputs go through it so that a wave stores whole rows of the tile.
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  if (ks > 1 || (!SWIGLU && p.out_type == OutType::F32)) {
-    const int64_t pitch = SWIGLU ? 2 * (int64_t)N : N;
-    const bool wide = (N & 3) == 0, raw = ks > 1;
-    uint32_t *const out = raw ? reinterpret_cast<uint32_t *>(p.partial) + (int64_t)kz * M * pitch
-                              : static_cast<uint32_t *>(p.out);
+  // + 0 .. 3 of each weight tile.  Lanes exchange pieces until each has 16
+  // bytes of y and a store covers 16 tokens by 64 bytes.
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // (nothing goes to LDS after the end)
+  const int em = lane & 15, es = lane >> 4 & 1;
+  const bool raw = ks > 1, wide = raw || (!SWIGLU && p.out_type == OutType::F32);
+  const int64_t pitch = raw && SWIGLU ? 2 * (int64_t)N : N;
+  char *const to = raw ? reinterpret_cast<char *>(p.partial + (int64_t)kz * M * pitch)
+                       : static_cast<char *>(p.out);
+  const int n0 = nt * TN + wn * (TN / 2);
+  // 16 bytes of outputs of S bytes
+  auto store = [&](auto size, int64_t m, int n, int64_t shift, const u32x4 v) {
+    constexpr int S = decltype(size)::value, E = 16 / S;
+    if (m >= M || n >= N) return;
+    char *const o = to + (m * pitch + shift + n) * S;
+    if (N % E == 0) {
+      *reinterpret_cast<u32x4 *>(o) = v;
+    } else {
 #pragma unroll
-    for (int h = 0; h < P32; ++h) {   // the tokens of wave row h (or of both)
-      if (h > 0) __syncthreads();
-      if (P32 == 1 || wm == h) {
-#pragma unroll
-        for (int t = 0; t < FM; ++t) {
-          const int r = (P32 == 1 ? wm * FM * 32 : 0) + t * 32 + lr;
-          const float sx = sxl[(wm * FM + t) * 32 + lr];
-#pragma unroll
-          for (int f = 0; f < FN; ++f)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const f32x4 sw = *reinterpret_cast<const f32x4 *>(swl + (2 * f + wn) * 32 + 8 * q + 4 * lh);
-              u32x4 v;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int s = acc[f][t][4 * q + e];
-                v[e] = raw ? (uint32_t)s : __float_as_uint(i8_value(s, sx, sw[e]));
-              }
-              const int col = SWIGLU ? f / (FN / 2) * TN + wn * (TN / 2) + f % (FN / 2) * 32
-                                     : wn * (TN / 2) + f * 32;
-              *reinterpret_cast<u32x4 *>(lds + r * PITCH32 + (col + 8 * q + 4 * lh) * 4) = v;
-            }
-        }
-      }
-      __syncthreads();
-      constexpr int LANES = BN / 4 < 64 ? BN / 4 : 64, RW = 64 / LANES;   // lanes of a row, rows of a wave
-      const int c = lane % LANES * 4;
-      const int n = nt * TN + (SWIGLU ? c % TN : c);
-      const int64_t at = n + (SWIGLU && c >= TN ? N : 0);
-      if (n < N)
-        for (int r = wave * RW + lane / LANES; r < BM / P32; r += 4 * RW) {
-          const int64_t m = m0 + h * (BM / 2) + r;
-          if (m >= M) break;
-          const u32x4 v = *reinterpret_cast<const u32x4 *>(lds + r * PITCH32 + c * 4);
-          uint32_t *o = out + m * pitch + at;
-          if (wide) *reinterpret_cast<u32x4 *>(o) = v;
-          else
-            for (int e = 0; e < 4 && n + e < N; ++e)
-              o[e] = reinterpret_cast<const uint32_t *>(lds + r * PITCH32)[c + e];
+      for (int e = 0; e < E; ++e)
+        if (n + e < N) {
+          if constexpr (S == 4) reinterpret_cast<uint32_t *>(o)[e] = v[e];
+          else reinterpret_cast<uint16_t *>(o)[e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
         }
     }
-    return;
-  }
-  constexpr int FO = SWIGLU ? FN / 2 : FN;
+  };
+  // a: two 16-byte pieces of rows 0 .. 31 (halves of the wave), b: the two
+  // behind them -> a: the four of rows 0 .. 15, b: of rows 16 .. 31
+  auto gather = [](u32x4 &a, u32x4 &b) {
 #pragma unroll
-  for (int t = 0; t < FM; ++t) {
-    const int r = (wm * FM + t) * 32 + lr;
-    const float sx = sxl[r];
+    for (int e = 0; e < 4; ++e) {
+      const auto s = __builtin_amdgcn_permlane16_swap(a[e], b[e], false, false);
+      a[e] = s[0];
+      b[e] = s[1];
+    }
+  };
+  auto scales4 = [&](int f, int q) {
+    return *reinterpret_cast<const f32x4 *>(swl + (2 * f + wn) * 32 + 8 * q + 4 * lh);
+  };
+  if (wide) {
+#pragma unroll
+    for (int f = 0; f < FN; ++f) {
+      const int n = n0 + (SWIGLU ? f % (FN / 2) : f) * 32 + 4 * lh + 8 * es;
+      const int64_t shift = SWIGLU && f >= FN / 2 ? N : 0;
+#pragma unroll
+      for (int q = 0; q < 4; q += 2) {
+        const f32x4 sw[2] = {scales4(f, q), scales4(f, q + 1)};
+#pragma unroll
+        for (int t = 0; t < FM; ++t) {
+          const int r = (wm * FM + t) * 32;
+          const float sx = sxl[r + lr];
+          u32x4 v[2];
+#pragma unroll
+          for (int d = 0; d < 2; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int a_ = acc[f][t][4 * (q + d) + e];
+              v[d][e] = raw ? (uint32_t)a_ : __float_as_uint(i8_value(a_, sx, sw[d][e]));
+            }
+          gather(v[0], v[1]);
+          store(std::integral_constant<int, 4>{}, m0 + r + em, n + 8 * q, shift, v[0]);
+          store(std::integral_constant<int, 4>{}, m0 + r + 16 + em, n + 8 * q, shift, v[1]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  } else {
+    constexpr int FO = SWIGLU ? FN / 2 : FN;
 #pragma unroll
     for (int f = 0; f < FO; ++f)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int c = 8 * q + 4 * lh;
-        const f32x4 sw = *reinterpret_cast<const f32x4 *>(swl + (2 * f + wn) * 32 + c);
-        float v[4];
+      for (int t = 0; t < FM; ++t) {
+        const int r = (wm * FM + t) * 32;
+        const float sx = sxl[r + lr];
+        u32x4 v[2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = i8_value(acc[f][t][4 * q + e], sx, sw[e]);
-        if constexpr (SWIGLU) {
-          const f32x4 su = *reinterpret_cast<const f32x4 *>(swl + (2 * (f + FO) + wn) * 32 + c);
+        for (int d = 0; d < 2; ++d) {   // columns 16 d .. 16 d + 15 of the tile
+          u32x2 h[2];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            v[e] = silu_mul(v[e], i8_value(acc[f + FO][t][4 * q + e], sx, su[e]));
+          for (int c = 0; c < 2; ++c) {
+            const int q = 2 * d + c;
+            const f32x4 sw = scales4(f, q);
+            float z[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[e] = i8_value(acc[f][t][4 * q + e], sx, sw[e]);
+            if constexpr (SWIGLU) {
+              const f32x4 su = scales4(f + FO, q);
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                z[e] = silu_mul(z[e], i8_value(acc[f + FO][t][4 * q + e], sx, su[e]));
+            }
+            h[c] = u32x2{i8_pack_bf16(z[0], z[1]), i8_pack_bf16(z[2], z[3])};
+          }
+          // the lower half of the wave takes the first 8 columns, the upper the next
+          const auto lo = __builtin_amdgcn_permlane32_swap(h[0][0], h[1][0], false, false);
+          const auto hi = __builtin_amdgcn_permlane32_swap(h[0][1], h[1][1], false, false);
+          v[d] = u32x4{lo[0], hi[0], lo[1], hi[1]};
         }
-        *reinterpret_cast<u32x2 *>(lds + r * PITCH16 + (wn * (TN / 2) + f * 32 + c) * 2) =
-            u32x2{f32_to_bf16_bits(v[0]) | (f32_to_bf16_bits(v[1]) << 16),
-                  f32_to_bf16_bits(v[2]) | (f32_to_bf16_bits(v[3]) << 16)};
+        gather(v[0], v[1]);
+        const int n = n0 + f * 32 + 8 * lh + 16 * es;
+        store(std::integral_constant<int, 2>{}, m0 + r + em, n, 0, v[0]);
+        store(std::integral_constant<int, 2>{}, m0 + r + 16 + em, n, 0, v[1]);
+        __builtin_amdgcn_sched_barrier(0);
       }
   }
-  __syncthreads();
-  constexpr int LANES = TN / 8, RW = 64 / LANES;
-  const int c = lane % LANES * 8;
-  const int n = nt * TN + c;
-  const bool wide = (N & 7) == 0;
-  if (n < N)
-    for (int r = wave * RW + lane / LANES; r < BM; r += 4 * RW) {
-      const int64_t m = m0 + r;
-      if (m >= M) break;
-      const u32x4 v = *reinterpret_cast<const u32x4 *>(lds + r * PITCH16 + c * 2);
-      uint16_t *o = static_cast<uint16_t *>(p.out) + m * N + n;
-      if (wide) *reinterpret_cast<u32x4 *>(o) = v;
-      else
-        for (int e = 0; e < 8 && n + e < N; ++e)
-          o[e] = reinterpret_cast<const uint16_t *>(lds + r * PITCH16)[c + e];
-    }
 }
 
 // Adds the K parts and applies the epilogue, an output per thread.
@@ -373,31 +376,81 @@ __global__ __launch_bounds__(256) void i8_reduce_kernel(const I8GemmArgs p) {
   }
 }
 
-template <int FN, int FM, int R, int G, bool SWIGLU>
+template <int FN, int FM, int R, int G, int PER_CU, bool SWIGLU>
 hipError_t launch_tile(const I8GemmArgs &a, hipStream_t s) {
   constexpr int bm = 64 * FM, tn = SWIGLU ? 32 * FN : 64 * FN;
   int64_t items = (int64_t)((a.N + tn - 1) / tn) * ((a.M + bm - 1) / bm) * a.ksplit;
   items = (items + kI8Xcds - 1) / kI8Xcds * kI8Xcds;
-  launch_kernel((i8_gemm_kernel<FN, FM, R, G, SWIGLU>), dim3((unsigned)items), dim3(256), 0, s, a);
+  launch_kernel((i8_gemm_kernel<FN, FM, R, G, PER_CU, SWIGLU>), dim3((unsigned)items), dim3(256), 0,
+                s, a);
   return hipGetLastError();
 }
 template <bool SWIGLU>
 hipError_t launch_plan(const I8GemmArgs &a, const I8Plan &pl, hipStream_t s) {
-  switch (pl.bm) {
-    case 64: return launch_tile<4, 1, 3, 2, SWIGLU>(a, s);
-    case 128: return launch_tile<4, 2, 3, 2, SWIGLU>(a, s);
-    case 192: return launch_tile<4, 3, 2, 4, SWIGLU>(a, s);
-    default: return launch_tile<4, 4, 2, 4, SWIGLU>(a, s);
+  switch (pl.fn * 8 + pl.fm) {
+    case 4 * 8 + 4: return launch_tile<4, 4, 2, 4, 1, SWIGLU>(a, s);
+    case 4 * 8 + 3: return launch_tile<4, 3, 2, 4, 1, SWIGLU>(a, s);
+    case 4 * 8 + 2: return launch_tile<4, 2, 2, 2, 1, SWIGLU>(a, s);
+    case 4 * 8 + 1: return launch_tile<4, 1, 3, 2, 1, SWIGLU>(a, s);
+    case 2 * 8 + 2: return launch_tile<2, 2, 2, 2, 2, SWIGLU>(a, s);
+    case 2 * 8 + 1: return launch_tile<2, 1, 3, 2, 2, SWIGLU>(a, s);
+    default: break;
   }
+  if constexpr (!SWIGLU) {
+    if (pl.fn == 1 && pl.fm == 1) return launch_tile<1, 1, 4, 1, 2, false>(a, s);
+  }
+  return hipErrorInvalidValue;
 }
+
+// Tiles, and what a round of them over the CUs takes: per block of 128 columns,
+// and to start and store.  Fitted to measurements of every tile and number of
+// parts at 11 shapes and 33 to 2048 rows (the choice then takes 0.7% longer than
+// the best one on average, 8.5% at most).
+struct I8Tile {
+  int fn, fm;
+  double block_us, ends_us;
+};
+constexpr I8Tile kI8Tiles[] = {{1, 1, 0.21, 1.0}, {2, 1, 0.35, 1.7}, {4, 1, 0.62, 3.0},
+                               {2, 2, 0.41, 2.0}, {4, 2, 0.78, 3.4}, {4, 3, 0.97, 6.0},
+                               {4, 4, 1.24, 8.7}};
+constexpr int kI8MaxParts = 16;
 
 }  // namespace
 
+// The least estimate: rounds of tiles over the CUs; for K parts, which only fill
+// up a single round, another launch and the sums' way through memory.
 I8Plan i8_gemm_plan(bool swiglu, int64_t M, int64_t N, int64_t K) {
   I8Plan best;
-  best.bm = M <= 64 ? 64 : M <= 128 ? 128 : M <= 1024 ? 192 : 256;
-  (void)swiglu; (void)N; (void)K;
+  const int64_t KB = (K + kI8Block - 1) / kI8Block, width = swiglu ? 2 * N : N;
+  double best_us = 0.0;
+  for (const I8Tile &t : kI8Tiles) {
+    if (swiglu && t.fn % 2) continue;
+    const int64_t tn = 64 * t.fn / (swiglu ? 2 : 1), bm = 64 * t.fm;
+    const int64_t tiles = ((N + tn - 1) / tn) * ((M + bm - 1) / bm);
+    for (int64_t ks = 1; ks <= kI8MaxParts && ks <= KB && (ks == 1 || tiles * ks <= kI8CUs); ++ks) {
+      const int64_t rounds = (tiles * ks + kI8CUs - 1) / kI8CUs;
+      double us = (double)rounds * ((double)((KB + ks - 1) / ks) * t.block_us + t.ends_us);
+      if (ks > 1) us += 3.9 + (double)ks * M * width * 8.0 / 4.6e6;
+      if (best_us == 0.0 || us < best_us) {
+        best_us = us;
+        best.fn = t.fn;
+        best.fm = t.fm;
+        best.ksplit = (int)ks;
+      }
+    }
+  }
+  best.partial_ints = best.ksplit > 1 ? (size_t)best.ksplit * M * width : 0;
   return best;
+}
+
+// Parts fill one round of at least ceil(N / 256) tiles (gate and up rows
+// together: ceil(N / 128)), and their sums at most 256 of the largest tiles.
+size_t i8_gemm_max_partial(bool swiglu, int64_t M, int64_t N, int64_t K) {
+  const int64_t tn = swiglu ? 128 : 256, width = swiglu ? 2 * N : N;
+  const int64_t KB = (K + kI8Block - 1) / kI8Block;
+  const int64_t parts = std::min({(int64_t)kI8MaxParts, KB, kI8CUs / ((N + tn - 1) / tn)});
+  if (parts < 2) return 0;
+  return (size_t)std::min(parts * M * width, (int64_t)kI8CUs * 256 * 256);
 }
 
 hipError_t launch_i8_gemm(bool swiglu, const I8GemmArgs &args, const I8Plan &pl, hipStream_t s) {

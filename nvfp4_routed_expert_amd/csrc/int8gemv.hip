@@ -20,7 +20,8 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kI8Line = 128;             // columns of a block
-constexpr int kI8XBytes = 20 * 1024;     // x's codes in LDS of the QX form, at most
+constexpr int kI8XBytes = 20 * 1024;     // x's codes in LDS of the QX form, at most,
+constexpr int kI8XBytesFew = 52 * 1024;  // and with at most a workgroup per CU
 
 // bytes of LDS for M rows of codes: 16 bytes apart from a multiple of the banks
 __host__ __device__ constexpr int64_t i8_x_bytes(int64_t M, int64_t K) {
@@ -51,7 +52,7 @@ __global__ __launch_bounds__(64 * NW) void i8_gemv_kernel(const I8GemvArgs p) {
 
   // ---- the ring: a load fills 8 rows of 128 bytes, lane l position l % 8 of
   // row l / 8, which holds granule (l % 8) ^ (l / 8)
-  __amdgpu_buffer_rsrc_t wbuf[4], xbuf[8];
+  __amdgpu_buffer_rsrc_t wbuf[8], xbuf[8];
 #pragma unroll
   for (int h = 0; h < 2 * NT; ++h) wbuf[h] = f8_buffer(p.w[h / 2], r0 + h % 2 * 8, N, K);
   if constexpr (!QX) {
@@ -223,10 +224,12 @@ hipError_t launch_gemv(const I8GemvArgs &a, hipStream_t s) {
 }  // namespace
 
 bool i8_gemv_supported(bool swiglu, int64_t M, int64_t N, int64_t K) {
-  return M >= 1 && M <= 64 && (M <= (swiglu ? 32 : 16) || N * K < (M <= 32 ? 48 : 32) * 1000000);
+  return M >= 1 && (M <= 16 || (M <= 32 && (swiglu || (N <= 8192 && N * K < 70000000))));
 }
 bool i8_gemv_quantises(bool swiglu, int64_t M, int64_t N, int64_t K) {
-  return i8_gemv_supported(swiglu, M, N, K) && M <= 16 && i8_x_bytes(M, K) <= kI8XBytes;
+  if (!i8_gemv_supported(swiglu, M, N, K)) return false;
+  const int64_t bytes = i8_x_bytes(M, K);
+  return (M <= 16 && bytes <= kI8XBytes) || (bytes <= kI8XBytesFew && N <= 16 * 256);
 }
 
 hipError_t launch_i8_gemv(bool swiglu, const I8GemvArgs &a, hipStream_t s) {
@@ -234,25 +237,26 @@ hipError_t launch_i8_gemv(bool swiglu, const I8GemvArgs &a, hipStream_t s) {
       (!a.xs && !i8_gemv_quantises(swiglu, a.M, a.N, a.K)))
     return hipErrorInvalidValue;
   if (!a.xs) {
-    const bool small = i8_x_bytes(a.M, a.K) <= 10 * 1024;
+    const int64_t bytes = i8_x_bytes(a.M, a.K);
+    if (a.M > 16 || bytes > kI8XBytes)
+      return swiglu ? launch_gemv<4, true, true, 8, 2, kI8XBytesFew>(a, s)
+                    : launch_gemv<4, false, true, 8, 2, kI8XBytesFew>(a, s);
+    const bool small = bytes <= 10 * 1024;
     if (swiglu)
-      return small ? launch_gemv<2, true, true, 4, 4, 10 * 1024>(a, s)
-                   : launch_gemv<2, true, true, 4, 3, kI8XBytes>(a, s);
-    return small ? launch_gemv<2, false, true, 4, 4, 10 * 1024>(a, s)
+      return small ? launch_gemv<2, true, true, 4, 2, 10 * 1024>(a, s)
+                   : launch_gemv<2, true, true, 4, 2, kI8XBytes>(a, s);
+    return small ? launch_gemv<2, false, true, 4, 2, 10 * 1024>(a, s)
                  : launch_gemv<2, false, true, 8, 2, kI8XBytes>(a, s);
   }
-  if (a.M <= 8)
-    return swiglu ? launch_gemv<1, true, false, 4, 3>(a, s)
-                  : launch_gemv<1, false, false, 8, 3>(a, s);
-  switch ((a.M + 15) / 16 + (swiglu ? 4 : 0)) {
-    case 1: return launch_gemv<2, false, false, 8, 2>(a, s);
-    case 2: return launch_gemv<4, false, false, 8, 2>(a, s);
-    case 3: return launch_gemv<6, false, false, 4, 3>(a, s);
-    case 4: return launch_gemv<8, false, false, 4, 3>(a, s);
-    case 5: return launch_gemv<2, true, false, 8, 2>(a, s);
-    case 6: return launch_gemv<4, true, false, 8, 2>(a, s);
-    case 7: return launch_gemv<6, true, false, 4, 3>(a, s);
-    default: return launch_gemv<8, true, false, 4, 2>(a, s);
+  switch ((a.M + 7) / 8) {
+    case 1:
+      return swiglu ? launch_gemv<1, true, false, 4, 2>(a, s) : launch_gemv<1, false, false, 4, 2>(a, s);
+    case 2:
+      return swiglu ? launch_gemv<2, true, false, 4, 2>(a, s) : launch_gemv<2, false, false, 4, 2>(a, s);
+    case 3:
+      return swiglu ? launch_gemv<3, true, false, 4, 2>(a, s) : launch_gemv<3, false, false, 4, 2>(a, s);
+    default:
+      return swiglu ? launch_gemv<4, true, false, 4, 2>(a, s) : launch_gemv<4, false, false, 4, 2>(a, s);
   }
 }
 

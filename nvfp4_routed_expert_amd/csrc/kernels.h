@@ -407,14 +407,17 @@ struct I8GemmArgs {
   int ksplit;
   int32_t *partial;       // [ksplit][M][N, or 2 N: gate then up sums]
 };
-// Tokens of a tile and K parts for a problem; a split needs partial_ints words
-// of workspace.
+// Tile (64 fn weight rows, gate and up rows together in the gate/up form, by
+// 64 fm tokens) and K parts for a problem; a split needs partial_ints words of
+// workspace.
 struct I8Plan {
-  int bm = 0;
+  int fn = 0, fm = 0;
   int ksplit = 1;
   size_t partial_ints = 0;
 };
 I8Plan i8_gemm_plan(bool swiglu, int64_t M, int64_t N, int64_t K);
+// At least the partial_ints of any 1 .. M rows.
+size_t i8_gemm_max_partial(bool swiglu, int64_t M, int64_t N, int64_t K);
 hipError_t launch_i8_gemm(bool swiglu, const I8GemmArgs &a, const I8Plan &pl, hipStream_t s);
 
 // The same product for a few rows (int8gemv.hip), where _supported says so.  xs

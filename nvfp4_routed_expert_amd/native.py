@@ -139,6 +139,8 @@ def lib():
                                 ctypes.POINTER(Int8Matrix), ctypes.POINTER(Int8Matrix), _vp, _i32,
                                 _vp, _sz, _vp]),
             "int8_mlp_workspace_size": (_sz, [_i64, _i64, _i64, ctypes.c_int]),
+            "int8_debug_plan": (ctypes.c_int, [ctypes.c_int, _i64, _i64, _i64,
+                                               ctypes.POINTER(_i32), ctypes.POINTER(_i32)]),
             "rms_norm_quantize": (_i32, [ctypes.POINTER(RmsNormArgs), _i64, _i64, _vp]),
             "moe_layer_decode": (_i32, [_vp, _i64, ctypes.POINTER(MoeLayerC), ctypes.c_int, _vp,
                                         _vp, _vp, _i32, _vp, _sz, _vp]),
@@ -177,7 +179,7 @@ def exported_symbols():
             "fp8_block_quantize", "fp8_block_linear", "fp8_block_linear_workspace_size",
             "fp8_block_mlp", "fp8_block_mlp_workspace_size", "fp8_block_debug_plan",
             "int8_quantize", "int8_linear", "int8_linear_workspace_size", "int8_mlp",
-            "int8_mlp_workspace_size", "rms_norm_quantize",
+            "int8_mlp_workspace_size", "int8_debug_plan", "rms_norm_quantize",
             "moe_layer_decode", "moe_layer_decode_workspace_size", "moe_layer_debug_plan",
             "nvfp4_set_ffn_stage_events",
             "nvfp4_set_ffn_separate_h_quant", "nvfp4_read_probe",
@@ -828,6 +830,15 @@ def int8_mlp(x, gate, up, down, x_scales=None, out_dtype=torch.bfloat16, workspa
                           *(ctypes.byref(m) for m in mats.values()), y.data_ptr(), _dt(y.dtype),
                           ws[1], ws[2], _stream_of(dev)))
     return y
+
+
+def int8_debug_plan(M, N, K, gate_up=False):
+    """(rows of x of a tile, rows of W, parts of K) of an int8 product, (0, 0, 0)
+    where the form for a few rows takes it."""
+    columns, parts = _i32(), _i32()
+    rows = lib().int8_debug_plan(int(gate_up), M, N, K, ctypes.byref(columns),
+                                 ctypes.byref(parts))
+    return rows, columns.value, parts.value
 
 
 class RmsNorm(NamedTuple):

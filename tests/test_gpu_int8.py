@@ -396,3 +396,118 @@ def test_a_dense_block(T):
     again = native.fp8_block_quantize(torch.from_numpy(n).to(DEV))
     assert torch.equal(f.codes, again[0]) and torch.equal(f.scales, again[1])
     assert torch.equal(got, native.fp8_block_linear(again[0], *w8, x_scales=again[1]))
+
+
+# ---- every tile of the batch form ------------------------------------------------------
+
+# (M, N, K, rows of x of a tile, rows of W, parts): every tile with K whole and
+# in parts, last tiles of one row and of all but one, odd N, K with a last block
+# of 32, 64, 96 and 128 columns, parts of different lengths.
+TILE_SHAPES = [(129, 19, 32, 64, 64, 1), (63, 23, 64, 64, 64, 1), (193, 25, 3232, 64, 64, 13),
+               (63, 31, 3264, 64, 64, 13), (513, 1797, 32, 64, 128, 1), (511, 2389, 64, 64, 128, 1),
+               (513, 585, 8288, 64, 128, 5), (511, 689, 10688, 64, 128, 5),
+               (513, 6581, 32, 64, 256, 1), (319, 10881, 64, 64, 256, 1),
+               (63, 16845, 9600, 64, 256, 3), (1025, 1929, 32, 128, 128, 1),
+               (639, 3449, 64, 128, 128, 1), (641, 521, 12192, 128, 128, 8),
+               (639, 793, 10560, 128, 128, 6), (641, 5931, 32, 128, 256, 1),
+               (1023, 4167, 64, 128, 256, 1), (257, 7071, 12640, 128, 256, 3),
+               (1537, 5113, 32, 192, 256, 1), (1535, 5559, 64, 192, 256, 1),
+               (577, 6605, 8928, 192, 256, 2), (575, 7291, 9152, 192, 256, 2),
+               (2049, 6073, 672, 256, 256, 1), (1279, 9783, 704, 256, 256, 1),
+               (255, 16761, 11648, 256, 256, 3)]
+# (T, I, H, ...) of the gate and up products
+MLP_TILE_SHAPES = [(65, 32, 32, 64, 128, 1), (63, 32, 64, 64, 128, 1), (65, 32, 1568, 64, 128, 13),
+                   (63, 32, 1600, 64, 128, 13), (129, 8288, 32, 64, 256, 1),
+                   (319, 5568, 64, 64, 256, 1), (63, 8352, 9600, 64, 256, 3),
+                   (1025, 992, 32, 128, 128, 1), (1023, 1056, 64, 128, 128, 1),
+                   (129, 1824, 4000, 128, 128, 4), (1023, 352, 5696, 128, 128, 3),
+                   (1025, 1952, 32, 128, 256, 1), (1023, 2240, 64, 128, 256, 1),
+                   (385, 8256, 32, 192, 256, 1), (575, 6560, 64, 192, 256, 1),
+                   (1537, 1312, 9120, 192, 256, 2), (1535, 1376, 10432, 192, 256, 2),
+                   (1281, 4672, 672, 256, 256, 1), (1279, 5120, 704, 256, 256, 1),
+                   (255, 8352, 11264, 256, 256, 3), (66, 8768, 10304, 128, 256, 3)]
+
+
+def dev_codes(n, k, seed, scale=1.0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    q = torch.randint(-128, 128, (n, k), generator=g, dtype=torch.int8, device=DEV)
+    return q, (torch.rand(n, generator=g, device=DEV) * 1e-3 + 1e-4) * scale
+
+
+def dev_linear(x, xs, w, ws):
+    """As linear_ref, on the device (64-bit sums of integers: exact)."""
+    return ((x.double() @ w.double().t()).float() * xs[:, None]) * ws[None, :]
+
+
+@pytest.mark.parametrize("M,N,K,rows,columns,parts", TILE_SHAPES)
+def test_linear_of_every_tile(M, N, K, rows, columns, parts):
+    say("tile", M, N, K)
+    assert native.int8_debug_plan(M, N, K) == (rows, columns, parts)
+    (x, xs), (w, ws) = dev_codes(M, K, M), dev_codes(N, K, N)
+    ref = dev_linear(x, xs, w, ws)
+    for dt in (torch.float32, torch.bfloat16):
+        buf = torch.full(((M + rows) * N,), 7.0, dtype=dt, device=DEV)   # (rows behind the last)
+        out = buf[:M * N].view(M, N)
+        native.int8_linear(x, w, ws, x_scales=xs, out=out)
+        assert torch.equal(out, ref.to(dt)) and torch.all(buf[M * N:] == 7.0)
+
+
+@pytest.mark.parametrize("T,I,H,rows,columns,parts", MLP_TILE_SHAPES)
+def test_mlp_of_every_tile(T, I, H, rows, columns, parts):
+    """As test_mlp, on the device: an h whose rounding expf may decide moves its
+    code by at most one (or, as the row's maximum, all by one and the scale by
+    2^-7)."""
+    say("mlp tile", T, I, H)
+    assert native.int8_debug_plan(T, I, H, gate_up=True) == (rows, columns, parts)
+    x, xs = dev_codes(T, H, T)
+    gate, up, down = (dev_codes(n, k, s, 20.0 / k ** 0.5)
+                      for s, (n, k) in ((1, (I, H)), (2, (I, H)), (3, (H, I))))
+    xs = xs * 100
+    g, u = dev_linear(x, xs, *gate).double(), dev_linear(x, xs, *up).double()
+    h64 = g / (1 + torch.exp(-g)) * u
+    dh = h64.abs() * 2.0 ** -20
+    h = h64.bfloat16()
+    loose = (h64 - dh).bfloat16() != (h64 + dh).bfloat16()
+    assert loose.double().mean() < 0.01
+    q, s = quantize_ref(h.float().cpu().numpy())
+    q, s = torch.from_numpy(q.astype(np.int8)).to(DEV), torch.from_numpy(s).to(DEV)
+    ref = dev_linear(q, s, *down).double()
+    hf = h.double().abs()
+    moves = (loose & (hf >= 0.98 * hf.amax(1, keepdim=True))).any(1, keepdim=True)
+    per = torch.where(moves, 1.01 + q.double().abs() * 2.0 ** -7, loose.double()) * s[:, None]
+    bound = per @ (down[0].double().abs() * down[1][:, None]).t()
+    bound = torch.where(loose.any(1, keepdim=True), bound + 2.0 ** -21 * (ref.abs() + bound),
+                        torch.zeros_like(bound))
+    y = native.int8_mlp(x, gate, up, down, x_scales=xs, out_dtype=torch.float32)
+    over = (y.double() - ref).abs() - bound
+    assert (over <= 0).all(), f"{(over > 0).sum().item()} outside, worst {over.max().item()}"
+    assert torch.equal(native.int8_mlp(x, gate, up, down, x_scales=xs), y.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("M,N,K", [(16, 33, 1216), (17, 70, 640), (9, 100, 1120), (31, 4096, 1600),
+                                   (32, 4112, 1600), (32, 8192, 96), (17, 8193, 96), (32, 64, 17408),
+                                   (1, 50, 9984), (1, 50, 10240), (1, 50, 20352), (1, 50, 20480),
+                                   (4, 30, 5088), (4, 30, 5120), (24, 40, 131040)])
+def test_linear_at_the_rules(M, N, K):
+    """Either side of the rules: x quantised inside (in little, in more LDS, with
+    a workgroup per CU) or by a launch; few rows or a batch."""
+    test_linear(M, N, K)
+
+
+@pytest.mark.parametrize("T,H,I", [(1, 17440, 64), (1, 64, 17440), (16, 1024, 32), (17, 2048, 96),
+                                   (32, 96, 4128), (32, 1568, 160), (33, 160, 1568), (24, 32, 8224)])
+def test_mlp_at_the_rules(T, H, I):
+    test_mlp(T, H, I)
+
+
+@pytest.mark.parametrize("M", [1, 6])
+def test_large_weights_equal_their_parts(M):
+    """Weights past the size from which they are loaded as used once: columns of
+    y as with the rows of W alone."""
+    H, I, part = 5120, 13056, 384
+    say("large weights", M)
+    x = acts(M, H, 3).to(DEV)
+    w, ws = dev_codes(2 * I, H, 5)
+    y = native.int8_linear(x, w, ws)
+    assert torch.equal(y[:, -part:], native.int8_linear(x, w[-part:].contiguous(),
+                                                        ws[-part:].contiguous()))

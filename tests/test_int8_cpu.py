@@ -218,3 +218,40 @@ def test_binding_refusals():
         native.rms_norm_quantize(x, g, codes="int8")
     with pytest.raises(ValueError, match=r"\[T, H\]"):
         native.rms_norm_quantize(x[0], g, codes="int8")
+
+
+def test_the_shapes_of_the_gpu_tests_take_the_tiles_they_name():
+    """The plan is host code: a changed rule shows here, before the GPU tests of
+    the tiles lose what they are for."""
+    from test_gpu_int8 import MLP_TILE_SHAPES, TILE_SHAPES
+    for M, N, K, *plan in TILE_SHAPES:
+        assert native.int8_debug_plan(M, N, K) == tuple(plan), (M, N, K)
+    for T, I, H, *plan in MLP_TILE_SHAPES:
+        assert native.int8_debug_plan(T, I, H, gate_up=True) == tuple(plan), (T, I, H)
+    tiles = {(64, 64), (64, 128), (64, 256), (128, 128), (128, 256), (192, 256), (256, 256)}
+    kinds = lambda shapes: {(s[3], s[4], s[5] > 1) for s in shapes}
+    assert kinds(TILE_SHAPES) == {(*t, split) for t in tiles for split in (False, True)}
+    assert kinds(MLP_TILE_SHAPES) == {(*t, split) for t in tiles - {(64, 64)}
+                                      for split in (False, True)}
+    assert native.int8_debug_plan(16, 4096, 4096) == (0, 0, 0)
+    assert native.int8_debug_plan(32, 4096, 4096, gate_up=True) == (0, 0, 0)
+    for bad in ((0, 64, 64), (64, 0, 64), (64, 64, 0), (-1, 64, 64)):
+        assert native.int8_debug_plan(*bad) == (0, 0, 0)
+    assert native.lib().int8_debug_plan(0, 64, 64, 64, None, None) > 0
+
+
+@pytest.mark.parametrize("N,K", MONOTONE)
+def test_parts_fit_the_workspace(N, K):
+    """The sums of a call's parts fit what the query of any larger batch names
+    for them (what is left of the workspace holds x's codes and scales)."""
+    L = native.lib()
+    for gate_up in (False, True):
+        n = (N + 31) // 32 * 32 if gate_up else N
+        for M in [*range(1, 700, 3), 1023, 1500, 2049, 5000]:
+            parts = native.int8_debug_plan(M, n, K, gate_up)[2]
+            if parts < 2:
+                continue
+            words = parts * M * n * (2 if gate_up else 1)
+            size = L.int8_mlp_workspace_size(M, K, n, 1) if gate_up else \
+                L.int8_linear_workspace_size(M, n, K, 1)
+            assert size >= 4 * words, (M, n, K, gate_up)
