@@ -134,8 +134,8 @@ __device__ __forceinline__ void store_f8(uint8_t *codes, int64_t at, float *scal
 }
 
 // Rows of at most P pieces of 8 columns per lane: p.waves waves a row.
-template <bool XF32, int RES, bool NORM, RowCodes FMT, int P>
-__global__ __launch_bounds__(1024) void row_kernel(const RowArgs p) {
+template <bool XF32, int RES, bool NORM, RowCodes FMT, int P, int THREADS>
+__global__ __launch_bounds__(THREADS) void row_kernel(const RowArgs p) {
 #pragma clang fp contract(off)
   __shared__ double sums[16];
   __shared__ float tops[16];
@@ -148,6 +148,7 @@ __global__ __launch_bounds__(1024) void row_kernel(const RowArgs p) {
   for (int64_t row0 = (int64_t)blockIdx.x * per; row0 < p.rows; row0 += (int64_t)gridDim.x * per) {
     const int64_t row = row0 + mine;
     const bool ok = row < p.rows;
+    if (waves > 1 && row0 != (int64_t)blockIdx.x * per) __syncthreads();   // (sums and tops are read)
     Raw8<XF32> rx[P];
     Raw8<RES == 2> rr[P];
 #pragma unroll
@@ -207,6 +208,7 @@ __global__ __launch_bounds__(1024) void row_kernel(const RowArgs p) {
       }
     }
     if constexpr (FMT == RowCodes::FP8) {
+      if (!p.codes) continue;   // (y alone)
       const int cb = (cols + kF8Block - 1) / kF8Block;
 #pragma unroll
       for (int j = 0; j < P; ++j) {
@@ -228,7 +230,6 @@ __global__ __launch_bounds__(1024) void row_kernel(const RowArgs p) {
       }
       if (ok && t == 0) p.scales[row] = s;
     }
-    if (waves > 1) __syncthreads();   // (sums and tops are read)
   }
 }
 
@@ -308,7 +309,7 @@ __global__ __launch_bounds__(1024) void row_long_kernel(const RowArgs p) {
       for (int i = 0; i < 8; ++i) v[i] = 0.0f;
       if (in) value(col, v);
       if (in && p.y) store8(p.y, row * cols + col, p.y_f32, v);
-      if (FMT == RowCodes::FP8)
+      if (FMT == RowCodes::FP8 && p.codes)
         store_f8(p.codes, row * cols + col, p.scales, row * cb + col / kF8Block, v, in);
       if (FMT == RowCodes::INT8 && in) store_i8(p.codes, row * cols + col, v, inv);
     }
@@ -318,23 +319,37 @@ __global__ __launch_bounds__(1024) void row_long_kernel(const RowArgs p) {
 
 constexpr int64_t kRowMaxPieces = 16 * 64 * 4;
 
+// Waves of a row.  Many rows: up to 5 pieces a lane (2048 rows of 5120 to int8:
+// 1 wave 16.2 us, 2 waves 14.6, 4 15.3, 8 17.2, 16 23.3; 4096 of 2048: 1 wave
+// 11.9, 4 13.4, 16 33.7).  A few rows take more waves, up to 8 per CU, for
+// their latency.
+int row_waves(int64_t rows, int64_t pieces) {
+  int waves = 1;
+  while (waves < 16 && (pieces > waves * 64 * 5 || (pieces > waves * 64 && rows * waves <= 1024)))
+    waves *= 2;
+  return waves;
+}
+
 template <bool XF32, int RES, bool NORM, RowCodes FMT>
 hipError_t launch_pieces(RowArgs a, hipStream_t s) {
   const int64_t pieces = a.cols / 8;
-  int waves = 1;
-  while (waves < 16 && pieces > waves * 64) waves *= 2;
-  a.waves = waves;
-  const int threads = waves < 4 ? 256 : waves * 64;
-  const int per = threads / 64 / waves;
+  const int waves = a.waves = row_waves(a.rows, pieces);
+  const int threads = waves < 4 ? 256 : waves * 64, per = threads / 64 / waves;
   int64_t grid = (a.rows + per - 1) / per;
   if (grid > kRowMaxGrid) grid = kRowMaxGrid;
   const dim3 g((unsigned)grid), b(threads);
-  if (pieces <= waves * 64)
-    launch_kernel((row_kernel<XF32, RES, NORM, FMT, 1>), g, b, 0, s, a);
-  else if (pieces <= waves * 128)
-    launch_kernel((row_kernel<XF32, RES, NORM, FMT, 2>), g, b, 0, s, a);
-  else
-    launch_kernel((row_kernel<XF32, RES, NORM, FMT, 4>), g, b, 0, s, a);
+  const int n = (int)((pieces + waves * 64 - 1) / (waves * 64));   // pieces of a lane
+  if (waves == 16) {
+    if (n <= 1) launch_kernel((row_kernel<XF32, RES, NORM, FMT, 1, 1024>), g, b, 0, s, a);
+    else if (n == 2) launch_kernel((row_kernel<XF32, RES, NORM, FMT, 2, 1024>), g, b, 0, s, a);
+    else launch_kernel((row_kernel<XF32, RES, NORM, FMT, 4, 1024>), g, b, 0, s, a);
+  } else {
+    if (n <= 1) launch_kernel((row_kernel<XF32, RES, NORM, FMT, 1, 512>), g, b, 0, s, a);
+    else if (n == 2) launch_kernel((row_kernel<XF32, RES, NORM, FMT, 2, 512>), g, b, 0, s, a);
+    else if (n == 3) launch_kernel((row_kernel<XF32, RES, NORM, FMT, 3, 512>), g, b, 0, s, a);
+    else if (n == 4) launch_kernel((row_kernel<XF32, RES, NORM, FMT, 4, 512>), g, b, 0, s, a);
+    else launch_kernel((row_kernel<XF32, RES, NORM, FMT, 5, 512>), g, b, 0, s, a);
+  }
   return hipGetLastError();
 }
 
@@ -363,11 +378,8 @@ hipError_t launch_rows(const RowArgs &a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_rms_norm(const RowArgs &a, RowCodes codes, hipStream_t s) {
-  switch (codes) {
-    case RowCodes::FP8: return launch_rows<true, RowCodes::FP8>(a, s);
-    case RowCodes::INT8: return launch_rows<true, RowCodes::INT8>(a, s);
-    default: return launch_rows<true, RowCodes::NONE>(a, s);
-  }
+  return codes == RowCodes::INT8 ? launch_rows<true, RowCodes::INT8>(a, s)
+                                 : launch_rows<true, RowCodes::FP8>(a, s);
 }
 
 hipError_t launch_i8_quantize(const void *x, InType t, int64_t rows, int64_t cols, int64_t ld,
