@@ -744,11 +744,10 @@ def _rows_stride(name, x, dev=None):
     """Row stride of a matrix of rows (unit column stride, on dev)."""
     if dev is not None and x.device != dev:
         raise ValueError(f"{name} is on {x.device}, x on {dev}")
-    rows, cols = x.shape
     ld, step = x.stride()
-    if cols > 1 and step != 1:
+    if step != 1 and x.shape[1] > 1:
         raise ValueError(f"{name} must have unit column stride")
-    return ld if rows > 1 else _round_up(cols, 8)
+    return ld if x.shape[0] > 1 else _round_up(x.shape[1], 8)
 
 
 def int8_quantize(x, out=None):
@@ -775,14 +774,16 @@ def int8_quantize(x, out=None):
 
 
 def _int8_rows(x, x_scales, cols):
-    """Checks the left operand of an int8 product."""
+    """Checks the left operand of an int8 product; the address of its scales."""
     if x.dim() != 2 or x.shape[1] != cols:
         raise ValueError(f"x {tuple(x.shape)} does not match a weight of {cols} columns")
+    want = torch.bfloat16 if x_scales is None else torch.int8
+    if x.dtype is not want:
+        raise TypeError(f"x is {x.dtype}, expected {want}")
     if x_scales is None:
-        _expect("x", x, x.shape, torch.bfloat16)
-    else:
-        _expect("x", x, x.shape, torch.int8)
-        _expect("x_scales", x_scales, (x.shape[0],), torch.float32)
+        return None
+    _expect("x_scales", x_scales, (x.shape[0],), torch.float32)
+    return x_scales.data_ptr()
 
 
 def int8_linear(x, codes, scales, x_scales=None, out_dtype=torch.bfloat16, workspace=None,
@@ -792,7 +793,7 @@ def int8_linear(x, codes, scales, x_scales=None, out_dtype=torch.bfloat16, works
     codes of int8_quantize(x) or rms_norm_quantize(codes="int8").  out must not
     overlap x."""
     m = _int8_matrix("W", codes, scales)
-    _int8_rows(x, x_scales, m.cols)
+    xs = _int8_rows(x, x_scales, m.cols)
     M, K = x.shape
     dev = _device_of(x, rows=x, codes=codes, scales=scales, x_scales=x_scales, out=out,
                      workspace=workspace)
@@ -802,10 +803,10 @@ def int8_linear(x, codes, scales, x_scales=None, out_dtype=torch.bfloat16, works
         _expect("out", out, (M, m.rows), out.dtype)
         y = out
     L = lib()
-    ws = _scratch(L.int8_linear_workspace_size(M, m.rows, K, x_scales is not None), dev, workspace)
+    keep, ws, n = _scratch(L.int8_linear_workspace_size(M, m.rows, K, xs is not None), dev,
+                           workspace)
     with _on(dev):
-        _check(L.int8_linear(x.data_ptr(), None if x_scales is None else x_scales.data_ptr(), M,
-                             ctypes.byref(m), y.data_ptr(), _dt(y.dtype), ws[1], ws[2],
+        _check(L.int8_linear(x.data_ptr(), xs, M, m, y.data_ptr(), _dt(y.dtype), ws, n,
                              _stream_of(dev)))
     return y
 
@@ -813,22 +814,25 @@ def int8_linear(x, codes, scales, x_scales=None, out_dtype=torch.bfloat16, works
 def int8_mlp(x, gate, up, down, x_scales=None, out_dtype=torch.bfloat16, workspace=None, out=None):
     """y [T, H] = down(silu(x Wg^T) * (x Wu^T)) with int8 weights: gate, up
     ([I, H]) and down ([H, I]) are (codes, scales) pairs from int8_quantize(w).
-    x [T, H] bf16, or codes with their x_scales; h is quantised per token."""
-    mats = {n: _int8_matrix(n, *p) for n, p in (("gate", gate), ("up", up), ("down", down))}
-    I, H = mats["gate"].rows, mats["gate"].cols
-    _int8_rows(x, x_scales, H)
+    x [T, H] bf16, or codes with their x_scales; h is quantised per token.  out
+    must not overlap x."""
+    g, u, d = _int8_matrix("gate", *gate), _int8_matrix("up", *up), _int8_matrix("down", *down)
+    I, H = g.rows, g.cols
+    xs = _int8_rows(x, x_scales, H)
     T = x.shape[0]
     dev = _device_of(x, rows=x, gate=gate[0], up=up[0], down=down[0], gate_scales=gate[1],
                      up_scales=up[1], down_scales=down[1], x_scales=x_scales, out=out,
                      workspace=workspace)
-    y = out if out is not None else torch.empty((T, H), dtype=out_dtype, device=dev)
-    _expect("out", y, (T, H), y.dtype)
+    if out is None:
+        y = torch.empty((T, H), dtype=out_dtype, device=dev)
+    else:
+        _expect("out", out, (T, H), out.dtype)
+        y = out
     L = lib()
-    ws = _scratch(L.int8_mlp_workspace_size(T, H, I, x_scales is not None), dev, workspace)
+    keep, ws, n = _scratch(L.int8_mlp_workspace_size(T, H, I, xs is not None), dev, workspace)
     with _on(dev):
-        _check(L.int8_mlp(x.data_ptr(), None if x_scales is None else x_scales.data_ptr(), T,
-                          *(ctypes.byref(m) for m in mats.values()), y.data_ptr(), _dt(y.dtype),
-                          ws[1], ws[2], _stream_of(dev)))
+        _check(L.int8_mlp(x.data_ptr(), xs, T, g, u, d, y.data_ptr(), _dt(y.dtype), ws, n,
+                          _stream_of(dev)))
     return y
 
 
@@ -868,38 +872,57 @@ def rms_norm_quantize(x, weight, residual=None, eps=1e-6, codes=None, y_dtype=No
         raise ValueError(f"x must be [T, H], got {tuple(x.shape)}")
     T, H = x.shape
     fmt, code_t = _NORM_CODES[codes]
-    o = out if out is not None else RmsNorm(None, None, None, None)
-    dev = _device_of(x, weight=weight, y=o.y, codes=o.codes, scales=o.scales)
-    _expect("weight", weight, (H,), weight.dtype)
-    a = RmsNormArgs()
-    a.x, a.x_dtype, a.ld_x = x.data_ptr(), _dt(x.dtype), _rows_stride("x", x)
-    a.weight, a.weight_dtype, a.eps = weight.data_ptr(), _dt(weight.dtype), eps
-    total = None
-    if residual is not None:
+    dev = _device_of(x, weight=weight)
+    if weight.shape != (H,):
+        raise ValueError(f"weight has shape {tuple(weight.shape)}, expected {(H,)}")
+    y = q = s = total = None
+    if out is not None:
+        y, q, s, total = out
+        _device_of(x, y=y, codes=q, scales=s)
+    r_ptr = t_ptr = None
+    r_type = r_ld = t_ld = 0
+    if residual is None:
+        total = None
+    else:
         _expect("residual", residual, (T, H), residual.dtype)
-        a.residual, a.residual_dtype = residual.data_ptr(), _dt(residual.dtype)
-        a.ld_residual = _rows_stride("residual", residual, dev)
-        total = o.residual
+        r_ptr, r_type = residual.data_ptr(), _dt(residual.dtype)
+        r_ld = _rows_stride("residual", residual, dev)
         if total is None:
             total = torch.empty((T, H), dtype=residual.dtype, device=dev)
-        _expect("out.residual", total, (T, H), residual.dtype)
-        a.residual_out = total.data_ptr()
-        a.ld_residual_out = _rows_stride("out.residual", total, dev)
-    y = q = s = None
-    if y_dtype is not None:
-        y = torch.empty((T, H), dtype=y_dtype, device=dev) if o.y is None else o.y
-        _expect("y", y, (T, H), y_dtype)
-        a.y, a.y_dtype = y.data_ptr(), _dt(y_dtype)
-    if fmt:
+            t_ld = H
+        else:
+            _expect("out.residual", total, (T, H), residual.dtype)
+            t_ld = _rows_stride("out.residual", total, dev)
+        t_ptr = total.data_ptr()
+    y_ptr = q_ptr = s_ptr = None
+    y_type = 0
+    if y_dtype is None:
+        y = None
+    else:
+        y_type = _dt(y_dtype)
+        if y is None:
+            y = torch.empty((T, H), dtype=y_dtype, device=dev)
+        else:
+            _expect("y", y, (T, H), y_dtype)
+        y_ptr = y.data_ptr()
+    if not fmt:
+        q = s = None
+    else:
         shape = (T, _fp8_blocks(H)) if fmt == 1 else (T,)
-        q = torch.empty((T, H), dtype=code_t, device=dev) if o.codes is None else o.codes
-        s = torch.empty(shape, dtype=torch.float32, device=dev) if o.scales is None else o.scales
-        _expect("codes", q, (T, H), code_t)
-        _expect("scales", s, shape, torch.float32)
-        a.codes, a.scales = q.data_ptr(), s.data_ptr()
-    a.format = fmt
+        if q is None:
+            q = torch.empty((T, H), dtype=code_t, device=dev)
+        else:
+            _expect("codes", q, (T, H), code_t)
+        if s is None:
+            s = torch.empty(shape, dtype=torch.float32, device=dev)
+        else:
+            _expect("scales", s, shape, torch.float32)
+        q_ptr, s_ptr = q.data_ptr(), s.data_ptr()
+    a = RmsNormArgs(x.data_ptr(), _dt(x.dtype), _rows_stride("x", x), r_ptr, r_type, r_ld, t_ptr,
+                    t_ld, weight.data_ptr(), _dt(weight.dtype), eps, y_ptr, y_type, fmt, q_ptr,
+                    s_ptr)
     with _on(dev):
-        _check(lib().rms_norm_quantize(ctypes.byref(a), T, H, _stream_of(dev)))
+        _check(lib().rms_norm_quantize(a, T, H, _stream_of(dev)))
     return RmsNorm(y, q, s, total)
 
 
