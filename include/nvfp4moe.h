@@ -679,11 +679,13 @@ size_t int8_mlp_workspace_size(int64_t T, int64_t H, int64_t I, int quantised);
  * of M rows with an int8 W [N, K] runs (gate_up: the gate and up products of
  * int8_mlp, N = I and K = H): returns the rows of x of a tile of the batch
  * form (64, 128, 192 or 256), sets *columns to its rows of W (gate and up
- * together) and *parts to the parts that K is split into; 0, 0 and 0 for the
- * form for a few rows, and for sizes below 1.  Either pointer may be NULL.
+ * together), *parts to the parts that K is split into and *main to the columns
+ * of y that these tiles take (a second launch takes any others in smaller
+ * tiles); all 0 for the form for a few rows, and for sizes below 1.  The
+ * pointers may be NULL.
  */
 int int8_debug_plan(int gate_up, int64_t M, int64_t N, int64_t K, int32_t *columns,
-                    int32_t *parts);
+                    int32_t *parts, int64_t *main);
 
 /*
  * rms_norm_quantize: the front of a block.  Per token t of T, over H columns:

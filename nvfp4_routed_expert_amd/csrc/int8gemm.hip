@@ -255,7 +255,7 @@ __global__ __launch_bounds__(256, PER_CU) void i8_gemm_kernel(const I8GemmArgs p
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // (nothing goes to LDS after the end)
   const int em = lane & 15, es = lane >> 4 & 1;
   const bool raw = ks > 1, wide = raw || (!SWIGLU && p.out_type == OutType::F32);
-  const int64_t pitch = raw && SWIGLU ? 2 * (int64_t)N : N;
+  const int64_t pitch = raw ? (SWIGLU ? 2 * (int64_t)N : N) : p.ld;
   char *const to = raw ? reinterpret_cast<char *>(p.partial + (int64_t)kz * M * pitch)
                        : static_cast<char *>(p.out);
   const int n0 = nt * TN + wn * (TN / 2);
@@ -356,23 +356,52 @@ __global__ __launch_bounds__(256, PER_CU) void i8_gemm_kernel(const I8GemmArgs p
   }
 }
 
-// Adds the K parts and applies the epilogue, an output per thread.
-template <bool SWIGLU>
+// Adds the K parts and applies the epilogue: E outputs of a row per thread (4,
+// or 1 where rows are not whole quads).
+template <bool SWIGLU, int E>
 __global__ __launch_bounds__(256) void i8_reduce_kernel(const I8GemmArgs p) {
-  const int64_t n_out = p.M * p.N, width = SWIGLU ? 2 * (int64_t)p.N : p.N;
+  const int64_t n_out = p.M * p.N / E, width = SWIGLU ? 2 * (int64_t)p.N : p.N;
+  const int64_t part = p.M * width;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n_out; i += (int64_t)gridDim.x * 256) {
-    const int64_t m = i / p.N;
-    const int n = (int)(i - m * p.N);
+    const int64_t m = i * E / p.N;
+    const int n = (int)(i * E - m * p.N);
     const int32_t *s = p.partial + m * width + n;
-    int g = 0, u = 0;
-    for (int z = 0; z < p.ksplit; ++z) {
-      g += s[z * p.M * width];
-      if (SWIGLU) u += s[z * p.M * width + p.N];
+    int g[E], u[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) g[e] = u[e] = 0;
+#pragma unroll 4
+    for (int z = 0; z < p.ksplit; ++z, s += part) {
+      if constexpr (E == 4) {
+        const i32x4 v = *reinterpret_cast<const i32x4 *>(s);
+#pragma unroll
+        for (int e = 0; e < E; ++e) g[e] += v[e];
+        if constexpr (SWIGLU) {
+          const i32x4 w = *reinterpret_cast<const i32x4 *>(s + p.N);
+#pragma unroll
+          for (int e = 0; e < E; ++e) u[e] += w[e];
+        }
+      } else {
+        g[0] += s[0];
+        if constexpr (SWIGLU) u[0] += s[p.N];
+      }
     }
-    float v = i8_value(g, p.xs[m], p.ws[0][n]);
-    if (SWIGLU) v = silu_mul(v, i8_value(u, p.xs[m], p.ws[1][n]));
-    if (p.out_type == OutType::F32) static_cast<float *>(p.out)[i] = v;
-    else static_cast<uint16_t *>(p.out)[i] = (uint16_t)f32_to_bf16_bits(v);
+    const float sx = p.xs[m];
+    float v[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      v[e] = i8_value(g[e], sx, p.ws[0][n + e]);
+      if (SWIGLU) v[e] = silu_mul(v[e], i8_value(u[e], sx, p.ws[1][n + e]));
+    }
+    if (p.out_type == OutType::F32) {
+      float *o = static_cast<float *>(p.out) + i * E;
+      if constexpr (E == 4) *reinterpret_cast<f32x4 *>(o) = f32x4{v[0], v[1], v[2], v[3]};
+      else o[0] = v[0];
+    } else {
+      uint16_t *o = static_cast<uint16_t *>(p.out) + i * E;
+      if constexpr (E == 4)
+        *reinterpret_cast<u32x2 *>(o) = u32x2{i8_pack_bf16(v[0], v[1]), i8_pack_bf16(v[2], v[3])};
+      else o[0] = (uint16_t)f32_to_bf16_bits(v[0]);
+    }
   }
 }
 
@@ -386,8 +415,8 @@ hipError_t launch_tile(const I8GemmArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 template <bool SWIGLU>
-hipError_t launch_plan(const I8GemmArgs &a, const I8Plan &pl, hipStream_t s) {
-  switch (pl.fn * 8 + pl.fm) {
+hipError_t launch_plan(const I8GemmArgs &a, int fn, int fm, hipStream_t s) {
+  switch (fn * 8 + fm) {
     case 4 * 8 + 4: return launch_tile<4, 4, 2, 4, 1, SWIGLU>(a, s);
     case 4 * 8 + 3: return launch_tile<4, 3, 2, 4, 1, SWIGLU>(a, s);
     case 4 * 8 + 2: return launch_tile<4, 2, 2, 2, 1, SWIGLU>(a, s);
@@ -397,7 +426,7 @@ hipError_t launch_plan(const I8GemmArgs &a, const I8Plan &pl, hipStream_t s) {
     default: break;
   }
   if constexpr (!SWIGLU) {
-    if (pl.fn == 1 && pl.fm == 1) return launch_tile<1, 1, 4, 1, 2, false>(a, s);
+    if (fn == 1 && fm == 1) return launch_tile<1, 1, 4, 1, 2, false>(a, s);
   }
   return hipErrorInvalidValue;
 }
@@ -418,26 +447,46 @@ constexpr int kI8MaxParts = 16;
 }  // namespace
 
 // The least estimate: rounds of tiles over the CUs; for K parts, which only fill
-// up a single round, another launch and the sums' way through memory.
+// up a single round, another launch and the sums' way through memory; for two
+// launches, whole rounds of one tile and then the columns that are left, in a
+// tile of their own.  Two have to promise 5% and to begin with 256 weight rows a
+// tile: 1024 rows of 17408 x 5120 98.4 and 85.6 us (promised 21%), MLP of 512
+// tokens, 5120 / 17408, 180 and 172; 1024 rows of 5120 x 17408, with tiles of
+// 128 rows first, 100 and 127 (promised 4%).
 I8Plan i8_gemm_plan(bool swiglu, int64_t M, int64_t N, int64_t K) {
-  I8Plan best;
   const int64_t KB = (K + kI8Block - 1) / kI8Block, width = swiglu ? 2 * N : N;
+  auto rounds_us = [&](const I8Tile &t, int64_t tiles, int64_t ks) {
+    return (double)((tiles * ks + kI8CUs - 1) / kI8CUs) *
+           ((double)((KB + ks - 1) / ks) * t.block_us + t.ends_us);
+  };
+  auto columns = [&](const I8Tile &t) { return 64 * t.fn / (swiglu ? 2 : 1); };
+  auto tiles_of = [&](const I8Tile &t, int64_t n) {
+    return ((n + columns(t) - 1) / columns(t)) * ((M + 64 * t.fm - 1) / (64 * t.fm));
+  };
+  auto fits = [&](const I8Tile &t) { return !swiglu || t.fn % 2 == 0; };
+  I8Plan best;
   double best_us = 0.0;
-  for (const I8Tile &t : kI8Tiles) {
-    if (swiglu && t.fn % 2) continue;
-    const int64_t tn = 64 * t.fn / (swiglu ? 2 : 1), bm = 64 * t.fm;
-    const int64_t tiles = ((N + tn - 1) / tn) * ((M + bm - 1) / bm);
-    for (int64_t ks = 1; ks <= kI8MaxParts && ks <= KB && (ks == 1 || tiles * ks <= kI8CUs); ++ks) {
-      const int64_t rounds = (tiles * ks + kI8CUs - 1) / kI8CUs;
-      double us = (double)rounds * ((double)((KB + ks - 1) / ks) * t.block_us + t.ends_us);
-      if (ks > 1) us += 3.9 + (double)ks * M * width * 8.0 / 4.6e6;
-      if (best_us == 0.0 || us < best_us) {
-        best_us = us;
-        best.fn = t.fn;
-        best.fm = t.fm;
-        best.ksplit = (int)ks;
-      }
+  auto offer = [&](double us, const I8Plan &p) {
+    if (best_us == 0.0 || us < best_us) {
+      best_us = us;
+      best = p;
     }
+  };
+  for (const I8Tile &t : kI8Tiles) {
+    if (!fits(t)) continue;
+    const int64_t tiles = tiles_of(t, N);
+    for (int64_t ks = 1; ks <= kI8MaxParts && ks <= KB && (ks == 1 || tiles * ks <= kI8CUs); ++ks)
+      offer(rounds_us(t, tiles, ks) + (ks > 1 ? 3.9 + (double)ks * M * width * 8.0 / 4.6e6 : 0.0),
+            I8Plan{t.fn, t.fm, (int)ks, N, 0, 0, 0});
+    // whole rounds, of as many columns as fill them
+    const int64_t m_tiles = (M + 64 * t.fm - 1) / (64 * t.fm);
+    const int64_t main = kI8CUs * (tiles / kI8CUs) / m_tiles * columns(t);
+    if (t.fn < 4 || main < 1 || main >= N) continue;
+    const double main_us = rounds_us(t, tiles_of(t, main), 1) + 3.0;
+    for (const I8Tile &r : kI8Tiles)
+      if (fits(r))
+        offer((main_us + rounds_us(r, tiles_of(r, N - main), 1)) / 0.95,
+              I8Plan{t.fn, t.fm, 1, main, r.fn, r.fm, 0});
   }
   best.partial_ints = best.ksplit > 1 ? (size_t)best.ksplit * M * width : 0;
   return best;
@@ -456,13 +505,30 @@ size_t i8_gemm_max_partial(bool swiglu, int64_t M, int64_t N, int64_t K) {
 hipError_t launch_i8_gemm(bool swiglu, const I8GemmArgs &args, const I8Plan &pl, hipStream_t s) {
   I8GemmArgs a = args;
   a.ksplit = pl.ksplit;
+  a.ld = a.N;
   if (a.ksplit > 1 && !a.partial) return hipErrorInvalidValue;
-  const hipError_t e = swiglu ? launch_plan<true>(a, pl, s) : launch_plan<false>(a, pl, s);
-  if (e != hipSuccess || a.ksplit <= 1) return e;
-  const int64_t blocks = (a.M * a.N + 255) / 256;
-  const dim3 grid((unsigned)(blocks < 1 << 20 ? blocks : 1 << 20));
-  if (swiglu) launch_kernel(i8_reduce_kernel<true>, grid, dim3(256), 0, s, a);
-  else launch_kernel(i8_reduce_kernel<false>, grid, dim3(256), 0, s, a);
+  auto launch = [&](const I8GemmArgs &b, int fn, int fm) {
+    return swiglu ? launch_plan<true>(b, fn, fm, s) : launch_plan<false>(b, fn, fm, s);
+  };
+  a.N = (int)pl.main;
+  hipError_t e = launch(a, pl.fn, pl.fm);
+  if (e != hipSuccess) return e;
+  if (pl.main < a.ld) {   // the columns from `main` on
+    a.N = (int)(a.ld - pl.main);
+    for (int i = 0; i < (swiglu ? 2 : 1); ++i) {
+      a.w[i] += pl.main * a.K;
+      a.ws[i] += pl.main;
+    }
+    a.out = static_cast<char *>(a.out) + pl.main * (a.out_type == OutType::F32 ? 4 : 2);
+    return launch(a, pl.rest_fn, pl.rest_fm);
+  }
+  if (a.ksplit <= 1) return hipSuccess;
+  const bool quads = a.N % 4 == 0;
+  const int64_t blocks = (a.M * a.N / (quads ? 4 : 1) + 255) / 256;
+  const dim3 grid((unsigned)(blocks < 1 << 20 ? blocks : 1 << 20)), block(256);
+  if (swiglu) launch_kernel((i8_reduce_kernel<true, 4>), grid, block, 0, s, a);
+  else if (quads) launch_kernel((i8_reduce_kernel<false, 4>), grid, block, 0, s, a);
+  else launch_kernel((i8_reduce_kernel<false, 1>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 

@@ -405,14 +405,18 @@ struct I8GemmArgs {
   void *out;              // [M, N]; gate/up form: h, bf16
   OutType out_type;
   int ksplit;
+  int64_t ld;             // row pitch of out (set by the launcher)
   int32_t *partial;       // [ksplit][M][N, or 2 N: gate then up sums]
 };
 // Tile (64 fn weight rows, gate and up rows together in the gate/up form, by
 // 64 fm tokens) and K parts for a problem; a split needs partial_ints words of
-// workspace.
+// workspace.  Columns of y from `main` on go in a second launch, in tiles of
+// rest_fn, rest_fm (main = N: none do).
 struct I8Plan {
   int fn = 0, fm = 0;
   int ksplit = 1;
+  int64_t main = 0;
+  int rest_fn = 0, rest_fm = 0;
   size_t partial_ints = 0;
 };
 I8Plan i8_gemm_plan(bool swiglu, int64_t M, int64_t N, int64_t K);

@@ -140,7 +140,8 @@ def lib():
                                 _vp, _sz, _vp]),
             "int8_mlp_workspace_size": (_sz, [_i64, _i64, _i64, ctypes.c_int]),
             "int8_debug_plan": (ctypes.c_int, [ctypes.c_int, _i64, _i64, _i64,
-                                               ctypes.POINTER(_i32), ctypes.POINTER(_i32)]),
+                                               ctypes.POINTER(_i32), ctypes.POINTER(_i32),
+                                               ctypes.POINTER(_i64)]),
             "rms_norm_quantize": (_i32, [ctypes.POINTER(RmsNormArgs), _i64, _i64, _vp]),
             "moe_layer_decode": (_i32, [_vp, _i64, ctypes.POINTER(MoeLayerC), ctypes.c_int, _vp,
                                         _vp, _vp, _i32, _vp, _sz, _vp]),
@@ -837,12 +838,12 @@ def int8_mlp(x, gate, up, down, x_scales=None, out_dtype=torch.bfloat16, workspa
 
 
 def int8_debug_plan(M, N, K, gate_up=False):
-    """(rows of x of a tile, rows of W, parts of K) of an int8 product, (0, 0, 0)
-    where the form for a few rows takes it."""
-    columns, parts = _i32(), _i32()
+    """(rows of x of a tile, rows of W, parts of K, columns of y in these tiles)
+    of an int8 product; zeros where the form for a few rows takes it."""
+    columns, parts, main = _i32(), _i32(), _i64()
     rows = lib().int8_debug_plan(int(gate_up), M, N, K, ctypes.byref(columns),
-                                 ctypes.byref(parts))
-    return rows, columns.value, parts.value
+                                 ctypes.byref(parts), ctypes.byref(main))
+    return rows, columns.value, parts.value, main.value
 
 
 class RmsNorm(NamedTuple):

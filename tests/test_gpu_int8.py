@@ -442,7 +442,7 @@ def dev_linear(x, xs, w, ws):
 @pytest.mark.parametrize("M,N,K,rows,columns,parts", TILE_SHAPES)
 def test_linear_of_every_tile(M, N, K, rows, columns, parts):
     say("tile", M, N, K)
-    assert native.int8_debug_plan(M, N, K) == (rows, columns, parts)
+    assert native.int8_debug_plan(M, N, K) == (rows, columns, parts, N)
     (x, xs), (w, ws) = dev_codes(M, K, M), dev_codes(N, K, N)
     ref = dev_linear(x, xs, w, ws)
     for dt in (torch.float32, torch.bfloat16):
@@ -458,7 +458,7 @@ def test_mlp_of_every_tile(T, I, H, rows, columns, parts):
     code by at most one (or, as the row's maximum, all by one and the scale by
     2^-7)."""
     say("mlp tile", T, I, H)
-    assert native.int8_debug_plan(T, I, H, gate_up=True) == (rows, columns, parts)
+    assert native.int8_debug_plan(T, I, H, gate_up=True) == (rows, columns, parts, I)
     x, xs = dev_codes(T, H, T)
     gate, up, down = (dev_codes(n, k, s, 20.0 / k ** 0.5)
                       for s, (n, k) in ((1, (I, H)), (2, (I, H)), (3, (H, I))))
@@ -511,3 +511,54 @@ def test_large_weights_equal_their_parts(M):
     y = native.int8_linear(x, w, ws)
     assert torch.equal(y[:, -part:], native.int8_linear(x, w[-part:].contiguous(),
                                                         ws[-part:].contiguous()))
+
+
+# Products in two launches: (M, N, K, rows of x of a tile, rows of W, columns of
+# y of the first launch); N odd, even and whole, K with every last block.
+TWO_LAUNCHES = [(787, 19315, 928, 128, 256, 18688), (927, 16919, 288, 192, 256, 13056),
+                (1425, 10922, 800, 256, 256, 10752), (1024, 17408, 1280, 256, 256, 16384)]
+MLP_TWO_LAUNCHES = [(522, 13472, 288, 192, 256, 10880), (396, 16800, 1312, 256, 256, 16384)]
+
+
+@pytest.mark.parametrize("M,N,K,rows,columns,main", TWO_LAUNCHES)
+def test_linear_in_two_launches(M, N, K, rows, columns, main):
+    say("two launches", M, N, K)
+    assert native.int8_debug_plan(M, N, K) == (rows, columns, 1, main)
+    (x, xs), (w, ws) = dev_codes(M, K, M), dev_codes(N, K, N)
+    ref = dev_linear(x, xs, w, ws)
+    for dt in (torch.float32, torch.bfloat16):
+        buf = torch.full(((M + rows) * N,), 7.0, dtype=dt, device=DEV)
+        out = buf[:M * N].view(M, N)
+        native.int8_linear(x, w, ws, x_scales=xs, out=out)
+        assert torch.equal(out, ref.to(dt)) and torch.all(buf[M * N:] == 7.0)
+
+
+@pytest.mark.parametrize("T,I,H,rows,columns,main", MLP_TWO_LAUNCHES)
+def test_mlp_in_two_launches(T, I, H, rows, columns, main):
+    """The columns of h of either launch, seen through a down projection that
+    keeps them: y as with the gate and up rows of one launch alone."""
+    say("mlp two launches", T, I, H)
+    assert native.int8_debug_plan(T, I, H, gate_up=True) == (rows, columns, 1, main)
+    x, xs = dev_codes(T, H, T)
+    gate, up = (dev_codes(I, H, s, 20.0 / H ** 0.5) for s in (1, 2))
+    xs = xs * 100
+    g, u = dev_linear(x, xs, *gate).double(), dev_linear(x, xs, *up).double()
+    h64 = g / (1 + torch.exp(-g)) * u
+    lo, hi = ((h64 - d * h64.abs() * 2.0 ** -20).bfloat16() for d in (1, -1))
+    h = h64.bfloat16()
+    top = h.float().abs().amax(1, keepdim=True)
+    # identity rows of a down projection: y[t][j] = code of h[t][j] times the scale
+    at = torch.randperm(I, generator=_gen(3))[:H].sort()[0].to(DEV)
+    down = torch.zeros((H, I), dtype=torch.int8, device=DEV)
+    down[torch.arange(H, device=DEV), at] = 1
+    y = native.int8_mlp(x, gate, up, (down, torch.ones(H, device=DEV)), x_scales=xs,
+                        out_dtype=torch.float32)
+    # one code of the row's scale (and 2^-7 of it where the maximum may move), fp32 steps
+    step = top / 127 * (0.5 + 2.0 ** -6) + h[:, at].float().abs() * 2.0 ** -7
+    assert ((y - h[:, at].float()).abs() <= step).all()
+    sure = (lo == hi).all(1)                  # rows whose h expf does not decide: exact
+    q, s = quantize_ref(h.float().cpu().numpy())
+    want = torch.from_numpy((q.astype(F32) * s[:, None]).astype(F32)).to(DEV)[:, at]
+    assert torch.equal(y[sure], want[sure])
+
+

@@ -223,21 +223,25 @@ def test_binding_refusals():
 def test_the_shapes_of_the_gpu_tests_take_the_tiles_they_name():
     """The plan is host code: a changed rule shows here, before the GPU tests of
     the tiles lose what they are for."""
-    from test_gpu_int8 import MLP_TILE_SHAPES, TILE_SHAPES
+    from test_gpu_int8 import MLP_TILE_SHAPES, MLP_TWO_LAUNCHES, TILE_SHAPES, TWO_LAUNCHES
+    for shapes, gate_up in ((TWO_LAUNCHES, False), (MLP_TWO_LAUNCHES, True)):
+        for M, N, K, rows, columns, main in shapes:
+            assert main < N
+            assert native.int8_debug_plan(M, N, K, gate_up) == (rows, columns, 1, main)
     for M, N, K, *plan in TILE_SHAPES:
-        assert native.int8_debug_plan(M, N, K) == tuple(plan), (M, N, K)
+        assert native.int8_debug_plan(M, N, K) == (*plan, N), (M, N, K)
     for T, I, H, *plan in MLP_TILE_SHAPES:
-        assert native.int8_debug_plan(T, I, H, gate_up=True) == tuple(plan), (T, I, H)
+        assert native.int8_debug_plan(T, I, H, gate_up=True) == (*plan, I), (T, I, H)
     tiles = {(64, 64), (64, 128), (64, 256), (128, 128), (128, 256), (192, 256), (256, 256)}
     kinds = lambda shapes: {(s[3], s[4], s[5] > 1) for s in shapes}
     assert kinds(TILE_SHAPES) == {(*t, split) for t in tiles for split in (False, True)}
     assert kinds(MLP_TILE_SHAPES) == {(*t, split) for t in tiles - {(64, 64)}
                                       for split in (False, True)}
-    assert native.int8_debug_plan(16, 4096, 4096) == (0, 0, 0)
-    assert native.int8_debug_plan(32, 4096, 4096, gate_up=True) == (0, 0, 0)
+    assert native.int8_debug_plan(16, 4096, 4096) == (0, 0, 0, 0)
+    assert native.int8_debug_plan(32, 4096, 4096, gate_up=True) == (0, 0, 0, 0)
     for bad in ((0, 64, 64), (64, 0, 64), (64, 64, 0), (-1, 64, 64)):
-        assert native.int8_debug_plan(*bad) == (0, 0, 0)
-    assert native.lib().int8_debug_plan(0, 64, 64, 64, None, None) > 0
+        assert native.int8_debug_plan(*bad) == (0, 0, 0, 0)
+    assert native.lib().int8_debug_plan(0, 64, 64, 64, None, None, None) > 0
 
 
 @pytest.mark.parametrize("N,K", MONOTONE)
