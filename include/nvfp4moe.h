@@ -645,8 +645,8 @@ nvfp4_status int8_quantize(const void *x, nvfp4_dtype x_dtype, int64_t rows, int
  * int8_quantize.  x_scales set: x holds int8 codes [M, K] with x_scales [M]
  * (quantised once for several projections, or by rms_norm_quantize).
  * Requires K % 32 == 0, K <= 131040 (the sum of codes -128 stays below 2^31),
- * M, N <= 2^24, M * N <= 2^36; y must not overlap x, x_scales or the
- * workspace.
+ * M, N <= 2^24, M * N <= 2^36; neither y nor the workspace may overlap an
+ * input or each other.
  * workspace: int8_linear_workspace_size bytes (device, 16-byte aligned;
  * enough for every smaller M too), scratch only; quantised: x_scales is set.
  */
@@ -664,7 +664,7 @@ size_t int8_linear_workspace_size(int64_t M, int64_t N, int64_t K, int quantised
  * quantised per token as int8_quantize does.  x as in int8_linear: bf16 with
  * x_scales NULL, or codes and their scales.  y [T, H] bf16 or f32.  Requires
  * H % 32 == 0, I % 32 == 0, H, I <= 131040, T <= 2^24, T * H and T * I <= 2^36;
- * y must not overlap x, x_scales or the workspace.
+ * neither y nor the workspace may overlap an input or each other.
  * workspace: int8_mlp_workspace_size bytes (device, 16-byte aligned; enough
  * for every smaller T too), scratch only.
  */

@@ -1760,15 +1760,30 @@ static nvfp4_status check_int8_batch(int64_t M, int64_t width, const char *name)
                 (long long)width);
   return NVFP4_OK;
 }
-// y may lie over nothing that the call reads or keeps.
-static nvfp4_status check_int8_output(const void *y, size_t ny, const void *x, size_t nx,
-                                      const float *xs, size_t ns, const void *ws, size_t nw) {
-  if (ranges_overlap(y, ny, x, nx)) return fail(NVFP4_ERR_INVALID_ARGUMENT, "y overlaps x");
-  if (xs && ranges_overlap(y, ny, xs, ns))
-    return fail(NVFP4_ERR_INVALID_ARGUMENT, "y overlaps x_scales");
-  if (nw > 0 && ranges_overlap(y, ny, ws, nw))
+// Neither y nor the workspace may lie over anything that the call reads, nor
+// over each other.
+struct Span {
+  const void *at;
+  size_t bytes;
+  const char *name;
+};
+static nvfp4_status check_int8_memory(const Span &y, const Span &workspace, const Span *in, int n) {
+  for (int i = 0; i < n; ++i) {
+    if (in[i].bytes == 0 || !in[i].at) continue;
+    if (ranges_overlap(y.at, y.bytes, in[i].at, in[i].bytes))
+      return fail(NVFP4_ERR_INVALID_ARGUMENT, "y overlaps %s", in[i].name);
+    if (workspace.bytes > 0 && ranges_overlap(workspace.at, workspace.bytes, in[i].at, in[i].bytes))
+      return fail(NVFP4_ERR_INVALID_ARGUMENT, "the workspace overlaps %s", in[i].name);
+  }
+  if (workspace.bytes > 0 && ranges_overlap(y.at, y.bytes, workspace.at, workspace.bytes))
     return fail(NVFP4_ERR_INVALID_ARGUMENT, "y overlaps the workspace");
   return NVFP4_OK;
+}
+static Span codes_of(const int8_matrix *w, const char *name) {
+  return Span{w->codes, (size_t)(w->rows * w->cols), name};
+}
+static Span scales_of(const int8_matrix *w, const char *name) {
+  return Span{w->scales, (size_t)w->rows * 4, name};
 }
 
 // One product: x codes with their scales, or bf16 with xs null where the form
@@ -1832,9 +1847,12 @@ nvfp4_status int8_linear(const void *x, const float *x_scales, int64_t M, const 
                                               int8_partial(false, M, N, K, false));
   TRY(check_workspace(workspace, workspace_bytes, c.used));
   if (M == 0) return NVFP4_OK;
-  TRY(check_int8_output(y, (size_t)(M * N) * dtype_size(y_dtype), x,
-                        (size_t)(M * K) * (x_scales ? 1 : 2), x_scales, (size_t)M * 4, workspace,
-                        c.used));
+  const Span in[] = {{x, (size_t)(M * K) * (x_scales ? 1 : 2), "x"},
+                     {x_scales, (size_t)M * 4, "x_scales"},
+                     codes_of(w, "w->codes"),
+                     scales_of(w, "w->scales")};
+  TRY(check_int8_memory(Span{y, (size_t)(M * N) * dtype_size(y_dtype), "y"},
+                        Span{workspace, c.used, "workspace"}, in, 4));
   const void *xq = x;
   const float *xs = x_scales;
   if (ws.xq) {
@@ -1881,9 +1899,16 @@ nvfp4_status int8_mlp(const void *x, const float *x_scales, int64_t T, const int
                                        int8_mlp_partial(T, H, I, false));
   TRY(check_workspace(workspace, workspace_bytes, c.used));
   if (T == 0) return NVFP4_OK;
-  TRY(check_int8_output(y, (size_t)(T * H) * dtype_size(y_dtype), x,
-                        (size_t)(T * H) * (x_scales ? 1 : 2), x_scales, (size_t)T * 4, workspace,
-                        c.used));
+  const Span in[] = {{x, (size_t)(T * H) * (x_scales ? 1 : 2), "x"},
+                     {x_scales, (size_t)T * 4, "x_scales"},
+                     codes_of(w_gate, "w_gate->codes"),
+                     scales_of(w_gate, "w_gate->scales"),
+                     codes_of(w_up, "w_up->codes"),
+                     scales_of(w_up, "w_up->scales"),
+                     codes_of(w_down, "w_down->codes"),
+                     scales_of(w_down, "w_down->scales")};
+  TRY(check_int8_memory(Span{y, (size_t)(T * H) * dtype_size(y_dtype), "y"},
+                        Span{workspace, c.used, "workspace"}, in, 8));
   const void *xq = x, *hq = ws.h;
   const float *xs = x_scales, *hs = nullptr;
   if (ws.xq) {

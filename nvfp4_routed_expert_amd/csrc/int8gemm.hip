@@ -475,6 +475,7 @@ I8Plan i8_gemm_plan(bool swiglu, int64_t M, int64_t N, int64_t K) {
   for (const I8Tile &t : kI8Tiles) {
     if (!fits(t)) continue;
     const int64_t tiles = tiles_of(t, N);
+    if (tiles >= (int64_t)1 << 23) continue;   // (less than 2^32 work-items; 256 x 256 tiles are fewer)
     for (int64_t ks = 1; ks <= kI8MaxParts && ks <= KB && (ks == 1 || tiles * ks <= kI8CUs); ++ks)
       offer(rounds_us(t, tiles, ks) + (ks > 1 ? 3.9 + (double)ks * M * width * 8.0 / 4.6e6 : 0.0),
             I8Plan{t.fn, t.fm, (int)ks, N, 0, 0, 0});

@@ -880,11 +880,12 @@ def rms_norm_quantize(x, weight, residual=None, eps=1e-6, codes=None, y_dtype=No
     if out is not None:
         y, q, s, total = out
         _device_of(x, y=y, codes=q, scales=s)
+        if ((y is not None and y_dtype is None) or (not fmt and (q is not None or s is not None))
+                or (total is not None and residual is None)):
+            raise ValueError("out holds tensors for what is not asked for")
     r_ptr = t_ptr = None
     r_type = r_ld = t_ld = 0
-    if residual is None:
-        total = None
-    else:
+    if residual is not None:
         _expect("residual", residual, (T, H), residual.dtype)
         r_ptr, r_type = residual.data_ptr(), _dt(residual.dtype)
         r_ld = _rows_stride("residual", residual, dev)
@@ -897,18 +898,14 @@ def rms_norm_quantize(x, weight, residual=None, eps=1e-6, codes=None, y_dtype=No
         t_ptr = total.data_ptr()
     y_ptr = q_ptr = s_ptr = None
     y_type = 0
-    if y_dtype is None:
-        y = None
-    else:
+    if y_dtype is not None:
         y_type = _dt(y_dtype)
         if y is None:
             y = torch.empty((T, H), dtype=y_dtype, device=dev)
         else:
             _expect("y", y, (T, H), y_dtype)
         y_ptr = y.data_ptr()
-    if not fmt:
-        q = s = None
-    else:
+    if fmt:
         shape = (T, _fp8_blocks(H)) if fmt == 1 else (T,)
         if q is None:
             q = torch.empty((T, H), dtype=code_t, device=dev)

@@ -72,6 +72,10 @@ def test_linear_validation():
         assert lin(y=y, xs=E, dt=1) == 1 and "overlaps x" in _last()
     assert lin(y=F, xs=F + 16) == 1 and "x_scales" in _last()
     assert lin(y=E + 64) == 1 and "workspace" in _last()
+    assert lin(y=A + 64) == 1 and "w->codes" in _last()
+    assert lin(y=B + 64) == 1 and "w->scales" in _last()
+    for at, name in ((C, "x"), (A, "w->codes"), (B, "w->scales")):
+        assert lin(wsp=at) == 1 and "workspace overlaps " + name in _last()
     assert lin(x=None, y=None, M=0, wsp=None, wsb=0) == 0
     assert lin(x=None, y=None, M=0, wsp=None, wsb=0, w=mat(64, 80)) == 2
 
@@ -94,6 +98,10 @@ def test_mlp_validation():
     assert mlp(x=C + 4) == 3 and mlp(y=D + 4) == 3 and mlp(xs=F + 4) == 3
     assert mlp(wsb=need - 256) == 4
     assert mlp(y=C + 16) == 1 and mlp(xs=D, y=D) == 1 and mlp(y=E) == 1
+    for name in ("w_gate", "w_up", "w_down"):
+        m = mat(96, 64, F, F + (1 << 30)) if name == "w_down" else mat(64, 96, F, F + (1 << 30))
+        for y in (F + 16, F + (1 << 30)):
+            assert mlp(**{name[2:]: m}, y=y) == 1 and name in _last()
     assert mlp(x=None, y=None, T=0, wsb=0) == 0
 
 
@@ -218,6 +226,18 @@ def test_binding_refusals():
         native.rms_norm_quantize(x, g, codes="int8")
     with pytest.raises(ValueError, match=r"\[T, H\]"):
         native.rms_norm_quantize(x[0], g, codes="int8")
+
+
+def test_norm_refuses_outputs_nobody_asked_for():
+    x, g = torch.zeros((4, 96), dtype=torch.bfloat16), torch.ones(96)
+    class Cuda(torch.Tensor):          # a host tensor that passes for one on a device
+        is_cuda = True
+    x, g = x.as_subclass(Cuda), g.as_subclass(Cuda)
+    o = lambda **k: native.RmsNorm(*(k.get(n) for n in ("y", "codes", "scales", "residual")))
+    for kw, out in (({"codes": "int8"}, o(y=x)), ({"codes": "int8"}, o(residual=x)),
+                    ({"y_dtype": torch.float32}, o(codes=x)), ({"y_dtype": torch.float32}, o(scales=x))):
+        with pytest.raises(ValueError, match="not asked for"):
+            native.rms_norm_quantize(x, g, out=out, **kw)
 
 
 def test_the_shapes_of_the_gpu_tests_take_the_tiles_they_name():
