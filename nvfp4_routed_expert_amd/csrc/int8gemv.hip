@@ -47,8 +47,13 @@ __global__ __launch_bounds__(64 * NW) void i8_gemv_kernel(const I8GemvArgs p) {
   const int K = p.K, N = p.N, M = p.M;
   const int KB = (K + kI8Line - 1) / kI8Line;
   const int r0 = blockIdx.x * 16;                  // first output column
-  const int mine = (KB - wave + NW - 1) / NW;      // this wave's blocks: wave, wave + NW, ...
+  const int mine = (KB - wave + NW - 1) / NW;      // this wave's blocks: every NW-th
   const int xp = KB * kI8Line + 16;                // QX: pitch of a row of codes
+  const int rot = (int)(blockIdx.x % KB);
+  auto block_of = [&](int i) {   // (each workgroup begins at another block)
+    const int b = wave + NW * i + rot;
+    return b < KB ? b : b - KB;
+  };
 
   // ---- the ring: a load fills 8 rows of 128 bytes, lane l position l % 8 of
   // row l / 8, which holds granule (l % 8) ^ (l / 8)
@@ -63,7 +68,7 @@ __global__ __launch_bounds__(64 * NW) void i8_gemv_kernel(const I8GemvArgs p) {
   const int off_ = (lane >> 3) * K + gran * 16, last = K - gran * 16;
   uint8_t *const ring = lds + wave * (D * SLOT);
   auto load = [&](int i, int slot) {
-    const int at = __builtin_amdgcn_readfirstlane((wave + NW * i) * kI8Line);
+    const int at = __builtin_amdgcn_readfirstlane(i < mine ? block_of(i) * kI8Line : K);
     const int off = off_ | (at < last ? 0 : kOutside);   // (granules past K: zero codes)
 #pragma unroll
     for (int h = 0; h < LS; ++h)
@@ -145,7 +150,7 @@ __global__ __launch_bounds__(64 * NW) void i8_gemv_kernel(const I8GemvArgs p) {
   int slot = 0;
 #pragma unroll 1
   for (int i = 0; i < mine; ++i) {
-    const int b = __builtin_amdgcn_readfirstlane(wave + NW * i);
+    const int b = __builtin_amdgcn_readfirstlane(block_of(i));
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"((D - 1) * LS) : "memory");
     const uint8_t *st = ring + slot * SLOT;
     i32x4 wq[NT][2], xq[MT][2];
