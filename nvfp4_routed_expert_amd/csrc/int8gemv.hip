@@ -28,12 +28,12 @@ __host__ __device__ constexpr int64_t i8_x_bytes(int64_t M, int64_t K) {
   return M * ((K + kI8Line - 1) / kI8Line * kI8Line + 16);
 }
 
-// STREAM: the weights are loaded as used once.  XT: groups of 8 rows of x.
-// XCAP: bytes for x's codes (QX).
-template <int XT, bool SWIGLU, bool QX, int NW, int D, int XCAP, bool STREAM>
+// STREAM: the weights are loaded as used once.  XT: groups of 8 rows of x.  NR:
+// tiles of 16 rows of each matrix.  XCAP: bytes for x's codes (QX).
+template <int XT, int NR, bool SWIGLU, bool QX, int NW, int D, int XCAP, bool STREAM>
 __global__ __launch_bounds__(64 * NW) void i8_gemv_kernel(const I8GemvArgs p) {
 #pragma clang fp contract(off)
-  constexpr int NT = SWIGLU ? 2 : 1, MT = (XT + 1) / 2;   // tiles of 16 rows of w, x
+  constexpr int NT = SWIGLU ? 2 * NR : NR, MT = (XT + 1) / 2;   // tiles of 16 rows of w, x
   constexpr int SLOT = 2048 * NT + (QX ? 0 : 1024 * XT);  // a block: 1 KB for 8 rows
   constexpr int LS = SLOT / 1024;                  // loads of a block
   constexpr int RED = NW * NT * 16 * (MT * 16 + 1) * 4;
@@ -46,7 +46,7 @@ __global__ __launch_bounds__(64 * NW) void i8_gemv_kernel(const I8GemvArgs p) {
   const int lr = lane & 15, lg = lane >> 4;
   const int K = p.K, N = p.N, M = p.M;
   const int KB = (K + kI8Line - 1) / kI8Line;
-  const int r0 = blockIdx.x * 16;                  // first output column
+  const int r0 = blockIdx.x * (16 * NR);           // first output column
   const int mine = (KB - wave + NW - 1) / NW;      // this wave's blocks: every NW-th
   const int xp = KB * kI8Line + 16;                // QX: pitch of a row of codes
   const int rot = (int)(blockIdx.x % KB);
@@ -59,7 +59,7 @@ __global__ __launch_bounds__(64 * NW) void i8_gemv_kernel(const I8GemvArgs p) {
   // row l / 8, which holds granule (l % 8) ^ (l / 8)
   __amdgpu_buffer_rsrc_t wbuf[8], xbuf[8];
 #pragma unroll
-  for (int h = 0; h < 2 * NT; ++h) wbuf[h] = f8_buffer(p.w[h / 2], r0 + h % 2 * 8, N, K);
+  for (int h = 0; h < 2 * NT; ++h) wbuf[h] = f8_buffer(p.w[h / (2 * NR)], r0 + h % (2 * NR) * 8, N, K);
   if constexpr (!QX) {
 #pragma unroll
     for (int h = 0; h < XT; ++h) xbuf[h] = f8_buffer(p.x, h * 8, M, K);
@@ -196,8 +196,8 @@ __global__ __launch_bounds__(64 * NW) void i8_gemv_kernel(const I8GemvArgs p) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) red[wave][t * 16 + 4 * lg + e][j * 16 + lr] = acc[t][j][e];
   __syncthreads();
-  for (int i = tid; i < 16 * M; i += 64 * NW) {
-    const int c = i % 16, m = i / 16;   // consecutive threads: consecutive columns
+  for (int i = tid; i < 16 * NR * M; i += 64 * NW) {
+    const int c = i % (16 * NR), m = i / (16 * NR);   // consecutive threads: consecutive columns
     const int n = r0 + c;
     if (n >= N) continue;
     const float sx = QX ? i8_scale(__uint_as_float(top[m])) : p.xs[m];
@@ -208,7 +208,7 @@ __global__ __launch_bounds__(64 * NW) void i8_gemv_kernel(const I8GemvArgs p) {
     if constexpr (SWIGLU) {
       int u = 0;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) u += red[w][16 + c][m];
+      for (int w = 0; w < NW; ++w) u += red[w][16 * NR + c][m];
       v = v / (1.0f + expf(-v)) * i8_value(u, sx, p.ws[1][n]);
     }
     if (p.out_type == OutType::F32) static_cast<float *>(p.out)[(int64_t)m * N + n] = v;
@@ -216,13 +216,13 @@ __global__ __launch_bounds__(64 * NW) void i8_gemv_kernel(const I8GemvArgs p) {
   }
 }
 
-template <int XT, bool SWIGLU, bool QX, int NW, int D, int XCAP = 0>
+template <int XT, int NR, bool SWIGLU, bool QX, int NW, int D, int XCAP = 0>
 hipError_t launch_gemv(const I8GemvArgs &a, hipStream_t s) {
-  const dim3 grid((unsigned)((a.N + 15) / 16)), block(64 * NW);
+  const dim3 grid((unsigned)((a.N + 16 * NR - 1) / (16 * NR))), block(64 * NW);
   if ((int64_t)a.N * a.K * (SWIGLU ? 2 : 1) > 128000000)
-    launch_kernel((i8_gemv_kernel<XT, SWIGLU, QX, NW, D, XCAP, true>), grid, block, 0, s, a);
+    launch_kernel((i8_gemv_kernel<XT, NR, SWIGLU, QX, NW, D, XCAP, true>), grid, block, 0, s, a);
   else
-    launch_kernel((i8_gemv_kernel<XT, SWIGLU, QX, NW, D, XCAP, false>), grid, block, 0, s, a);
+    launch_kernel((i8_gemv_kernel<XT, NR, SWIGLU, QX, NW, D, XCAP, false>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 
@@ -244,24 +244,35 @@ hipError_t launch_i8_gemv(bool swiglu, const I8GemvArgs &a, hipStream_t s) {
   if (!a.xs) {
     const int64_t bytes = i8_x_bytes(a.M, a.K);
     if (a.M > 16 || bytes > kI8XBytes)
-      return swiglu ? launch_gemv<4, true, true, 8, 2, kI8XBytesFew>(a, s)
-                    : launch_gemv<4, false, true, 8, 2, kI8XBytesFew>(a, s);
+      return swiglu ? launch_gemv<4, 1, true, true, 8, 2, kI8XBytesFew>(a, s)
+                    : launch_gemv<4, 1, false, true, 8, 2, kI8XBytesFew>(a, s);
     const bool small = bytes <= 10 * 1024;
     if (swiglu)
-      return small ? launch_gemv<2, true, true, 4, 2, 10 * 1024>(a, s)
-                   : launch_gemv<2, true, true, 4, 2, kI8XBytes>(a, s);
-    return small ? launch_gemv<2, false, true, 4, 2, 10 * 1024>(a, s)
-                 : launch_gemv<2, false, true, 8, 2, kI8XBytes>(a, s);
+      return small ? launch_gemv<2, 1, true, true, 4, 2, 10 * 1024>(a, s)
+                   : launch_gemv<2, 1, true, true, 4, 2, kI8XBytes>(a, s);
+    return small ? launch_gemv<2, 1, false, true, 4, 2, 10 * 1024>(a, s)
+                 : launch_gemv<2, 1, false, true, 8, 2, kI8XBytes>(a, s);
   }
-  switch ((a.M + 7) / 8) {
-    case 1:
-      return swiglu ? launch_gemv<1, true, false, 4, 2>(a, s) : launch_gemv<1, false, false, 4, 2>(a, s);
-    case 2:
-      return swiglu ? launch_gemv<2, true, false, 4, 2>(a, s) : launch_gemv<2, false, false, 4, 2>(a, s);
-    case 3:
-      return swiglu ? launch_gemv<3, true, false, 4, 2>(a, s) : launch_gemv<3, false, false, 4, 2>(a, s);
-    default:
-      return swiglu ? launch_gemv<4, true, false, 4, 2>(a, s) : launch_gemv<4, false, false, 4, 2>(a, s);
+  if (swiglu) switch ((a.M + 7) / 8) {
+      case 1: return launch_gemv<1, 1, true, false, 4, 2>(a, s);
+      case 2: return launch_gemv<2, 1, true, false, 4, 2>(a, s);
+      case 3: return launch_gemv<3, 1, true, false, 4, 2>(a, s);
+      default: return launch_gemv<4, 1, true, false, 4, 2>(a, s);
+    }
+  // 16 weight rows a workgroup leave a quarter to a half of the CUs with two of
+  // them and the others with one; 32 rows also halve what is read of x.  16 rows
+  // of x, 5120 x 17408: 22.2 us with 16 weight rows, 18.4 with 32; 8192 x 8192
+  // (two workgroups a CU) 11.9 and 12.4.
+  const bool two = a.M > 4 && a.N > 16 * 256 && a.N <= 24 * 256;
+  switch ((a.M + 7) / 8 + (two ? 4 : 0)) {
+    case 1: return launch_gemv<1, 1, false, false, 4, 2>(a, s);
+    case 2: return launch_gemv<2, 1, false, false, 4, 2>(a, s);
+    case 3: return launch_gemv<3, 1, false, false, 4, 2>(a, s);
+    case 4: return launch_gemv<4, 1, false, false, 4, 2>(a, s);
+    case 5: return launch_gemv<1, 2, false, false, 4, 2>(a, s);
+    case 6: return launch_gemv<2, 2, false, false, 4, 2>(a, s);
+    case 7: return launch_gemv<3, 2, false, false, 4, 2>(a, s);
+    default: return launch_gemv<4, 2, false, false, 4, 2>(a, s);
   }
 }
 

@@ -562,3 +562,9 @@ def test_mlp_in_two_launches(T, I, H, rows, columns, main):
     assert torch.equal(y[sure], want[sure])
 
 
+@pytest.mark.parametrize("M", [4, 5, 8, 9, 16, 17, 24, 25, 32])
+@pytest.mark.parametrize("N", [4096, 4112, 4128, 5000, 6144, 6145])
+def test_linear_of_two_row_tiles(M, N):
+    """Codes given: 16 or 32 weight rows a workgroup, each number of groups of 8
+    rows of x, odd last tiles."""
+    test_linear(M, N, 416)
