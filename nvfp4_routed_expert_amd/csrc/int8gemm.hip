@@ -5,6 +5,34 @@
 //
 // The sum is exact in 32-bit integers (K <= 131040, codes -128 .. 127), so no
 // order of it changes the result, and K may be split over workgroups freely.
+//
+// Large tiles: four waves, one per SIMD, each with up to 4 x 4 tiles of 32 x 32
+// (v_mfma_i32_32x32x32_i8, 16 sums a lane and tile in the accumulation
+// registers).  A wave tile of 128 x 128 reads 64 bytes of LDS per 2048
+// multiply-adds; eight waves of 128 x 64, two per SIMD, would read half as much
+// again, and the LDS would then bound them (128 bytes a cycle for reads and
+// direct loads together).
+// The tokens of a block of 128 columns are held in registers while the weight
+// tiles pass by in groups; a group's rows are free in LDS as soon as they are
+// read, one barrier a group, so that two blocks of LDS give loads nearly two
+// blocks of time.  Weights are the A operand: a lane's sums are columns of one
+// token.
+//
+// Measured: M = 2048, N = 17408, K = 5120 164 to 178 us, 2.0 to 2.2 PFLOP/s (a
+// library product of the same size, without the scales, 181 to 204); 8192 x 8192
+// x 8192 426 to 434 us, 2.5 PFLOP/s (441).  What bounds it is power: the matrix
+// unit is busy for 61% of the cycles, at 1.74 GHz instead of 2.4; with operands
+// of zeros the same product takes 148 us.  Of a tile's 60 us, 3 are the first
+// loads, 47 the loop (0.97 to 1.2 us a block, 0.71 on zeros) and 4 to 7 the
+// stores.
+// Slower, or no faster: a workgroup that stays and loads its next tile while it
+// stores (184 us, with the same stores 184 against 178: loads wait behind
+// stores); outputs through LDS (184) or in pieces of 32 bytes (178, but 8192^3
+// 468 against 434); two barriers a block instead of four (179); eight token
+// tiles side by side on an XCD instead of four (8192^3 434 against 422); small
+// tiles with a wave per quarter of K, or with whole blocks and no barriers (30.4
+// us for 128 rows, 17408 x 5120, against 33 and 36); blocks of K in another
+// order on each workgroup (no difference).
 #include "int8.h"
 #include "kernels.h"
 
@@ -21,7 +49,8 @@ constexpr int kI8Block = 128;          // columns of a step of the ring: a cache
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
 // A workgroup of four waves, one per SIMD, two by two: FN tiles of 32 weight
-// rows by FM tiles of 32 tokens each.
+// rows by FM tiles of 32 tokens each.  R: blocks in LDS, G: groups of weight
+// tiles of a block.
 template <int FN, int FM, int R, int G, int PER_CU, bool SWIGLU>
 __global__ __launch_bounds__(256, PER_CU) void i8_gemm_kernel(const I8GemmArgs p) {
   static_assert(FN % G == 0 && (!SWIGLU || FN % 2 == 0), "groups of whole tiles");
@@ -357,7 +386,8 @@ __global__ __launch_bounds__(256, PER_CU) void i8_gemm_kernel(const I8GemmArgs p
 }
 
 // Adds the K parts and applies the epilogue: E outputs of a row per thread (4,
-// or 1 where rows are not whole quads).
+// or 1 where rows are not whole quads).  Bounded by memory: 3 parts of 512 x 5120
+// 9.5 us, 3.8 TB/s (an output a thread 11.4).
 template <bool SWIGLU, int E>
 __global__ __launch_bounds__(256) void i8_reduce_kernel(const I8GemmArgs p) {
   const int64_t n_out = p.M * p.N / E, width = SWIGLU ? 2 * (int64_t)p.N : p.N;

@@ -13,6 +13,15 @@
 // QX: x is bf16 and each workgroup quantises it into LDS while its first
 // weights are on their way; that saves a launch.  Otherwise x's codes come
 // through the ring with the weights.
+//
+// Every workgroup begins at another block of K: with all at the same one, rows
+// whose pitch is a multiple of 4096 bytes meet in few memory channels (16 rows,
+// 11008 x 4096: 11.4 us, and 9.8 with it; 8192 x 8192: 13.8 and 12.2).
+//
+// Measured: N = 17408, K = 5120, one row 15.5 us (5.8 TB/s), 16 rows from codes
+// 16.9; N = 5120, K = 17408, 8 rows 14.9; a gated MLP of 4 tokens, 5120 / 17408,
+// 53.8 us (5.0 TB/s).  4 waves with 2 blocks each: 3 blocks 17.4, 6 blocks 18.9,
+// 8 waves with 4 blocks 23.0 where 2 take 17.2 (one row from codes, 17408 x 5120).
 #include "int8.h"
 #include "kernels.h"
 
@@ -20,8 +29,8 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kI8Line = 128;             // columns of a block
-constexpr int kI8XBytes = 20 * 1024;     // x's codes in LDS of the QX form, at most,
-constexpr int kI8XBytesFew = 52 * 1024;  // and with at most a workgroup per CU
+// x's codes in LDS of the QX form: little, some, and with a workgroup per CU
+constexpr int kI8XBytesFew = 10 * 1024, kI8XBytes = 20 * 1024, kI8XBytesMost = 32 * 1024;
 
 // bytes of LDS for M rows of codes: 16 bytes apart from a multiple of the banks
 __host__ __device__ constexpr int64_t i8_x_bytes(int64_t M, int64_t K) {
@@ -228,13 +237,28 @@ hipError_t launch_gemv(const I8GemvArgs &a, hipStream_t s) {
 
 }  // namespace
 
+// Up to 16 rows every size (8192 x 8192, 16 rows: 11.9 us, as a batch 15.2; 11008
+// x 4096 9.6 and 9.7).  Up to 32 rows where x, which every workgroup reads, stays
+// small beside the weights and tiles of 64 rows would not fill the CUs: 32 rows,
+// 4096 x 14336 12.0 us and 14.2, 6144 x 6144 10.4 and 12.3, but 5120 x 17408 29.6
+// and 20.7, 11008 x 4096 10.8 and 9.9.  Gate and up: 24 tokens, 5120 / 17408, the
+// MLP 62.7 us and 70.1 as a batch.
 bool i8_gemv_supported(bool swiglu, int64_t M, int64_t N, int64_t K) {
   return M >= 1 && (M <= 16 || (M <= 32 && (swiglu || (N <= 8192 && N * K < 70000000))));
 }
+// x quantised inside, by every workgroup, where that costs less than a launch:
+// with a workgroup per CU at most (16 rows, 2048 x 2048: 8.1 us, with a launch
+// 10.2); where all of them read little (one row, 17408 x 5120: 15.6 and 18.7; 3
+// rows 20.1 and 18.5; gate and up, MLP of 1 and 3 tokens, 5120 / 17408: 50.2 and
+// 53.3, 62.0 and 53.6); with up to two a CU and no up matrix (2 rows, 8192 x 8192:
+// 13.6 and 16.1; 3 rows, 11008 x 4096, 12.8 and 12.0).
 bool i8_gemv_quantises(bool swiglu, int64_t M, int64_t N, int64_t K) {
   if (!i8_gemv_supported(swiglu, M, N, K)) return false;
-  const int64_t bytes = i8_x_bytes(M, K);
-  return (M <= 16 && bytes <= kI8XBytes) || (bytes <= kI8XBytesFew && N <= 16 * 256);
+  const int64_t bytes = i8_x_bytes(M, K), groups = (N + 15) / 16;
+  if (groups <= 256) return bytes <= kI8XBytesMost;
+  if (M > 16) return false;
+  return bytes <= kI8XBytesFew ? groups * bytes <= 8500000
+                               : !swiglu && groups <= 512 && bytes <= kI8XBytes;
 }
 
 hipError_t launch_i8_gemv(bool swiglu, const I8GemvArgs &a, hipStream_t s) {
@@ -244,14 +268,13 @@ hipError_t launch_i8_gemv(bool swiglu, const I8GemvArgs &a, hipStream_t s) {
   if (!a.xs) {
     const int64_t bytes = i8_x_bytes(a.M, a.K);
     if (a.M > 16 || bytes > kI8XBytes)
-      return swiglu ? launch_gemv<4, 1, true, true, 8, 2, kI8XBytesFew>(a, s)
-                    : launch_gemv<4, 1, false, true, 8, 2, kI8XBytesFew>(a, s);
-    const bool small = bytes <= 10 * 1024;
-    if (swiglu)
-      return small ? launch_gemv<2, 1, true, true, 4, 2, 10 * 1024>(a, s)
-                   : launch_gemv<2, 1, true, true, 4, 2, kI8XBytes>(a, s);
-    return small ? launch_gemv<2, 1, false, true, 4, 2, 10 * 1024>(a, s)
-                 : launch_gemv<2, 1, false, true, 8, 2, kI8XBytes>(a, s);
+      return swiglu ? launch_gemv<4, 1, true, true, 8, 2, kI8XBytesMost>(a, s)
+                    : launch_gemv<4, 1, false, true, 8, 2, kI8XBytesMost>(a, s);
+    if (bytes <= kI8XBytesFew)
+      return swiglu ? launch_gemv<2, 1, true, true, 4, 2, kI8XBytesFew>(a, s)
+                    : launch_gemv<2, 1, false, true, 4, 2, kI8XBytesFew>(a, s);
+    return swiglu ? launch_gemv<2, 1, true, true, 8, 2, kI8XBytes>(a, s)
+                  : launch_gemv<2, 1, false, true, 8, 2, kI8XBytes>(a, s);
   }
   if (swiglu) switch ((a.M + 7) / 8) {
       case 1: return launch_gemv<1, 1, true, false, 4, 2>(a, s);

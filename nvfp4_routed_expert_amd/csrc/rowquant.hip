@@ -14,6 +14,13 @@
 // Bounded by memory: each element is read once and written once per output.  A
 // row stays in the registers of 1 to 16 waves between its sum, its maximum and
 // its conversion.
+//
+// Measured: 2048 x 5120 bf16 with a bf16 residual to int8 14.3 us, 5.2 TB/s (a
+// copy of 1 GiB moves 5.2), to E4M3 15.6, 4096 x 8192 42.5 (5.5); int8 weights of
+// 17408 x 5120 from f32 81 us, 5.5 TB/s, from bf16 42 us, 6.3 TB/s; one row of 5120
+// 3.9 us on the GPU, most of it the 64-bit quotient and root and two latencies.
+// Loads marked as used once: f32 weights 81 us, 2048 x 5120 f32 10.8 us instead of
+// 9.4.
 #include "int8.h"
 #include "kernels.h"
 
@@ -233,7 +240,7 @@ __global__ __launch_bounds__(THREADS) void row_kernel(const RowArgs p) {
   }
 }
 
-// Rows of any length: a workgroup of 16 waves per row, the row read again for
+// Rows of any length (past 32768 columns): a workgroup of 16 waves per row, the row read again for
 // its conversion (and for its maximum).  With a residual the later passes read
 // the sum that the same lane stored, so that it may replace the residual or x.
 template <bool NORM, RowCodes FMT>

@@ -568,3 +568,23 @@ def test_linear_of_two_row_tiles(M, N):
     """Codes given: 16 or 32 weight rows a workgroup, each number of groups of 8
     rows of x, odd last tiles."""
     test_linear(M, N, 416)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 4112, 10080), (1, 4112, 10208), (15, 4112, 640),
+                                   (16, 4112, 608), (17, 4112, 96), (2, 8192, 10112),
+                                   (2, 8192, 10240), (2, 8208, 10112), (1, 13600, 10112),
+                                   (1, 12800, 10112), (3, 4096, 10752), (3, 4096, 10880),
+                                   (32, 4096, 992), (32, 4096, 1056)])
+def test_where_x_is_quantised(M, N, K):
+    """Either side of the rules by which a product quantises x itself: the bits
+    of the product on the quantiser's codes, for gate and up as well."""
+    say("quantised inside", M, N, K)
+    x = acts(M, K, 7).to(DEV)
+    q, s = native.int8_quantize(x)
+    w, ws = dev_codes(N, K, N)
+    for dt in (torch.float32, torch.bfloat16):
+        y = native.int8_linear(x, w, ws, out_dtype=dt)
+        assert torch.equal(y, dev_linear(q, s, w, ws).to(dt))
+    N = N // 32 * 32
+    mats = (w[:N], ws[:N].contiguous()), dev_codes(N, K, 2), dev_codes(K, N, 3)
+    assert torch.equal(native.int8_mlp(x, *mats), native.int8_mlp(q, *mats, x_scales=s))
