@@ -588,3 +588,37 @@ def test_where_x_is_quantised(M, N, K):
     N = N // 32 * 32
     mats = (w[:N], ws[:N].contiguous()), dev_codes(N, K, 2), dev_codes(K, N, 3)
     assert torch.equal(native.int8_mlp(x, *mats), native.int8_mlp(q, *mats, x_scales=s))
+
+
+# Products with more than 2^31 bytes of codes of x, of W, or elements of y; the
+# rows and columns at their ends, where an offset of 32 bits would be another.
+LONG = [(70000, 80, 33024), (100, 70000, 33024), (70000, 33000, 64), (16, 70000, 33024)]
+
+
+@pytest.mark.parametrize("M,N,K", LONG)
+def test_linear_past_32_bits(M, N, K):
+    say("long", M, N, K)
+    g = torch.Generator(device=DEV).manual_seed(M)
+    x, w = (torch.randint(-128, 128, (r, K), generator=g, dtype=torch.int8, device=DEV)
+            for r in (M, N))
+    xs, ws = (torch.rand(r, generator=g, device=DEV) * 1e-3 + 1e-4 for r in (M, N))
+    y = native.int8_linear(x, w, ws, x_scales=xs)
+    m, n = max(0, M - 24), max(0, N - 96)
+    for r, c in ((slice(m, M), slice(n, N)), (slice(0, 24), slice(n, N)), (slice(m, M), slice(0, 96))):
+        part = native.int8_linear(x[r], w[c], ws[c].clone(), x_scales=xs[r].clone())
+        assert torch.equal(y[r, c], part)
+        ref = linear_ref(x[r].cpu().numpy(), xs[r].cpu().numpy(), w[c].cpu().numpy(),
+                         ws[c].cpu().numpy())
+        same(part, ref, (r, c))
+
+
+@pytest.mark.parametrize("rows,cols", [(140000, 16384), (65600, 33024)])
+def test_quantize_past_32_bits(rows, cols):
+    say("long quantise", rows, cols)
+    g = torch.Generator(device=DEV).manual_seed(rows)
+    x = torch.empty((rows, cols), dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    q, s = native.int8_quantize(x)
+    for r in (slice(0, 5), slice(rows // 2, rows // 2 + 5), slice(rows - 5, rows)):
+        ref, top = quantize_ref(x[r].float().cpu().numpy())
+        assert torch.equal(q[r].cpu().long(), torch.from_numpy(ref))
+        assert torch.equal(s[r].cpu(), torch.from_numpy(top))

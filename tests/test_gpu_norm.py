@@ -195,3 +195,19 @@ def test_norm_in_a_graph():
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+@pytest.mark.parametrize("T,H", [(140000, 16384), (65600, 33024)])
+@pytest.mark.parametrize("codes", ["int8", "fp8"])
+def test_norm_past_32_bits(T, H, codes):
+    """More than 2^31 elements: the first, middle and last rows."""
+    say("long norm", T, H, codes)
+    g = torch.Generator(device=DEV).manual_seed(T)
+    x, res = (torch.empty((T, H), dtype=BF, device=DEV).normal_(generator=g) for _ in range(2))
+    w = acts(1, H, H)[0]
+    rows = [slice(0, 3), slice(T // 2, T // 2 + 3), slice(T - 3, T)]
+    was = [(x[r].cpu(), res[r].cpu()) for r in rows]
+    out = native.rms_norm_quantize(x, w.to(DEV), residual=res, codes=codes, y_dtype=BF,
+                                   out=native.RmsNorm(None, None, None, res))
+    for r, (a, b) in zip(rows, was):
+        check(native.RmsNorm(*(t[r] for t in out)), *norm_ref(a, w, b), codes, BF)
