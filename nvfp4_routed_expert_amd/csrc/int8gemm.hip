@@ -453,27 +453,31 @@ hipError_t launch_plan(const I8GemmArgs &a, int fn, int fm, hipStream_t s) {
     case 4 * 8 + 3: return launch_tile<4, 3, 2, 4, 1, SWIGLU>(a, s);
     case 4 * 8 + 2: return launch_tile<4, 2, 2, 2, 1, SWIGLU>(a, s);
     case 4 * 8 + 1: return launch_tile<4, 1, 3, 2, 1, SWIGLU>(a, s);
+    case 2 * 8 + 3: return launch_tile<2, 3, 3, 2, 1, SWIGLU>(a, s);
     case 2 * 8 + 2: return launch_tile<2, 2, 2, 2, 2, SWIGLU>(a, s);
     case 2 * 8 + 1: return launch_tile<2, 1, 3, 2, 2, SWIGLU>(a, s);
     default: break;
   }
   if constexpr (!SWIGLU) {
     if (fn == 1 && fm == 1) return launch_tile<1, 1, 4, 1, 2, false>(a, s);
+    if (fn == 1 && fm == 3) return launch_tile<1, 3, 4, 1, 1, false>(a, s);
   }
   return hipErrorInvalidValue;
 }
 
 // Tiles, and what a round of them over the CUs takes: per block of 128 columns,
-// and to start and store.  Fitted to measurements of every tile and number of
-// parts at 11 shapes and 33 to 2048 rows (the choice then takes 0.7% longer than
-// the best one on average, 8.5% at most).
+// and to start and store.  Fitted to 6900 measurements, every tile and number of
+// parts at 25 shapes and 33 to 8192 rows with weights that are in no cache (the
+// choice then takes 0.9% longer than the best one on average, 20% at most).
+// Tiles of 192 rows of x: 640 rows of 8192 x 8192 48 us, without them 61; 1024 of
+// 5120 x 5120 32.7 and 41.8.
 struct I8Tile {
   int fn, fm;
   double block_us, ends_us;
 };
-constexpr I8Tile kI8Tiles[] = {{1, 1, 0.21, 1.0}, {2, 1, 0.35, 1.7}, {4, 1, 0.62, 3.0},
-                               {2, 2, 0.41, 2.0}, {4, 2, 0.78, 3.4}, {4, 3, 0.97, 6.0},
-                               {4, 4, 1.24, 8.7}};
+constexpr I8Tile kI8Tiles[] = {{1, 1, 0.25, 1.3}, {2, 1, 0.41, 1.5}, {4, 1, 0.71, 2.7},
+                               {2, 2, 0.57, 1.7}, {4, 2, 0.86, 4.5}, {1, 3, 0.46, 2.9},
+                               {2, 3, 0.68, 3.7}, {4, 3, 0.98, 6.1}, {4, 4, 1.22, 9.1}};
 constexpr int kI8MaxParts = 16;
 
 }  // namespace
@@ -481,10 +485,9 @@ constexpr int kI8MaxParts = 16;
 // The least estimate: rounds of tiles over the CUs; for K parts, which only fill
 // up a single round, another launch and the sums' way through memory; for two
 // launches, whole rounds of one tile and then the columns that are left, in a
-// tile of their own.  Two have to promise 5% and to begin with 256 weight rows a
-// tile: 1024 rows of 17408 x 5120 98.4 and 85.6 us (promised 21%), MLP of 512
-// tokens, 5120 / 17408, 180 and 172; 1024 rows of 5120 x 17408, with tiles of
-// 128 rows first, 100 and 127 (promised 4%).
+// tile of their own.  Two begin with 256 weight rows a tile: 1024 rows of 17408 x
+// 5120 103 us in one launch and 91 in two, MLP of 512 tokens, 5120 / 17408, 177
+// and 171; 1024 rows of 5120 x 17408, with tiles of 128 rows first, 100 and 127.
 I8Plan i8_gemm_plan(bool swiglu, int64_t M, int64_t N, int64_t K) {
   const int64_t KB = (K + kI8Block - 1) / kI8Block, width = swiglu ? 2 * N : N;
   auto rounds_us = [&](const I8Tile &t, int64_t tiles, int64_t ks) {
@@ -509,7 +512,7 @@ I8Plan i8_gemm_plan(bool swiglu, int64_t M, int64_t N, int64_t K) {
     const int64_t tiles = tiles_of(t, N);
     if (tiles >= (int64_t)1 << 23) continue;   // (less than 2^32 work-items; 256 x 256 tiles are fewer)
     for (int64_t ks = 1; ks <= kI8MaxParts && ks <= KB && (ks == 1 || tiles * ks <= kI8CUs); ++ks)
-      offer(rounds_us(t, tiles, ks) + (ks > 1 ? 3.9 + (double)ks * M * width * 8.0 / 4.6e6 : 0.0),
+      offer(rounds_us(t, tiles, ks) + (ks > 1 ? 3.5 + (double)ks * M * width * 8.0 / 6.4e6 : 0.0),
             I8Plan{t.fn, t.fm, (int)ks, N, 0, 0, 0});
     // whole rounds, of as many columns as fill them
     const int64_t m_tiles = (M + 64 * t.fm - 1) / (64 * t.fm);
@@ -518,7 +521,7 @@ I8Plan i8_gemm_plan(bool swiglu, int64_t M, int64_t N, int64_t K) {
     const double main_us = rounds_us(t, tiles_of(t, main), 1) + 3.0;
     for (const I8Tile &r : kI8Tiles)
       if (fits(r))
-        offer((main_us + rounds_us(r, tiles_of(r, N - main), 1)) / 0.95,
+        offer(main_us + rounds_us(r, tiles_of(r, N - main), 1),
               I8Plan{t.fn, t.fm, 1, main, r.fn, r.fm, 0});
   }
   best.partial_ints = best.ksplit > 1 ? (size_t)best.ksplit * M * width : 0;

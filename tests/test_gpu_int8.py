@@ -404,28 +404,38 @@ def test_a_dense_block(T):
 # in parts, last tiles of one row and of all but one, odd N, K with a last block
 # of 32, 64, 96 and 128 columns, parts of different lengths.
 TILE_SHAPES = [(129, 19, 32, 64, 64, 1), (63, 23, 64, 64, 64, 1), (193, 25, 3232, 64, 64, 13),
-               (63, 31, 3264, 64, 64, 13), (513, 1797, 32, 64, 128, 1), (511, 2389, 64, 64, 128, 1),
-               (513, 585, 8288, 64, 128, 5), (511, 689, 10688, 64, 128, 5),
-               (513, 6581, 32, 64, 256, 1), (319, 10881, 64, 64, 256, 1),
-               (63, 16845, 9600, 64, 256, 3), (1025, 1929, 32, 128, 128, 1),
+               (63, 31, 3264, 64, 64, 13), (513, 1797, 32, 64, 128, 1),
+               (511, 2389, 64, 64, 128, 1), (513, 585, 8288, 64, 128, 5),
+               (511, 689, 10688, 64, 128, 5), (513, 6581, 32, 64, 256, 1),
+               (319, 10881, 64, 64, 256, 1), (63, 16845, 9600, 64, 256, 3),
+               (257, 4295, 9184, 64, 256, 3), (1025, 1929, 32, 128, 128, 1),
                (639, 3449, 64, 128, 128, 1), (641, 521, 12192, 128, 128, 8),
-               (639, 793, 10560, 128, 128, 6), (641, 5931, 32, 128, 256, 1),
-               (1023, 4167, 64, 128, 256, 1), (257, 7071, 12640, 128, 256, 3),
-               (1537, 5113, 32, 192, 256, 1), (1535, 5559, 64, 192, 256, 1),
-               (577, 6605, 8928, 192, 256, 2), (575, 7291, 9152, 192, 256, 2),
-               (2049, 6073, 672, 256, 256, 1), (1279, 9783, 704, 256, 256, 1),
-               (255, 16761, 11648, 256, 256, 3)]
+               (127, 8751, 8000, 128, 128, 3), (383, 19401, 448, 128, 256, 1),
+               (513, 11823, 1120, 128, 256, 1), (255, 9119, 6816, 128, 256, 3),
+               (257, 4313, 10208, 128, 256, 5), (767, 2911, 2144, 192, 64, 1),
+               (577, 3311, 1344, 192, 64, 1), (191, 3829, 11680, 192, 64, 4),
+               (961, 1339, 5920, 192, 64, 2), (769, 5295, 1248, 192, 128, 1),
+               (767, 7327, 992, 192, 128, 1), (959, 1465, 9632, 192, 128, 4),
+               (961, 1459, 10976, 192, 128, 3), (961, 9253, 160, 192, 256, 1),
+               (575, 17179, 7840, 192, 256, 1), (191, 12481, 11712, 192, 256, 5),
+               (769, 3933, 11648, 192, 256, 3), (2049, 6073, 672, 256, 256, 1),
+               (1279, 9783, 704, 256, 256, 1), (255, 16761, 11648, 256, 256, 3),
+               (1025, 5985, 12480, 256, 256, 2)]
 # (T, I, H, ...) of the gate and up products
-MLP_TILE_SHAPES = [(65, 32, 32, 64, 128, 1), (63, 32, 64, 64, 128, 1), (65, 32, 1568, 64, 128, 13),
-                   (63, 32, 1600, 64, 128, 13), (129, 8288, 32, 64, 256, 1),
-                   (319, 5568, 64, 64, 256, 1), (63, 8352, 9600, 64, 256, 3),
-                   (1025, 992, 32, 128, 128, 1), (1023, 1056, 64, 128, 128, 1),
-                   (129, 1824, 4000, 128, 128, 4), (1023, 352, 5696, 128, 128, 3),
-                   (1025, 1952, 32, 128, 256, 1), (1023, 2240, 64, 128, 256, 1),
-                   (385, 8256, 32, 192, 256, 1), (575, 6560, 64, 192, 256, 1),
-                   (1537, 1312, 9120, 192, 256, 2), (1535, 1376, 10432, 192, 256, 2),
-                   (1281, 4672, 672, 256, 256, 1), (1279, 5120, 704, 256, 256, 1),
-                   (255, 8352, 11264, 256, 256, 3), (66, 8768, 10304, 128, 256, 3)]
+MLP_TILE_SHAPES = [(65, 32, 32, 64, 128, 1), (63, 32, 64, 64, 128, 1),
+                   (65, 32, 1568, 64, 128, 13), (63, 32, 1600, 64, 128, 13),
+                   (129, 8288, 32, 64, 256, 1), (319, 5568, 64, 64, 256, 1),
+                   (63, 8352, 9600, 64, 256, 3), (1025, 992, 32, 128, 128, 1),
+                   (1023, 1056, 64, 128, 128, 1), (129, 1824, 4000, 128, 128, 4),
+                   (127, 7392, 12928, 128, 128, 2), (511, 7296, 512, 128, 256, 1),
+                   (641, 4640, 1280, 128, 256, 1), (66, 8768, 10304, 128, 256, 3),
+                   (127, 8768, 12384, 128, 256, 3), (383, 5696, 320, 192, 128, 1),
+                   (961, 2208, 736, 192, 128, 1), (383, 2560, 10272, 192, 128, 3),
+                   (385, 2688, 6112, 192, 128, 2), (577, 7776, 1184, 192, 256, 1),
+                   (767, 6464, 1120, 192, 256, 1), (769, 1216, 12032, 192, 256, 5),
+                   (383, 5664, 11616, 192, 256, 2), (1279, 5120, 704, 256, 256, 1),
+                   (1281, 5088, 800, 256, 256, 1), (255, 8352, 11264, 256, 256, 3),
+                   (769, 2464, 12992, 256, 256, 3)]
 
 
 def dev_codes(n, k, seed, scale=1.0):
@@ -515,8 +525,9 @@ def test_large_weights_equal_their_parts(M):
 
 # Products in two launches: (M, N, K, rows of x of a tile, rows of W, columns of
 # y of the first launch); N odd, even and whole, K with every last block.
-TWO_LAUNCHES = [(787, 19315, 928, 128, 256, 18688), (927, 16919, 288, 192, 256, 13056),
-                (1425, 10922, 800, 256, 256, 10752), (1024, 17408, 1280, 256, 256, 16384)]
+TWO_LAUNCHES = [(787, 19315, 928, 192, 256, 13056), (927, 16919, 288, 192, 256, 13056),
+                (1425, 10922, 800, 192, 256, 8192), (1024, 17408, 1280, 256, 256, 16384),
+                (984, 17388, 416, 256, 256, 16384)]
 MLP_TWO_LAUNCHES = [(522, 13472, 288, 192, 256, 10880), (396, 16800, 1312, 256, 256, 16384)]
 
 
