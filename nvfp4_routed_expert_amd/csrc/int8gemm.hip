@@ -468,7 +468,10 @@ hipError_t launch_plan(const I8GemmArgs &a, int fn, int fm, hipStream_t s) {
 // Tiles, and what a round of them over the CUs takes: per block of 128 columns,
 // and to start and store.  Fitted to 6900 measurements, every tile and number of
 // parts at 25 shapes and 33 to 8192 rows with weights that are in no cache (the
-// choice then takes 0.9% longer than the best one on average, 20% at most).
+// choice then takes 1.1% longer than the best one on average, 20% at most); the
+// launch that joins parts is priced to lose ties, which weights in a cache, where
+// it weighs more, would turn (24 rows, 17408 x 5120: from memory 24.8 us with and
+// without three parts, from a cache 21.1 and 16.4).
 // Tiles of 192 rows of x: 640 rows of 8192 x 8192 48 us, without them 61; 1024 of
 // 5120 x 5120 32.7 and 41.8.
 struct I8Tile {
@@ -512,7 +515,7 @@ I8Plan i8_gemm_plan(bool swiglu, int64_t M, int64_t N, int64_t K) {
     const int64_t tiles = tiles_of(t, N);
     if (tiles >= (int64_t)1 << 23) continue;   // (less than 2^32 work-items; 256 x 256 tiles are fewer)
     for (int64_t ks = 1; ks <= kI8MaxParts && ks <= KB && (ks == 1 || tiles * ks <= kI8CUs); ++ks)
-      offer(rounds_us(t, tiles, ks) + (ks > 1 ? 3.5 + (double)ks * M * width * 8.0 / 6.4e6 : 0.0),
+      offer(rounds_us(t, tiles, ks) + (ks > 1 ? 4.2 + (double)ks * M * width * 8.0 / 6.4e6 : 0.0),
             I8Plan{t.fn, t.fm, (int)ks, N, 0, 0, 0});
     // whole rounds, of as many columns as fill them
     const int64_t m_tiles = (M + 64 * t.fm - 1) / (64 * t.fm);

@@ -411,10 +411,10 @@ TILE_SHAPES = [(129, 19, 32, 64, 64, 1), (63, 23, 64, 64, 64, 1), (193, 25, 3232
                (257, 4295, 9184, 64, 256, 3), (1025, 1929, 32, 128, 128, 1),
                (639, 3449, 64, 128, 128, 1), (641, 521, 12192, 128, 128, 8),
                (127, 8751, 8000, 128, 128, 3), (383, 19401, 448, 128, 256, 1),
-               (513, 11823, 1120, 128, 256, 1), (255, 9119, 6816, 128, 256, 3),
+               (513, 11823, 1120, 128, 256, 1), (255, 10289, 8064, 128, 256, 3),
                (257, 4313, 10208, 128, 256, 5), (767, 2911, 2144, 192, 64, 1),
                (577, 3311, 1344, 192, 64, 1), (191, 3829, 11680, 192, 64, 4),
-               (961, 1339, 5920, 192, 64, 2), (769, 5295, 1248, 192, 128, 1),
+               (961, 1319, 10016, 192, 64, 2), (769, 5295, 1248, 192, 128, 1),
                (767, 7327, 992, 192, 128, 1), (959, 1465, 9632, 192, 128, 4),
                (961, 1459, 10976, 192, 128, 3), (961, 9253, 160, 192, 256, 1),
                (575, 17179, 7840, 192, 256, 1), (191, 12481, 11712, 192, 256, 5),
@@ -431,11 +431,10 @@ MLP_TILE_SHAPES = [(65, 32, 32, 64, 128, 1), (63, 32, 64, 64, 128, 1),
                    (641, 4640, 1280, 128, 256, 1), (66, 8768, 10304, 128, 256, 3),
                    (127, 8768, 12384, 128, 256, 3), (383, 5696, 320, 192, 128, 1),
                    (961, 2208, 736, 192, 128, 1), (383, 2560, 10272, 192, 128, 3),
-                   (385, 2688, 6112, 192, 128, 2), (577, 7776, 1184, 192, 256, 1),
-                   (767, 6464, 1120, 192, 256, 1), (769, 1216, 12032, 192, 256, 5),
-                   (383, 5664, 11616, 192, 256, 2), (1279, 5120, 704, 256, 256, 1),
-                   (1281, 5088, 800, 256, 256, 1), (255, 8352, 11264, 256, 256, 3),
-                   (769, 2464, 12992, 256, 256, 3)]
+                   (385, 1696, 9088, 192, 128, 3), (577, 7776, 1184, 192, 256, 1),
+                   (767, 6464, 1120, 192, 256, 1), (769, 2784, 12384, 192, 256, 2),
+                   (1279, 5120, 704, 256, 256, 1), (1281, 5088, 800, 256, 256, 1),
+                   (255, 8352, 11264, 256, 256, 3), (769, 2464, 12992, 256, 256, 3)]
 
 
 def dev_codes(n, k, seed, scale=1.0):
@@ -615,7 +614,8 @@ def test_linear_past_32_bits(M, N, K):
     xs, ws = (torch.rand(r, generator=g, device=DEV) * 1e-3 + 1e-4 for r in (M, N))
     y = native.int8_linear(x, w, ws, x_scales=xs)
     m, n = max(0, M - 24), max(0, N - 96)
-    for r, c in ((slice(m, M), slice(n, N)), (slice(0, 24), slice(n, N)), (slice(m, M), slice(0, 96))):
+    for r, c in ((slice(m, M), slice(n, N)), (slice(0, 24), slice(n, N)),
+                 (slice(m, M), slice(0, 96))):
         part = native.int8_linear(x[r], w[c], ws[c].clone(), x_scales=xs[r].clone())
         assert torch.equal(y[r, c], part)
         ref = linear_ref(x[r].cpu().numpy(), xs[r].cpu().numpy(), w[c].cpu().numpy(),
