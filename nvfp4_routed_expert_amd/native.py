@@ -741,14 +741,14 @@ def _int8_matrix(name, codes, scales):
     return Int8Matrix(codes.data_ptr(), scales.data_ptr(), n, k)
 
 
-def _rows_stride(name, x, dev=None):
-    """Row stride of a matrix of rows (unit column stride, on dev)."""
+def _rows_stride(name, x, rows, cols, dev=None):
+    """Row stride of x [rows, cols] (unit column stride, on dev)."""
     if dev is not None and x.device != dev:
         raise ValueError(f"{name} is on {x.device}, x on {dev}")
     ld, step = x.stride()
-    if step != 1 and x.shape[1] > 1:
+    if step != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
-    return ld if x.shape[0] > 1 else _round_up(x.shape[1], 8)
+    return ld if rows > 1 else _round_up(cols, 8)
 
 
 def int8_quantize(x, out=None):
@@ -758,10 +758,10 @@ def int8_quantize(x, out=None):
     if x.dim() != 2:
         raise ValueError(f"x must be [rows, cols], got {tuple(x.shape)}")
     rows, cols = x.shape
-    ld = _rows_stride("x", x)
+    ld = _rows_stride("x", x, rows, cols)
     if out is None:
         dev = _device_of(x)
-        codes = torch.empty((rows, cols), dtype=torch.int8, device=dev)
+        codes = torch.empty(rows, cols, dtype=torch.int8, device=dev)
         scales = torch.empty(rows, dtype=torch.float32, device=dev)
     else:
         codes, scales = out
@@ -799,7 +799,7 @@ def int8_linear(x, codes, scales, x_scales=None, out_dtype=torch.bfloat16, works
     dev = _device_of(x, rows=x, codes=codes, scales=scales, x_scales=x_scales, out=out,
                      workspace=workspace)
     if out is None:
-        y = torch.empty((M, m.rows), dtype=out_dtype, device=dev)
+        y = torch.empty(M, m.rows, dtype=out_dtype, device=dev)
     else:
         _expect("out", out, (M, m.rows), out.dtype)
         y = out
@@ -825,7 +825,7 @@ def int8_mlp(x, gate, up, down, x_scales=None, out_dtype=torch.bfloat16, workspa
                      up_scales=up[1], down_scales=down[1], x_scales=x_scales, out=out,
                      workspace=workspace)
     if out is None:
-        y = torch.empty((T, H), dtype=out_dtype, device=dev)
+        y = torch.empty(T, H, dtype=out_dtype, device=dev)
     else:
         _expect("out", out, (T, H), out.dtype)
         y = out
@@ -888,35 +888,35 @@ def rms_norm_quantize(x, weight, residual=None, eps=1e-6, codes=None, y_dtype=No
     if residual is not None:
         _expect("residual", residual, (T, H), residual.dtype)
         r_ptr, r_type = residual.data_ptr(), _dt(residual.dtype)
-        r_ld = _rows_stride("residual", residual, dev)
+        r_ld = _rows_stride("residual", residual, T, H, dev)
         if total is None:
-            total = torch.empty((T, H), dtype=residual.dtype, device=dev)
+            total = torch.empty(T, H, dtype=residual.dtype, device=dev)
             t_ld = H
         else:
             _expect("out.residual", total, (T, H), residual.dtype)
-            t_ld = _rows_stride("out.residual", total, dev)
+            t_ld = _rows_stride("out.residual", total, T, H, dev)
         t_ptr = total.data_ptr()
     y_ptr = q_ptr = s_ptr = None
     y_type = 0
     if y_dtype is not None:
         y_type = _dt(y_dtype)
         if y is None:
-            y = torch.empty((T, H), dtype=y_dtype, device=dev)
+            y = torch.empty(T, H, dtype=y_dtype, device=dev)
         else:
             _expect("y", y, (T, H), y_dtype)
         y_ptr = y.data_ptr()
     if fmt:
         shape = (T, _fp8_blocks(H)) if fmt == 1 else (T,)
         if q is None:
-            q = torch.empty((T, H), dtype=code_t, device=dev)
+            q = torch.empty(T, H, dtype=code_t, device=dev)
         else:
             _expect("codes", q, (T, H), code_t)
         if s is None:
-            s = torch.empty(shape, dtype=torch.float32, device=dev)
+            s = torch.empty(*shape, dtype=torch.float32, device=dev)
         else:
             _expect("scales", s, shape, torch.float32)
         q_ptr, s_ptr = q.data_ptr(), s.data_ptr()
-    a = RmsNormArgs(x.data_ptr(), _dt(x.dtype), _rows_stride("x", x), r_ptr, r_type, r_ld, t_ptr,
+    a = RmsNormArgs(x.data_ptr(), _dt(x.dtype), _rows_stride("x", x, T, H), r_ptr, r_type, r_ld, t_ptr,
                     t_ld, weight.data_ptr(), _dt(weight.dtype), eps, y_ptr, y_type, fmt, q_ptr,
                     s_ptr)
     with _on(dev):
@@ -974,7 +974,7 @@ def moe_layer_decode(x, router_w, weights: ExpertWeights, k, renormalize=True, b
     if route_out is None:
         route_out = (torch.empty((T, k), dtype=torch.int32, device=dev),
                      torch.empty((T, k), dtype=torch.float32, device=dev))
-    y = out if out is not None else torch.empty((T, H), dtype=out_dtype, device=dev)
+    y = out if out is not None else torch.empty(T, H, dtype=out_dtype, device=dev)
     _expect("out", y, (T, H), y.dtype)
     L = lib()
     ws = _workspace(L.moe_layer_decode_workspace_size(T, H, I, E, k, Is), dev, workspace)
