@@ -681,8 +681,8 @@ size_t int8_mlp_workspace_size(int64_t T, int64_t H, int64_t I, int quantised);
  * form (64, 128, 192 or 256), sets *columns to its rows of W (gate and up
  * together), *parts to the parts that K is split into and *main to the columns
  * of y that these tiles take (a second launch takes any others in smaller
- * tiles); all 0 for the form for a few rows, and for sizes below 1.  The
- * pointers may be NULL.
+ * tiles); all 0 for the form for a few rows, and for sizes that no call takes.
+ * The pointers may be NULL.
  */
 int int8_debug_plan(int gate_up, int64_t M, int64_t N, int64_t K, int32_t *columns,
                     int32_t *parts, int64_t *main);

@@ -1928,7 +1928,9 @@ nvfp4_status int8_mlp(const void *x, const float *x_scales, int64_t T, const int
 
 int int8_debug_plan(int gate_up, int64_t M, int64_t N, int64_t K, int32_t *columns,
                     int32_t *parts, int64_t *main) {
-  const bool batch = M >= 1 && N >= 1 && K >= 1 && !i8_gemv_supported(gate_up != 0, M, N, K);
+  const bool in = M >= 1 && N >= 1 && K >= 1 && M <= kInt8MaxRows && N <= kInt8MaxRows &&
+                  K <= kInt8MaxCols && M * N <= kInt8MaxOutputs;
+  const bool batch = in && !i8_gemv_supported(gate_up != 0, M, N, K);
   I8Plan p;
   if (batch) p = i8_gemm_plan(gate_up != 0, M, N, K);
   if (columns) *columns = 64 * p.fn;

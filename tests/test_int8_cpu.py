@@ -260,7 +260,9 @@ def test_the_shapes_of_the_gpu_tests_take_the_tiles_they_name():
                                       for split in (False, True)}
     assert native.int8_debug_plan(16, 4096, 4096) == (0, 0, 0, 0)
     assert native.int8_debug_plan(32, 4096, 4096, gate_up=True) == (0, 0, 0, 0)
-    for bad in ((0, 64, 64), (64, 0, 64), (64, 64, 0), (-1, 64, 64)):
+    for bad in ((0, 64, 64), (64, 0, 64), (64, 64, 0), (-1, 64, 64), (2 ** 24 + 1, 64, 64),
+                (64, 2 ** 24 + 1, 64), (64, 64, 131072), (2 ** 19, 2 ** 18, 64),
+                (2 ** 62, 2 ** 62, 2 ** 62)):
         assert native.int8_debug_plan(*bad) == (0, 0, 0, 0)
     assert native.lib().int8_debug_plan(0, 64, 64, 64, None, None, None) > 0
 
