@@ -18,10 +18,11 @@
 // whose pitch is a multiple of 4096 bytes meet in few memory channels (16 rows,
 // 11008 x 4096: 11.4 us, and 9.8 with it; 8192 x 8192: 13.8 and 12.2).
 //
-// Measured: N = 17408, K = 5120, one row 15.5 us (5.8 TB/s), 16 rows from codes
-// 16.9; N = 5120, K = 17408, 8 rows 14.9; a gated MLP of 4 tokens, 5120 / 17408,
-// 53.8 us (5.0 TB/s).  4 waves with 2 blocks each: 3 blocks 17.4, 6 blocks 18.9,
-// 8 waves with 4 blocks 23.0 where 2 take 17.2 (one row from codes, 17408 x 5120).
+// Measured: N = 17408, K = 5120, one row 16.9 us from memory (5.3 TB/s), 14.7 with
+// the same weights again; 16 rows from codes 21.9 and 16.0; N = 5120, K = 17408, 8
+// rows 21.0 and 15.0; a gated MLP of 4 tokens, 5120 / 17408, 57.2 and 52.2 us (4.7
+// and 5.1 TB/s).  4 waves with 2 blocks each: 3 blocks 17.4, 6 blocks 18.9, 8
+// waves with 4 blocks 23.0 where 2 take 17.2 (one row from codes, 17408 x 5120).
 #include "int8.h"
 #include "kernels.h"
 
@@ -228,7 +229,14 @@ __global__ __launch_bounds__(64 * NW) void i8_gemv_kernel(const I8GemvArgs p) {
 template <int XT, int NR, bool SWIGLU, bool QX, int NW, int D, int XCAP = 0>
 hipError_t launch_gemv(const I8GemvArgs &a, hipStream_t s) {
   const dim3 grid((unsigned)((a.N + 16 * NR - 1) / (16 * NR))), block(64 * NW);
-  if ((int64_t)a.N * a.K * (SWIGLU ? 2 : 1) > 128000000)
+  // Weights loaded as used once: past what the caches would keep; for up to 4 rows
+  // of long W already from 64 MB on (one row, 17408 x 5120, from memory 18.3 and
+  // 16.9 us, the same W again 15.4 and 14.7, two W in turn 15.3 and 16.3; 8192 x
+  // 8192 14.8 and 13.7, 13.8 and 12.4, 13.7 and 13.2).  Not so 8 rows (the same W
+  // again 15.2 and 16.1), wide W (5120 x 17408, 14.6 and 16.4) or gate and up (MLP
+  // of one token, 4096 / 11008, 25.9 and 28.4; from memory 30.3 and 29.0).
+  const int64_t bytes = (int64_t)a.N * a.K * (SWIGLU ? 2 : 1);
+  if (bytes > 128000000 || (!SWIGLU && a.M <= 4 && a.N >= a.K && bytes > 64000000))
     launch_kernel((i8_gemv_kernel<XT, NR, SWIGLU, QX, NW, D, XCAP, true>), grid, block, 0, s, a);
   else
     launch_kernel((i8_gemv_kernel<XT, NR, SWIGLU, QX, NW, D, XCAP, false>), grid, block, 0, s, a);

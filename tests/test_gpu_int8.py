@@ -522,6 +522,18 @@ def test_large_weights_equal_their_parts(M):
                                                         ws[-part:].contiguous()))
 
 
+@pytest.mark.parametrize("M", [1, 4, 5])
+def test_long_weights_equal_their_parts(M):
+    """As above, for the size from which up to 4 rows load them so."""
+    N, K, part = 12832, 5120, 384
+    say("long weights", M)
+    x = acts(M, K, 3).to(DEV)
+    w, ws = dev_codes(N, K, 5)
+    y = native.int8_linear(x, w, ws)
+    assert torch.equal(y[:, -part:], native.int8_linear(x, w[-part:].contiguous(),
+                                                        ws[-part:].contiguous()))
+
+
 # Products in two launches: (M, N, K, rows of x of a tile, rows of W, columns of
 # y of the first launch); N odd, even and whole, K with every last block.
 TWO_LAUNCHES = [(787, 19315, 928, 192, 256, 13056), (927, 16919, 288, 192, 256, 13056),
