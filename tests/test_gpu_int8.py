@@ -2,6 +2,7 @@
 sums are integers and every later step is one fp32 operation, so the quantiser
 and the product are compared bit for bit."""
 import sys
+import threading
 
 import numpy as np
 import pytest
@@ -313,6 +314,72 @@ def test_linear_on_two_streams_at_once():
             assert torch.equal(y, want[i % 2])
 
 
+def test_two_graphs_share_a_workspace():
+    """Two captured products in parts of K on one workspace, replayed in turn."""
+    say("graphs on one workspace")
+    N, K = 1000, 4128
+    sizes = (40, 130)
+    assert all(native.int8_debug_plan(M, N, K)[2] > 1 for M in sizes)
+    w, ws = (t.to(DEV) for t in codes(N, K, 71))
+    space = torch.full((native.lib().int8_linear_workspace_size(max(sizes), N, K, 0),), 0xFF,
+                       dtype=torch.uint8, device=DEV)
+    x = [acts(M, K, M).to(DEV) for M in sizes]
+    y = [torch.empty((M, N), dtype=torch.float32, device=DEV) for M in sizes]
+    graphs = []
+    for i in range(2):
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            native.int8_linear(x[i], w, ws, out=y[i], workspace=space)
+        torch.cuda.current_stream().wait_stream(s)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            native.int8_linear(x[i], w, ws, out=y[i], workspace=space)
+        graphs.append(g)
+    for seed in range(3):
+        for i, M in enumerate(sizes):
+            x[i].copy_(acts(M, K, 80 + seed + 10 * i))
+        want = [native.int8_linear(v, w, ws, out_dtype=torch.float32) for v in x]
+        torch.cuda.synchronize()
+        for i in (0, 1, 0):
+            y[i].fill_(7.0)
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(y, want))
+
+
+def test_calls_from_two_threads():
+    """Each thread on a stream of its own; also its refusals are its own."""
+    say("two threads")
+    H, I = 1024, 672
+    mats = [tuple(t.to(DEV) for t in codes(*sh, seed))
+            for seed, sh in ((61, (I, H)), (62, (I, H)), (63, (H, I)))]
+    xs = [acts(T, H, T).to(DEV) for T in (3, 90)]
+    want = [native.int8_mlp(x, *mats) for x in xs]
+    torch.cuda.synchronize()
+    got, errors = [[], []], [[], []]
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(8):
+                got[i].append(native.int8_mlp(xs[i], *mats))
+                try:
+                    native.int8_linear(xs[i], *mats[0], out=xs[i][:, :I].contiguous().view(-1, I),
+                                       workspace=torch.empty(16, dtype=torch.uint8, device=DEV)
+                                       if i else None)
+                except Exception as e:
+                    errors[i].append(str(e))
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert all(torch.equal(y, want[i]) for i in range(2) for y in got[i])
+    assert errors[0] == [] and len(errors[1]) == 8 and all("workspace" in e for e in errors[1])
+
+
 @pytest.mark.parametrize("N,K,rows", [(640, 4096, (455, 384, 385, 130, 65, 64, 20, 1)),
                                       (130, 18560, (150, 64, 65, 33, 2))])
 @pytest.mark.parametrize("pre", [False, True])
@@ -333,7 +400,9 @@ def test_workspace_of_the_largest_batch(N, K, rows, pre):
 
 
 @pytest.mark.parametrize("H,I,rows", [(512, 2080, (260, 200, 70, 65, 64, 33, 32, 1)),
-                                      (2080, 544, (130, 66, 40, 17, 5))])
+                                      (2080, 544, (130, 66, 40, 17, 5)),
+                                      (4128, 672, (260, 100, 65, 40, 33)),
+                                      (640, 4128, (260, 100, 65, 40, 33))])
 def test_mlp_workspace_of_the_largest_batch(H, I, rows):
     say("workspace mlp", H, I)
     mats = [tuple(t.to(DEV) for t in codes(*sh, seed))
