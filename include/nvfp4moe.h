@@ -53,7 +53,8 @@
  *   - K (the contraction length: cols, H or I) must be a positive multiple
  *     of 32, otherwise NVFP4_ERR_UNSUPPORTED_SHAPE.
  *   - Inputs must be finite; NaN or infinite activations, logits or weights
- *     are not checked and give unspecified results.
+ *     are not checked and give unspecified results (int8_quantize says what
+ *     the int8 operators do with them).
  *   - An empty batch (T = 0 tokens, or M = 0 rows for nvfp4_linear) is
  *     valid: the other arguments are checked as usual, the batch's empty
  *     arrays may be NULL, and nothing is computed.  The routing calls
@@ -629,6 +630,9 @@ typedef struct {
  * an fp32 operation rounded to nearest-even:
  *   a = amax |x|;  s = a > 0 ? max(a / 127, 2^-126) : 1;  i = 1 / s;
  *   code = rint(x * i)   (-127 .. 127).
+ * A row of x that holds a NaN or an infinity gets a scale that is not finite,
+ * its codes are unspecified, and int8_linear and int8_mlp give no finite y for
+ * it, also where they quantise x themselves; other rows are as without it.
  * codes and scales must not overlap x or each other.  Requires cols % 32 == 0,
  * cols <= 2^27, rows <= 2^24, ld_x >= cols, ld_x % 8 == 0, ld_x <= 2^31.
  */

@@ -6,7 +6,9 @@
 //   a = max |x|,  s = a > 0 ? max(a / 127, 2^-126) : 1,  i = 1 / s,
 //   code = rint(x * i),
 // which lies in -127 .. 127: x * i is within two roundings of a / s <= 127.
-// The floor keeps i finite (a row of subnormals would overflow it).
+// The floor keeps i finite (a row of subnormals would overflow it).  Maxima keep
+// NaN (gfx950's v_maximum3_f32, as fast as the one that drops it): a row that
+// holds a NaN or an infinity gets a scale that is not finite.
 #pragma once
 
 #include "fp8.h"
@@ -18,10 +20,15 @@ namespace nvfp4 {
 
 constexpr float kInt8Max = 127.0f;
 
+// The larger of two numbers, NaN if either is.
+__device__ __forceinline__ float i8_max(float a, float b) {
+  return __builtin_elementwise_maximum(a, b);
+}
+
 __device__ __forceinline__ float i8_scale(float amax) {
 #pragma clang fp contract(off)
   const float s = amax / kInt8Max;
-  return amax > 0.0f ? fmaxf(s, 0x1p-126f) : 1.0f;
+  return amax == 0.0f ? 1.0f : i8_max(s, 0x1p-126f);
 }
 
 // Four values (already times 1 / s, |v| < 2^22) -> four codes, element 0 in
@@ -49,15 +56,21 @@ __device__ __forceinline__ uint32_t i8_pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
 }
 
-// Maximum over a wave, in every lane.
+// Maximum (as i8_max) over the 16 lanes of a row, and over a wave, in every lane.
+__device__ __forceinline__ float i8_row16_max(float v) {
+  v = i8_max(v, f8_dpp<0xB1>(v));    // lane ^ 1
+  v = i8_max(v, f8_dpp<0x4E>(v));    // lane ^ 2
+  v = i8_max(v, f8_dpp<0x141>(v));   // 7 - i within 8
+  return i8_max(v, f8_dpp<0x140>(v));   // 15 - i within 16
+}
 __device__ __forceinline__ float i8_wave_max(float v) {
-  v = f8_row16_max(v);
+  v = i8_row16_max(v);
   const int b = __builtin_bit_cast(int, v);
   const float a0 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 0));
   const float a1 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 16));
   const float a2 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 32));
   const float a3 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 48));
-  return fmaxf(fmaxf(a0, a1), fmaxf(a2, a3));
+  return i8_max(i8_max(a0, a1), i8_max(a2, a3));
 }
 
 }  // namespace nvfp4

@@ -113,7 +113,7 @@ __global__ __launch_bounds__(64 * NW) void i8_gemv_kernel(const I8GemvArgs p) {
   if constexpr (QX) {
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     auto piece_top = [&](const u32x4 &r, int it) {
-      uint32_t m = 0u;   // bf16 magnitudes order as integers
+      uint32_t m = 0u;   // bf16 magnitudes order as integers, NaN above infinity
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const uint32_t lo = (r[e] << 16) & 0x7FFFFFFFu, hi = r[e] & 0x7FFF0000u;

@@ -111,7 +111,7 @@ __device__ __forceinline__ float row_max(float v, float *part, int wave, int fir
   if ((threadIdx.x & 63) == 0) part[wave] = v;
   __syncthreads();
   v = part[first];
-  for (int w = 1; w < waves; ++w) v = fmaxf(v, part[first + w]);
+  for (int w = 1; w < waves; ++w) v = i8_max(v, part[first + w]);
   return v;
 }
 
@@ -228,7 +228,7 @@ __global__ __launch_bounds__(THREADS) void row_kernel(const RowArgs p) {
 #pragma unroll
       for (int j = 0; j < P; ++j)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, __builtin_fabsf(v[j][i]));
+        for (int i = 0; i < 8; ++i) top = i8_max(top, __builtin_fabsf(v[j][i]));
       const float s = i8_scale(row_max(top, tops, wave, first, waves)), inv = 1.0f / s;
 #pragma unroll
       for (int j = 0; j < P; ++j) {
@@ -302,7 +302,7 @@ __global__ __launch_bounds__(1024) void row_long_kernel(const RowArgs p) {
       for (int64_t col = tid * 8; col < cols; col += 8192) {
         float v[8];
         value(col, v);
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, __builtin_fabsf(v[i]));
+        for (int i = 0; i < 8; ++i) top = i8_max(top, __builtin_fabsf(v[i]));
       }
       s = i8_scale(row_max(top, tops, wave, 0, 16));
       inv = 1.0f / s;

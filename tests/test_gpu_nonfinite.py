@@ -1,0 +1,103 @@
+"""A NaN or an infinity in a row of the int8 quantiser, of the RMS norm and of the
+int8 products: the row's scale, and every product of the row, is not finite, and
+the other rows are those of the batch without it, bit for bit."""
+import sys
+
+import pytest
+import torch
+
+from nvfp4_routed_expert_amd import native
+from test_gpu_int8 import acts, codes
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, FP = torch.bfloat16, torch.float32
+BAD = [float("nan"), float("inf"), float("-inf")]
+
+
+def say(*a):
+    print("[case]", *a, flush=True)
+    sys.stdout.flush()
+
+
+def rows_with(x, bad):
+    """x with `bad` in one element of each of some rows, and those rows."""
+    T, H = x.shape
+    places = {0: 0, T // 2: H // 2 + 3, T - 1: H - 1}
+    y = x.clone()
+    for row, col in places.items():
+        y[row, col] = bad
+    hit = torch.zeros(T, dtype=torch.bool)
+    hit[list(places)] = True
+    return y, hit
+
+
+# 1 to 16 waves a row, and rows past 32768 columns
+@pytest.mark.parametrize("T,H", [(1, 32), (9, 96), (7, 1056), (2100, 1056), (5, 5120), (1200, 5120),
+                                 (5, 17408), (6, 40960)])
+@pytest.mark.parametrize("bad", BAD)
+def test_quantize(T, H, bad):
+    for dtype in (BF, FP):
+        say("quantize", T, H, bad, dtype)
+        x = acts(T, H, T + H, dtype)
+        y, hit = rows_with(x, bad)
+        q, s = (t.cpu() for t in native.int8_quantize(y.to(DEV)))
+        q0, s0 = (t.cpu() for t in native.int8_quantize(x.to(DEV)))
+        assert not torch.isfinite(s[hit]).any()
+        assert torch.equal(s[~hit], s0[~hit]) and torch.equal(q[~hit], q0[~hit])
+
+
+@pytest.mark.parametrize("T,H", [(1, 32), (9, 96), (7, 1056), (2100, 1056), (5, 5120), (1200, 5120),
+                                 (5, 17408), (6, 40960)])
+@pytest.mark.parametrize("bad", BAD)
+def test_norm_int8(T, H, bad):
+    w = acts(1, H, 3)[0].to(DEV)
+    for res_type in (None, BF):
+        say("norm", T, H, bad, res_type)
+        x = acts(T, H, T + H)
+        res = None if res_type is None else acts(T, H, T + 1, res_type).to(DEV)
+        y, hit = rows_with(x, bad)
+        r = native.rms_norm_quantize(y.to(DEV), w, residual=res, codes="int8", y_dtype=BF)
+        r0 = native.rms_norm_quantize(x.to(DEV), w, residual=res, codes="int8", y_dtype=BF)
+        s, s0 = r.scales.cpu(), r0.scales.cpu()
+        assert not torch.isfinite(s[hit]).any()
+        assert torch.equal(s[~hit], s0[~hit])
+        assert torch.equal(r.codes.cpu()[~hit], r0.codes.cpu()[~hit])
+        assert torch.equal(r.y.cpu()[~hit], r0.y.cpu()[~hit])
+
+
+# few rows quantised inside (1 to 32 rows, rows of one and of several pieces), few
+# rows and batches behind a quantiser of their own
+@pytest.mark.parametrize("M,N,K", [(1, 300, 512), (2, 64, 96), (3, 300, 2080), (16, 1000, 544),
+                                   (31, 70, 640), (16, 2048, 2016), (8, 4200, 8224),
+                                   (4, 4200, 640), (40, 300, 1056), (300, 500, 288)])
+@pytest.mark.parametrize("bad", BAD)
+def test_linear(M, N, K, bad):
+    say("linear", M, N, K, bad)
+    x = acts(M, K, M * 7 + K)
+    y, hit = rows_with(x, bad)
+    w, ws = (t.to(DEV) for t in codes(N, K, N + K))
+    want = native.int8_linear(x.to(DEV), w, ws).cpu()
+    got = native.int8_linear(y.to(DEV), w, ws).cpu()
+    assert not torch.isfinite(got[hit]).any()
+    assert torch.equal(got[~hit], want[~hit])
+    q, s = native.int8_quantize(y.to(DEV))
+    parts = native.int8_linear(q, w, ws, x_scales=s).cpu()
+    assert torch.equal(got.view(torch.int16)[~hit], parts.view(torch.int16)[~hit])
+    assert torch.equal(torch.isnan(got), torch.isnan(parts))
+    assert torch.equal(got.nan_to_num(nan=0.0), parts.nan_to_num(nan=0.0))
+
+
+@pytest.mark.parametrize("T,H,I", [(1, 512, 1056), (3, 2080, 320), (16, 96, 2048), (40, 288, 160),
+                                   (300, 160, 288)])
+@pytest.mark.parametrize("bad", BAD)
+def test_mlp(T, H, I, bad):
+    say("mlp", T, H, I, bad)
+    x = acts(T, H, T * 7 + H)
+    y, hit = rows_with(x, bad)
+    gate, up, down = ([t.to(DEV) for t in codes(n, k, n + k + s)]
+                      for n, k, s in ((I, H, 0), (I, H, 1), (H, I, 2)))
+    want = native.int8_mlp(x.to(DEV), gate, up, down).cpu()
+    got = native.int8_mlp(y.to(DEV), gate, up, down).cpu()
+    assert not torch.isfinite(got[hit]).any()
+    assert torch.equal(got[~hit], want[~hit])
