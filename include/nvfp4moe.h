@@ -701,7 +701,9 @@ int int8_debug_plan(int gate_up, int64_t M, int64_t N, int64_t K, int32_t *colum
  *   y = n rounded to y's type; codes and scales = n quantised, without a
  *       rounding to y's type before, as fp8_block_quantize with block_rows = 1
  *       (RMS_NORM_FP8: E4M3 codes [T, H], scales [T, ceil(H / 128)]) or as
- *       int8_quantize (RMS_NORM_INT8: codes [T, H], scales [T]) does.
+ *       int8_quantize (RMS_NORM_INT8: codes [T, H], scales [T]) does.  A row
+ *       with a NaN or an infinity gets scales that are not finite, in E4M3 for
+ *       the blocks of n that hold one (its codes are unspecified, none is NaN).
  * Any of y and the codes may be left out, not both.  x, residual and
  * residual_out have row strides (elements, >= H, multiples of 8, <= 2^31); y,
  * codes and scales are contiguous.  residual_out may be residual itself (same

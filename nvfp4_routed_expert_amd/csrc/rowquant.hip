@@ -131,8 +131,9 @@ __device__ __forceinline__ void store_f8(uint8_t *codes, int64_t at, float *scal
 #pragma clang fp contract(off)
   float top = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = fmaxf(top, __builtin_fabsf(v[i]));
-  const float s = f8_scale(f8_row16_max(top)), inv = 1.0f / s;
+  for (int i = 0; i < 8; ++i) top = i8_max(top, __builtin_fabsf(v[i]));
+  top = i8_row16_max(top);
+  const float s = top == top ? f8_scale(top) : top, inv = 1.0f / s;   // (NaN stays, as in int8)
   if (!in) return;
   *reinterpret_cast<u32x2 *>(codes + at) =
       u32x2{f8_pack4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),

@@ -101,3 +101,36 @@ def test_mlp(T, H, I, bad):
     got = native.int8_mlp(y.to(DEV), gate, up, down).cpu()
     assert not torch.isfinite(got[hit]).any()
     assert torch.equal(got[~hit], want[~hit])
+
+
+@pytest.mark.parametrize("T,H", [(1, 32), (9, 96), (7, 1056), (2100, 1056), (5, 5120), (1200, 5120),
+                                 (5, 17408), (6, 40960)])
+@pytest.mark.parametrize("bad", BAD)
+def test_norm_fp8(T, H, bad):
+    """The scale of the 128 columns that hold it (a NaN: of all of the row's)."""
+    w = acts(1, H, 3)[0].to(DEV)
+    say("norm fp8", T, H, bad)
+    x = acts(T, H, T + H)
+    y, hit = rows_with(x, bad)
+    r = native.rms_norm_quantize(y.to(DEV), w, codes="fp8")
+    r0 = native.rms_norm_quantize(x.to(DEV), w, codes="fp8")
+    s, s0 = r.scales.cpu(), r0.scales.cpu()
+    pad = torch.nn.functional.pad(y.float(), (0, -H % 128)).view(T, -1, 128)
+    blocks = ~torch.isfinite(pad).all(2) if bad == bad else hit[:, None].expand(T, s.shape[1])
+    assert not torch.isfinite(s[blocks]).any()
+    assert torch.equal(s[~hit], s0[~hit])
+    assert torch.equal(r.codes.cpu()[~hit], r0.codes.cpu()[~hit])
+    assert (r.codes.cpu() & 0x7F != 0x7F).all()
+
+
+@pytest.mark.parametrize("T,H,N", [(1, 512, 300), (9, 1056, 96), (90, 2048, 500)])
+@pytest.mark.parametrize("bad", BAD)
+def test_norm_in_front_of_an_fp8_product(T, H, N, bad):
+    say("norm, fp8 product", T, H, N, bad)
+    x, w = acts(T, H, T + H), acts(1, H, 3)[0].to(DEV)
+    y, hit = rows_with(x, bad)
+    wq = native.fp8_block_quantize(acts(N, H, 5).to(DEV), 128)
+    got, want = (native.fp8_block_linear(r.codes, *wq, x_scales=r.scales).cpu() for r in
+                 (native.rms_norm_quantize(t.to(DEV), w, codes="fp8") for t in (y, x)))
+    assert not torch.isfinite(got[hit]).any()
+    assert torch.equal(got[~hit], want[~hit])
