@@ -392,48 +392,47 @@ __global__ __launch_bounds__(256, PER_CU) void i8_gemm_kernel(const I8GemmArgs p
 // 9.5 us, 3.8 TB/s (an output a thread 11.4).
 template <bool SWIGLU, int E>
 __global__ __launch_bounds__(256) void i8_reduce_kernel(const I8GemmArgs p) {
-  const int64_t n_out = p.M * p.N / E, width = SWIGLU ? 2 * (int64_t)p.N : p.N;
-  const int64_t part = p.M * width;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n_out; i += (int64_t)gridDim.x * 256) {
-    const int64_t m = i * E / p.N;
-    const int n = (int)(i * E - m * p.N);
-    const int32_t *s = p.partial + m * width + n;
-    int g[E], u[E];
+  const int64_t width = SWIGLU ? 2 * (int64_t)p.N : p.N, part = p.M * width;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= p.M * p.N / E) return;
+  const int64_t m = i * E / p.N;
+  const int n = (int)(i * E - m * p.N);
+  const int32_t *s = p.partial + m * width + n;
+  int g[E], u[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) g[e] = u[e] = 0;
+  for (int e = 0; e < E; ++e) g[e] = u[e] = 0;
 #pragma unroll 4
-    for (int z = 0; z < p.ksplit; ++z, s += part) {
-      if constexpr (E == 4) {
-        const i32x4 v = *reinterpret_cast<const i32x4 *>(s);
+  for (int z = 0; z < p.ksplit; ++z, s += part) {
+    if constexpr (E == 4) {
+      const i32x4 v = *reinterpret_cast<const i32x4 *>(s);
 #pragma unroll
-        for (int e = 0; e < E; ++e) g[e] += v[e];
-        if constexpr (SWIGLU) {
-          const i32x4 w = *reinterpret_cast<const i32x4 *>(s + p.N);
+      for (int e = 0; e < E; ++e) g[e] += v[e];
+      if constexpr (SWIGLU) {
+        const i32x4 w = *reinterpret_cast<const i32x4 *>(s + p.N);
 #pragma unroll
-          for (int e = 0; e < E; ++e) u[e] += w[e];
-        }
-      } else {
-        g[0] += s[0];
-        if constexpr (SWIGLU) u[0] += s[p.N];
+        for (int e = 0; e < E; ++e) u[e] += w[e];
       }
-    }
-    const float sx = p.xs[m];
-    float v[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      v[e] = i8_value(g[e], sx, p.ws[0][n + e]);
-      if (SWIGLU) v[e] = silu_mul(v[e], i8_value(u[e], sx, p.ws[1][n + e]));
-    }
-    if (p.out_type == OutType::F32) {
-      float *o = static_cast<float *>(p.out) + i * E;
-      if constexpr (E == 4) *reinterpret_cast<f32x4 *>(o) = f32x4{v[0], v[1], v[2], v[3]};
-      else o[0] = v[0];
     } else {
-      uint16_t *o = static_cast<uint16_t *>(p.out) + i * E;
-      if constexpr (E == 4)
-        *reinterpret_cast<u32x2 *>(o) = u32x2{i8_pack_bf16(v[0], v[1]), i8_pack_bf16(v[2], v[3])};
-      else o[0] = (uint16_t)f32_to_bf16_bits(v[0]);
+      g[0] += s[0];
+      if constexpr (SWIGLU) u[0] += s[p.N];
     }
+  }
+  const float sx = p.xs[m];
+  float v[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    v[e] = i8_value(g[e], sx, p.ws[0][n + e]);
+    if (SWIGLU) v[e] = silu_mul(v[e], i8_value(u[e], sx, p.ws[1][n + e]));
+  }
+  if (p.out_type == OutType::F32) {
+    float *o = static_cast<float *>(p.out) + i * E;
+    if constexpr (E == 4) *reinterpret_cast<f32x4 *>(o) = f32x4{v[0], v[1], v[2], v[3]};
+    else o[0] = v[0];
+  } else {
+    uint16_t *o = static_cast<uint16_t *>(p.out) + i * E;
+    if constexpr (E == 4)
+      *reinterpret_cast<u32x2 *>(o) = u32x2{i8_pack_bf16(v[0], v[1]), i8_pack_bf16(v[2], v[3])};
+    else o[0] = (uint16_t)f32_to_bf16_bits(v[0]);
   }
 }
 
@@ -563,8 +562,8 @@ hipError_t launch_i8_gemm(bool swiglu, const I8GemmArgs &args, const I8Plan &pl,
   }
   if (a.ksplit <= 1) return hipSuccess;
   const bool quads = a.N % 4 == 0;
-  const int64_t blocks = (a.M * a.N / (quads ? 4 : 1) + 255) / 256;
-  const dim3 grid((unsigned)(blocks < 1 << 20 ? blocks : 1 << 20)), block(256);
+  // (at least two parts in one round: at most 128 tiles, 2^23 outputs)
+  const dim3 grid((unsigned)((a.M * a.N / (quads ? 4 : 1) + 255) / 256)), block(256);
   if (swiglu) launch_kernel((i8_reduce_kernel<true, 4>), grid, block, 0, s, a);
   else if (quads) launch_kernel((i8_reduce_kernel<false, 4>), grid, block, 0, s, a);
   else launch_kernel((i8_reduce_kernel<false, 1>), grid, block, 0, s, a);
