@@ -50,11 +50,15 @@ __device__ __forceinline__ float i8_value(int sum, float sx, float sw) {
 }
 
 // Two fp32 values -> two bf16 codes, round to nearest even, a in the low half.
+// (The converter keeps every NaN; rounding the bits as an integer turns a NaN of
+// all ones into -0.)
 __device__ __forceinline__ uint32_t i8_pack_bf16(float a, float b) {
   typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
   typedef float f32x2 __attribute__((ext_vector_type(2)));
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
 }
+__device__ __forceinline__ uint16_t i8_bf16(float v) { return (uint16_t)i8_pack_bf16(v, v); }
+__device__ __forceinline__ float i8_round_bf16(float v) { return bf16_bits_to_f32(i8_bf16(v)); }
 
 // Maximum (as i8_max) over the 16 lanes of a row, and over a wave, in every lane.
 __device__ __forceinline__ float i8_row16_max(float v) {

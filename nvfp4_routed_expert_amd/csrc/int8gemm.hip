@@ -432,7 +432,7 @@ __global__ __launch_bounds__(256) void i8_reduce_kernel(const I8GemmArgs p) {
     uint16_t *o = static_cast<uint16_t *>(p.out) + i * E;
     if constexpr (E == 4)
       *reinterpret_cast<u32x2 *>(o) = u32x2{i8_pack_bf16(v[0], v[1]), i8_pack_bf16(v[2], v[3])};
-    else o[0] = (uint16_t)f32_to_bf16_bits(v[0]);
+    else o[0] = i8_bf16(v[0]);
   }
 }
 

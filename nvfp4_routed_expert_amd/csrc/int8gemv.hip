@@ -222,7 +222,7 @@ __global__ __launch_bounds__(64 * NW) void i8_gemv_kernel(const I8GemvArgs p) {
       v = v / (1.0f + expf(-v)) * i8_value(u, sx, p.ws[1][n]);
     }
     if (p.out_type == OutType::F32) static_cast<float *>(p.out)[(int64_t)m * N + n] = v;
-    else static_cast<uint16_t *>(p.out)[(int64_t)m * N + n] = (uint16_t)f32_to_bf16_bits(v);
+    else static_cast<uint16_t *>(p.out)[(int64_t)m * N + n] = i8_bf16(v);
   }
 }
 

@@ -64,8 +64,7 @@ __device__ __forceinline__ void store8(void *p, int64_t i, bool f32, const float
   } else {
     u32x4 w;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      w[j] = f32_to_bf16_bits(v[2 * j]) | (f32_to_bf16_bits(v[2 * j + 1]) << 16);
+    for (int j = 0; j < 4; ++j) w[j] = i8_pack_bf16(v[2 * j], v[2 * j + 1]);
     *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p) + i) = w;
   }
 }
@@ -184,7 +183,7 @@ __global__ __launch_bounds__(THREADS) void row_kernel(const RowArgs p) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           v[j][i] = v[j][i] + r[i];
-          if (RES == 1) v[j][i] = bf16_bits_to_f32(f32_to_bf16_bits(v[j][i]));
+          if (RES == 1) v[j][i] = i8_round_bf16(v[j][i]);
         }
         const int col = (j * step + t) * 8;
         if (ok && col < cols) store8(p.res_out, row * p.ld_out + col, RES == 2, v[j]);
@@ -277,7 +276,7 @@ __global__ __launch_bounds__(1024) void row_long_kernel(const RowArgs p) {
           read(p.res, p.res_f32, row * p.ld_res + col, r);
           for (int i = 0; i < 8; ++i) {
             v[i] = v[i] + r[i];
-            if (!p.res_f32) v[i] = bf16_bits_to_f32(f32_to_bf16_bits(v[i]));
+            if (!p.res_f32) v[i] = i8_round_bf16(v[i]);
           }
           store8(p.res_out, row * p.ld_out + col, p.res_f32, v);
         }

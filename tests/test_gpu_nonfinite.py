@@ -134,3 +134,41 @@ def test_norm_in_front_of_an_fp8_product(T, H, N, bad):
                  (native.rms_norm_quantize(t.to(DEV), w, codes="fp8") for t in (y, x)))
     assert not torch.isfinite(got[hit]).any()
     assert torch.equal(got[~hit], want[~hit])
+
+
+def all_ones(x, row, col):
+    """x with a NaN of all ones at one element."""
+    y = x.clone()
+    y.view(torch.int32)[row, col] = -1
+    assert torch.isnan(y[row, col])
+    return y
+
+
+@pytest.mark.parametrize("H", [96, 1056, 40960])
+def test_nan_of_all_ones_in_the_norm(H):
+    """Rounded to bf16 it stays NaN, in the sum and in y."""
+    T = 5
+    say("nan of all ones, norm", H)
+    x, w = acts(T, H, 1, FP), acts(1, H, 2)[0].to(DEV)
+    res = torch.zeros(T, H, dtype=BF)
+    y = all_ones(x, 2, 7)
+    for codes_ in ("int8", "fp8"):
+        r = native.rms_norm_quantize(y.to(DEV), w, residual=res.to(DEV), codes=codes_, y_dtype=BF)
+        assert torch.isnan(r.residual.cpu()[2, 7]) and torch.isnan(r.y.cpu()[2]).all()
+        assert not torch.isfinite(r.scales.cpu()[2]).any()
+        r0 = native.rms_norm_quantize(x.to(DEV), w, residual=res.to(DEV), codes=codes_, y_dtype=BF)
+        rest = [0, 1, 3, 4]
+        assert torch.equal(r.y.cpu()[rest], r0.y.cpu()[rest])
+        assert torch.equal(r.residual.cpu()[rest], r0.residual.cpu()[rest])
+
+
+# few rows; a batch; a batch in K parts, with rows of y that are not whole quads
+@pytest.mark.parametrize("M,N,K", [(3, 300, 512), (300, 500, 288), (40, 301, 8224), (40, 300, 8224)])
+def test_nan_of_all_ones_in_a_product(M, N, K):
+    say("nan of all ones, linear", M, N, K)
+    x = acts(M, K, 3, FP)
+    q, s = native.int8_quantize(all_ones(x, M - 1, K - 1).to(DEV))
+    w, ws = (t.to(DEV) for t in codes(N, K, N + K))
+    for scale in (s, all_ones(s.cpu()[:, None], M - 1, 0)[:, 0].to(DEV)):
+        y = native.int8_linear(q, w, ws, x_scales=scale).cpu()
+        assert torch.isnan(y[M - 1]).all() and torch.isfinite(y[:M - 1]).all()
