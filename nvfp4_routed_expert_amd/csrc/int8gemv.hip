@@ -1,8 +1,8 @@
 // int8 matrix product with a scale per token and per output channel, for a few
-// rows (M <= 64): one stream of the weights, shared by every row.
+// rows (M <= 32): one stream of the weights, shared by every row.
 //
-// Bounded by the weight stream (one byte per element for at most 64 tokens).
-// A workgroup owns 16 weight rows (16 gate and 16 up rows in the gate/up
+// Bounded by the weight stream (one byte per element for at most 32 tokens).
+// A workgroup owns 16 or 32 weight rows (16 gate and 16 up rows in the gate/up
 // form); its waves take the 128-column blocks of K in turn, so the workgroup
 // reads neighbouring lines of each of its rows at a time.  A wave's blocks
 // arrive in a ring of its own in LDS by direct loads, D ahead, eight whole
@@ -229,12 +229,15 @@ __global__ __launch_bounds__(64 * NW) void i8_gemv_kernel(const I8GemvArgs p) {
 template <int XT, int NR, bool SWIGLU, bool QX, int NW, int D, int XCAP = 0>
 hipError_t launch_gemv(const I8GemvArgs &a, hipStream_t s) {
   const dim3 grid((unsigned)((a.N + 16 * NR - 1) / (16 * NR))), block(64 * NW);
-  // Weights loaded as used once: past what the caches would keep; for up to 4 rows
-  // of long W already from 64 MB on (one row, 17408 x 5120, from memory 18.3 and
-  // 16.9 us, the same W again 15.4 and 14.7, two W in turn 15.3 and 16.3; 8192 x
-  // 8192 14.8 and 13.7, 13.8 and 12.4, 13.7 and 13.2).  Not so 8 rows (the same W
-  // again 15.2 and 16.1), wide W (5120 x 17408, 14.6 and 16.4) or gate and up (MLP
-  // of one token, 4096 / 11008, 25.9 and 28.4; from memory 30.3 and 29.0).
+  // Weights loaded as used once: past what the caches would keep, and up to 4 rows
+  // of N >= K from 64 MB on.  Over 30 shapes of 26 to 127 MB, 1 to 8 rows, it saves 3
+  // to 10% from memory wherever it was tried, and what it takes or saves with the
+  // weights in a cache decides: for those rows 17% less to 8% more (median 2% less;
+  // one row, 17408 x 5120, from memory 20.2 and 18.5 us, the same W again 16.4 and
+  // 15.8, two W in turn 16.4 and 17.1), for N < K 14% less to 15% more (5120 x 17408
+  // 24.3 and 22.4, 18.4 and 20.0, 18.5 and 21.2), for 8 rows 13% less to 17% more.
+  // Gate and up are left too (MLP of one token, 4096 / 11008, from memory 30.3 and
+  // 29.0, the same weights again 25.9 and 28.4).
   const int64_t bytes = (int64_t)a.N * a.K * (SWIGLU ? 2 : 1);
   if (bytes > 128000000 || (!SWIGLU && a.M <= 4 && a.N >= a.K && bytes > 64000000))
     launch_kernel((i8_gemv_kernel<XT, NR, SWIGLU, QX, NW, D, XCAP, true>), grid, block, 0, s, a);
@@ -245,21 +248,29 @@ hipError_t launch_gemv(const I8GemvArgs &a, hipStream_t s) {
 
 }  // namespace
 
-// Up to 16 rows every size (8192 x 8192, 16 rows: 11.9 us, as a batch 15.2; 11008
-// x 4096 9.6 and 9.7).  Up to 32 rows where x, which every workgroup reads, stays
-// small beside the weights and tiles of 64 rows would not fill the CUs: 32 rows,
-// 4096 x 14336 12.0 us and 14.2, 6144 x 6144 10.4 and 12.3, but 5120 x 17408 29.6
-// and 20.7, 11008 x 4096 10.8 and 9.9.  Gate and up: 24 tokens, 5120 / 17408, the
-// MLP 62.7 us and 70.1 as a batch.
+// Up to 16 rows every size (8192 x 8192, 16 rows: 14.5 us, as a batch 18.1; 1024 x
+// 8192 8.2 and 9.4; 64 x 4096 3.8 and 6.9).  Up to 32 rows where x, which every
+// workgroup reads, stays small beside the weights and tiles of 64 rows would not
+// fill the CUs: 32 rows, 4096 x 8192 11.1 us and 12.4, 8192 x 4096 11.1 and 13.1, but
+// 5120 x 17408 29.6 and 20.7, 11008 x 4096 10.8 and 9.9.  Gate and up: 24 tokens, 5120 /
+// 17408, the MLP 62.7 us and 70.1 as a batch.
+// K is not split over workgroups, which the batch form does: few weight rows of a
+// long K are faster there (one row, 512 x 17408, 13.1 us and 9.4; 32 rows, 1024 x 17408,
+// 18.0 and 11.5), but not up to K = 8192.  One row of bf16 is the faster one here all
+// the same (11.5 and 13.2), and no such case is told apart.
 bool i8_gemv_supported(bool swiglu, int64_t M, int64_t N, int64_t K) {
   return M >= 1 && (M <= 16 || (M <= 32 && (swiglu || (N <= 8192 && N * K < 70000000))));
 }
 // x quantised inside, by every workgroup, where that costs less than a launch:
-// with a workgroup per CU at most (16 rows, 2048 x 2048: 8.1 us, with a launch
-// 10.2); where all of them read little (one row, 17408 x 5120: 15.6 and 18.7; 3
-// rows 20.1 and 18.5; gate and up, MLP of 1 and 3 tokens, 5120 / 17408: 50.2 and
-// 53.3, 62.0 and 53.6); with up to two a CU and no up matrix (2 rows, 8192 x 8192:
-// 13.6 and 16.1; 3 rows, 11008 x 4096, 12.8 and 12.0).
+// with a workgroup per CU at most (16 rows, 2048 x 1024: 5.7 us, with a launch 6.0; one
+// row, 2048 x 17408, 12.8 and 18.1); where all of them read little (one row, 17408 x
+// 5120: 15.6 and 18.7; 3 rows 20.1 and 18.5; gate and up, MLP of 1 and 3 tokens, 5120 /
+// 17408: 50.2 and 53.3, 62.0 and 53.6); with up to two a CU and no up matrix (2 rows,
+// 8192 x 8192: 13.6 and 16.1).  Over 316 calls of 70 shapes with weights from memory
+// in a graph it is 12% faster where the rule takes it, 14% slower at the worst (24 rows
+// of 512 x 1024, 6.4 and 5.6); where it does not it would be faster, with weights from
+// memory, at 21 of 100, up to 26% (2 rows, 11008 x 5120, 12.6 and 16.0; with them in a
+// cache 3 rows of 11008 x 4096 take 12.8 and 12.0).
 bool i8_gemv_quantises(bool swiglu, int64_t M, int64_t N, int64_t K) {
   if (!i8_gemv_supported(swiglu, M, N, K)) return false;
   const int64_t bytes = i8_x_bytes(M, K), groups = (N + 15) / 16;
