@@ -20,11 +20,13 @@
 //
 // Measured: M = 2048, N = 17408, K = 5120 164 to 178 us, 2.0 to 2.2 PFLOP/s (a
 // library product of the same size, without the scales, 181 to 204); 8192 x 8192
-// x 8192 426 to 434 us, 2.5 PFLOP/s (441).  What bounds it is power: the matrix
-// unit is busy for 61% of the cycles, at 1.74 GHz instead of 2.4; with operands
-// of zeros the same product takes 148 us.  Of a tile's 60 us, 3 are the first
-// loads, 47 the loop (0.97 to 1.2 us a block, 0.71 on zeros) and 4 to 7 the
-// stores.
+// x 8192 426 to 434 us, 2.5 PFLOP/s (441).  The first in three rounds of 192 x 256
+// tiles, each 40 blocks of 1.16 us and 9.0 us to start and store (slope and
+// intercept of K = 1280 to 5120).  Two things bound it.  Power: on Gaussian codes
+// the card runs at 1.77 GHz (8192^3: 1.63), on zeros, with as many cycles, at 2.30
+// (profiled calls of 164 and 123 us; 433 and 303).  And the cycles without a matrix
+// instruction: the matrix unit is busy for 62% of them (8192^3: 74%), the rest are
+// starts, stores, the last round and waits for LDS and barriers.
 // Slower, or no faster: a workgroup that stays and loads its next tile while it
 // stores (184 us, with the same stores 184 against 178: loads wait behind
 // stores); outputs through LDS (184) or in pieces of 32 bytes (178, but 8192^3
@@ -465,9 +467,10 @@ hipError_t launch_plan(const I8GemmArgs &a, int fn, int fm, hipStream_t s) {
 }
 
 // Tiles, and what a round of them over the CUs takes: per block of 128 columns,
-// and to start and store.  Fitted to 6900 measurements, every tile and number of
-// parts at 25 shapes and 33 to 8192 rows with weights that are in no cache (the
-// choice then takes 1.1% longer than the best one on average, 20% at most); the
+// and to start and store.  Fitted to measurements of every tile and number of parts
+// at 25 shapes and 33 to 8192 rows with weights that are in no cache (over 323 of
+// these sizes the choice takes 1.0% longer than the best one, 20% at most).  A CU is
+// counted as running one tile at a time, also those small enough for two.  The
 // launch that joins parts is priced to lose ties, which weights in a cache, where
 // it weighs more, would turn (24 rows, 17408 x 5120: from memory 24.8 us with and
 // without three parts, from a cache 21.1 and 16.4).
