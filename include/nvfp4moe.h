@@ -615,8 +615,9 @@ int fp8_block_debug_plan(int gate_up, int64_t M, int64_t N, int64_t K, nvfp4_dty
  *   codes  int8 [R, C]  row-major, two's complement;
  *   scales float [R]    one per row: a token of activations, an output
  *          channel of a weight;
- *   and X[r][c] = code * scale[r].  Scales must be finite.  C must be a
- * multiple of 32, R is any number of rows.
+ *   and X[r][c] = code * scale[r].  Scales must be finite, but for those that
+ * int8_quantize and rms_norm_quantize give rows of NaN or infinities.  C must
+ * be a multiple of 32, R is any number of rows.
  */
 typedef struct {
   const int8_t *codes;     /* [rows, cols]                                  */
